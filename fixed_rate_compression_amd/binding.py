@@ -26,6 +26,7 @@ EXPORTED = ["cg_encoded_bytes", "cg_encode", "cg_decode", "cg_decode_gauged", "c
             "cg_gauge_apply", "cg_write_header", "cg_decode_error_workspace_bytes",
             "cg_decode_error", "cg_decode_error_noalloc", "cg_cache_error_summary", "cg_adamw_update", "cg_gauge_control",
             "cg_second_moment_workspace_bytes", "cg_second_moment", "cg_gauge_grad", "cg_gauge_heads",
+            "cg_attend_workspace_bytes", "cg_attend", "cg_append", "cg_evict",
             "cg_last_error"]
 
 CG_KEEP_KEYS, CG_KEEP_VALUES = 1, 2
@@ -65,6 +66,13 @@ class CgStats(ctypes.Structure):
                 ("sum_E", ctypes.c_double)]
 
 
+class CgAttn(ctypes.Structure):
+    _fields_ = [("layer", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("n_queries", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("lengths", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("q_batch_stride", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64)]
+
+
 class CodecGaugeError(RuntimeError):
     def __init__(self, fn, code, msg):
         super().__init__(f"{fn} failed with {code}: {msg}")
@@ -88,7 +96,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
         SP, GP, CP = ctypes.POINTER(CgShape), ctypes.POINTER(CgGauge), ctypes.POINTER(CgCodec)
-        U64P = ctypes.POINTER(ctypes.c_uint64)
+        U64P, AP = ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(CgAttn)
         sig = {
             "cg_encoded_bytes": [SP, CP, U64P, U64P, U64P],
             "cg_encode": [SP, P, GP, CP, I64, I64, P, U64, P, U64, P],
@@ -114,6 +122,10 @@ def lib():
             "cg_second_moment_workspace_bytes": [SP, I32, ctypes.POINTER(ctypes.c_size_t)],
             "cg_second_moment": [SP, P, I32, P, ctypes.c_size_t, P, P],
             "cg_gauge_grad": [I64, I32, P, P, P],
+            "cg_attend_workspace_bytes": [SP, GP, CP, AP, I32, ctypes.POINTER(ctypes.c_size_t)],
+            "cg_attend": [SP, P, U64, P, U64, GP, CP, AP, P, P, P, P, P, ctypes.c_size_t, P],
+            "cg_append": [SP, GP, CP, I32, I32, P, P, I64, I64, P, P, P, P, U64, P, U64, P],
+            "cg_evict": [SP, CP, I32, I32, I32, P, P, U64, P, U64, P, SP, P, U64, P, U64, P, P, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -361,6 +373,109 @@ def cg_write_header(shape, codec, layer, kv) -> bytes:
     _check("cg_write_header", lib().cg_write_header(ctypes.byref(shape), ctypes.byref(codec),
                                                     layer, kv, buf, CG_HEADER_BYTES))
     return buf.raw
+
+
+def _sized(name, t, dtype, count):
+    """A device array argument whose size and type the C call cannot see."""
+    if t is None or isinstance(t, int):
+        return _ptr(t)
+    import torch
+    if t.dtype != getattr(torch, dtype) or t.numel() < count:
+        raise ValueError(f"{name}: {count} values of {dtype} are needed, got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def _storage(shape):
+    return "bfloat16" if shape.dtype == CG_DTYPE_BF16 else "float32"
+
+
+def make_attn(layer, q_heads, n_queries, scale, causal=True, lengths=None, starts=None,
+              q_strides=(0, 0)) -> CgAttn:
+    """lengths, starts: device int32 [batch] (or None); q_strides: elements between
+    sequences and between queries of q (0: dense)."""
+    import torch
+    for name, t in (("lengths", lengths), ("starts", starts)):
+        if t is not None and not isinstance(t, int) and t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32, got {t.dtype}")
+    at = CgAttn(layer, q_heads, n_queries, 1 if causal else 0, scale, _ptr(lengths), _ptr(starts),
+                q_strides[0], q_strides[1])
+    at._keep = (lengths, starts)      # the struct holds raw pointers
+    return at
+
+
+def cg_attend_workspace_bytes(shape, gauge, codec, attn, with_mass=False):
+    b = ctypes.c_size_t()
+    _check("cg_attend_workspace_bytes", lib().cg_attend_workspace_bytes(
+        ctypes.byref(shape), ctypes.byref(gauge), ctypes.byref(codec), ctypes.byref(attn),
+        1 if with_mass else 0, ctypes.byref(b)))
+    return b.value
+
+
+def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=None, workspace=None,
+              stream=None):
+    """Attention of q [batch, n, q_heads, 128] (heads contiguous, the other strides those
+    of attn) over the encoded layer -> out (dense); see the header for lse and mass."""
+    rows = shape.batch * attn.n_queries * attn.q_heads
+    st = _storage(shape)
+    qp = q
+    if not isinstance(q, int):
+        if str(q.dtype) != "torch." + st:
+            raise ValueError(f"q must be {st}, got {q.dtype}")
+        if tuple(q.shape) != (shape.batch, attn.n_queries, attn.q_heads, shape.head_dim):
+            raise ValueError(f"q must be [batch, n, q_heads, head_dim], got {tuple(q.shape)}")
+        want = (attn.q_batch_stride or attn.n_queries * attn.q_heads * shape.head_dim,
+                attn.q_token_stride or attn.q_heads * shape.head_dim, shape.head_dim, 1)
+        if q.numel() and any(n > 1 and s != w for n, s, w in zip(q.shape, q.stride(), want)):
+            raise ValueError(f"q of strides {q.stride()} does not lie as attn says ({want})")
+        qp = q.data_ptr()
+    nblk = shape.token_capacity // codec.block_tokens if codec.block_tokens > 0 else 0
+    _check("cg_attend", lib().cg_attend(
+        ctypes.byref(shape), _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta),
+        ctypes.byref(gauge), ctypes.byref(codec), ctypes.byref(attn), qp,
+        _sized("out", out, st, rows * shape.head_dim), _sized("lse", lse, "float32", rows),
+        _sized("mass", mass, "float32", shape.layers * shape.batch * shape.heads * nblk),
+        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, meta, lengths=None,
+              starts=None, stream=None):
+    """k_new, v_new [batch, n_new, heads, 128] with contiguous heads and the same strides."""
+    st = _storage(shape)
+    row, bs, rs = shape.heads * shape.head_dim, 0, 0
+    ptrs = []
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if str(t.dtype) != "torch." + st:
+            raise ValueError(f"{name} must be {st}, got {t.dtype}")
+        if tuple(t.shape) != (shape.batch, n_new, shape.heads, shape.head_dim):
+            raise ValueError(f"{name} must be [batch, n_new, heads, head_dim], got {tuple(t.shape)}")
+        sb, sr, sh, sd = t.stride()
+        if (sh != shape.head_dim and shape.heads > 1) or sd != 1 or t.stride() != k_new.stride():
+            raise ValueError(f"{name} of strides {t.stride()}: contiguous heads and equal strides are needed")
+        if (shape.batch > 1 and sb == 0) or (n_new > 1 and sr == 0):
+            raise ValueError(f"{name}: rows of an expanded tensor")
+        bs, rs = (sb if shape.batch > 1 else 0), (sr if n_new > 1 else 0)
+        ptrs.append(t.data_ptr())
+    _check("cg_append", lib().cg_append(
+        ctypes.byref(shape), ctypes.byref(gauge), ctypes.byref(codec), layer, n_new, *ptrs, bs, rs,
+        _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
+        _sized("tail", tail, st, shape.layers * 2 * shape.batch * row * codec.block_tokens),
+        _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream(stream)))
+
+
+def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape, payload_out, meta_out,
+             mass_out, kept, lengths_out, lengths=None, stream=None):
+    """Keep `budget` blocks a head by mass; the output arrays may be the inputs (in place)."""
+    heads = shape.layers * shape.batch * shape.heads
+    nblk, nout = (s.token_capacity // codec.block_tokens if codec.block_tokens > 0 else 0
+                  for s in (shape, out_shape))
+    _check("cg_evict", lib().cg_evict(
+        ctypes.byref(shape), ctypes.byref(codec), budget, sink, recent,
+        _sized("mass", mass, "float32", heads * nblk), _ptr(payload), _nbytes(payload), _ptr(meta),
+        _nbytes(meta), _sized("lengths", lengths, "int32", shape.batch), ctypes.byref(out_shape),
+        _ptr(payload_out), _nbytes(payload_out), _ptr(meta_out), _nbytes(meta_out),
+        _sized("mass_out", mass_out, "float32", heads * nout),
+        _sized("kept", kept, "int32", heads * max(budget, 0)),
+        _sized("lengths_out", lengths_out, "int32", shape.batch), _stream(stream)))
 
 
 def cg_last_error() -> str:

@@ -1,0 +1,183 @@
+// cg_attend and its workspace: argument checks, the choice of splits, launches.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/codec_gauge.h"
+#include "attend.hpp"
+#include "cg_check.hpp"
+
+namespace {
+
+using cgh::error;
+
+struct Plan {
+  int64_t rows, tiles;
+  int splits, merge_rows;
+  bool few;  // one row tile: block sums come with the attention
+  int64_t entries;
+  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, qfrag_bytes, qrow_bytes;
+  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + qfrag_bytes + qrow_bytes; }
+};
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Workgroups that keep 256 compute units busy: three on each, with at least
+// 256 tokens (two units a wave) to a workgroup.
+constexpr int64_t kTargetWorkgroups = 768, kMinTokens = 256;
+
+Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {
+  Plan p{};
+  p.rows = (int64_t)t->n_queries * (t->q_heads / s->heads);
+  p.tiles = (p.rows + cga::ROWS - 1) / cga::ROWS;
+  p.few = p.tiles <= 1;
+  const int64_t fields = (int64_t)s->batch * s->heads, work = fields * p.tiles;
+  int64_t sp = work > 0 ? (kTargetWorkgroups + work - 1) / work : 1;
+  const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
+  if (sp > most) sp = most;
+  if (sp < 1) sp = 1;
+  p.splits = (int)sp;
+  p.merge_rows = fields * p.rows <= 2048 ? 1 : cga::ROWS;
+  const int64_t nblk = s->token_capacity / c->block_tokens;
+  p.entries = c->block_tokens == 64 ? 2 * nblk : nblk;
+  const bool parts = p.splits > 1;
+  p.o_bytes = parts ? up256((size_t)(fields * p.splits * p.rows) * cga::D * 4) : 0;
+  p.ml_bytes = parts || (mass && p.few) ? up256((size_t)(fields * p.splits * p.rows) * 8) : 0;
+  if (mass && p.few) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
+  if (mass && !p.few) {
+    p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
+    p.qfrag_bytes = up256((size_t)(fields * p.tiles) * 8 * 64 * 16);
+    p.qrow_bytes = up256((size_t)(fields * p.tiles) * cga::ROWS * 16);
+  }
+  return p;
+}
+
+int check_attn(const cg_shape *s, const cg_attn *t) {
+  if (!t) return error(CG_E_INVAL, "attn is NULL");
+  if (t->layer < 0 || t->layer >= s->layers) return error(CG_E_SHAPE, "layer outside the cache shape");
+  if (t->q_heads <= 0 || t->q_heads % s->heads) return error(CG_E_SHAPE, "q_heads must be a positive multiple of heads");
+  if (t->n_queries < 0) return error(CG_E_SHAPE, "n_queries < 0");
+  if (t->causal != 0 && t->causal != 1) return error(CG_E_INVAL, "causal must be 0 or 1");
+  if (!isfinite(t->scale)) return error(CG_E_INVAL, "scale is not finite");
+  if (((uintptr_t)t->lengths | (uintptr_t)t->starts) & 3u)
+    return error(CG_E_INVAL, "lengths and starts must be 4-byte aligned");
+  const int64_t token = (int64_t)t->q_heads * s->head_dim;
+  const int64_t ts = t->q_token_stride ? t->q_token_stride : token;
+  const int64_t bs = t->q_batch_stride ? t->q_batch_stride : token * t->n_queries;
+  const int64_t unit = s->dtype == CG_DTYPE_BF16 ? 8 : 4, far = (int64_t)1 << 40;
+  if (ts < 0 || bs < 0 || ts % unit || bs % unit || ts > far || bs > far)
+    return error(CG_E_INVAL, "query strides must be multiples of 16 bytes and not negative");
+  // bounds of the launches and of the workspace's sizes
+  const int64_t rows = (int64_t)t->n_queries * (t->q_heads / s->heads);
+  if (rows > (int64_t)1 << 26 || (int64_t)s->batch * s->heads > (int64_t)1 << 22 ||
+      (rows + 15) / 16 * s->batch * s->heads > (int64_t)1 << 27)
+    return error(CG_E_SHAPE, "too many query rows");
+  if ((int64_t)s->batch * s->heads * ((s->tokens + 31) / 32) > (int64_t)1 << 31)
+    return error(CG_E_SHAPE, "too many tokens for one launch");
+  return CG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec,
+                              const cg_attn *attn, int32_t with_mass, size_t *bytes) {
+  cgh::set_error("");
+  if (!bytes) return error(CG_E_INVAL, "bytes is NULL");
+  if (!gauge) return error(CG_E_INVAL, "gauge is NULL");
+  alignas(16) static const char any[16] = {};
+  int rc = cgh::check_cache8(shape, gauge, codec, any, UINT64_MAX, any, UINT64_MAX);
+  if (rc) return rc;
+  if ((rc = check_attn(shape, attn))) return rc;
+  *bytes = make_plan(shape, codec, attn, with_mass != 0).total();
+  return CG_OK;
+}
+
+int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, const void *meta,
+              uint64_t meta_cap, const cg_gauge *gauge, const cg_codec *codec, const cg_attn *attn,
+              const void *q, void *out, float *lse, float *mass, void *workspace, size_t ws_bytes,
+              void *stream) {
+  cgh::set_error("");
+  if (!gauge) return error(CG_E_INVAL, "gauge is NULL");
+  int rc = cgh::check_cache8(shape, gauge, codec, payload, payload_cap, meta, meta_cap);
+  if (rc) return rc;
+  if ((rc = check_attn(shape, attn))) return rc;
+  if (attn->n_queries == 0) return CG_OK;
+  if (!q || !out) return error(CG_E_INVAL, "q or out is NULL");
+  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15u)
+    return error(CG_E_INVAL, "q, out and workspace must be 16-byte aligned");
+  if (((uintptr_t)lse | (uintptr_t)mass) & 3u) return error(CG_E_INVAL, "lse and mass must be 4-byte aligned");
+  const int64_t esz = shape->dtype == CG_DTYPE_BF16 ? 2 : 4;
+  const int64_t token = (int64_t)attn->q_heads * shape->head_dim;
+  const int64_t ts = attn->q_token_stride ? attn->q_token_stride : token;
+  const int64_t bs = attn->q_batch_stride ? attn->q_batch_stride : token * attn->n_queries;
+  const char *q0 = (const char *)q, *o0 = (const char *)out;
+  const int64_t qb = ((shape->batch - 1) * bs + (attn->n_queries - 1) * ts + token) * esz;
+  const int64_t ob = (int64_t)shape->batch * attn->n_queries * token * esz;
+  if (q0 < o0 + ob && o0 < q0 + qb) return error(CG_E_INVAL, "q and out overlap");
+  const Plan p = make_plan(shape, codec, attn, mass != nullptr);
+  if (p.total() && (!workspace || ws_bytes < p.total()))
+    return error(CG_E_SIZE, "workspace missing or smaller than cg_attend_workspace_bytes");
+
+  cga::AttendArgs a{};
+  const int64_t fields = (int64_t)shape->batch * shape->heads, d = shape->head_dim;
+  const int64_t kf = (int64_t)attn->layer * 2 * fields, vf = kf + fields;
+  a.tcap = shape->token_capacity;
+  a.tokens = shape->tokens;
+  a.nblk = a.tcap / codec->block_tokens;
+  a.kpay = (const uint8_t *)payload + kf * a.tcap * d;
+  a.vpay = (const uint8_t *)payload + vf * a.tcap * d;
+  a.kmeta = (const float2 *)meta + kf * a.nblk;
+  a.vmeta = (const float2 *)meta + vf * a.nblk;
+  a.lengths = attn->lengths;
+  a.starts = attn->starts;
+  a.g = gauge->group;
+  a.gk = gauge->group ? gauge->G + (int64_t)attn->layer * 2 * shape->heads * d * gauge->group : nullptr;
+  a.gv = gauge->group ? a.gk + (int64_t)shape->heads * d * gauge->group : nullptr;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.mass = mass ? mass + (int64_t)attn->layer * fields * a.nblk : nullptr;
+  a.q_bs = bs;
+  a.q_ts = ts;
+  a.batch = shape->batch;
+  a.heads = shape->heads;
+  a.ratio = attn->q_heads / shape->heads;
+  a.n = attn->n_queries;
+  a.rows = (int32_t)p.rows;
+  a.tiles = (int32_t)p.tiles;
+  a.bshift = codec->block_tokens == 16 ? 4 : codec->block_tokens == 32 ? 5 : 6;
+  a.causal = attn->causal;
+  a.splits = p.splits;
+  a.merge_rows = p.merge_rows;
+  a.entries = p.entries;
+  a.c = (float)((double)attn->scale * 1.4426950408889634074);
+  char *w = (char *)workspace;
+  auto take = [&w](size_t n) { char *r = n ? w : nullptr; w += n; return r; };
+  a.part_o = (float *)take(p.o_bytes);
+  a.part_ml = (float2 *)take(p.ml_bytes);
+  a.bsum = (float2 *)take(p.bsum_bytes);
+  a.lse2 = (float *)take(p.lse2_bytes);
+  a.qfrag = (uint4 *)take(p.qfrag_bytes);
+  a.qrow = (float4 *)take(p.qrow_bytes);
+
+  const bool bf16 = shape->dtype == CG_DTYPE_BF16;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = cga::rows_launch(a, bf16, st);
+  if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
+  if (p.splits > 1 && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
+    return cgh::hip_error(e, "cg_attend merge launch");
+  if (mass && shape->tokens > 0) {
+    if (p.few) {
+      e = cga::mass_finish_launch(a, st);
+    } else {
+      e = cga::prepare_launch(a, bf16, st);
+      if (e == hipSuccess) e = cga::mass_many_launch(a, st);
+    }
+    if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
+  }
+  return CG_OK;
+}
+
+}  // extern "C"

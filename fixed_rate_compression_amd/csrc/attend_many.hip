@@ -1,0 +1,131 @@
+// Many query rows over the 8-bit cache: the gauged queries as matrix-core
+// operands, laid out once, and the second pass over the keys that gives the
+// weight each block received.
+#include "attend.hpp"
+
+namespace cga {
+
+// One workgroup per row tile: gauge, split into fp16 parts, and store in
+// operand order, with each row's factors and limit.
+template <bool BF16>
+__global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
+  __shared__ __align__(16) float xs[ROWS * PITCH], ys[ROWS * PITCH];
+  const int64_t id = blockIdx.x;
+  const int tile = (int)(id % a.tiles), bh = (int)(id / a.tiles);
+  const int h = bh % a.heads, b = bh / a.heads;
+  const int r0 = tile * ROWS, nr = min(ROWS, a.rows - r0);
+  load_rows<BF16>(a, b, h, r0, xs);
+  if (nr < ROWS)
+    for (int i = threadIdx.x; i < (ROWS - nr) * D; i += NTH) ys[(nr + (i >> 7)) * PITCH + (i & 127)] = 0.0f;
+  __syncthreads();
+  gauge_rows<false>(xs, nr, a.gk + (int64_t)h * D * a.g, a.g, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  QueryFrags q;
+  make_frags(ys, a.c, q);
+  const int lane = threadIdx.x;
+  uint4 *d = a.qfrag + id * 8 * 64 + lane;
+#pragma unroll
+  for (int s = 0; s < 4; s++) {
+    d[s * 64] = __builtin_bit_cast(uint4, q.hi[s]);
+    d[(4 + s) * 64] = __builtin_bit_cast(uint4, q.lo[s]);
+  }
+  if (lane < ROWS) {
+    const int len = seq_length(a, b);
+    const int lim = lane < nr ? query_limit(a, b, len, (r0 + lane) / a.ratio) : 0;
+    a.qrow[id * ROWS + lane] = make_float4(q.ca, q.cq, __int_as_float(lim), 0.0f);
+  }
+}
+
+// A wave owns 32 tokens (64 where a block has 64: twice 32) of one field, holds
+// their codes as operands and walks the row tiles: weights 2^(s - log2 sum),
+// summed over rows and tokens of a block in a fixed order by their one owner.
+__global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t groups) {
+  const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t wgs = (groups + 3) / 4;
+  const int bh = (int)(blockIdx.x / wgs);
+  const int64_t grpi = (blockIdx.x % wgs) * 4 + wave;
+  const int b = bh / a.heads;
+  const int len = seq_length(a, b);
+  const int tmax = limit_of(a, b, len, 0, a.n - 1);
+  const int per = a.bshift == 6 ? 2 : 1;
+  if (grpi * per * UNIT >= tmax) return;
+  const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D;
+  const float2 *km = a.kmeta + (int64_t)bh * a.nblk;
+  float total[2] = {0.0f, 0.0f};
+  for (int half = 0; half < per; half++) {
+    const int t0 = (int)(grpi * per + half) * UNIT;
+    if (t0 >= tmax) break;
+    h8_t kc[2][4];
+    float2 m[2];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      const int64_t tt = min((int64_t)t0 + 16 * t, a.tcap - 16);  // 16-token blocks: the capacity may end here
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const uint4 w = *(const uint4 *)(kf + (tt + row) * D + 64 * x + 16 * grp);
+        kc[t][2 * x] = codes8<true>(w.x, w.y);
+        kc[t][2 * x + 1] = codes8<true>(w.z, w.w);
+      }
+      m[t] = km[tt >> a.bshift];
+    }
+    float sum[2] = {0.0f, 0.0f};
+    for (int tile = 0; tile < a.tiles; tile++) {
+      const int r1 = min(a.rows, (tile + 1) * ROWS) - 1;
+      if (limit_of(a, b, len, tile * ROWS / a.ratio, r1 / a.ratio) <= t0) continue;
+      const int64_t id = (int64_t)bh * a.tiles + tile;
+      const uint4 *qf = a.qfrag + id * 8 * 64 + lane;
+      const float4 qr = a.qrow[id * ROWS + row];
+      const int lim = __float_as_int(qr.z);
+      const int r = tile * ROWS + row;
+      const float lse2 = r < a.rows ? a.lse2[(int64_t)bh * a.rows + r] : INFINITY;
+      f4_t z[2] = {f4_t{0.f, 0.f, 0.f, 0.f}, f4_t{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int s = 0; s < 8; s++) {
+        const h8_t qv = __builtin_bit_cast(h8_t, qf[s * 64]);
+        z[0] = mfma(kc[0][s & 3], qv, z[0]);
+        z[1] = mfma(kc[1][s & 3], qv, z[1]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const float A = m[t].y * qr.x, Bm = __builtin_fmaf(128.0f, m[t].y, m[t].x) * qr.y - lse2;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const float s = __builtin_fmaf(z[t][k], A, Bm);
+          sum[t] += t0 + 16 * t + 4 * grp + k < lim ? exp2_fast(s) : 0.0f;
+        }
+      }
+    }
+    total[0] += sum[0];
+    total[1] += sum[1];
+  }
+#pragma unroll
+  for (int t = 0; t < 2; t++)
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) total[t] += __shfl_xor(total[t], k);
+  if (lane) return;
+  float *out = a.mass + (int64_t)bh * a.nblk;
+  if (a.bshift == 4) {
+    out[2 * grpi] += total[0];
+    if (2 * grpi + 1 < a.nblk) out[2 * grpi + 1] += total[1];
+  } else {
+    out[grpi] += total[0] + total[1];
+  }
+}
+
+hipError_t prepare_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.tiles)), block(NTH);
+  if (bf16) hipLaunchKernelGGL(k_attend_prepare<true>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(k_attend_prepare<false>, grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t mass_many_launch(const AttendArgs &a, hipStream_t s) {
+  const int64_t span = a.bshift == 6 ? 2 * UNIT : UNIT, groups = (a.tokens + span - 1) / span;
+  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * ((groups + 3) / 4))), block(NTH);
+  hipLaunchKernelGGL(k_mass_many, grid, block, 0, s, a, groups);
+  return hipGetLastError();
+}
+
+}  // namespace cga

@@ -357,6 +357,28 @@ bool expm_frechet(int n, const double *M, const double *D, double *R, double *L)
   return expm_frechet_pade13(n, M, D, R, L);
 }
 void set_error(const char *msg) { g_err = msg; }
+int error(int code, const char *msg) { return fail(code, "%s", msg); }
+int hip_error(hipError_t e, const char *what) { return hip_fail(e, what); }
+int check_cache8(const cg_shape *s, const cg_gauge *g, const cg_codec *c, const void *payload,
+                 uint64_t payload_cap, const void *meta, uint64_t meta_cap) {
+  int rc;
+  if ((rc = check_shape(s))) return rc;
+  if ((rc = check_codec(c, s))) return rc;
+  if (c->backend != CG_BACKEND_BLOCK_UNIFORM || c->bits != 8)
+    return fail(CG_E_UNSUPPORTED, "this operator reads block-uniform caches of 8 bits");
+  if (g && (rc = check_gauge(g, s, c))) return rc;
+  if (s->kv != 2) return fail(CG_E_SHAPE, "the cache needs keys and values (kv = 2)");
+  if (s->token_capacity > (int64_t)0x7fffff00) return fail(CG_E_SHAPE, "token_capacity is over 2^31 - 256");
+  if (!payload || !meta) return fail(CG_E_INVAL, "payload or meta is NULL");
+  if (misaligned(payload) || misaligned(meta)) return fail(CG_E_INVAL, "payload and meta must be 16-byte aligned");
+  uint64_t need_p, need_m;
+  byte_counts(s, c, &need_p, &need_m);
+  if (payload_cap < need_p) return fail(CG_E_SIZE, "payload_cap %llu < %llu", (unsigned long long)payload_cap,
+                                        (unsigned long long)need_p);
+  if (meta_cap < need_m) return fail(CG_E_SIZE, "meta_cap %llu < %llu", (unsigned long long)meta_cap,
+                                     (unsigned long long)need_m);
+  return CG_OK;
+}
 }  // namespace cgh
 
 extern "C" {

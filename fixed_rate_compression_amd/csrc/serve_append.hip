@@ -1,0 +1,130 @@
+// New K/V rows into the 8-bit block-uniform cache: gauge and quantization of
+// the blocks they fall in, every sequence at its own position.
+//
+// A block's range is that of all its rows, so the block that receives a row
+// is encoded again from the raw rows (kept beside the cache, `tail`) and the
+// new ones.  Rows that are not there yet take no part in the range and their
+// codes are not written.  One workgroup takes a 64-row strip of one (K/V,
+// sequence, head), strips counted from the block of the first new row; the
+// gauge and the quantizer are the encoder's.  The raw rows of the last block
+// are stored by the workgroup that reads those of the first, after its reads.
+#include "cg_tile.hpp"
+#include "quant_kernels.hpp"
+#include "serve.hpp"
+
+namespace cgs {
+
+using namespace cgk;
+
+template <bool BF16, int G>
+__global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
+  __shared__ __align__(16) float xs[TILE_T * PITCH];
+  __shared__ float red[8];
+  constexpr size_t ESZ = BF16 ? 2 : 4;
+  int64_t id = blockIdx.x;
+  const int strip = (int)(id % a.tiles);
+  id /= a.tiles;
+  const int h = (int)(id % a.heads);
+  id /= a.heads;
+  const int b = (int)(id % a.batch), kind = (int)(id / a.batch);
+  const int64_t len = min(max(a.lengths ? (int64_t)a.lengths[b] : a.tokens, (int64_t)0), a.tokens);
+  const int64_t start = a.starts ? (int64_t)a.starts[b] : len - a.n;
+  const int64_t p0 = max(start, (int64_t)0), p1 = min(start + a.n, len);  // positions of the new rows
+  if (p1 <= p0) return;
+  const int BT = a.block;
+  const int64_t head = p0 / BT * BT, end = (p1 + BT - 1) / BT * BT;  // whole blocks
+  const int64_t tb = head + (int64_t)strip * TILE_T;
+  if (tb >= end) return;
+  const int nrows = (int)min((int64_t)TILE_T, end - tb);
+  const int64_t f = ((int64_t)kind * a.batch + b) * a.heads + h;
+  const uint8_t *src = (const uint8_t *)(kind ? a.v : a.k) + ((int64_t)b * a.batch_stride + (int64_t)h * D) * ESZ;
+  uint8_t *tail = (uint8_t *)a.tail + f * BT * D * ESZ;
+
+  TileGauge<G, false> tg;
+  if constexpr (G != 0) tg.load(a.gauges + ((int64_t)kind * a.heads + h) * D * G);
+  for (int i = threadIdx.x; i < nrows * 16; i += NT) {
+    const int r = i >> 4, c = (i & 15) * 8;
+    const int64_t p = tb + r;
+    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+    if (p < p1) {
+      const uint8_t *row = p >= p0 ? src + (p - start) * a.row_stride * ESZ : tail + (p - head) * D * ESZ;
+      if (BF16) {
+        const uint4 w = *(const uint4 *)(row + c * ESZ);
+        lo = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+        hi = make_float4(bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w));
+      } else {
+        lo = *(const float4 *)(row + c * ESZ);
+        hi = *(const float4 *)(row + c * ESZ + 16);
+      }
+    }
+    *(float4 *)(xs + r * PITCH + c) = lo;
+    *(float4 *)(xs + r * PITCH + c + 4) = hi;
+  }
+  __syncthreads();
+  if (strip == 0) {  // the raw rows of the last block
+    const int64_t q0 = max(p0, (p1 - 1) / BT * BT);
+    const int per = (int)(D * ESZ / 16);
+    for (int i = threadIdx.x; i < (int)(p1 - q0) * per; i += NT) {
+      const int64_t p = q0 + i / per;
+      *(uint4 *)(tail + (p % BT) * D * ESZ + 16 * (i % per)) =
+          *(const uint4 *)(src + (p - start) * a.row_stride * ESZ + 16 * (i % per));
+    }
+  }
+  if constexpr (G != 0) {
+    tg.apply(xs, nrows);
+    __syncthreads();
+  }
+  const int t = threadIdx.x >> 2, j = threadIdx.x & 3, w = threadIdx.x >> 6;
+  const bool active = t < nrows && tb + t < p1;
+  float v[32];
+  float mn = INFINITY, mx = -INFINITY;
+  if (active) {
+    cgq::read32(xs, t, j, v);
+#pragma unroll
+    for (int k = 0; k < 32; k++) {
+      mn = fminf(mn, v[k]);
+      mx = fmaxf(mx, v[k]);
+    }
+  }
+  mn = cgq::wave_min(mn);
+  mx = cgq::wave_max(mx);
+  if ((threadIdx.x & 63) == 0) {
+    red[2 * w] = mn;
+    red[2 * w + 1] = mx;
+  }
+  __syncthreads();
+  if (!active) return;
+  const int wpb = BT / 16, w0 = (t / BT) * wpb;
+  mn = red[2 * w0];
+  mx = red[2 * w0 + 1];
+  for (int k = 1; k < wpb; k++) {
+    mn = fminf(mn, red[2 * (w0 + k)]);
+    mx = fmaxf(mx, red[2 * (w0 + k) + 1]);
+  }
+  const cgq::Range r = cgq::make_range(mn, mx, 255);
+  uint32_t q[32], wd[8];
+#pragma unroll
+  for (int k = 0; k < 32; k++) q[k] = cgq::quant1(v[k], r, 255);
+  cgq::pack32<8>(q, wd);
+  cgq::store_words<8>(a.payload + (f * a.tcap + tb + t) * D + 32 * j, wd);
+  if (j == 0 && t % BT == 0) {
+    float *m = a.meta + 2 * (f * a.nblk + (tb + t) / BT);
+    m[0] = r.mn;
+    m[1] = r.scale;
+  }
+}
+
+hipError_t append_launch(const AppendArgs &a, bool bf16, int g, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)2 * a.batch * a.heads * a.tiles)), block(NT);
+#define CG_A(BF, GG)                                               \
+  if (bf16 == BF && g == GG) {                                     \
+    hipLaunchKernelGGL((k_append<BF, GG>), grid, block, 0, s, a);  \
+    return hipGetLastError();                                      \
+  }
+  CG_A(true, 0) CG_A(true, 8) CG_A(true, 16) CG_A(true, 32) CG_A(true, 128)
+  CG_A(false, 0) CG_A(false, 8) CG_A(false, 16) CG_A(false, 32) CG_A(false, 128)
+#undef CG_A
+  return hipErrorInvalidValue;
+}
+
+}  // namespace cgs

@@ -394,6 +394,109 @@ int cg_second_moment(const cg_shape *shape, const void *kv, int32_t g, void *wor
 int cg_write_header(const cg_shape *shape, const cg_codec *codec, int32_t layer, int32_t kv,
                     void *header_host, uint64_t cap);
 
+/*
+ * Serving on the encoded cache: append, attend, evict.
+ *
+ * These read and write a BLOCK_UNIFORM cache of 8 bits (block_tokens 16, 32 or
+ * 64; shape->kv == 2) where it lies: payload and meta as cg_encode lays them
+ * out, values x' = minimum + step * code in gauged coordinates.  Sequences of
+ * a batch have their own lengths:
+ *   lengths  device int32 [batch], valid rows of each sequence, with the rows
+ *            of the present step; NULL: shape->tokens.  Values outside
+ *            [0, tokens] count as the nearest of the two.
+ *   starts   device int32 [batch], position of each sequence's first query
+ *            (cg_attend) or new row (cg_append); NULL: lengths - n, the last n
+ *            positions.  Query or row i stands at starts + i; positions below
+ *            0 or at lengths and above are padding.
+ * shape->tokens only bounds the lengths (and sizes launches and workspaces),
+ * so calls recorded into a graph may be replayed as the lengths grow.
+ * Codes and ranges of rows behind a sequence's end are never looked at (a
+ * block's codes past its last row are read and left out).
+ */
+typedef struct cg_attn {
+  int32_t layer;          /* cache layer */
+  int32_t q_heads;        /* query heads, a multiple of shape->heads: query head
+                             j reads KV head j / (q_heads / heads) */
+  int32_t n_queries;      /* queries of each sequence, n >= 0 (0: nothing is done) */
+  int32_t causal;         /* 1: a query sees positions up to its own; 0: the
+                             whole sequence */
+  float scale;            /* factor of the scores, e.g. 1 / sqrt(head_dim); finite */
+  const int32_t *lengths;
+  const int32_t *starts;
+  int64_t q_batch_stride; /* elements between sequences / queries of q (0: dense), */
+  int64_t q_token_stride; /* multiples of 16 bytes; a query's heads are contiguous */
+} cg_attn;
+
+/* Device scratch of cg_attend (host only).  with_mass: nonzero if mass is given. */
+int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec,
+                              const cg_attn *attn, int32_t with_mass, size_t *bytes);
+
+/*
+ * Attention over the encoded rows: with k = G_K^T k' and v = G_V^T v' of the
+ * decoded (unrounded) values,
+ *   out[b][i][j] = sum_t p_t v_t,  p = softmax over the visible t of scale q . k_t
+ * computed as (G_K q) . k' and G_V^T (sum p v').
+ *   q     device, storage format, [batch][n_queries][q_heads][head_dim] (strides
+ *         above); out the same, dense; they must not overlap (CG_E_INVAL)
+ *   lse   device fp32 [batch][n_queries][q_heads] or NULL: log of the row's sum
+ *         of exp(score)
+ *   mass  device fp32 [layers][batch][heads][token_capacity / block_tokens] or
+ *         NULL: every block of the layer gains the sum of the weights that its
+ *         rows received from all visible queries and all heads of the group
+ * A query that sees nothing (padding, an empty sequence) gives zeros and an
+ * lse of -inf, and no mass.  Scores, sums and weights of a sum are fp32; the
+ * operands of the matrix products are fp16: queries in two parts (2^-22), for
+ * fp32 storage the weights too, for bf16 storage one part (2^-11 of a weight).
+ * The order of sums depends on the shape and the lengths only (deterministic).
+ * The workspace belongs to one call at a time.  Asynchronous on stream.
+ */
+int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, const void *meta,
+              uint64_t meta_cap, const cg_gauge *gauge, const cg_codec *codec, const cg_attn *attn,
+              const void *q, void *out, float *lse, float *mass, void *workspace, size_t ws_bytes,
+              void *stream);
+
+/*
+ * New K/V rows into one layer of the cache, each sequence at its own position.
+ *   k_new, v_new  device, storage format, [batch][n_new][heads][head_dim] with
+ *                 the given strides in elements (0: dense; multiples of 16 bytes)
+ *   tail          device, storage format, [layers][2][batch][heads][block_tokens]
+ *                 [head_dim]: the raw rows of every field's last block, slot
+ *                 position % block_tokens; read for the rows of the first new
+ *                 row's block that stand before it, and updated
+ * Every block that receives a row is encoded again from its raw rows: gauge
+ * (fp32 fmaf chains, any built group), range over the rows that are there,
+ * codes as in cg_encode.  Codes of rows behind the last are left as they were.
+ * The rows must continue the sequence (or rewrite rows of its last block).
+ */
+int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec, int32_t layer,
+              int32_t n_new, const void *k_new, const void *v_new, int64_t batch_stride,
+              int64_t row_stride, const int32_t *lengths, const int32_t *starts, void *tail,
+              void *payload, uint64_t payload_cap, void *meta, uint64_t meta_cap, void *stream);
+
+/*
+ * Eviction by accumulated attention weight, all layers: a (layer, sequence,
+ * head) with more than `budget` blocks keeps its first `sink`, its last
+ * `recent` (>= 1) and, of the others, those of the largest mass (ties: the
+ * lowest block; NaN is below every number); sequences within the budget keep
+ * all.  Kept blocks move to the front in order, codes and ranges as they are.
+ *   mass         [layers][batch][heads][token_capacity / block_tokens]
+ *   out_shape    the cache the blocks move to: same layers, batch and heads,
+ *                room for `budget` blocks; payload_out, meta_out, mass_out are
+ *                of its shape.  Either none of them overlaps its source, or all
+ *                are the sources and the capacity is the same (in place).
+ *                Blocks of payload_out and meta_out behind the kept ones are
+ *                left as they were, of mass_out set to 0.
+ *   kept         device int32 [layers][batch][heads][budget]: the blocks' former
+ *                numbers, -1 behind the last
+ *   lengths_out  device int32 [batch] (may be `lengths`): rows that are left; a
+ *                raw-row tail of cg_append stays valid
+ */
+int cg_evict(const cg_shape *shape, const cg_codec *codec, int32_t budget, int32_t sink, int32_t recent,
+             const float *mass, const void *payload, uint64_t payload_cap, const void *meta,
+             uint64_t meta_cap, const int32_t *lengths, const cg_shape *out_shape, void *payload_out,
+             uint64_t payload_out_cap, void *meta_out, uint64_t meta_out_cap, float *mass_out,
+             int32_t *kept, int32_t *lengths_out, void *stream);
+
 /* Message of the last error on the calling thread ("" if none). */
 const char *cg_last_error(void);
 

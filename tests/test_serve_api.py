@@ -1,0 +1,179 @@
+"""Refusals of the serving entry points: every argument is checked on the host
+before any device work (no GPU is touched here)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from fixed_rate_compression_amd import binding as cg
+
+P = 4096          # a 16-byte aligned address that is never dereferenced
+FAR = 1 << 40
+
+
+def shape(**kw):
+    a = dict(layers=2, kv=2, batch=2, heads=2, tokens=64, token_capacity=64, head_dim=128, dtype=cg.CG_DTYPE_BF16)
+    a.update(kw)
+    return cg.CgShape(**a)
+
+
+def codec(bits=8, block=32, backend=cg.CG_BACKEND_BLOCK_UNIFORM):
+    return cg.make_codec(backend, bits, block)
+
+
+def attn(**kw):
+    a = dict(layer=0, q_heads=4, n_queries=1, causal=1, scale=0.1, lengths=None, starts=None, q_batch_stride=0,
+             q_token_stride=0)
+    a.update(kw)
+    return cg.CgAttn(**a)
+
+
+def attend(sh=None, co=None, at=None, g=None, pay=P, cap=FAR, meta=P, mcap=FAR, q=P, out=FAR, lse=None, mass=None,
+           ws=P, wsb=FAR):
+    sh, co, at, g = sh or shape(), co or codec(), at or attn(), g or cg.make_gauge(0)
+    r = ctypes.byref
+    return cg.lib().cg_attend(r(sh), pay, cap, meta, mcap, r(g), r(co), r(at), q, out, lse, mass, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(sh=shape(kv=1)), cg.CG_E_SHAPE),
+    (dict(sh=shape(head_dim=64)), cg.CG_E_UNSUPPORTED),
+    (dict(sh=shape(tokens=65)), cg.CG_E_SHAPE),
+    (dict(sh=shape(token_capacity=1 << 31, tokens=4)), cg.CG_E_SHAPE),
+    (dict(co=codec(bits=4)), cg.CG_E_UNSUPPORTED),
+    (dict(co=codec(block=48)), cg.CG_E_UNSUPPORTED),
+    (dict(co=cg.make_codec(cg.CG_BACKEND_ZFP, 8)), cg.CG_E_UNSUPPORTED),
+    (dict(co=cg.make_codec(cg.CG_BACKEND_KIVI, 8, 32)), cg.CG_E_UNSUPPORTED),
+    (dict(g=cg.CgGauge(16, None)), cg.CG_E_INVAL),
+    (dict(g=cg.CgGauge(64, P)), cg.CG_E_UNSUPPORTED),
+    (dict(pay=None), cg.CG_E_INVAL),
+    (dict(pay=P + 8), cg.CG_E_INVAL),
+    (dict(meta=None), cg.CG_E_INVAL),
+    (dict(cap=2 * 2 * 2 * 2 * 64 * 128 - 1), cg.CG_E_SIZE),
+    (dict(mcap=2 * 2 * 2 * 2 * 2 * 8 - 1), cg.CG_E_SIZE),
+    (dict(at=attn(layer=2)), cg.CG_E_SHAPE),
+    (dict(at=attn(layer=-1)), cg.CG_E_SHAPE),
+    (dict(at=attn(q_heads=3)), cg.CG_E_SHAPE),
+    (dict(at=attn(q_heads=0)), cg.CG_E_SHAPE),
+    (dict(at=attn(n_queries=-1)), cg.CG_E_SHAPE),
+    (dict(at=attn(n_queries=1 << 30)), cg.CG_E_SHAPE),
+    (dict(at=attn(causal=2)), cg.CG_E_INVAL),
+    (dict(at=attn(scale=float("nan"))), cg.CG_E_INVAL),
+    (dict(at=attn(scale=float("inf"))), cg.CG_E_INVAL),
+    (dict(at=attn(lengths=P + 2)), cg.CG_E_INVAL),
+    (dict(at=attn(q_token_stride=516)), cg.CG_E_INVAL),
+    (dict(at=attn(q_batch_stride=-512)), cg.CG_E_INVAL),
+    (dict(q=None), cg.CG_E_INVAL),
+    (dict(q=P + 2), cg.CG_E_INVAL),
+    (dict(out=FAR + 8), cg.CG_E_INVAL),
+    (dict(out=P), cg.CG_E_INVAL),
+    (dict(q=P, out=P + 1024, at=attn(q_batch_stride=2048)), cg.CG_E_INVAL),
+    (dict(lse=P + 1), cg.CG_E_INVAL),
+    (dict(mass=P + 1), cg.CG_E_INVAL),
+    (dict(mass=P, ws=None), cg.CG_E_SIZE),
+    (dict(mass=P, wsb=16), cg.CG_E_SIZE),
+])
+def test_attend_refusals(kw, code):
+    assert attend(**kw) == code
+    assert cg.cg_last_error()
+
+
+def test_attend_nulls_and_nothing_to_do():
+    L, r, g = cg.lib(), ctypes.byref, cg.make_gauge(0)
+    sh, co, at = shape(), codec(), attn()
+    n = ctypes.c_size_t()
+    assert L.cg_attend(None, P, FAR, P, FAR, r(g), r(co), r(at), P, FAR, None, None, P, FAR, None) == cg.CG_E_INVAL
+    assert L.cg_attend(r(sh), P, FAR, P, FAR, None, r(co), r(at), P, FAR, None, None, P, FAR, None) == cg.CG_E_INVAL
+    assert L.cg_attend(r(sh), P, FAR, P, FAR, r(g), r(co), None, P, FAR, None, None, P, FAR, None) == cg.CG_E_INVAL
+    assert L.cg_attend_workspace_bytes(r(sh), r(g), r(co), r(at), 0, None) == cg.CG_E_INVAL
+    assert attend(at=attn(n_queries=0), q=None, out=None) == cg.CG_OK
+    assert L.cg_attend_workspace_bytes(r(sh), r(g), r(co), r(attn(n_queries=0)), 1, r(n)) == cg.CG_OK
+    # the workspace grows with the tokens' bound and never needs lengths
+    sizes = []
+    for T in (64, 4096, 65536):
+        assert L.cg_attend_workspace_bytes(r(shape(tokens=T, token_capacity=T)), r(g), r(co), r(at), 1, r(n)) == cg.CG_OK
+        sizes.append(n.value)
+    assert sizes[0] < sizes[1] < sizes[2]
+
+
+def append(sh=None, co=None, g=None, layer=0, n=1, k=P, v=P, bs=0, rs=0, ln=None, st=None, tail=FAR, pay=P, cap=FAR,
+           meta=P, mcap=FAR):
+    r = ctypes.byref
+    return cg.lib().cg_append(r(sh or shape()), r(g or cg.make_gauge(0)), r(co or codec()), layer, n, k, v, bs, rs, ln,
+                              st, tail, pay, cap, meta, mcap, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(sh=shape(kv=1)), cg.CG_E_SHAPE), (dict(co=codec(bits=6)), cg.CG_E_UNSUPPORTED),
+    (dict(g=cg.CgGauge(12, P)), cg.CG_E_SHAPE), (dict(layer=2), cg.CG_E_SHAPE), (dict(n=-1), cg.CG_E_SHAPE),
+    (dict(n=(1 << 31) - 1, sh=shape(batch=64)), cg.CG_E_SHAPE), (dict(k=None), cg.CG_E_INVAL),
+    (dict(v=P + 4), cg.CG_E_INVAL), (dict(tail=None), cg.CG_E_INVAL), (dict(tail=P), cg.CG_E_INVAL),
+    (dict(bs=-256), cg.CG_E_INVAL), (dict(rs=257), cg.CG_E_INVAL), (dict(ln=P + 1), cg.CG_E_INVAL),
+    (dict(st=P + 2), cg.CG_E_INVAL), (dict(cap=1000), cg.CG_E_SIZE), (dict(mcap=8), cg.CG_E_SIZE),
+    (dict(pay=None), cg.CG_E_INVAL),
+])
+def test_append_refusals(kw, code):
+    assert append(**kw) == code
+
+
+def test_append_of_nothing():
+    assert append(n=0, k=None, v=None, tail=None) == cg.CG_OK
+
+
+def evict(sh=None, co=None, budget=2, sink=0, recent=1, mass=P, pay=P, cap=FAR, meta=P, mcap=FAR, ln=None, osh=None,
+          po=FAR, pcap=FAR, mo=FAR, omcap=FAR, wo=FAR, kept=FAR, lo=FAR):
+    r = ctypes.byref
+    return cg.lib().cg_evict(r(sh or shape()), r(co or codec()), budget, sink, recent, mass, pay, cap, meta, mcap, ln,
+                             r(osh or shape()), po, pcap, mo, omcap, wo, kept, lo, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(co=codec(bits=4)), cg.CG_E_UNSUPPORTED), (dict(osh=shape(layers=1)), cg.CG_E_SHAPE),
+    (dict(osh=shape(batch=1)), cg.CG_E_SHAPE), (dict(osh=shape(heads=1)), cg.CG_E_SHAPE),
+    (dict(budget=3), cg.CG_E_SHAPE), (dict(budget=0), cg.CG_E_SHAPE), (dict(recent=0), cg.CG_E_SHAPE),
+    (dict(sink=-1), cg.CG_E_SHAPE), (dict(sink=2), cg.CG_E_SHAPE),
+    (dict(sink=(1 << 31) - 1, recent=(1 << 31) - 1), cg.CG_E_SHAPE),
+    (dict(mass=None), cg.CG_E_INVAL), (dict(kept=None), cg.CG_E_INVAL), (dict(lo=None), cg.CG_E_INVAL),
+    (dict(wo=None), cg.CG_E_INVAL), (dict(mass=P + 1), cg.CG_E_INVAL), (dict(po=P + 16), cg.CG_E_INVAL),
+    (dict(mo=P + 16), cg.CG_E_INVAL), (dict(wo=P + 4), cg.CG_E_INVAL), (dict(po=P), cg.CG_E_INVAL),
+    (dict(po=P, mo=P, wo=P, osh=shape(token_capacity=128)), cg.CG_E_INVAL),
+    (dict(ln=FAR + 4), cg.CG_E_INVAL), (dict(pcap=100), cg.CG_E_SIZE), (dict(omcap=8), cg.CG_E_SIZE),
+    (dict(po=None), cg.CG_E_INVAL),
+])
+def test_evict_refusals(kw, code):
+    assert evict(**kw) == code
+
+
+def test_binding_checks_types_and_sizes():
+    """What the C call cannot see of a tensor is checked before it."""
+    import torch
+    sh, co, g = shape(layers=1), codec(), cg.make_gauge(0)
+    pay, meta = torch.zeros(2 * 2 * 2 * 64 * 128, dtype=torch.uint8), torch.zeros(2 * 2 * 2 * 2 * 2)
+    q = torch.zeros(2, 1, 4, 128, dtype=torch.bfloat16)
+    at = attn()
+    for kw in (dict(q=q.float()), dict(q=q[:, :, :2]), dict(q=q.expand(2, 1, 4, 128)[:, :, :, :64]),
+               dict(out=torch.zeros(8)), dict(out=q[:1].clone()), dict(lse=torch.zeros(7)),
+               dict(lse=torch.zeros(8, dtype=torch.float64)), dict(mass=torch.zeros(7)),
+               dict(q=q[:1].expand(2, 1, 4, 128))):
+        a = dict(q=q, out=q.clone(), lse=None, mass=None)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            cg.cg_attend(sh, pay, meta, g, co, at, a["q"], a["out"], a["lse"], a["mass"], None, stream=0)
+    with pytest.raises(ValueError):
+        cg.make_attn(0, 4, 1, 0.1, lengths=torch.zeros(2, dtype=torch.int64))
+    k = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16)
+    tail = torch.zeros(1, 2, 2, 2, 32, 128, dtype=torch.bfloat16)
+    for kw in (dict(k=k.float()), dict(k=k[:, :, :1]), dict(v=k[:1].expand(2, 1, 2, 128)), dict(tail=tail[:, :1].clone()),
+               dict(k=k.transpose(2, 3).contiguous().transpose(2, 3)), dict(lengths=torch.zeros(2, dtype=torch.int64)),
+               dict(lengths=torch.zeros(1, dtype=torch.int32))):
+        a = dict(k=k, v=k.clone(), tail=tail, lengths=None)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            cg.cg_append(sh, g, co, 0, 1, a["k"], a["v"], a["tail"], pay, meta, a["lengths"], stream=0)
+    w, kept, ln = torch.zeros(8), torch.zeros(8, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for kw in (dict(mass=w[:7]), dict(kept=kept[:7]), dict(kept=kept.long()), dict(lo=ln[:1]), dict(wo=w.double())):
+        a = dict(mass=w, kept=kept, lo=ln, wo=w.clone())
+        a.update(kw)
+        with pytest.raises(ValueError):
+            cg.cg_evict(sh, co, 2, 0, 1, a["mass"], pay, meta, sh, pay.clone(), meta.clone(), a["wo"], a["kept"],
+                        a["lo"], ln.clone(), stream=0)
