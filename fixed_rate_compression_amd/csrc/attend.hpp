@@ -15,10 +15,14 @@
 // a dword of codes costs two byte permutes and no conversion.
 //
 // Query rows: a KV head's rows are (query i, head j of the group), row
-// i ratio + j; a row tile is 16 of them.  q' is held as two fp16 parts
-// (q' 2^sh = hi + lo within 2^-22, sh putting the row's largest magnitude in
-// [2^13, 2^14)); sum q' is that of the parts, so a rounding of q' perturbs
-// the query and not the balance of the two terms of s_t.
+// i ratio + j; a row tile is 16 of them.  q' is scaled by a power of two that
+// puts the row's largest magnitude in [2^13, 2^14) and held in two fixed-point
+// parts, hi a multiple of 2^4 and lo of 2^-7 (2^-22 of the largest): each
+// part's sum over 128 centred codes is a whole number of at most 2^24 units,
+// so the matrix cores, which round their fp32 sums towards zero, add it
+// without a rounding (as two floating parts in one sum, fp32 outputs were off
+// by 1e-5, now by 1e-6).  sum q' is that of the parts, so a rounding of q'
+// perturbs the query and not the balance of the two terms of s_t.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -63,11 +67,13 @@ struct AttendArgs {
 // rows [0, rows) of every field over its tokens, one workgroup per (field,
 // row tile, split); splits > 1 leaves parts for merge_launch
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
+// the same for many rows, one workgroup per (field, 128 rows, split); fills
+// qfrag, qrow where they are given
+hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // block weights: few rows from the attention's block sums, many rows from a
 // second pass over the keys with the rows' sums known
 hipError_t mass_finish_launch(const AttendArgs &a, hipStream_t s);
-hipError_t prepare_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t mass_many_launch(const AttendArgs &a, hipStream_t s);
 
 // ---------------------------------------------------------------------------
@@ -103,11 +109,16 @@ __device__ __forceinline__ uint32_t bytes2(uint32_t w) {
   return __builtin_amdgcn_perm(0u, w, 0x0c000c00u | ((J + 1) << 16) | J);
 }
 
-// codes 2^-24 less 128 2^-24, exact in fp16's subnormals
+// codes as subnormals -> (code - 128) 2^-9, one packed multiply-add, exact.  The
+// matrix cores align the products of a sum by their exponent fields and cut
+// what lies below: with subnormal operands, whose significands begin with
+// zeros, sums of weights of unlike sizes kept 17 bits, with these 24.
 __device__ __forceinline__ uint32_t centred(uint32_t w) {
-  const h2_t c = __builtin_bit_cast(h2_t, 0x80808080u);
-  return __builtin_bit_cast(uint32_t, (h2_t)(__builtin_bit_cast(h2_t, w) + c));
+  const h2_t up = {(_Float16)32768.0f, (_Float16)32768.0f}, c = {(_Float16)-0.25f, (_Float16)-0.25f};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(h2_t, w), up, c));
 }
+constexpr float kCodeUnit = 16777216.0f;  // 2^24: codes as they are
+constexpr float kCentredUnit = 512.0f;    // 2^9: centred codes
 
 // 8 consecutive codes (two dwords) as fp16 subnormals, CENTRED: less 128
 template <bool CENTRED>
@@ -225,9 +236,11 @@ __device__ __forceinline__ void gauge_rows(const float *xs, int nr, const float 
 // its row at step s, the order in which 16-byte loads of key rows arrive.
 struct QueryFrags {
   h8_t hi[4], lo[4];
-  float ca, cq;  // score = acc (step ca) + minimum cq
+  float ca, cq;  // score = (sum of q' code) step ca + minimum cq
 };
 
+// TWO: two fixed-point parts; else one fp16 part, each channel rounded to 2^-11
+template <bool TWO>
 __device__ __forceinline__ void make_frags(const float *xs, float c, QueryFrags &f) {
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
   float x[4][8];
@@ -253,17 +266,24 @@ __device__ __forceinline__ void make_frags(const float *xs, float c, QueryFrags 
 #pragma unroll
     for (int k = 0; k < 4; k++) {
       const float p = x[s][2 * k] * up, q = x[s][2 * k + 1] * up;
-      wh[k] = pack_f16x2(p, q);
-      const f2_t h = unpack_f16x2(wh[k]);
-      wl[k] = pack_f16x2(p - h.x, q - h.y);
-      const f2_t l = unpack_f16x2(wl[k]);
-      sum += (h.x + l.x) + (h.y + l.y);
+      if constexpr (TWO) {
+        const float ph = rintf(p * 0.0625f) * 16.0f, qh = rintf(q * 0.0625f) * 16.0f;
+        const float pl = rintf((p - ph) * 128.0f) * 0.0078125f, ql = rintf((q - qh) * 128.0f) * 0.0078125f;
+        wh[k] = pack_f16x2(ph, qh);  // both parts are exact in fp16
+        wl[k] = pack_f16x2(pl, ql);
+        sum += (ph + pl) + (qh + ql);
+      } else {
+        wh[k] = pack_f16x2(p, q);
+        wl[k] = 0u;
+        const f2_t h = unpack_f16x2(wh[k]);
+        sum += h.x + h.y;
+      }
     }
     f.hi[s] = as_h8(wh[0], wh[1], wh[2], wh[3]);
     f.lo[s] = as_h8(wl[0], wl[1], wl[2], wl[3]);
   }
   const float down = c * __builtin_ldexpf(1.0f, -sh);
-  f.ca = down * 16777216.0f;  // 2^24: the codes enter as code 2^-24
+  f.ca = down;
   f.cq = down * row_sum(sum);
 }
 

@@ -25,14 +25,18 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Workgroups that keep 256 compute units busy: three on each, with at least
 // 256 tokens (two units a wave) to a workgroup.
 constexpr int64_t kTargetWorkgroups = 768, kMinTokens = 256;
+// 128-row tiles: two workgroups fit a compute unit
+constexpr int64_t kTargetTiles = 512;
 
 Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {
   Plan p{};
   p.rows = (int64_t)t->n_queries * (t->q_heads / s->heads);
   p.tiles = (p.rows + cga::ROWS - 1) / cga::ROWS;
   p.few = p.tiles <= 1;
-  const int64_t fields = (int64_t)s->batch * s->heads, work = fields * p.tiles;
-  int64_t sp = work > 0 ? (kTargetWorkgroups + work - 1) / work : 1;
+  const int64_t fields = (int64_t)s->batch * s->heads;
+  const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
+  const int64_t target = p.few ? kTargetWorkgroups : kTargetTiles;
+  int64_t sp = work > 0 ? (p.few ? (target + work - 1) / work : target / work) : 1;
   const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
   if (sp > most) sp = most;
   if (sp < 1) sp = 1;
@@ -164,17 +168,12 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
 
   const bool bf16 = shape->dtype == CG_DTYPE_BF16;
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = cga::rows_launch(a, bf16, st);
+  hipError_t e = p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
   if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
   if (p.splits > 1 && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
     return cgh::hip_error(e, "cg_attend merge launch");
   if (mass && shape->tokens > 0) {
-    if (p.few) {
-      e = cga::mass_finish_launch(a, st);
-    } else {
-      e = cga::prepare_launch(a, bf16, st);
-      if (e == hipSuccess) e = cga::mass_many_launch(a, st);
-    }
+    e = p.few ? cga::mass_finish_launch(a, st) : cga::mass_many_launch(a, st);
     if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
   }
   return CG_OK;

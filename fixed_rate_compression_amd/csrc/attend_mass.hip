@@ -1,41 +1,9 @@
-// Many query rows over the 8-bit cache: the gauged queries as matrix-core
-// operands, laid out once, and the second pass over the keys that gives the
-// weight each block received.
+// The weight each block of the 8-bit cache received from many query rows: a
+// second pass over the keys with the queries' operands and the rows' log-sums
+// that the attention left.
 #include "attend.hpp"
 
 namespace cga {
-
-// One workgroup per row tile: gauge, split into fp16 parts, and store in
-// operand order, with each row's factors and limit.
-template <bool BF16>
-__global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
-  __shared__ __align__(16) float xs[ROWS * PITCH], ys[ROWS * PITCH];
-  const int64_t id = blockIdx.x;
-  const int tile = (int)(id % a.tiles), bh = (int)(id / a.tiles);
-  const int h = bh % a.heads, b = bh / a.heads;
-  const int r0 = tile * ROWS, nr = min(ROWS, a.rows - r0);
-  load_rows<BF16>(a, b, h, r0, xs);
-  if (nr < ROWS)
-    for (int i = threadIdx.x; i < (ROWS - nr) * D; i += NTH) ys[(nr + (i >> 7)) * PITCH + (i & 127)] = 0.0f;
-  __syncthreads();
-  gauge_rows<false>(xs, nr, a.gk + (int64_t)h * D * a.g, a.g, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
-  __syncthreads();
-  if (threadIdx.x >= 64) return;
-  QueryFrags q;
-  make_frags(ys, a.c, q);
-  const int lane = threadIdx.x;
-  uint4 *d = a.qfrag + id * 8 * 64 + lane;
-#pragma unroll
-  for (int s = 0; s < 4; s++) {
-    d[s * 64] = __builtin_bit_cast(uint4, q.hi[s]);
-    d[(4 + s) * 64] = __builtin_bit_cast(uint4, q.lo[s]);
-  }
-  if (lane < ROWS) {
-    const int len = seq_length(a, b);
-    const int lim = lane < nr ? query_limit(a, b, len, (r0 + lane) / a.ratio) : 0;
-    a.qrow[id * ROWS + lane] = make_float4(q.ca, q.cq, __int_as_float(lim), 0.0f);
-  }
-}
 
 // A wave owns 32 tokens (64 where a block has 64: twice 32) of one field, holds
 // their codes as operands and walks the row tiles: weights 2^(s - log2 sum),
@@ -80,13 +48,19 @@ __global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t g
       const int lim = __float_as_int(qr.z);
       const int r = tile * ROWS + row;
       const float lse2 = r < a.rows ? a.lse2[(int64_t)bh * a.rows + r] : INFINITY;
-      f4_t z[2] = {f4_t{0.f, 0.f, 0.f, 0.f}, f4_t{0.f, 0.f, 0.f, 0.f}};
+      const f4_t none = f4_t{0.f, 0.f, 0.f, 0.f};
+      f4_t z[2] = {none, none}, zl[2] = {none, none};
 #pragma unroll
-      for (int s = 0; s < 8; s++) {
-        const h8_t qv = __builtin_bit_cast(h8_t, qf[s * 64]);
-        z[0] = mfma(kc[0][s & 3], qv, z[0]);
-        z[1] = mfma(kc[1][s & 3], qv, z[1]);
+      for (int s = 0; s < 4; s++) {
+        const h8_t qh = __builtin_bit_cast(h8_t, qf[s * 64]), ql = __builtin_bit_cast(h8_t, qf[(4 + s) * 64]);
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+          z[t] = mfma(kc[t][s], qh, z[t]);
+          zl[t] = mfma(kc[t][s], ql, zl[t]);
+        }
       }
+      z[0] += zl[0];
+      z[1] += zl[1];
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         const float A = m[t].y * qr.x, Bm = __builtin_fmaf(128.0f, m[t].y, m[t].x) * qr.y - lse2;
@@ -112,13 +86,6 @@ __global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t g
   } else {
     out[grpi] += total[0] + total[1];
   }
-}
-
-hipError_t prepare_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.tiles)), block(NTH);
-  if (bf16) hipLaunchKernelGGL(k_attend_prepare<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_attend_prepare<false>, grid, block, 0, s, a);
-  return hipGetLastError();
 }
 
 hipError_t mass_many_launch(const AttendArgs &a, hipStream_t s) {

@@ -113,7 +113,8 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
   gauge_rows<false>(xs, nr, a.gk + (int64_t)h * D * a.g, a.g, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
   __syncthreads();
   QueryFrags q;
-  make_frags(ys, a.c, q);
+  make_frags<true>(ys, a.c, q);
+  q.ca *= BF16 ? kCodeUnit : kCentredUnit;
   __syncthreads();
 
   // what this lane's row sees; rows that are not there see everything, and
@@ -140,15 +141,16 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
     float s[2][4];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      f4_t z = f4_t{0.f, 0.f, 0.f, 0.f};
+      f4_t z = f4_t{0.f, 0.f, 0.f, 0.f}, zl = z;
 #pragma unroll
       for (int x = 0; x < 2; x++) {
         const h8_t c0 = codes8<!BF16>(u.k[t][x].x, u.k[t][x].y), c1 = codes8<!BF16>(u.k[t][x].z, u.k[t][x].w);
         z = mfma(c0, q.hi[2 * x], z);
         z = mfma(c1, q.hi[2 * x + 1], z);
-        z = mfma(c0, q.lo[2 * x], z);
-        z = mfma(c1, q.lo[2 * x + 1], z);
+        zl = mfma(c0, q.lo[2 * x], zl);
+        zl = mfma(c1, q.lo[2 * x + 1], zl);
       }
+      z += zl;
       const float A = u.km[t].y * q.ca, Bm = (BF16 ? u.km[t].x : __builtin_fmaf(128.0f, u.km[t].y, u.km[t].x)) * q.cq;
 #pragma unroll
       for (int r = 0; r < 4; r++) s[t][r] = __builtin_fmaf(z[r], A, Bm);
@@ -253,8 +255,8 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
   {
     const bool some = st.m > -INFINITY;
     const float k = some ? exp2_fast(st.m - M) : 0.0f;
-    // true sums: acc 2^24 / f (the codes' and the weights' scales)
-    const float ks = some ? k * exp2_fast(15.0f - (st.m - st.mo)) : 0.0f;
+    // true sums: acc 2^9 / f (the codes' and the weights' scales)
+    const float ks = some ? k * exp2_fast(st.mo - st.m) : 0.0f;
     float *o = lds + (wave * ROWS + row) * PITCH;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
