@@ -54,7 +54,7 @@ struct AttendArgs {
   float2 *bsum;                  // [b][h][entry][rows] (block sum, its maximum)
   float *lse2;                   // [b][h][rows] log2 of the row's sum (many rows with mass)
   uint4 *qfrag;                  // [b][h][tile][hi/lo][step][lane] fp16 query operands
-  float4 *qrow;                  // [b][h][16 tiles] (score factor, minimum factor, limit bits, 0)
+  float2 *qrow;                  // [b][h][16 tiles] (score factor, minimum factor)
   int64_t tcap, tokens, nblk;
   int64_t q_bs, q_ts;            // query strides (elements)
   int64_t entries;               // block-sum entries of a field
@@ -67,8 +67,8 @@ struct AttendArgs {
 // rows [0, rows) of every field over its tokens, one workgroup per (field,
 // row tile, split); splits > 1 leaves parts for merge_launch
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
-// the same for many rows, one workgroup per (field, 128 rows, split); fills
-// qfrag, qrow where they are given
+// the same for many rows, one workgroup per (field, 128 rows, split),
+// after one that lays the gauged queries out (qfrag, qrow)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // block weights: few rows from the attention's block sums, many rows from a

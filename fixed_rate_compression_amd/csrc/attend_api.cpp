@@ -48,10 +48,10 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   p.o_bytes = parts ? up256((size_t)(fields * p.splits * p.rows) * cga::D * 4) : 0;
   p.ml_bytes = parts || (mass && p.few) ? up256((size_t)(fields * p.splits * p.rows) * 8) : 0;
   if (mass && p.few) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
-  if (mass && !p.few) {
-    p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
+  if (!p.few) {
+    if (mass) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
     p.qfrag_bytes = up256((size_t)(fields * p.tiles) * 8 * 64 * 16);
-    p.qrow_bytes = up256((size_t)(fields * p.tiles) * cga::ROWS * 16);
+    p.qrow_bytes = up256((size_t)(fields * p.tiles) * cga::ROWS * 8);
   }
   return p;
 }
@@ -164,7 +164,7 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.bsum = (float2 *)take(p.bsum_bytes);
   a.lse2 = (float *)take(p.lse2_bytes);
   a.qfrag = (uint4 *)take(p.qfrag_bytes);
-  a.qrow = (float4 *)take(p.qrow_bytes);
+  a.qrow = (float2 *)take(p.qrow_bytes);
 
   const bool bf16 = shape->dtype == CG_DTYPE_BF16;
   hipStream_t st = (hipStream_t)stream;

@@ -44,9 +44,9 @@ __global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t g
       if (limit_of(a, b, len, tile * ROWS / a.ratio, r1 / a.ratio) <= t0) continue;
       const int64_t id = (int64_t)bh * a.tiles + tile;
       const uint4 *qf = a.qfrag + id * 8 * 64 + lane;
-      const float4 qr = a.qrow[id * ROWS + row];
-      const int lim = __float_as_int(qr.z);
+      const float2 qr = a.qrow[id * ROWS + row];
       const int r = tile * ROWS + row;
+      const int lim = r < a.rows ? query_limit(a, b, len, r / a.ratio) : 0;
       const float lse2 = r < a.rows ? a.lse2[(int64_t)bh * a.rows + r] : INFINITY;
       const f4_t none = f4_t{0.f, 0.f, 0.f, 0.f};
       f4_t z[2] = {none, none}, zl[2] = {none, none};
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t g
       z[1] += zl[1];
 #pragma unroll
       for (int t = 0; t < 2; t++) {
-        const float A = m[t].y * qr.x, Bm = __builtin_fmaf(128.0f, m[t].y, m[t].x) * qr.y - lse2;
+        const float A = m[t].y * qr.x * kCentredUnit, Bm = __builtin_fmaf(128.0f, m[t].y, m[t].x) * qr.y - lse2;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
           const float s = __builtin_fmaf(z[t][k], A, Bm);
