@@ -232,22 +232,23 @@ __device__ __forceinline__ void gauge_rows(const float *xs, int nr, const float 
 }
 
 // The fp16 operands of 16 gauged rows xs [16][PITCH]: lane (row = lane % 16,
-// grp = lane / 16) holds channels 64 (s / 2) + 16 grp + 8 (s % 2) + 0 .. 7 of
-// its row at step s, the order in which 16-byte loads of key rows arrive.
+// grp = lane / 16) holds 8 channels of its row at step s: BYTES: 64 (s / 2) +
+// 16 grp + 8 (s % 2) + 0 .. 7, the order in which 16-byte loads of key codes
+// arrive; else 32 s + 8 grp + 0 .. 7.
 struct QueryFrags {
   h8_t hi[4], lo[4];
   float ca, cq;  // score = (sum of q' code) step ca + minimum cq
 };
 
 // TWO: two fixed-point parts; else one fp16 part, each channel rounded to 2^-11
-template <bool TWO>
+template <bool TWO, bool BYTES>
 __device__ __forceinline__ void make_frags(const float *xs, float c, QueryFrags &f) {
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
   float x[4][8];
   float mx = 0.0f;
 #pragma unroll
   for (int s = 0; s < 4; s++) {
-    const float *p = xs + row * PITCH + 64 * (s >> 1) + 16 * grp + 8 * (s & 1);
+    const float *p = xs + row * PITCH + (BYTES ? 64 * (s >> 1) + 16 * grp + 8 * (s & 1) : 32 * s + 8 * grp);
     const float4 u = *(const float4 *)p, v = *(const float4 *)(p + 4);
     x[s][0] = u.x; x[s][1] = u.y; x[s][2] = u.z; x[s][3] = u.w;
     x[s][4] = v.x; x[s][5] = v.y; x[s][6] = v.z; x[s][7] = v.w;

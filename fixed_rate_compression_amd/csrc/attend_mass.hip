@@ -31,10 +31,9 @@ __global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t g
     for (int t = 0; t < 2; t++) {
       const int64_t tt = min((int64_t)t0 + 16 * t, a.tcap - 16);  // 16-token blocks: the capacity may end here
 #pragma unroll
-      for (int x = 0; x < 2; x++) {
-        const uint4 w = *(const uint4 *)(kf + (tt + row) * D + 64 * x + 16 * grp);
-        kc[t][2 * x] = codes8<true>(w.x, w.y);
-        kc[t][2 * x + 1] = codes8<true>(w.z, w.w);
+      for (int x = 0; x < 4; x++) {
+        const uint2 w = *(const uint2 *)(kf + (tt + row) * D + 32 * x + 8 * grp);
+        kc[t][x] = codes8<true>(w.x, w.y);
       }
       m[t] = km[tt >> a.bshift];
     }

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
   gauge_rows<false>(xs, nr, a.gk + (int64_t)h * D * a.g, a.g, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
   __syncthreads();
   QueryFrags q;
-  make_frags<true>(ys, a.c, q);
+  make_frags<true, true>(ys, a.c, q);
   q.ca *= BF16 ? kCodeUnit : kCentredUnit;
   __syncthreads();
 

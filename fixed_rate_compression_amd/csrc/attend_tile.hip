@@ -2,13 +2,14 @@
 // and drafted tokens, bound by the vector units that make the weights.
 //
 // A workgroup takes 128 query rows of one KV head, 32 to each of its four
-// waves (two row tiles), and walks the tokens 64 at a time: the codes and
-// ranges of a stage go through registers into LDS while another is worked on,
-// one barrier a stage.  The products are those of the
-// few-row kernel (attend_rows.hip) with the codes read from LDS and each
-// widened operand used for both row tiles.  Rows of 16-byte pieces are stored
-// with piece ^ (row % 8), so the 16 rows that a key operand's lanes read at
-// one piece lie in different banks.
+// waves, and walks the tokens 32 at a time: a unit's codes go
+// through registers, are widened to centred fp16 once for the four waves and
+// laid in LDS while another unit is worked on, one barrier a unit.  Widening
+// at the use, from codes in LDS, took 96 of 244 vector instructions a wave
+// and unit.  Keys are read as rows, values transposed by the LDS; the row
+// pitches spread both over the banks.  The products are 32 x 32 (tokens x rows,
+// channels x rows), which leaves a lane one row: half the matrix instructions
+// and half the arithmetic on a row's state of 16 x 16 ones.
 //
 // The running maximum is not looked for: a lane's sum of weights tells whether
 // one of them has outgrown its scale, and only then (and where a row sees its
@@ -19,254 +20,261 @@
 
 namespace cga {
 
-constexpr int STAGE = 64;        // tokens of a stage
-constexpr int TROWS = 128;       // query rows of a workgroup
-constexpr int WT = 2;            // row tiles of a wave
-constexpr int CODES = STAGE * D; // bytes of a stage's key (value) codes
+constexpr int TROWS = 128;            // query rows of a workgroup
+constexpr int WROWS = 32;             // of a wave
+constexpr int KP = 2 * D + 16;        // LDS pitch of a token's keys, fp16: 16 tokens' 16-byte pieces in all 64 banks
+constexpr int VP = 2 * D + 64;        // of its values: 4 tokens' 64-byte pieces in all 64 banks
+constexpr int KBYTES = UNIT * KP, VBYTES = UNIT * VP;
+// LDS of the token loop: a unit's keys are read a turn before its values
+constexpr int KBUF = 0, VBUF = 2 * KBYTES, MBUF = VBUF + 3 * VBYTES, LOBUF = MBUF + 3 * 32;
+
+typedef float f16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f16_t mfma32(h8_t a, h8_t b, f16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
 
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));  // stays in registers through a loop (a uint4 member did not)
 
-struct StageRegs {
-  u4_t k0, k1, v0, v1;
+struct UnitRegs {
+  u4_t k, v;
   float2 m;
 };
 
-// stage tokens [t0, t0 + 64) into registers; tokens past the capacity repeat
-// its last rows
-__device__ __forceinline__ void fetch_stage(const AttendArgs &a, const uint8_t *kf, const uint8_t *vf,
-                                            const float2 *km, const float2 *vm, int t0, StageRegs &s) {
+// a unit's codes into registers: 16 bytes of a key and a value row to a thread;
+// tokens past the capacity repeat its last row
+__device__ __forceinline__ void fetch_unit(const AttendArgs &a, const uint8_t *kf, const uint8_t *vf,
+                                           const float2 *km, const float2 *vm, int un, UnitRegs &s) {
   const int i = threadIdx.x;
-  const int64_t ta = min((int64_t)t0 + (i >> 3), a.tcap - 1), tb = min((int64_t)t0 + 32 + (i >> 3), a.tcap - 1);
-  s.k0 = *(const u4_t *)(kf + ta * D + 16 * (i & 7));
-  s.k1 = *(const u4_t *)(kf + tb * D + 16 * (i & 7));
-  s.v0 = *(const u4_t *)(vf + ta * D + 16 * (i & 7));
-  s.v1 = *(const u4_t *)(vf + tb * D + 16 * (i & 7));
-  // four 16-token tiles: key ranges, value ranges (lanes 0 .. 7 store them)
-  const int64_t blk = min(((int64_t)t0 + 16 * (i & 3)) >> a.bshift, a.nblk - 1);
-  s.m = ((i & 4) ? vm : km)[blk];
+  const int64_t t = min((int64_t)un * UNIT + (i >> 3), a.tcap - 1);
+  s.k = *(const u4_t *)(kf + t * D + 16 * (i & 7));
+  s.v = *(const u4_t *)(vf + t * D + 16 * (i & 7));
+  // two 16-token tiles: key ranges, value ranges (lanes 0 .. 3 store them)
+  const int64_t blk = min(((int64_t)un * UNIT + 16 * (i & 1)) >> a.bshift, a.nblk - 1);
+  s.m = ((i & 2) ? vm : km)[blk];
 }
 
-// LDS of the token loop: a stage's keys are read from one unit before its
-// values, so values take three buffers and keys two
-constexpr int KBUF = 0, VBUF = 2 * CODES, MBUF = VBUF + 3 * CODES, LOBUF = MBUF + 3 * 64;
-
-template <bool CENTRE_K>
-__device__ __forceinline__ void put_stage(unsigned char *lds, int stage, int tmax, const StageRegs &s) {
+// widened (centred) into LDS, once for the four waves
+__device__ __forceinline__ void put_unit(unsigned char *lds, int un, int tmax, const UnitRegs &s) {
   const int i = threadIdx.x;
-  const int r = i >> 3, off = r * D + 16 * ((i & 7) ^ (r & 7));  // the same piece order 32 rows on
-  unsigned char *k = lds + KBUF + (stage & 1) * CODES, *v = lds + VBUF + (stage % 3) * CODES;
-  *(u4_t *)(k + off) = s.k0;
-  *(u4_t *)(k + 32 * D + off) = s.k1;
-  *(u4_t *)(v + off) = s.v0;
-  *(u4_t *)(v + 32 * D + off) = s.v1;
-  if (i < 8) {
-    float2 m = s.m;
-    if ((i & 4) || CENTRE_K) m.x = __builtin_fmaf(128.0f, m.y, m.x);  // the value of code 128
-    if (stage * STAGE + 16 * (i & 3) >= tmax) m = make_float2(0.f, 0.f);  // a block that holds no row yet
-    *(float2 *)(lds + MBUF + (stage % 3) * 64 + 8 * i) = m;
+  unsigned char *k = lds + KBUF + (un & 1) * KBYTES + (i >> 3) * KP + 32 * (i & 7);
+  unsigned char *v = lds + VBUF + (un % 3) * VBYTES + (i >> 3) * VP + 32 * (i & 7);
+  *(h8_t *)k = codes8<true>(s.k.x, s.k.y);
+  *(h8_t *)(k + 16) = codes8<true>(s.k.z, s.k.w);
+  *(h8_t *)v = codes8<true>(s.v.x, s.v.y);
+  *(h8_t *)(v + 16) = codes8<true>(s.v.z, s.v.w);
+  if (i < 4) {
+    const bool there = un * UNIT + 16 * (i & 1) < tmax;  // a block that holds no row yet is not looked at
+    const float mid = __builtin_fmaf(128.0f, s.m.y, s.m.x);  // the value of code 128
+    *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * i) = make_float2(there ? mid : 0.0f, there ? s.m.y : 0.0f);
   }
 }
 
+// a lane's row (the same in lanes l and l + 32 but for l and mv), as in
+// attend_rows.hip, but mu is -inf while the row has seen nothing
 struct TileState {
-  float m, mu, mo, f, l, mv;  // as in attend_rows.hip, but mu is -inf while the row has seen nothing
+  float m, mu, mo, f, l, mv;
 };
 
-// the weights of a unit and what goes with them
+// the queries of a wave: channels 16 s + 8 half + 0 .. 7 of row lane % 32 at step s
+struct TileQueries {
+  h8_t hi[8];
+  float ca, cq;
+};
+
+// the weights of a unit and what goes with them; NB ranges to a unit (two
+// where blocks have 16 tokens)
+template <int NB>
 struct UnitWeights {
-  float p[WT][2][4], ps[WT][2], w[WT][2];  // weights, their sums, value factors
-  float mid[2];                            // the tiles' values of code 128
+  float p[16];
+  float ps[NB], w[NB], mid[NB];  // sums of weights, value factors, values of code 128
 };
 
-template <int J>
-__device__ __forceinline__ h8_t value_frag(const uint2 (&v)[2][4]) {
-  constexpr int B = J & 3;
-  uint32_t w[2][4];
+// scores of a unit: z = K Q^T, z[r] that of token 8 (r / 4) + 4 half + r % 4,
+// from the keys at kb (this lane's token and piece)
+template <bool LO>
+__device__ __forceinline__ void unit_scores(const unsigned char *kb, const TileQueries &q, const unsigned char *lo,
+                                            f16_t &z) {
+  f16_t zl;
 #pragma unroll
-  for (int t = 0; t < 2; t++)
+  for (int r = 0; r < 16; r++) z[r] = zl[r] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++) w[t][i] = J < 4 ? v[t][i].x : v[t][i].y;
-  return as_h8(centred(byte_pair<B>(w[0][0], w[0][1])), centred(byte_pair<B>(w[0][2], w[0][3])),
-               centred(byte_pair<B>(w[1][0], w[1][1])), centred(byte_pair<B>(w[1][2], w[1][3])));
+  for (int s = 0; s < 8; s++) {
+    const h8_t c = *(const h8_t *)(kb + 32 * s);
+    z = mfma32(c, q.hi[s], z);
+    if constexpr (LO) zl = mfma32(c, *(const h8_t *)(lo + 1024 * s), zl);
+  }
+  if constexpr (LO) z += zl;
 }
 
-// scores of a unit: z = K Q^T from the key codes at kb
-template <bool BF16, bool LO>
-__device__ __forceinline__ void unit_scores(const unsigned char *kb, const QueryFrags (&q)[WT], const unsigned char *lo,
-                                            f4_t (&z)[WT][2]) {
-  const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
+template <int NB>
+__device__ __forceinline__ void sum_weights(UnitWeights<NB> &o) {
+  float h[2];
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    f4_t zl[WT];
-#pragma unroll
-    for (int t = 0; t < WT; t++) zl[t] = z[t][u] = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const uint4 w = *(const uint4 *)(kb + (16 * u + row) * D + 16 * ((4 * x + grp) ^ (row & 7)));
-      const h8_t c0 = codes8<!BF16>(w.x, w.y), c1 = codes8<!BF16>(w.z, w.w);
-#pragma unroll
-      for (int t = 0; t < WT; t++) {
-        z[t][u] = mfma(c0, q[t].hi[2 * x], z[t][u]);
-        z[t][u] = mfma(c1, q[t].hi[2 * x + 1], z[t][u]);
-        if constexpr (LO) {
-          zl[t] = mfma(c0, *(const h8_t *)(lo + (4 * t + 2 * x) * 1024), zl[t]);
-          zl[t] = mfma(c1, *(const h8_t *)(lo + (4 * t + 2 * x + 1) * 1024), zl[t]);
-        }
-      }
-    }
-    if constexpr (LO) {
-#pragma unroll
-      for (int t = 0; t < WT; t++) z[t][u] += zl[t];
-    }
+    const float *p = o.p + 8 * u;
+    h[u] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+  }
+  if constexpr (NB == 2) {
+    o.ps[0] = h[0];
+    o.ps[1] = h[1];
+  } else {
+    o.ps[0] = h[0] + h[1];
   }
 }
 
-// weights of a unit; vis[t]: tokens of the unit, less 4 grp, that this lane's row
+// weights of a unit; vis: tokens of the unit, less 4 half, that the lane's row
 // sees (MASKED).  Returns whether some weight is too large for its scale (or
 // infinite: a row that has seen nothing yet).
-template <bool MASKED>
-__device__ __forceinline__ bool unit_weights(const float2 *mt, const QueryFrags (&q)[WT], const f4_t (&z)[WT][2],
-                                             const int (&vis)[WT], const TileState (&st)[WT], UnitWeights &o) {
-  float over = 0.0f;
-  float2 mk[2], mv[2];
+template <bool MASKED, int NB>
+__device__ __forceinline__ bool unit_weights(const float2 *mt, const TileQueries &q, const f16_t &z, int vis,
+                                             const TileState &st, UnitWeights<NB> &o) {
 #pragma unroll
-  for (int u = 0; u < 2; u++) {
-    mk[u] = mt[u];
-    mv[u] = mt[4 + u];
-    o.mid[u] = mv[u].x;
-  }
+  for (int u = 0; u < NB; u++) {
+    const float2 mk = mt[u], mv = mt[2 + u];
+    o.mid[u] = mv.x;
+    o.w[u] = mv.y * st.f;
+    const float A = mk.y * q.ca, B = __builtin_fmaf(mk.x, q.cq, -st.mu);
 #pragma unroll
-  for (int t = 0; t < WT; t++) {
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      const float A = mk[u].y * q[t].ca, B = __builtin_fmaf(mk[u].x, q[t].cq, -st[t].mu);
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const float s = __builtin_fmaf(z[t][u][r], A, B);
-        o.p[t][u][r] = exp2_fast(MASKED && 16 * u + r >= vis[t] ? -INFINITY : s);
-      }
-      o.ps[t][u] = (o.p[t][u][0] + o.p[t][u][1]) + (o.p[t][u][2] + o.p[t][u][3]);
-      o.w[t][u] = mv[u].y * st[t].f;
+    for (int k = 0; k < 16 / NB; k++) {
+      const int r = 16 / NB * u + k;
+      const float s = __builtin_fmaf(z[r], A, B);
+      o.p[r] = exp2_fast(MASKED && 8 * (r >> 2) + (r & 3) >= vis ? -INFINITY : s);
     }
-    over = fmaxf(fmaxf(over, (o.ps[t][0] + o.ps[t][1]) * 128.0f),
-                 fmaxf(o.ps[t][0] * o.w[t][0], o.ps[t][1] * o.w[t][1]));
   }
+  sum_weights(o);
+  float over = o.ps[0] * 128.0f;
+  if constexpr (NB == 2) over = fmaxf(over, o.ps[1] * 128.0f);
+#pragma unroll
+  for (int u = 0; u < NB; u++) over = fmaxf(over, o.ps[u] * o.w[u]);
   return over > 32768.0f;
 }
 
-// raise the rows' maxima to the unit's scores, rescale what was summed, and
+__device__ __forceinline__ float pair_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+
+// raise the row's maximum to the unit's scores, rescale what was summed, and
 // form the unit's weights again (rare: the scores are not kept for it)
-template <bool BF16, bool LO>
+template <bool LO, int NB>
 __device__ __forceinline__ void raise(const unsigned char *kb, const unsigned char *lo, const float2 *mt,
-                                      const QueryFrags (&q)[WT], const int (&vis)[WT], TileState (&st)[WT],
-                                      f4_t (&acc)[WT][8], UnitWeights &o) {
-  f4_t z[WT][2];
+                                      const TileQueries &q, int vis, TileState &st, f16_t (&acc)[4],
+                                      UnitWeights<NB> &o) {
+  f16_t z;
   uint32_t again = 0;  // unknown to the compiler: the operands of the rare second product are not kept for it
   asm volatile("" : "+v"(again));
-  unit_scores<BF16, LO>(kb + again, q, lo + again, z);
-  o.mid[0] = mt[4].x;
-  o.mid[1] = mt[5].x;
+  unit_scores<LO>(kb + again, q, lo + again, z);
+  float mx = -INFINITY, mv = -INFINITY;
 #pragma unroll
-  for (int t = 0; t < WT; t++) {
-    float s[2][4], mx[2], lv[2];
+  for (int u = 0; u < NB; u++) {
+    const float2 mk = mt[u];
+    const float A = mk.y * q.ca, B = mk.x * q.cq;
+    float t = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      const float A = mt[u].y * q[t].ca, B = mt[u].x * q[t].cq;
-#pragma unroll
-      for (int r = 0; r < 4; r++) s[u][r] = 16 * u + r < vis[t] ? __builtin_fmaf(z[t][u][r], A, B) : -INFINITY;
-      mx[u] = fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3]));
-      lv[u] = __builtin_amdgcn_logf(mt[4 + u].y);
+    for (int k = 0; k < 16 / NB; k++) {
+      const int r = 16 / NB * u + k;
+      o.p[r] = 8 * (r >> 2) + (r & 3) < vis ? __builtin_fmaf(z[r], A, B) : -INFINITY;
+      t = fmaxf(t, o.p[r]);
     }
-    const float mn = fmaxf(st[t].m, row_max(fmaxf(mx[0], mx[1])));
-    float on = fmaxf(st[t].mo, row_max(fmaxf(mx[0] + lv[0], mx[1] + lv[1])));
-    const bool some = mn > -INFINITY;
-    if (some) on = fmaxf(on, mn - 80.0f);
-    const float al = st[t].m > -INFINITY ? exp2_fast(st[t].m - mn) : 0.0f;
-    const float ao = st[t].mo > -INFINITY ? exp2_fast(st[t].mo - on) : 0.0f;
-    st[t].l *= al;
-    st[t].mv *= al;
+    mx = fmaxf(mx, t);
+    mv = fmaxf(mv, t + __builtin_amdgcn_logf(mt[2 + u].y));  // log2; -inf for a constant block
+  }
+  const float mn = fmaxf(st.m, pair_max(mx));
+  float on = fmaxf(st.mo, pair_max(mv));
+  const bool some = mn > -INFINITY;
+  if (some) on = fmaxf(on, mn - 80.0f);  // keeps 2^(m - mo) finite beside weights that vanish
+  const float al = st.m > -INFINITY ? exp2_fast(st.m - mn) : 0.0f;
+  const float ao = st.mo > -INFINITY ? exp2_fast(st.mo - on) : 0.0f;
+  st.l *= al;
+  st.mv *= al;
 #pragma unroll
-    for (int j = 0; j < 8; j++) acc[t][j] *= ao;
-    st[t].m = st[t].mu = mn;
-    st[t].mo = on;
-    st[t].f = some ? exp2_fast(mn - on + 9.0f) : 1.0f;
-    const float mu = some ? mn : 0.0f;
+  for (int j = 0; j < 4; j++) acc[j] *= ao;
+  st.m = st.mu = mn;
+  st.mo = on;
+  st.f = some ? exp2_fast(mn - on + 9.0f) : 1.0f;
+  const float mu = some ? mn : 0.0f;
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
+  for (int r = 0; r < 16; r++) o.p[r] = exp2_fast(o.p[r] - mu);
+  sum_weights(o);
 #pragma unroll
-      for (int r = 0; r < 4; r++) o.p[t][u][r] = exp2_fast(s[u][r] - mu);
-      o.ps[t][u] = (o.p[t][u][0] + o.p[t][u][1]) + (o.p[t][u][2] + o.p[t][u][3]);
-      o.w[t][u] = mt[4 + u].y * st[t].f;
-    }
+  for (int u = 0; u < NB; u++) {
+    o.mid[u] = mt[2 + u].x;
+    o.w[u] = mt[2 + u].y * st.f;
   }
 }
 
-// a unit's weights as operands, its sums into the rows' state
+// a unit's weights as operands (tokens 16 x + ..), its sums into the row's state
 template <bool BF16>
 struct UnitOperands {
-  h8_t hi[WT], lo[WT];  // lo: fp32 storage only
+  h8_t hi[2], lo[2];  // lo: fp32 storage only
 };
 
-template <bool BF16>
-__device__ __forceinline__ void take_weights(const UnitWeights &o, TileState (&st)[WT], UnitOperands<BF16> &P) {
+template <bool BF16, int NB>
+__device__ __forceinline__ void take_weights(const UnitWeights<NB> &o, TileState &st, UnitOperands<BF16> &P) {
 #pragma unroll
-  for (int t = 0; t < WT; t++) {
-    uint32_t ph[2][2], pl[2][2];
-    st[t].l += o.ps[t][0] + o.ps[t][1];
+  for (int u = 0; u < NB; u++) {
+    st.l += o.ps[u];
+    st.mv = __builtin_fmaf(o.mid[u], o.ps[u], st.mv);
+  }
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      st[t].mv = __builtin_fmaf(o.mid[u], o.ps[t][u], st[t].mv);
+  for (int x = 0; x < 2; x++) {
+    uint32_t ph[4], pl[4];
+    const float w = o.w[NB == 2 ? x : 0];
 #pragma unroll
-      for (int k = 0; k < 2; k++) {
-        const float x = o.p[t][u][2 * k] * o.w[t][u], y = o.p[t][u][2 * k + 1] * o.w[t][u];
-        ph[u][k] = pack_f16x2(x, y);
-        if constexpr (!BF16) {
-          const f2_t hh = unpack_f16x2(ph[u][k]);
-          pl[u][k] = pack_f16x2(x - hh.x, y - hh.y);
-        }
+    for (int k = 0; k < 4; k++) {
+      const float a = o.p[8 * x + 2 * k] * w, b = o.p[8 * x + 2 * k + 1] * w;
+      ph[k] = pack_f16x2(a, b);
+      if constexpr (!BF16) {
+        const f2_t hh = unpack_f16x2(ph[k]);
+        pl[k] = pack_f16x2(a - hh.x, b - hh.y);
       }
     }
-    P.hi[t] = as_h8(ph[0][0], ph[0][1], ph[1][0], ph[1][1]);
-    if constexpr (!BF16) P.lo[t] = as_h8(pl[0][0], pl[0][1], pl[1][0], pl[1][1]);
+    P.hi[x] = as_h8(ph[0], ph[1], ph[2], ph[3]);
+    if constexpr (!BF16) P.lo[x] = as_h8(pl[0], pl[1], pl[2], pl[3]);
   }
 }
 
-// acc += V^T P^T of a unit, from the value codes at vl[i] (lane offsets of tokens
-// 4 grp + i; the second tile 16 rows on)
+// 4 tokens x 16 channels of fp16 values as an operand half: lane n of 16 names
+// 4 channels of token n / 4 and receives the 4 tokens of channel n
+// (transposing LDS read)
+typedef short s4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ s4_t transposed(const unsigned char *p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t *)p);
+}
+
+// acc += V^T P^T of a unit, from the values at vb (this lane's token and piece);
+// acc[j][r]: channel 32 j + 8 (r / 4) + 4 half + r % 4
 template <bool BF16>
-__device__ __forceinline__ void unit_values(const unsigned char *vb, const int (&vl)[4], const UnitOperands<BF16> &P,
-                                            f4_t (&acc)[WT][8]) {
-  uint2 v[2][4];
+__device__ __forceinline__ void unit_values(const unsigned char *vb, const UnitOperands<BF16> &P, f16_t (&acc)[4]) {
 #pragma unroll
-  for (int u = 0; u < 2; u++)
+  for (int x = 0; x < 2; x++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) v[u][i] = *(const uint2 *)(vb + vl[i] + 16 * D * u);
-#define CG_PV(J)                                                   \
-  {                                                                \
-    const h8_t vj = value_frag<J>(v);                              \
-    _Pragma("unroll") for (int t = 0; t < WT; t++) {               \
-      acc[t][J] = mfma(vj, P.hi[t], acc[t][J]);                       \
-      if constexpr (!BF16) acc[t][J] = mfma(vj, P.lo[t], acc[t][J]); \
-    }                                                              \
-  }
-  CG_PV(0) CG_PV(1) CG_PV(2) CG_PV(3) CG_PV(4) CG_PV(5) CG_PV(6) CG_PV(7)
-#undef CG_PV
+    for (int j = 0; j < 4; j++) {
+      const s4_t a = transposed(vb + 16 * x * VP + 64 * j), b = transposed(vb + (16 * x + 8) * VP + 64 * j);
+      const h8_t vj = __builtin_bit_cast(h8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+      acc[j] = mfma32(vj, P.hi[x], acc[j]);
+      if constexpr (!BF16) acc[j] = mfma32(vj, P.lo[x], acc[j]);
+    }
 }
 
 // LO: the queries' second fp16 part takes part (fp32 storage, or where log-sums
-// or weights are asked for); else a query is rounded to 2^-11 of a channel
-template <bool BF16, bool LO>
+// or weights are asked for); else a query is rounded to 2^-11 of a channel.
+// NB: ranges to a unit of 32 tokens.
+template <bool BF16, bool LO, int NB>
 __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   static_assert(BF16 || LO, "fp32 storage takes both parts");
-  constexpr int LOOP_LDS = LOBUF + (LO ? 4 * WT * 4096 : 0), END_LDS = TROWS * PITCH * 4;
+  constexpr int LOOP_LDS = LOBUF + (LO ? 4 * 8192 : 0), END_LDS = TROWS * PITCH * 4;
   __shared__ __align__(16) unsigned char lds[LOOP_LDS > END_LDS ? LOOP_LDS : END_LDS];
-  const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
+  const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5, n = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fields = a.batch * a.heads, groups = (a.rows + TROWS - 1) / TROWS;
   int64_t id = blockIdx.x;
   const int bh = (int)(id % fields);  // a head's workgroups share an XCD's L2 where the heads are a multiple of 8
   id /= fields;
   const int split = (int)(id % a.splits);
-  const int grpi = groups - 1 - (int)(id / a.splits);  // the longest first
+  // the longest first; where all are resident at once (two to a compute unit) the
+  // second half runs from the shortest up, beside the first half's longest
+  const int turn_of = (int)(id / a.splits), first = (groups + 1) / 2;
+  const bool paired = (int64_t)gridDim.x <= 512 && a.splits == 1;
+  const int grpi = paired && turn_of >= first ? turn_of - first : groups - 1 - turn_of;
   const int h = bh % a.heads, b = bh / a.heads;
   const int r0 = grpi * TROWS, nr = min(TROWS, a.rows - r0);
   const int len = seq_length(a, b);
@@ -274,124 +282,106 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
   const int tmax = limit_of(a, b, len, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
-  const int stages = (tmax + STAGE - 1) / STAGE;
-  const int s0 = (int)((int64_t)stages * split / a.splits), s1 = (int)((int64_t)stages * (split + 1) / a.splits);
-  StageRegs nx;
-  if (s0 < s1) fetch_stage(a, kf, vf, km, vm, s0 * STAGE, nx);
+  const int units = (tmax + UNIT - 1) / UNIT;
+  const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
+  UnitRegs nx;
+  if (u0 < u1) fetch_unit(a, kf, vf, km, vm, u0, nx);
 
-  // gauged queries as operands (a wave past the last tile takes the last one's)
-  QueryFrags q[WT];
+  // gauged queries as operands (a wave past the last row tile takes the last one's)
+  TileQueries q;
+  const unsigned char *lo = lds + LOBUF + wave * 8192 + lane * 16;
+  const int wr = r0 + wave * WROWS + row;  // the lane's row
+  {
+    const int64_t tile = (int64_t)bh * a.tiles + min(wr >> 4, a.tiles - 1);
+    const uint4 *f = a.qfrag + tile * 8 * 64;
+    const float2 x = a.qrow[tile * ROWS + n];
+    q.ca = x.x * kCentredUnit;
+    q.cq = x.y;
 #pragma unroll
-  for (int t = 0; t < WT; t++) {
-    const int tile = min((r0 >> 4) + wave * WT + t, a.tiles - 1);
-    const uint4 *f = a.qfrag + ((int64_t)bh * a.tiles + tile) * 8 * 64 + lane;
-    const float2 x = a.qrow[((int64_t)bh * a.tiles + tile) * ROWS + row];
-    q[t].ca = x.x * (BF16 ? kCodeUnit : kCentredUnit);
-    q[t].cq = x.y;
-#pragma unroll
-    for (int s = 0; s < 4; s++) {
-      q[t].hi[s] = __builtin_bit_cast(h8_t, f[s * 64]);
-      if constexpr (LO) *(uint4 *)(lds + LOBUF + ((wave * WT + t) * 4 + s) * 1024 + lane * 16) = f[(4 + s) * 64];
+    for (int s = 0; s < 8; s++) {
+      const int c = 2 * s + half, at = (c >> 2) * 64 + (c & 3) * 16 + n;  // the 8 channels from 8 c on
+      q.hi[s] = __builtin_bit_cast(h8_t, f[at]);
+      if constexpr (LO) *(uint4 *)(lds + LOBUF + wave * 8192 + s * 1024 + lane * 16) = f[4 * 64 + at];
     }
   }
-  int lim[WT], all = tmax;  // what the lane's rows see; rows that are not there see everything
+  // what the row sees; rows that are not there see everything
+  const int lim = wr < a.rows ? query_limit(a, b, len, wr / a.ratio) : tmax;
+  int all = lim;
 #pragma unroll
-  for (int t = 0; t < WT; t++) {
-    const int r = r0 + (wave * WT + t) * ROWS + row;
-    lim[t] = r < a.rows ? query_limit(a, b, len, r / a.ratio) : tmax;
-    all = min(all, lim[t]);
-  }
-#pragma unroll
-  for (int k = 1; k < 16; k <<= 1) all = min(all, __shfl_xor(all, k));
+  for (int k = 1; k < 32; k <<= 1) all = min(all, __shfl_xor(all, k));
   all = __builtin_amdgcn_readfirstlane(all);
 
-  TileState st[WT];
-  f4_t acc[WT][8];
+  TileState st;
+  st.m = st.mo = st.mu = -INFINITY;
+  st.l = st.mv = 0.0f;
+  st.f = 1.0f;
+  f16_t acc[4];
 #pragma unroll
-  for (int t = 0; t < WT; t++) {
-    st[t].m = st[t].mo = st[t].mu = -INFINITY;
-    st[t].l = st[t].mv = 0.0f;
-    st[t].f = 1.0f;
+  for (int j = 0; j < 4; j++)
 #pragma unroll
-    for (int j = 0; j < 8; j++) acc[t][j] = f4_t{0.f, 0.f, 0.f, 0.f};
-  }
-  const unsigned char *lo = lds + LOBUF + wave * WT * 4096 + lane * 16;
-  int vl[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int r = 4 * grp + i;
-    vl[i] = r * D + 16 * ((row >> 1) ^ (r & 7)) + 8 * (row & 1);
-  }
-  const auto keys_at = [&](int un) { return lds + KBUF + ((un >> 1) & 1) * CODES + (un & 1) * UNIT * D; };
-  const auto values_at = [&](int un) { return lds + VBUF + ((un >> 1) % 3) * CODES + (un & 1) * UNIT * D; };
-  const auto ranges_at = [&](int un) { return (const float2 *)(lds + MBUF + ((un >> 1) % 3) * 64) + (un & 1) * 2; };
+    for (int r = 0; r < 16; r++) acc[j][r] = 0.0f;
+  const auto keys_at = [&](int un) { return lds + KBUF + (un & 1) * KBYTES + row * KP + 16 * half; };
+  const auto values_at = [&](int un) {
+    return lds + VBUF + (un % 3) * VBYTES + (4 * half + (n >> 2)) * VP + 32 * ((lane >> 4) & 1) + 8 * (n & 3);
+  };
+  const auto ranges_at = [&](int un) { return (const float2 *)(lds + MBUF + (un % 3) * 32); };
 
   // One unit ahead: a turn forms the scores and weights of the next unit beside
   // the value product of the present one, so matrix and vector work of both
   // lie in one block for the scheduler.
-  if (s0 < s1) {
-    const int u0 = 2 * s0, u1 = min(2 * s1, (tmax + UNIT - 1) / UNIT);
-    UnitWeights o;
+  if (u0 < u1) {
+    UnitWeights<NB> o;
     UnitOperands<BF16> P;
-    int vis[WT];
-    put_stage<!BF16>(lds, s0, tmax, nx);
-    if (s0 + 1 < s1) fetch_stage(a, kf, vf, km, vm, (s0 + 1) * STAGE, nx);
+    put_unit(lds, u0, tmax, nx);
+    fetch_unit(a, kf, vf, km, vm, u0 + 1, nx);  // units past the last are fetched (rows that exist) and not used
+    put_unit(lds, u0 + 1, tmax, nx);
+    fetch_unit(a, kf, vf, km, vm, u0 + 2, nx);
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < WT; t++) vis[t] = lim[t] - u0 * UNIT - 4 * grp;
-    raise<BF16, LO>(keys_at(u0), lo, ranges_at(u0), q, vis, st, acc, o);
+    raise<LO, NB>(keys_at(u0), lo, ranges_at(u0), q, lim - u0 * UNIT - 4 * half, st, acc, o);
     const auto turn = [&](int un, auto masked) {
-      if (un & 1) {
-        __syncthreads();  // the next stage is there
-      } else {
-        const int sg = un >> 1;
-        if (sg + 1 < s1) put_stage<!BF16>(lds, sg + 1, tmax, nx);
-        if (sg + 2 < s1) fetch_stage(a, kf, vf, km, vm, (sg + 2) * STAGE, nx);
-      }
+      __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
+      put_unit(lds, un + 2, tmax, nx);
+      fetch_unit(a, kf, vf, km, vm, un + 3, nx);
       const float2 *mt = ranges_at(un + 1);
-#pragma unroll
-      for (int t = 0; t < WT; t++) vis[t] = lim[t] - (un + 1) * UNIT - 4 * grp;
-      take_weights<BF16>(o, st, P);
-      f4_t z[WT][2];
-      unit_scores<BF16, LO>(keys_at(un + 1), q, lo, z);
-      unit_values<BF16>(values_at(un), vl, P, acc);
-      const bool up = unit_weights<decltype(masked)::value>(mt, q, z, vis, st, o);
-      if (__any(up)) raise<BF16, LO>(keys_at(un + 1), lo, mt, q, vis, st, acc, o);
+      const int vis = lim - (un + 1) * UNIT - 4 * half;
+      take_weights<BF16, NB>(o, st, P);
+      f16_t z;
+      unit_scores<LO>(keys_at(un + 1), q, lo, z);
+      unit_values<BF16>(values_at(un), P, acc);
+      const bool up = unit_weights<decltype(masked)::value, NB>(mt, q, z, vis, st, o);
+      if (__any(up)) raise<LO, NB>(keys_at(un + 1), lo, mt, q, vis, st, acc, o);
     };
     // units that every row of the wave sees whole, then the others
     const int ua = min(u1 - 1, max(all / UNIT - 1, u0));
     for (int un = u0; un < ua; un++) turn(un, std::false_type{});
     for (int un = max(ua, u0); un + 1 < u1; un++) turn(un, std::true_type{});
-    take_weights<BF16>(o, st, P);
-    unit_values<BF16>(values_at(u1 - 1), vl, P, acc);
+    take_weights<BF16, NB>(o, st, P);
+    unit_values<BF16>(values_at(u1 - 1), P, acc);
   }
   __syncthreads();
 
   // rows' sums, scaled as they stand, into LDS; then parts or outputs
   float *us = (float *)lds;
-#pragma unroll
-  for (int t = 0; t < WT; t++) {
-    const int rr = (wave * WT + t) * ROWS + row;
-    const float L = row_sum(st[t].l), mvs = row_sum(st[t].mv);
-    const bool some = st[t].m > -INFINITY;
+  {
+    const int rr = wave * WROWS + row;
+    const float L = st.l + __shfl_xor(st.l, 32), mvs = st.mv + __shfl_xor(st.mv, 32);
+    const bool some = st.m > -INFINITY;
     const float inv = a.splits > 1 ? 1.0f : L > 0.0f ? 1.0f / L : 0.0f;
-    const float ks = some ? inv * exp2_fast(st[t].mo - st[t].m) : 0.0f;
+    const float ks = some ? inv * exp2_fast(st.mo - st.m) : 0.0f;
     const float k = some ? inv * mvs : 0.0f;
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
-      float v[8];
+    for (int j = 0; j < 4; j++)
 #pragma unroll
-      for (int j = 0; j < 8; j++) v[j] = __builtin_fmaf(acc[t][j][r], ks, k);
-      float *o = us + rr * PITCH + 8 * (4 * grp + r);
-      *(float4 *)o = make_float4(v[0], v[1], v[2], v[3]);
-      *(float4 *)(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    if (grp == 0 && rr < nr) {
+      for (int r = 0; r < 16; r += 4)
+        *(float4 *)(us + rr * PITCH + 32 * j + 2 * r + 4 * half) =
+            make_float4(__builtin_fmaf(acc[j][r], ks, k), __builtin_fmaf(acc[j][r + 1], ks, k),
+                        __builtin_fmaf(acc[j][r + 2], ks, k), __builtin_fmaf(acc[j][r + 3], ks, k));
+    if (half == 0 && rr < nr) {
       if (a.splits > 1) {
-        a.part_ml[((int64_t)bh * a.splits + split) * a.rows + r0 + rr] = make_float2(st[t].m, L);
+        a.part_ml[((int64_t)bh * a.splits + split) * a.rows + wr] = make_float2(st.m, L);
       } else {
-        if (a.lse) store_lse(a, b, h, r0 + rr, st[t].m, L);
-        if (a.lse2) a.lse2[(int64_t)bh * a.rows + r0 + rr] = L > 0.0f ? st[t].m + __builtin_log2f(L) : INFINITY;
+        if (a.lse) store_lse(a, b, h, wr, st.m, L);
+        if (a.lse2) a.lse2[(int64_t)bh * a.rows + wr] = L > 0.0f ? st.m + __builtin_log2f(L) : INFINITY;
       }
     }
   }
@@ -427,7 +417,7 @@ __global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
   const int lane = threadIdx.x & 63, tile = tile0 + (int)(threadIdx.x >> 6);
   if (tile >= a.tiles) return;
   QueryFrags q;
-  make_frags<LO>(ys[threadIdx.x >> 6], a.c, q);
+  make_frags<LO, false>(ys[threadIdx.x >> 6], a.c, q);
   uint4 *d = a.qfrag + ((int64_t)bh * a.tiles + tile) * 8 * 64 + lane;
 #pragma unroll
   for (int s = 0; s < 4; s++) {
@@ -441,16 +431,17 @@ hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const int64_t groups = (a.rows + TROWS - 1) / TROWS;
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * groups * a.splits)), block(NTH);
   const dim3 pre((unsigned)((int64_t)a.batch * a.heads * ((a.tiles + 3) / 4)));
-  if (!bf16) {
-    hipLaunchKernelGGL((k_attend_prepare<false, true>), pre, block, 0, s, a);
-    hipLaunchKernelGGL((k_attend_tile<false, true>), grid, block, 0, s, a);
-  } else if (a.lse || a.mass) {
-    hipLaunchKernelGGL((k_attend_prepare<true, true>), pre, block, 0, s, a);
-    hipLaunchKernelGGL((k_attend_tile<true, true>), grid, block, 0, s, a);
-  } else {
-    hipLaunchKernelGGL((k_attend_prepare<true, false>), pre, block, 0, s, a);
-    hipLaunchKernelGGL((k_attend_tile<true, false>), grid, block, 0, s, a);
+  const bool two = a.bshift == 4;  // ranges to a unit
+#define CG_T(BF, LO)                                                                           \
+  {                                                                                            \
+    hipLaunchKernelGGL((k_attend_prepare<BF, LO>), pre, block, 0, s, a);                       \
+    if (two) hipLaunchKernelGGL((k_attend_tile<BF, LO, 2>), grid, block, 0, s, a);             \
+    else hipLaunchKernelGGL((k_attend_tile<BF, LO, 1>), grid, block, 0, s, a);                 \
   }
+  if (!bf16) CG_T(false, true)
+  else if (a.lse || a.mass) CG_T(true, true)
+  else CG_T(true, false)
+#undef CG_T
   return hipGetLastError();
 }
 
