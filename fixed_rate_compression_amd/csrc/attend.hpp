@@ -38,6 +38,7 @@ using cgk::PITCH;
 constexpr int ROWS = 16;  // query rows of a row tile (one matrix-core operand)
 constexpr int UNIT = 32;  // tokens of a unit of work
 constexpr int NTH = 256;  // threads of a workgroup
+constexpr int MERGE_SPLITS = 1024;  // splits at most
 
 struct AttendArgs {
   const uint8_t *kpay, *vpay;    // codes of the layer's key / value fields, field (b, h) at (b heads + h) tcap 128
@@ -53,14 +54,14 @@ struct AttendArgs {
   float2 *part_ml;               // [b][h][split][rows] (maximum, sum of weights)
   float2 *bsum;                  // [b][h][entry][rows] (block sum, its maximum)
   float *lse2;                   // [b][h][rows] log2 of the row's sum (many rows with mass)
+  float *mpart;                  // [part][b][h][nblk] parts of the blocks' weights (many rows)
   uint4 *qfrag;                  // [b][h][tile][hi/lo][step][lane] fp16 query operands
   float2 *qrow;                  // [b][h][16 tiles] (score factor, minimum factor)
   int64_t tcap, tokens, nblk;
   int64_t q_bs, q_ts;            // query strides (elements)
   int64_t entries;               // block-sum entries of a field
   int32_t batch, heads, ratio, n, rows, tiles;  // rows = n ratio, tiles = ceil(rows / 16)
-  int32_t g, bshift, causal, splits;
-  int32_t merge_rows;             // rows a merge workgroup takes
+  int32_t g, bshift, causal, splits, mparts;
   float c;                       // scale log2(e)
 };
 
@@ -168,66 +169,101 @@ __device__ __forceinline__ int limit_of(const AttendArgs &a, int b, int len, int
   return a.causal ? (int)hi + 1 : len;
 }
 
-// query rows [r0, r0 + 16) of (b, h) as fp32 into xs [16][PITCH]; rows past
-// the last one are zero
+// this thread's 8 channels of one of the query rows [r0, r0 + 16) of (b, h) as
+// fp32; rows past the last one are zero
+struct RowPart {
+  f4_t lo, hi;
+};
+
 template <bool BF16>
-__device__ __forceinline__ void load_rows(const AttendArgs &a, int b, int h, int r0, float *xs) {
+__device__ __forceinline__ RowPart load_row_part(const AttendArgs &a, int b, int h, int r0) {
   const int r = r0 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;
-  float *d = xs + (threadIdx.x >> 4) * PITCH + c;
-  float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+  RowPart p;
+  p.lo = p.hi = f4_t{0.f, 0.f, 0.f, 0.f};
   if (r < a.rows) {
     const int i = r / a.ratio, j = r - i * a.ratio;
     const int64_t off = (int64_t)b * a.q_bs + (int64_t)i * a.q_ts + (int64_t)(h * a.ratio + j) * D + c;
     if (BF16) {
       const uint4 w = *(const uint4 *)((const uint16_t *)a.q + off);
-      lo = make_float4(cgk::bf16lo(w.x), cgk::bf16hi(w.x), cgk::bf16lo(w.y), cgk::bf16hi(w.y));
-      hi = make_float4(cgk::bf16lo(w.z), cgk::bf16hi(w.z), cgk::bf16lo(w.w), cgk::bf16hi(w.w));
+      p.lo = f4_t{cgk::bf16lo(w.x), cgk::bf16hi(w.x), cgk::bf16lo(w.y), cgk::bf16hi(w.y)};
+      p.hi = f4_t{cgk::bf16lo(w.z), cgk::bf16hi(w.z), cgk::bf16lo(w.w), cgk::bf16hi(w.w)};
     } else {
-      const float4 *p = (const float4 *)((const float *)a.q + off);
-      lo = p[0];
-      hi = p[1];
+      const f4_t *x = (const f4_t *)((const float *)a.q + off);
+      p.lo = x[0];
+      p.hi = x[1];
     }
   }
-  *(float4 *)d = lo;
-  *(float4 *)(d + 4) = hi;
+  return p;
 }
 
-// y = G x (INV: G^T x) for `nr` rows of xs [16][PITCH], fmaf chains over a
-// group's channels in index order; thread (c, half) owns channel c of rows
-// half, half + 2, ..  emit(row, c, value) takes the results.
-template <bool INV, typename Emit>
-__device__ __forceinline__ void gauge_rows(const float *xs, int nr, const float *__restrict__ gh, int g, Emit emit) {
+// into xs [16][PITCH]
+__device__ __forceinline__ void put_row_part(float *xs, const RowPart &p) {
+  float *d = xs + (threadIdx.x >> 4) * PITCH + (threadIdx.x & 15) * 8;
+  *(f4_t *)d = p.lo;
+  *(f4_t *)(d + 4) = p.hi;
+}
+
+// y = G x (INV: G^T x) for rows of xs [NR][PITCH], fmaf chains over a group's
+// channels in index order; thread (c, half) owns channel c of rows half,
+// half + 2, ...  The first 32 weights of the thread's chain are loaded apart
+// from their use, so that they travel beside other loads.
+constexpr int GCHUNK = 32;
+struct GaugeWeights {
+  float w[GCHUNK];
+};
+
+template <bool INV>
+__device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, int k0, GaugeWeights &x) {
+  if (g == 0) return;
+  const int c = threadIdx.x & (D - 1), cg = c & (g - 1);  // g is a power of two
+  const float *gp = gh + (int64_t)(c - cg) * g + (INV ? cg : cg * g);
+#pragma unroll
+  for (int k = 0; k < GCHUNK; k += 8) {
+    if (k0 + k < g) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) x.w[k + e] = gp[INV ? (k0 + k + e) * g : k0 + k + e];
+    }
+  }
+}
+
+// gw: load_gauge's for k0 = 0; emit(row, c, value) takes the results of rows < nr
+template <bool INV, int NR, typename Emit>
+__device__ __forceinline__ void gauge_rows(const float *xs, int nr, const float *__restrict__ gh, int g,
+                                           const GaugeWeights &first, Emit emit) {
   const int c = threadIdx.x & (D - 1), half = threadIdx.x >> 7;
   if (g == 0) {
     for (int r = half; r < nr; r += 2) emit(r, c, xs[r * PITCH + c]);
     return;
   }
-  const int cg = c & (g - 1), base = c - cg;  // g is a power of two
-  const float *gp = gh + (int64_t)base * g + (INV ? cg : cg * g);
-  float acc[8];
+  const int base = c - (c & (g - 1));
+  float acc[NR / 2];
 #pragma unroll
-  for (int r = 0; r < 8; r++) acc[r] = 0.0f;
-  for (int k0 = 0; k0 < g; k0 += 8) {
-    float w[8];
+  for (int r = 0; r < NR / 2; r++) acc[r] = 0.0f;
+  GaugeWeights x = first;
+  for (int k0 = 0; k0 < g; k0 += GCHUNK) {
+    if (k0) load_gauge<INV>(gh, g, k0, x);
 #pragma unroll
-    for (int k = 0; k < 8; k++) w[k] = INV ? gp[(k0 + k) * g] : gp[k0 + k];
+    for (int k = 0; k < GCHUNK; k += 8) {
+      if (k0 + k < g) {
+        const float *w = x.w + k;
 #pragma unroll
-    for (int r = 0; r < 8; r++) {
-      const int row = half + 2 * r;
-      if (row < nr) {
-        const float *x = xs + row * PITCH + base + k0;
-        const float4 p = *(const float4 *)x, q = *(const float4 *)(x + 4);
-        float v = acc[r];
-        v = __builtin_fmaf(w[0], p.x, v); v = __builtin_fmaf(w[1], p.y, v);
-        v = __builtin_fmaf(w[2], p.z, v); v = __builtin_fmaf(w[3], p.w, v);
-        v = __builtin_fmaf(w[4], q.x, v); v = __builtin_fmaf(w[5], q.y, v);
-        v = __builtin_fmaf(w[6], q.z, v); v = __builtin_fmaf(w[7], q.w, v);
-        acc[r] = v;
+        for (int r = 0; r < NR / 2; r++) {
+          if (half + 2 * r < nr) {
+            const float *p = xs + (half + 2 * r) * PITCH + base + k0 + k;
+            const f4_t u = *(const f4_t *)p, v = *(const f4_t *)(p + 4);
+            float t = acc[r];
+            t = __builtin_fmaf(w[0], u[0], t); t = __builtin_fmaf(w[1], u[1], t);
+            t = __builtin_fmaf(w[2], u[2], t); t = __builtin_fmaf(w[3], u[3], t);
+            t = __builtin_fmaf(w[4], v[0], t); t = __builtin_fmaf(w[5], v[1], t);
+            t = __builtin_fmaf(w[6], v[2], t); t = __builtin_fmaf(w[7], v[3], t);
+            acc[r] = t;
+          }
+        }
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < 8; r++)
+  for (int r = 0; r < NR / 2; r++)
     if (half + 2 * r < nr) emit(half + 2 * r, c, acc[r]);
 }
 

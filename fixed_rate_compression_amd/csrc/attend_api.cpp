@@ -13,20 +13,22 @@ using cgh::error;
 
 struct Plan {
   int64_t rows, tiles;
-  int splits, merge_rows;
+  int splits, mparts;
   bool few;  // one row tile: block sums come with the attention
   int64_t entries;
-  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, qfrag_bytes, qrow_bytes;
-  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + qfrag_bytes + qrow_bytes; }
+  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, mpart_bytes, qfrag_bytes, qrow_bytes;
+  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + mpart_bytes + qfrag_bytes + qrow_bytes; }
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workgroups that keep 256 compute units busy: three on each, with at least
-// 256 tokens (two units a wave) to a workgroup.
-constexpr int64_t kTargetWorkgroups = 768, kMinTokens = 256;
+// Workgroups that keep 256 compute units busy: four on each (their LDS),
+// with at least 256 tokens (two units a wave) to a workgroup.
+constexpr int64_t kTargetWorkgroups = 1024, kMinTokens = 256;
 // 128-row tiles: two workgroups fit a compute unit
 constexpr int64_t kTargetTiles = 512;
+// weights of many rows: four workgroups to a compute unit, four row steps at least to each
+constexpr int64_t kTargetMass = 1024;
 
 Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {
   Plan p{};
@@ -39,9 +41,9 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   int64_t sp = work > 0 ? (p.few ? (target + work - 1) / work : target / work) : 1;
   const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
   if (sp > most) sp = most;
+  if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
   if (sp < 1) sp = 1;
   p.splits = (int)sp;
-  p.merge_rows = fields * p.rows <= 2048 ? 1 : cga::ROWS;
   const int64_t nblk = s->token_capacity / c->block_tokens;
   p.entries = c->block_tokens == 64 ? 2 * nblk : nblk;
   const bool parts = p.splits > 1;
@@ -49,7 +51,14 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   p.ml_bytes = parts || (mass && p.few) ? up256((size_t)(fields * p.splits * p.rows) * 8) : 0;
   if (mass && p.few) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
   if (!p.few) {
-    if (mass) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
+    if (mass) {  // 256 tokens and a part of the rows to a workgroup
+      const int64_t groups = fields * ((s->tokens + 255) / 256), steps = (p.rows + 31) / 32;
+      int64_t mp = groups > 0 ? (kTargetMass + groups - 1) / groups : 1;
+      if (mp > (steps + 3) / 4) mp = (steps + 3) / 4;
+      p.mparts = (int)mp;
+      p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
+      p.mpart_bytes = up256((size_t)(mp * fields * nblk) * 4);
+    }
     p.qfrag_bytes = up256((size_t)(fields * p.tiles) * 8 * 64 * 16);
     p.qrow_bytes = up256((size_t)(fields * p.tiles) * cga::ROWS * 8);
   }
@@ -154,7 +163,6 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.bshift = codec->block_tokens == 16 ? 4 : codec->block_tokens == 32 ? 5 : 6;
   a.causal = attn->causal;
   a.splits = p.splits;
-  a.merge_rows = p.merge_rows;
   a.entries = p.entries;
   a.c = (float)((double)attn->scale * 1.4426950408889634074);
   char *w = (char *)workspace;
@@ -163,6 +171,8 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.part_ml = (float2 *)take(p.ml_bytes);
   a.bsum = (float2 *)take(p.bsum_bytes);
   a.lse2 = (float *)take(p.lse2_bytes);
+  a.mpart = (float *)take(p.mpart_bytes);
+  a.mparts = p.mparts;
   a.qfrag = (uint4 *)take(p.qfrag_bytes);
   a.qrow = (float2 *)take(p.qrow_bytes);
 

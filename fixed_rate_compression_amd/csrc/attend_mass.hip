@@ -1,96 +1,189 @@
 // The weight each block of the 8-bit cache received from many query rows: a
 // second pass over the keys with the queries' operands and the rows' log-sums
-// that the attention left.
+// that the attention left.  No row's state is carried, so the work splits over
+// tokens and rows alike; a workgroup's share of a block's sum goes to a slot of
+// its own and the slots are added in order (no atomics: the same bits every time).
 #include "attend.hpp"
 
 namespace cga {
 
-// A wave owns 32 tokens (64 where a block has 64: twice 32) of one field, holds
-// their codes as operands and walks the row tiles: weights 2^(s - log2 sum),
-// summed over rows and tokens of a block in a fixed order by their one owner.
-__global__ __launch_bounds__(NTH) void k_mass_many(const AttendArgs a, int64_t groups) {
-  const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
+typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+
+constexpr int QT = 32;                  // query rows of a step
+constexpr int QBYTES = 2 * 8 * 64 * 16; // their operands, two row tiles
+constexpr int QSTEP = QBYTES + QT * 16; // and (score factor, minimum factor, log-sum, limit) of each row
+
+struct QueryRegs {
+  u4_t q0, q1, q2, q3;
+  float4 r;
+};
+
+__device__ __forceinline__ void fetch_queries(const AttendArgs &a, int bh, int b, int len, int step, QueryRegs &s) {
+  const int i = threadIdx.x;
+  const int64_t t0 = (int64_t)bh * a.tiles + min(2 * step, a.tiles - 1);
+  const int64_t t1 = (int64_t)bh * a.tiles + min(2 * step + 1, a.tiles - 1);
+  const u4_t *p0 = (const u4_t *)(a.qfrag + t0 * 512), *p1 = (const u4_t *)(a.qfrag + t1 * 512);
+  s.q0 = p0[i];
+  s.q1 = p0[256 + i];
+  s.q2 = p1[i];
+  s.q3 = p1[256 + i];
+  const int row = i & (QT - 1), r = step * QT + row, rr = min(r, a.rows - 1);
+  const float2 f = a.qrow[(int64_t)bh * a.tiles * ROWS + rr];
+  s.r = make_float4(f.x * kCentredUnit, f.y, a.lse2[(int64_t)bh * a.rows + rr],
+                    __int_as_float(r < a.rows ? query_limit(a, b, len, r / a.ratio) : 0));
+}
+
+__device__ __forceinline__ void put_queries(unsigned char *buf, const QueryRegs &s) {
+  u4_t *d = (u4_t *)buf;
+  const int i = threadIdx.x;
+  d[i] = s.q0;
+  d[256 + i] = s.q1;
+  d[512 + i] = s.q2;
+  d[768 + i] = s.q3;
+  if (i < QT) *(float4 *)(buf + QBYTES + 16 * i) = s.r;
+}
+
+// A workgroup: 256 tokens of a field, 64 to a wave (held as operands), against
+// a part of the query rows, 32 at a time through LDS.  NB: blocks to 32 tokens
+// (one also where a block has 64).
+template <int NB>
+__global__ __launch_bounds__(NTH, 2) void k_mass_many(const AttendArgs a) {
+  __shared__ __align__(16) unsigned char lds[2 * QSTEP];
+  const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5, n = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wgs = (groups + 3) / 4;
-  const int bh = (int)(blockIdx.x / wgs);
-  const int64_t grpi = (blockIdx.x % wgs) * 4 + wave;
+  const int fields = a.batch * a.heads, tgroups = (int)((a.tokens + 255) / 256);
+  int64_t id = blockIdx.x;
+  const int bh = (int)(id % fields);
+  id /= fields;
+  const int part = (int)(id % a.mparts), tg = (int)(id / a.mparts);
   const int b = bh / a.heads;
   const int len = seq_length(a, b);
   const int tmax = limit_of(a, b, len, 0, a.n - 1);
-  const int per = a.bshift == 6 ? 2 : 1;
-  if (grpi * per * UNIT >= tmax) return;
+  const int w0 = tg * 256;
+  if (w0 >= tmax) return;
+  // the row steps that see one of these tokens, this workgroup's part of them
+  const int64_t start = a.starts ? (int64_t)a.starts[b] : (int64_t)len - a.n;
+  const int64_t i0 = a.causal ? max((int64_t)w0 - start, (int64_t)0) : 0;
+  const int steps = (a.rows + QT - 1) / QT;
+  const int s_lo = (int)min(i0 * a.ratio / QT, (int64_t)steps);
+  const int s0 = s_lo + (int)((int64_t)(steps - s_lo) * part / a.mparts);
+  const int s1 = s_lo + (int)((int64_t)(steps - s_lo) * (part + 1) / a.mparts);
+  const int t0 = w0 + 64 * wave;
+
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk;
-  float total[2] = {0.0f, 0.0f};
-  for (int half = 0; half < per; half++) {
-    const int t0 = (int)(grpi * per + half) * UNIT;
-    if (t0 >= tmax) break;
-    h8_t kc[2][4];
-    float2 m[2];
+  QueryRegs nx;
+  if (s0 < s1) fetch_queries(a, bh, b, len, s0, nx);
+  h8_t kc[2][8];
+  float2 m[2][NB];
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-      const int64_t tt = min((int64_t)t0 + 16 * t, a.tcap - 16);  // 16-token blocks: the capacity may end here
+  for (int u = 0; u < 2; u++) {
+    const int64_t t = min((int64_t)t0 + 32 * u + row, a.tcap - 1);  // tokens past the capacity repeat its last row
 #pragma unroll
-      for (int x = 0; x < 4; x++) {
-        const uint2 w = *(const uint2 *)(kf + (tt + row) * D + 32 * x + 8 * grp);
-        kc[t][x] = codes8<true>(w.x, w.y);
-      }
-      m[t] = km[tt >> a.bshift];
+    for (int s = 0; s < 8; s++) {
+      const uint2 w = *(const uint2 *)(kf + t * D + 16 * s + 8 * half);
+      kc[u][s] = codes8<true>(w.x, w.y);
     }
-    float sum[2] = {0.0f, 0.0f};
-    for (int tile = 0; tile < a.tiles; tile++) {
-      const int r1 = min(a.rows, (tile + 1) * ROWS) - 1;
-      if (limit_of(a, b, len, tile * ROWS / a.ratio, r1 / a.ratio) <= t0) continue;
-      const int64_t id = (int64_t)bh * a.tiles + tile;
-      const uint4 *qf = a.qfrag + id * 8 * 64 + lane;
-      const float2 qr = a.qrow[id * ROWS + row];
-      const int r = tile * ROWS + row;
-      const int lim = r < a.rows ? query_limit(a, b, len, r / a.ratio) : 0;
-      const float lse2 = r < a.rows ? a.lse2[(int64_t)bh * a.rows + r] : INFINITY;
-      const f4_t none = f4_t{0.f, 0.f, 0.f, 0.f};
-      f4_t z[2] = {none, none}, zl[2] = {none, none};
 #pragma unroll
-      for (int s = 0; s < 4; s++) {
-        const h8_t qh = __builtin_bit_cast(h8_t, qf[s * 64]), ql = __builtin_bit_cast(h8_t, qf[(4 + s) * 64]);
+    for (int k = 0; k < NB; k++) {
+      const int64_t tt = (int64_t)t0 + 32 * u + 16 * k;
+      float2 x = km[min(tt >> a.bshift, a.nblk - 1)];
+      x.x = __builtin_fmaf(128.0f, x.y, x.x);
+      m[u][k] = tt < tmax ? x : make_float2(0.f, 0.f);  // a block that holds no row yet
+    }
+  }
+  float sum[2][NB];
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-          z[t] = mfma(kc[t][s], qh, z[t]);
-          zl[t] = mfma(kc[t][s], ql, zl[t]);
-        }
-      }
-      z[0] += zl[0];
-      z[1] += zl[1];
+  for (int u = 0; u < 2; u++)
 #pragma unroll
-      for (int t = 0; t < 2; t++) {
-        const float A = m[t].y * qr.x * kCentredUnit, Bm = __builtin_fmaf(128.0f, m[t].y, m[t].x) * qr.y - lse2;
+    for (int k = 0; k < NB; k++) sum[u][k] = 0.0f;
+  if (s0 < s1) put_queries(lds, nx);
+  if (s0 + 1 < s1) fetch_queries(a, bh, b, len, s0 + 1, nx);
+  for (int st = s0; st < s1; st++) {
+    __syncthreads();
+    const unsigned char *buf = lds + ((st - s0) & 1) * QSTEP;
+    if (st + 1 < s1) put_queries(lds + ((st + 1 - s0) & 1) * QSTEP, nx);
+    if (st + 2 < s1) fetch_queries(a, bh, b, len, st + 2, nx);
+    const unsigned char *qb = buf + (row >> 4) * 8192 + 16 * n;
+    f16_t z[2], zl[2];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const float s = __builtin_fmaf(z[t][k], A, Bm);
-          sum[t] += t0 + 16 * t + 4 * grp + k < lim ? exp2_fast(s) : 0.0f;
-        }
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) z[u][r] = zl[u][r] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 8; s++) {
+      const int c = 2 * s + half, at = ((c >> 2) * 64 + (c & 3) * 16) * 16;
+      const h8_t qh = *(const h8_t *)(qb + at), ql = *(const h8_t *)(qb + 4096 + at);
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        z[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc[u][s], qh, z[u], 0, 0, 0);
+        zl[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc[u][s], ql, zl[u], 0, 0, 0);
       }
     }
-    total[0] += sum[0];
-    total[1] += sum[1];
+    const float4 rp = *(const float4 *)(buf + QBYTES + 16 * row);
+    const int lim = __float_as_int(rp.w) - t0 - 4 * half;
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      z[u] += zl[u];
+#pragma unroll
+      for (int k = 0; k < NB; k++) {
+        const float A = m[u][k].y * rp.x, B = __builtin_fmaf(m[u][k].x, rp.y, -rp.z);
+        float p[16 / NB];
+#pragma unroll
+        for (int e = 0; e < 16 / NB; e++) {
+          const int r = 16 / NB * k + e;
+          const float s = __builtin_fmaf(z[u][r], A, B);
+          p[e] = exp2_fast(32 * u + 8 * (r >> 2) + (r & 3) < lim ? s : -INFINITY);
+        }
+#pragma unroll
+        for (int w = 8 / NB; w >= 1; w >>= 1)
+#pragma unroll
+          for (int e = 0; e < w; e++) p[e] += p[e + w];
+        sum[u][k] += p[0];
+      }
+    }
   }
 #pragma unroll
-  for (int t = 0; t < 2; t++)
+  for (int u = 0; u < 2; u++)
 #pragma unroll
-    for (int k = 1; k < 64; k <<= 1) total[t] += __shfl_xor(total[t], k);
+    for (int k = 0; k < NB; k++)
+#pragma unroll
+      for (int x = 1; x < 64; x <<= 1) sum[u][k] += __shfl_xor(sum[u][k], x);
   if (lane) return;
-  float *out = a.mass + (int64_t)bh * a.nblk;
-  if (a.bshift == 4) {
-    out[2 * grpi] += total[0];
-    if (2 * grpi + 1 < a.nblk) out[2 * grpi + 1] += total[1];
-  } else {
-    out[grpi] += total[0] + total[1];
+  float *out = a.mpart + ((int64_t)part * fields + bh) * a.nblk;
+  if (a.bshift == 6) {
+    if (t0 < tmax) out[t0 >> 6] = sum[0][0] + sum[1][0];
+    return;
   }
+#pragma unroll
+  for (int u = 0; u < 2; u++)
+#pragma unroll
+    for (int k = 0; k < NB; k++) {
+      const int t = t0 + 32 * u + 16 * k;
+      if (t < tmax) out[t >> a.bshift] = sum[u][k];
+    }
+}
+
+__global__ __launch_bounds__(NTH) void k_mass_add(const AttendArgs a) {
+  const int fields = a.batch * a.heads;
+  const int64_t chunks = (a.nblk + NTH - 1) / NTH, blk = (blockIdx.x % chunks) * NTH + threadIdx.x;
+  const int bh = (int)(blockIdx.x / chunks), b = bh / a.heads;
+  if (blk >= a.nblk || (blk << a.bshift) >= limit_of(a, b, seq_length(a, b), 0, a.n - 1)) return;
+  float w = 0.0f;
+#pragma unroll 8
+  for (int p = 0; p < a.mparts; p++) w += a.mpart[((int64_t)p * fields + bh) * a.nblk + blk];
+  a.mass[(int64_t)bh * a.nblk + blk] += w;
 }
 
 hipError_t mass_many_launch(const AttendArgs &a, hipStream_t s) {
-  const int64_t span = a.bshift == 6 ? 2 * UNIT : UNIT, groups = (a.tokens + span - 1) / span;
-  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * ((groups + 3) / 4))), block(NTH);
-  hipLaunchKernelGGL(k_mass_many, grid, block, 0, s, a, groups);
+  const int64_t fields = (int64_t)a.batch * a.heads, tg = (a.tokens + 255) / 256;
+  const dim3 grid((unsigned)(fields * tg * a.mparts)), block(NTH);
+  if (a.bshift == 4) hipLaunchKernelGGL(k_mass_many<2>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(k_mass_many<1>, grid, block, 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_mass_add, dim3((unsigned)(fields * ((a.nblk + NTH - 1) / NTH))), block, 0, s, a);
   return hipGetLastError();
 }
 

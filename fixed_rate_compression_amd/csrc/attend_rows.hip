@@ -93,6 +93,11 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
   const int h = (int)(id % a.heads), b = (int)(id / a.heads);
   const int bh = b * a.heads + h;
   const int r0 = tile * ROWS, nr = min(ROWS, a.rows - r0);
+  // on their way first: what does not wait for the sequence's length
+  const float *gk = a.gk + (int64_t)h * D * a.g;
+  const RowPart qp = load_row_part<BF16>(a, b, h, r0);
+  GaugeWeights gw;
+  load_gauge<false>(gk, a.g, 0, gw);
   const int len = seq_length(a, b);
   const int tmax = limit_of(a, b, len, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
@@ -106,11 +111,11 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
 
   // gauged query rows
   float *xs = lds, *ys = lds + ROWS * PITCH;
-  load_rows<BF16>(a, b, h, r0, xs);
+  put_row_part(xs, qp);
   if (nr < ROWS)
     for (int i = threadIdx.x; i < (ROWS - nr) * D; i += NTH) ys[(nr + (i >> 7)) * PITCH + (i & 127)] = 0.0f;
   __syncthreads();
-  gauge_rows<false>(xs, nr, a.gk + (int64_t)h * D * a.g, a.g, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
+  gauge_rows<false, ROWS>(xs, nr, gk, a.g, gw, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
   __syncthreads();
   QueryFrags q;
   make_frags<true, true>(ys, a.c, q);
@@ -302,46 +307,108 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
     v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
     *(float4 *)(lds + r * PITCH + c) = v;  // this thread alone reads row r's channels c .. c + 3
   }
+  const float *gv = a.gv + (int64_t)h * D * a.g;
+  load_gauge<true>(gv, a.g, 0, gw);
   __syncthreads();
-  gauge_rows<true>(lds, nr, a.gv + (int64_t)h * D * a.g, a.g,
-                   [&](int r, int c, float v) { store_out<BF16>(a, b, h, r0 + r, c, v); });
+  gauge_rows<true, ROWS>(lds, nr, gv, a.g, gw, [&](int r, int c, float v) { store_out<BF16>(a, b, h, r0 + r, c, v); });
 }
 
-// Joins the splits of `merge_rows` rows: weights 2^(m_s - M), the inverse
-// gauge, the output and the log of the sum.
+// Joins the splits of one row, a workgroup to a row: 2^(m_s - M) of every
+// split, eight groups of 32 lanes adding every eighth split's sums, then the
+// inverse gauge.  For few rows with many splits.
 template <bool BF16>
 __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
-  __shared__ __align__(16) float us[ROWS * PITCH];
-  __shared__ __align__(16) float part[D];
-  const int nt = (a.rows + a.merge_rows - 1) / a.merge_rows;
+  __shared__ __align__(16) float part[8][D];
+  __shared__ __align__(16) float us[PITCH];
+  __shared__ float wt[MERGE_SPLITS];
+  __shared__ float2 red[4];
   const int64_t id = blockIdx.x;
-  const int r0 = (int)(id % nt) * a.merge_rows, bh = (int)(id / nt);
+  const int r = (int)(id % a.rows), bh = (int)(id / a.rows);
   const int h = bh % a.heads, b = bh / a.heads;
-  const int nr = min(a.merge_rows, a.rows - r0);
-  const int c = threadIdx.x & (D - 1), half = threadIdx.x >> 7;
-  for (int r = 0; r < nr; r++) {
-    const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r0 + r;
-    const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r0 + r) * D + c;
-    float M = -INFINITY;
+  const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r;
+  const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r) * D;
+  const int S = a.splits, t = threadIdx.x;
+  // this thread's part of G_V, on its way while the sums are joined
+  const float *gv = a.gv + (int64_t)h * D * a.g;
+  GaugeWeights gw;
+  load_gauge<true>(gv, a.g, 0, gw);
+  float M = -INFINITY;
+  for (int s = t; s < S; s += NTH) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
+#pragma unroll
+  for (int k = 32; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor(M, k));
+  if ((t & 63) == 0) red[t >> 6].x = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
+  float L = 0.0f;
+  for (int s = t; s < S; s += NTH) {
+    const float2 x = pm[(int64_t)s * a.rows];
+    const float k = x.x > -INFINITY ? exp2_fast(x.x - M) : 0.0f;
+    wt[s] = k;
+    L += x.y * k;
+  }
+#pragma unroll
+  for (int k = 32; k >= 1; k >>= 1) L += __shfl_xor(L, k);
+  if ((t & 63) == 0) red[t >> 6].y = L;
+  __syncthreads();
+  L = (red[0].y + red[1].y) + (red[2].y + red[3].y);
+  const int grp = t >> 5, c4 = 4 * (t & 31);
+  float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = grp; s < S; s += 8) {
+    const float k = wt[s];
+    const float4 x = *(const float4 *)(po + (int64_t)s * a.rows * D + c4);
+    u.x += x.x * k; u.y += x.y * k; u.z += x.z * k; u.w += x.w * k;
+  }
+  *(float4 *)&part[grp][c4] = u;
+  __syncthreads();
+  if (t == 0 && a.lse) store_lse(a, b, h, r, M, L);
+  if (t < D) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; k++) v += part[k][t];
+    us[t] = L > 0.0f ? v / L : 0.0f;
+  }
+  __syncthreads();
+  gauge_rows<true, 2>(us, 1, gv, a.g, gw, [&](int, int cc, float v) { store_out<BF16>(a, b, h, r, cc, v); });
+}
+
+// The same for many rows with few splits: 16 rows to a workgroup, a row to a
+// wave at a time.
+template <bool BF16>
+__global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
+  __shared__ __align__(16) float us[ROWS * PITCH];
+  const int64_t id = blockIdx.x;
+  const int r0 = (int)(id % a.tiles) * ROWS, bh = (int)(id / a.tiles);
+  const int h = bh % a.heads, b = bh / a.heads, nr = min(ROWS, a.rows - r0);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float *gv = a.gv + (int64_t)h * D * a.g;
+  GaugeWeights gw;
+  load_gauge<true>(gv, a.g, 0, gw);
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int rr = wave + 4 * i, r = min(r0 + rr, a.rows - 1);
+    const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r;
+    const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r) * D + 2 * lane;
+    float M = -INFINITY, L = 0.0f;
     for (int s = 0; s < a.splits; s++) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
-    float L = 0.0f, u = 0.0f;
+    float2 u = make_float2(0.f, 0.f);
+#pragma unroll 4
     for (int s = 0; s < a.splits; s++) {
-      const float2 x = pm[(int64_t)s * a.rows];
+      const float2 x = pm[(int64_t)s * a.rows], y = *(const float2 *)(po + (int64_t)s * a.rows * D);
       const float k = x.x > -INFINITY ? exp2_fast(x.x - M) : 0.0f;
       L += x.y * k;
-      if ((s & 1) == half) u += po[(int64_t)s * a.rows * D] * k;
+      u.x += y.x * k;
+      u.y += y.y * k;
     }
-    if (half) part[c] = u;
-    __syncthreads();
-    if (!half) us[r * PITCH + c] = L > 0.0f ? (u + part[c]) / L : 0.0f;
-    if (threadIdx.x == 0) {
-      if (a.lse) store_lse(a, b, h, r0 + r, M, L);
-      if (a.lse2) a.lse2[(int64_t)bh * a.rows + r0 + r] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    *(float2 *)(us + rr * PITCH + 2 * lane) = make_float2(u.x * inv, u.y * inv);
+    if (lane == 0 && rr < nr) {
+      if (a.lse) store_lse(a, b, h, r, M, L);
+      if (a.lse2) a.lse2[(int64_t)bh * a.rows + r] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
     }
-    __syncthreads();
   }
-  gauge_rows<true>(us, nr, a.gv + (int64_t)h * D * a.g, a.g,
-                   [&](int r, int cc, float v) { store_out<BF16>(a, b, h, r0 + r, cc, v); });
+  __syncthreads();
+  gauge_rows<true, ROWS>(us, nr, gv, a.g, gw, [&](int r, int cc, float v) { store_out<BF16>(a, b, h, r0 + r, cc, v); });
 }
 
 // Block weights of few rows from the sums the attention left: mass[block] +=
@@ -389,10 +456,16 @@ hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
 }
 
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
-  const int64_t nt = (a.rows + a.merge_rows - 1) / a.merge_rows;
-  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * nt)), block(NTH);
-  if (bf16) hipLaunchKernelGGL(k_attend_merge<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_attend_merge<false>, grid, block, 0, s, a);
+  const int64_t fields = (int64_t)a.batch * a.heads;
+  if (a.tiles > 1) {
+    const dim3 grid((unsigned)(fields * a.tiles)), block(NTH);
+    if (bf16) hipLaunchKernelGGL(k_attend_merge_many<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_attend_merge_many<false>, grid, block, 0, s, a);
+  } else {
+    const dim3 grid((unsigned)(fields * a.rows)), block(NTH);
+    if (bf16) hipLaunchKernelGGL(k_attend_merge<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_attend_merge<false>, grid, block, 0, s, a);
+  }
   return hipGetLastError();
 }
 

@@ -54,18 +54,20 @@ __device__ __forceinline__ void fetch_unit(const AttendArgs &a, const uint8_t *k
   s.m = ((i & 2) ? vm : km)[blk];
 }
 
-// widened (centred) into LDS, once for the four waves
+// widened into LDS, once for the four waves (keys centred where both query
+// parts take part: then their sums are exact)
+template <bool LO>
 __device__ __forceinline__ void put_unit(unsigned char *lds, int un, int tmax, const UnitRegs &s) {
   const int i = threadIdx.x;
   unsigned char *k = lds + KBUF + (un & 1) * KBYTES + (i >> 3) * KP + 32 * (i & 7);
   unsigned char *v = lds + VBUF + (un % 3) * VBYTES + (i >> 3) * VP + 32 * (i & 7);
-  *(h8_t *)k = codes8<true>(s.k.x, s.k.y);
-  *(h8_t *)(k + 16) = codes8<true>(s.k.z, s.k.w);
+  *(h8_t *)k = codes8<LO>(s.k.x, s.k.y);
+  *(h8_t *)(k + 16) = codes8<LO>(s.k.z, s.k.w);
   *(h8_t *)v = codes8<true>(s.v.x, s.v.y);
   *(h8_t *)(v + 16) = codes8<true>(s.v.z, s.v.w);
   if (i < 4) {
     const bool there = un * UNIT + 16 * (i & 1) < tmax;  // a block that holds no row yet is not looked at
-    const float mid = __builtin_fmaf(128.0f, s.m.y, s.m.x);  // the value of code 128
+    const float mid = LO || (i & 2) ? __builtin_fmaf(128.0f, s.m.y, s.m.x) : s.m.x;  // the value of code 128 (0)
     *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * i) = make_float2(there ? mid : 0.0f, there ? s.m.y : 0.0f);
   }
 }
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
     const int64_t tile = (int64_t)bh * a.tiles + min(wr >> 4, a.tiles - 1);
     const uint4 *f = a.qfrag + tile * 8 * 64;
     const float2 x = a.qrow[tile * ROWS + n];
-    q.ca = x.x * kCentredUnit;
+    q.ca = x.x * (LO ? kCentredUnit : kCodeUnit);
     q.cq = x.y;
 #pragma unroll
     for (int s = 0; s < 8; s++) {
@@ -332,15 +334,15 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   if (u0 < u1) {
     UnitWeights<NB> o;
     UnitOperands<BF16> P;
-    put_unit(lds, u0, tmax, nx);
+    put_unit<LO>(lds, u0, tmax, nx);
     fetch_unit(a, kf, vf, km, vm, u0 + 1, nx);  // units past the last are fetched (rows that exist) and not used
-    put_unit(lds, u0 + 1, tmax, nx);
+    put_unit<LO>(lds, u0 + 1, tmax, nx);
     fetch_unit(a, kf, vf, km, vm, u0 + 2, nx);
     __syncthreads();
     raise<LO, NB>(keys_at(u0), lo, ranges_at(u0), q, lim - u0 * UNIT - 4 * half, st, acc, o);
     const auto turn = [&](int un, auto masked) {
       __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
-      put_unit(lds, un + 2, tmax, nx);
+      put_unit<LO>(lds, un + 2, tmax, nx);
       fetch_unit(a, kf, vf, km, vm, un + 3, nx);
       const float2 *mt = ranges_at(un + 1);
       const int vis = lim - (un + 1) * UNIT - 4 * half;
@@ -361,6 +363,9 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   __syncthreads();
 
   // rows' sums, scaled as they stand, into LDS; then parts or outputs
+  const float *gv = a.gv + (int64_t)h * D * a.g;
+  GaugeWeights gw;
+  load_gauge<true>(gv, a.g, 0, gw);
   float *us = (float *)lds;
   {
     const int rr = wave * WROWS + row;
@@ -392,32 +397,41 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
       *(float4 *)(po + 4 * (int64_t)i) = *(const float4 *)(us + (i / (D / 4)) * PITCH + 4 * (i % (D / 4)));
     return;
   }
-  for (int t = 0; t * ROWS < nr; t++)
-    gauge_rows<true>(us + t * ROWS * PITCH, min(ROWS, nr - t * ROWS), a.gv + (int64_t)h * D * a.g, a.g,
-                     [&](int r, int c, float v) { store_out<BF16>(a, b, h, r0 + t * ROWS + r, c, v); });
+  for (int t = 0; t < nr; t += 64)
+    gauge_rows<true, 64>(us + t * PITCH, min(64, nr - t), gv, a.g, gw,
+                         [&](int r, int c, float v) { store_out<BF16>(a, b, h, r0 + t + r, c, v); });
 }
 
 // One workgroup per four row tiles: gauge, split into the operands' parts and
 // store in operand order, with each row's factors.
 template <bool BF16, bool LO>
 __global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
-  __shared__ __align__(16) float xs[4][ROWS * PITCH], ys[4][ROWS * PITCH];
+  __shared__ __align__(16) float xs[4 * ROWS * PITCH];
   const int quads = (a.tiles + 3) / 4;
   const int64_t id = blockIdx.x;
   const int tile0 = (int)(id % quads) * 4, bh = (int)(id / quads);
   const int h = bh % a.heads, b = bh / a.heads;
+  const float *gk = a.gk + (int64_t)h * D * a.g;
+  GaugeWeights gw;
+  load_gauge<false>(gk, a.g, 0, gw);
+  RowPart p[4];
 #pragma unroll
-  for (int t = 0; t < 4; t++) load_rows<BF16>(a, b, h, (tile0 + t) * ROWS, xs[t]);
+  for (int t = 0; t < 4; t++) p[t] = load_row_part<BF16>(a, b, h, (tile0 + t) * ROWS);
+#pragma unroll
+  for (int t = 0; t < 4; t++) put_row_part(xs + t * ROWS * PITCH, p[t]);
   __syncthreads();
-#pragma unroll 1
-  for (int t = 0; t < 4; t++)
-    gauge_rows<false>(xs[t], ROWS, a.gk + (int64_t)h * D * a.g, a.g,
-                      [&](int r, int c, float v) { ys[t][r * PITCH + c] = v; });
-  __syncthreads();
+  if (a.g) {  // in place: every thread has its results before any is stored
+    float y[2 * ROWS];
+    gauge_rows<false, 4 * ROWS>(xs, 4 * ROWS, gk, a.g, gw, [&](int r, int c, float v) { y[r >> 1] = v; });
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2 * ROWS; r++) xs[(2 * r + (threadIdx.x >> 7)) * PITCH + (threadIdx.x & (D - 1))] = y[r];
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 63, tile = tile0 + (int)(threadIdx.x >> 6);
   if (tile >= a.tiles) return;
   QueryFrags q;
-  make_frags<LO, false>(ys[threadIdx.x >> 6], a.c, q);
+  make_frags<LO, false>(xs + (threadIdx.x >> 6) * ROWS * PITCH, a.c, q);
   uint4 *d = a.qfrag + ((int64_t)bh * a.tiles + tile) * 8 * 64 + lane;
 #pragma unroll
   for (int s = 0; s < 4; s++) {
