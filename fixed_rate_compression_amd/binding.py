@@ -375,14 +375,25 @@ def cg_write_header(shape, codec, layer, kv) -> bytes:
     return buf.raw
 
 
+_dtypes = {}
+
+
+def _dtype(name):
+    """torch's dtype of that name (looked up once)."""
+    d = _dtypes.get(name)
+    if d is None:
+        import torch
+        d = _dtypes[name] = getattr(torch, name)
+    return d
+
+
 def _sized(name, t, dtype, count):
     """A device array argument whose size and type the C call cannot see."""
     if t is None or isinstance(t, int):
-        return _ptr(t)
-    import torch
-    if t.dtype != getattr(torch, dtype) or t.numel() < count:
-        raise ValueError(f"{name}: {count} values of {dtype} are needed, got {t.numel()} of {t.dtype}")
-    return _ptr(t)
+        return t
+    if t.dtype != _dtype(dtype) or t.numel() < count or not t.is_contiguous():
+        raise ValueError(f"{name}: {count} contiguous values of {dtype} are needed, got {t.numel()} of {t.dtype}")
+    return t.data_ptr()
 
 
 def _storage(shape):
@@ -393,9 +404,8 @@ def make_attn(layer, q_heads, n_queries, scale, causal=True, lengths=None, start
               q_strides=(0, 0)) -> CgAttn:
     """lengths, starts: device int32 [batch] (or None); q_strides: elements between
     sequences and between queries of q (0: dense)."""
-    import torch
     for name, t in (("lengths", lengths), ("starts", starts)):
-        if t is not None and not isinstance(t, int) and t.dtype != torch.int32:
+        if t is not None and not isinstance(t, int) and t.dtype != _dtype("int32"):
             raise ValueError(f"{name} must be int32, got {t.dtype}")
     at = CgAttn(layer, q_heads, n_queries, 1 if causal else 0, scale, _ptr(lengths), _ptr(starts),
                 q_strides[0], q_strides[1])
@@ -415,26 +425,24 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
               stream=None):
     """Attention of q [batch, n, q_heads, 128] (heads contiguous, the other strides those
     of attn) over the encoded layer -> out (dense); see the header for lse and mass."""
-    rows = shape.batch * attn.n_queries * attn.q_heads
-    st = _storage(shape)
-    qp = q
+    batch, n, heads, d = shape.batch, attn.n_queries, attn.q_heads, shape.head_dim
+    rows, st = batch * n * heads, _storage(shape)
     if not isinstance(q, int):
-        if str(q.dtype) != "torch." + st:
-            raise ValueError(f"q must be {st}, got {q.dtype}")
-        if tuple(q.shape) != (shape.batch, attn.n_queries, attn.q_heads, shape.head_dim):
-            raise ValueError(f"q must be [batch, n, q_heads, head_dim], got {tuple(q.shape)}")
-        want = (attn.q_batch_stride or attn.n_queries * attn.q_heads * shape.head_dim,
-                attn.q_token_stride or attn.q_heads * shape.head_dim, shape.head_dim, 1)
-        if q.numel() and any(n > 1 and s != w for n, s, w in zip(q.shape, q.stride(), want)):
-            raise ValueError(f"q of strides {q.stride()} does not lie as attn says ({want})")
-        qp = q.data_ptr()
-    nblk = shape.token_capacity // codec.block_tokens if codec.block_tokens > 0 else 0
-    _check("cg_attend", lib().cg_attend(
-        ctypes.byref(shape), _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta),
-        ctypes.byref(gauge), ctypes.byref(codec), ctypes.byref(attn), qp,
-        _sized("out", out, st, rows * shape.head_dim), _sized("lse", lse, "float32", rows),
-        _sized("mass", mass, "float32", shape.layers * shape.batch * shape.heads * nblk),
-        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        if q.dtype != _dtype(st) or q.shape != (batch, n, heads, d):
+            raise ValueError(f"q must be {st} [batch, n, q_heads, head_dim], got {q.dtype} {tuple(q.shape)}")
+        sb, sn, sh, sd = q.stride()
+        if rows and ((batch > 1 and sb != (attn.q_batch_stride or n * heads * d)) or
+                     (n > 1 and sn != (attn.q_token_stride or heads * d)) or (heads > 1 and sh != d) or sd != 1):
+            raise ValueError(f"q of strides {q.stride()} does not lie as attn says")
+        q = q.data_ptr()
+    blk = codec.block_tokens
+    rc = lib().cg_attend(
+        shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, attn, q,
+        _sized("out", out, st, rows * d), _sized("lse", lse, "float32", rows),
+        _sized("mass", mass, "float32", shape.layers * batch * shape.heads * (shape.token_capacity // blk if blk > 0 else 0)),
+        _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if rc != CG_OK:
+        _check("cg_attend", rc)
 
 
 def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, meta, lengths=None,
@@ -444,9 +452,9 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
     row, bs, rs = shape.heads * shape.head_dim, 0, 0
     ptrs = []
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if str(t.dtype) != "torch." + st:
+        if t.dtype != _dtype(st):
             raise ValueError(f"{name} must be {st}, got {t.dtype}")
-        if tuple(t.shape) != (shape.batch, n_new, shape.heads, shape.head_dim):
+        if t.shape != (shape.batch, n_new, shape.heads, shape.head_dim):
             raise ValueError(f"{name} must be [batch, n_new, heads, head_dim], got {tuple(t.shape)}")
         sb, sr, sh, sd = t.stride()
         if (sh != shape.head_dim and shape.heads > 1) or sd != 1 or t.stride() != k_new.stride():

@@ -62,6 +62,7 @@ struct AttendArgs {
   int64_t entries;               // block-sum entries of a field
   int32_t batch, heads, ratio, n, rows, tiles;  // rows = n ratio, tiles = ceil(rows / 16)
   int32_t g, bshift, causal, splits, mparts;
+  int32_t waves;  // of a few-row workgroup: 4 or 8
   float c;                       // scale log2(e)
 };
 
@@ -140,33 +141,53 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // sum / maximum over the four lanes of one row (lane, lane ^ 16, ^ 32, ^ 48)
 __device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
 __device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 
-// tokens of sequence b
-__device__ __forceinline__ int seq_length(const AttendArgs &a, int b) {
-  const int64_t n = a.lengths ? (int64_t)a.lengths[b] : a.tokens;
-  return (int)min(max(n, (int64_t)0), a.tokens);
+// a sequence's length and the position of its first query, loaded once
+struct Sequence {
+  int len;
+  int64_t start;
+};
+__device__ __forceinline__ Sequence load_sequence(const AttendArgs &a, int b) {
+  // both loads at once, from a place that is there where an array is not
+  const int32_t *any = (const int32_t *)a.q;
+  const int32_t n = *(a.lengths ? a.lengths + b : any), p = *(a.starts ? a.starts + b : any);
+  Sequence s;
+  s.len = a.lengths ? (int)min(max((int64_t)n, (int64_t)0), a.tokens) : (int)a.tokens;
+  s.start = a.starts ? (int64_t)p : (int64_t)s.len - a.n;
+  return s;
 }
 
-// tokens query i of sequence b sees: none unless it stands inside the sequence
-__device__ __forceinline__ int query_limit(const AttendArgs &a, int b, int len, int i) {
-  const int64_t pos = (a.starts ? (int64_t)a.starts[b] : (int64_t)len - a.n) + i;
-  if (pos < 0 || pos >= len) return 0;
-  return a.causal ? (int)pos + 1 : len;
+// tokens query i sees: none unless it stands inside the sequence
+__device__ __forceinline__ int query_limit(const AttendArgs &a, const Sequence &q, int i) {
+  const int64_t pos = q.start + i;
+  if (pos < 0 || pos >= q.len) return 0;
+  return a.causal ? (int)pos + 1 : q.len;
+}
+
+// first unit of part `part` of `parts` nearly equal ones
+__device__ __forceinline__ int split_begin(int units, int part, int parts) {
+  const int each = (int)((uint32_t)units / (uint32_t)parts), more = units - each * parts;
+  return each * part + min(part, more);
 }
 
 // the largest limit of queries [i0, i1]
-__device__ __forceinline__ int limit_of(const AttendArgs &a, int b, int len, int i0, int i1) {
-  const int64_t p0 = a.starts ? (int64_t)a.starts[b] : (int64_t)len - a.n;
-  const int64_t lo = max(p0 + i0, (int64_t)0), hi = min(p0 + i1, (int64_t)len - 1);
+__device__ __forceinline__ int limit_of(const AttendArgs &a, const Sequence &q, int i0, int i1) {
+  const int64_t lo = max(q.start + i0, (int64_t)0), hi = min(q.start + i1, (int64_t)q.len - 1);
   if (lo > hi) return 0;
-  return a.causal ? (int)hi + 1 : len;
+  return a.causal ? (int)hi + 1 : q.len;
 }
 
 // this thread's 8 channels of one of the query rows [r0, r0 + 16) of (b, h) as
@@ -181,7 +202,7 @@ __device__ __forceinline__ RowPart load_row_part(const AttendArgs &a, int b, int
   RowPart p;
   p.lo = p.hi = f4_t{0.f, 0.f, 0.f, 0.f};
   if (r < a.rows) {
-    const int i = r / a.ratio, j = r - i * a.ratio;
+    const int i = (int)((uint32_t)r / (uint32_t)a.ratio), j = r - i * a.ratio;
     const int64_t off = (int64_t)b * a.q_bs + (int64_t)i * a.q_ts + (int64_t)(h * a.ratio + j) * D + c;
     if (BF16) {
       const uint4 w = *(const uint4 *)((const uint16_t *)a.q + off);
@@ -203,68 +224,77 @@ __device__ __forceinline__ void put_row_part(float *xs, const RowPart &p) {
   *(f4_t *)(d + 4) = p.hi;
 }
 
-// y = G x (INV: G^T x) for rows of xs [NR][PITCH], fmaf chains over a group's
-// channels in index order; thread (c, half) owns channel c of rows half,
-// half + 2, ...  The first 32 weights of the thread's chain are loaded apart
-// from their use, so that they travel beside other loads.
-constexpr int GCHUNK = 32;
-struct GaugeWeights {
-  float w[GCHUNK];
+// y = G x (INV: G^T x) for 16-row tiles in LDS, on the matrix cores: an fp32
+// 16x16x4 product adds its four terms as fused multiply-adds, so the result is
+// a chain of them over a group's channels (groups of 8 run as 16 with zeros).
+// Wave w owns channels 32 w .. + 31; the weights are loaded apart from their
+// use, beside other loads.  On the vector units the same for four rows and
+// groups of 16 took 2000 cycles, most of it waiting.
+struct GaugeFrag {
+  f4_t b[2][8];  // output block nb, terms 16 s + 4 (lane / 16) + 0 .. 3 for channel lane % 16
 };
 
 template <bool INV>
-__device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, int k0, GaugeWeights &x) {
+__device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, GaugeFrag &f) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, kr = lane >> 4, n = lane & 15;
+  const int ge = max(g, 16);
   if (g == 0) return;
-  const int c = threadIdx.x & (D - 1), cg = c & (g - 1);  // g is a power of two
-  const float *gp = gh + (int64_t)(c - cg) * g + (INV ? cg : cg * g);
 #pragma unroll
-  for (int k = 0; k < GCHUNK; k += 8) {
-    if (k0 + k < g) {
+  for (int s = 0; s < 8; s++) {
+    if (16 * s < ge) {
 #pragma unroll
-      for (int e = 0; e < 8; e++) x.w[k + e] = gp[INV ? (k0 + k + e) * g : k0 + k + e];
+      for (int nb = 0; nb < 2; nb++) {
+        const int col = 32 * wave + 16 * nb + n, base = col & ~(ge - 1);  // sizes are powers of two
+        const int c = col & (g - 1), k = base + 16 * s + 4 * kr, kk = k & (g - 1);
+        const float *gp = gh + (int64_t)(col - c) * g;
+        f4_t w;
+        if constexpr (INV) {
+#pragma unroll
+          for (int e = 0; e < 4; e++) w[e] = gp[(kk + e) * g + c];
+        } else {
+          w = f4_t{gp[c * g + kk], gp[c * g + kk + 1], gp[c * g + kk + 2], gp[c * g + kk + 3]};
+        }
+        f.b[nb][s] = g >= 16 || (k ^ col) < 8 ? w : f4_t{0.f, 0.f, 0.f, 0.f};
+      }
     }
   }
 }
 
-// gw: load_gauge's for k0 = 0; emit(row, c, value) takes the results of rows < nr
-template <bool INV, int NR, typename Emit>
-__device__ __forceinline__ void gauge_rows(const float *xs, int nr, const float *__restrict__ gh, int g,
-                                           const GaugeWeights &first, Emit emit) {
-  const int c = threadIdx.x & (D - 1), half = threadIdx.x >> 7;
-  if (g == 0) {
-    for (int r = half; r < nr; r += 2) emit(r, c, xs[r * PITCH + c]);
-    return;
-  }
-  const int base = c - (c & (g - 1));
-  float acc[NR / 2];
+// tiles [0, T) of xs -> ys, both [16 T][PITCH]; IN_PLACE: the workgroup meets
+// between the reads and the writes (ys == xs).  The caller's barriers stand
+// before and after.
+template <int T, bool IN_PLACE>
+__device__ __forceinline__ void gauge_tiles(const float *xs, float *ys, int g, const GaugeFrag &f) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, kr = lane >> 4, n = lane & 15;
+  const int ge = max(g, 16);
+  f4_t acc[T][2];
 #pragma unroll
-  for (int r = 0; r < NR / 2; r++) acc[r] = 0.0f;
-  GaugeWeights x = first;
-  for (int k0 = 0; k0 < g; k0 += GCHUNK) {
-    if (k0) load_gauge<INV>(gh, g, k0, x);
+  for (int t = 0; t < T; t++) acc[t][0] = acc[t][1] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < GCHUNK; k += 8) {
-      if (k0 + k < g) {
-        const float *w = x.w + k;
+  for (int s = 0; s < 8; s++) {
+    if (16 * s < ge) {
 #pragma unroll
-        for (int r = 0; r < NR / 2; r++) {
-          if (half + 2 * r < nr) {
-            const float *p = xs + (half + 2 * r) * PITCH + base + k0 + k;
-            const f4_t u = *(const f4_t *)p, v = *(const f4_t *)(p + 4);
-            float t = acc[r];
-            t = __builtin_fmaf(w[0], u[0], t); t = __builtin_fmaf(w[1], u[1], t);
-            t = __builtin_fmaf(w[2], u[2], t); t = __builtin_fmaf(w[3], u[3], t);
-            t = __builtin_fmaf(w[4], v[0], t); t = __builtin_fmaf(w[5], v[1], t);
-            t = __builtin_fmaf(w[6], v[2], t); t = __builtin_fmaf(w[7], v[3], t);
-            acc[r] = t;
-          }
+      for (int t = 0; t < T; t++) {
+        const float *row = xs + (16 * t + n) * PITCH + 16 * s + 4 * kr;
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++) {
+          const f4_t x = *(const f4_t *)(row + ((32 * wave + 16 * nb) & ~(ge - 1)));
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            acc[t][nb] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], f.b[nb][s][e], acc[t][nb], 0, 0, 0);
         }
       }
     }
   }
+  if (IN_PLACE) __syncthreads();
 #pragma unroll
-  for (int r = 0; r < NR / 2; r++)
-    if (half + 2 * r < nr) emit(half + 2 * r, c, acc[r]);
+  for (int t = 0; t < T; t++)
+#pragma unroll
+    for (int nb = 0; nb < 2; nb++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) ys[(16 * t + 4 * kr + j) * PITCH + 32 * wave + 16 * nb + n] = acc[t][nb][j];
 }
 
 // The fp16 operands of 16 gauged rows xs [16][PITCH]: lane (row = lane % 16,
@@ -276,61 +306,80 @@ struct QueryFrags {
   float ca, cq;  // score = (sum of q' code) step ca + minimum cq
 };
 
-// TWO: two fixed-point parts; else one fp16 part, each channel rounded to 2^-11
-template <bool TWO, bool BYTES>
-__device__ __forceinline__ void make_frags(const float *xs, float c, QueryFrags &f) {
+// TWO: two fixed-point parts; else one fp16 part, each channel rounded to 2^-11.
+// Steps [S0, S0 + NS) only; cq is then their part of it.
+template <bool TWO, bool BYTES, int NS>
+__device__ __forceinline__ void make_frags(const float *xs, float c, int s0, QueryFrags &f) {
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
-  float x[4][8];
+  const float *rp = xs + row * PITCH;
   float mx = 0.0f;
 #pragma unroll
-  for (int s = 0; s < 4; s++) {
-    const float *p = xs + row * PITCH + (BYTES ? 64 * (s >> 1) + 16 * grp + 8 * (s & 1) : 32 * s + 8 * grp);
-    const float4 u = *(const float4 *)p, v = *(const float4 *)(p + 4);
-    x[s][0] = u.x; x[s][1] = u.y; x[s][2] = u.z; x[s][3] = u.w;
-    x[s][4] = v.x; x[s][5] = v.y; x[s][6] = v.z; x[s][7] = v.w;
-#pragma unroll
-    for (int k = 0; k < 8; k++) mx = fmaxf(mx, fabsf(x[s][k]));
+  for (int s = 0; s < 8; s++) {  // the row's largest magnitude, a quarter of the row to a lane
+    const f4_t u = *(const f4_t *)(rp + 32 * grp + 4 * s);
+    mx = fmaxf(fmaxf(mx, fabsf(u[0])), fmaxf(fabsf(u[1]), fmaxf(fabsf(u[2]), fabsf(u[3]))));
   }
   mx = row_max(mx);
-  // power-of-two factor that puts the row's maximum into [2^13, 2^14)
+  // power-of-two factor that puts it into [2^13, 2^14)
   const int ex = mx > 0.0f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
   const int sh = min(max(13 - ex, -100), 100);
-  const float up = __builtin_ldexpf(1.0f, sh);
+  const float up = __uint_as_float((uint32_t)(127 + sh) << 23), un = __uint_as_float((uint32_t)(127 - sh) << 23);
+  constexpr float H = 1.5f * 134217728.0f, L = 1.5f * 65536.0f;  // x + H - H rounds to multiples of 2^4, L of 2^-7
   float sum = 0.0f;
 #pragma unroll
-  for (int s = 0; s < 4; s++) {
+  for (int e = 0; e < NS; e++) {
+    const int s = s0 + e;
+    const float *p = rp + (BYTES ? 64 * (s >> 1) + 16 * grp + 8 * (s & 1) : 32 * s + 8 * grp);
+    const f4_t u = *(const f4_t *)p, v = *(const f4_t *)(p + 4);
     uint32_t wh[4], wl[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const float p = x[s][2 * k] * up, q = x[s][2 * k + 1] * up;
+      const float x = (k < 2 ? u[2 * k] : v[2 * k - 4]) * up, y = (k < 2 ? u[2 * k + 1] : v[2 * k - 3]) * up;
       if constexpr (TWO) {
-        const float ph = rintf(p * 0.0625f) * 16.0f, qh = rintf(q * 0.0625f) * 16.0f;
-        const float pl = rintf((p - ph) * 128.0f) * 0.0078125f, ql = rintf((q - qh) * 128.0f) * 0.0078125f;
-        wh[k] = pack_f16x2(ph, qh);  // both parts are exact in fp16
-        wl[k] = pack_f16x2(pl, ql);
-        sum += (ph + pl) + (qh + ql);
+        const float xh = (x + H) - H, yh = (y + H) - H;
+        const float xl = ((x - xh) + L) - L, yl = ((y - yh) + L) - L;
+        wh[k] = pack_f16x2(xh, yh);  // both parts are exact in fp16
+        wl[k] = pack_f16x2(xl, yl);
+        sum += (xh + xl) + (yh + yl);
       } else {
-        wh[k] = pack_f16x2(p, q);
+        wh[k] = pack_f16x2(x, y);
         wl[k] = 0u;
         const f2_t h = unpack_f16x2(wh[k]);
         sum += h.x + h.y;
       }
     }
-    f.hi[s] = as_h8(wh[0], wh[1], wh[2], wh[3]);
-    f.lo[s] = as_h8(wl[0], wl[1], wl[2], wl[3]);
+    f.hi[e] = as_h8(wh[0], wh[1], wh[2], wh[3]);
+    f.lo[e] = as_h8(wl[0], wl[1], wl[2], wl[3]);
   }
-  const float down = c * __builtin_ldexpf(1.0f, -sh);
-  f.ca = down;
-  f.cq = down * row_sum(sum);
+  f.ca = c * un;
+  f.cq = f.ca * row_sum(sum);
 }
 
-// one output row element (b, query row r of head h, channel c)
+// one output element (b, query row r of head h, channel c)
 template <bool BF16>
 __device__ __forceinline__ void store_out(const AttendArgs &a, int b, int h, int r, int c, float v) {
   const int i = r / a.ratio, j = r - i * a.ratio;
   const int64_t off = (((int64_t)b * a.n + i) * a.heads * a.ratio + h * a.ratio + j) * D + c;
   if (BF16) ((uint16_t *)a.out)[off] = (uint16_t)cgk::bf16_rne(v);
   else ((float *)a.out)[off] = v;
+}
+
+// rows [r0, r0 + nr) of (b, h) from LDS [][PITCH], 16 bytes (8 values) a thread
+template <bool BF16>
+__device__ __forceinline__ void store_rows(const AttendArgs &a, int b, int h, int r0, int nr, const float *ys) {
+  for (int x = threadIdx.x; x < nr * 16; x += NTH) {
+    const int r = r0 + (x >> 4), c = 8 * (x & 15);
+    const float *y = ys + (x >> 4) * PITCH + c;
+    const f4_t lo = *(const f4_t *)y, hi = *(const f4_t *)(y + 4);
+    const int i = (int)((uint32_t)r / (uint32_t)a.ratio), j = r - i * a.ratio;
+    const int64_t off = (((int64_t)b * a.n + i) * a.heads * a.ratio + h * a.ratio + j) * D + c;
+    if (BF16) {
+      *(uint4 *)((uint16_t *)a.out + off) = make_uint4(cgk::pack_bf16x2(lo[0], lo[1]), cgk::pack_bf16x2(lo[2], lo[3]),
+                                                       cgk::pack_bf16x2(hi[0], hi[1]), cgk::pack_bf16x2(hi[2], hi[3]));
+    } else {
+      *(f4_t *)((float *)a.out + off) = lo;
+      *(f4_t *)((float *)a.out + off + 4) = hi;
+    }
+  }
 }
 
 __device__ __forceinline__ void store_lse(const AttendArgs &a, int b, int h, int r, float m, float l) {

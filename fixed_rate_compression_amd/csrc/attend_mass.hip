@@ -19,7 +19,7 @@ struct QueryRegs {
   float4 r;
 };
 
-__device__ __forceinline__ void fetch_queries(const AttendArgs &a, int bh, int b, int len, int step, QueryRegs &s) {
+__device__ __forceinline__ void fetch_queries(const AttendArgs &a, int bh, const Sequence &sq, int step, QueryRegs &s) {
   const int i = threadIdx.x;
   const int64_t t0 = (int64_t)bh * a.tiles + min(2 * step, a.tiles - 1);
   const int64_t t1 = (int64_t)bh * a.tiles + min(2 * step + 1, a.tiles - 1);
@@ -31,7 +31,7 @@ __device__ __forceinline__ void fetch_queries(const AttendArgs &a, int bh, int b
   const int row = i & (QT - 1), r = step * QT + row, rr = min(r, a.rows - 1);
   const float2 f = a.qrow[(int64_t)bh * a.tiles * ROWS + rr];
   s.r = make_float4(f.x * kCentredUnit, f.y, a.lse2[(int64_t)bh * a.rows + rr],
-                    __int_as_float(r < a.rows ? query_limit(a, b, len, r / a.ratio) : 0));
+                    __int_as_float(r < a.rows ? query_limit(a, sq, (int)((uint32_t)r / (uint32_t)a.ratio)) : 0));
 }
 
 __device__ __forceinline__ void put_queries(unsigned char *buf, const QueryRegs &s) {
@@ -52,29 +52,26 @@ __global__ __launch_bounds__(NTH, 2) void k_mass_many(const AttendArgs a) {
   __shared__ __align__(16) unsigned char lds[2 * QSTEP];
   const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5, n = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fields = a.batch * a.heads, tgroups = (int)((a.tokens + 255) / 256);
-  int64_t id = blockIdx.x;
-  const int bh = (int)(id % fields);
-  id /= fields;
-  const int part = (int)(id % a.mparts), tg = (int)(id / a.mparts);
+  const int fields = a.batch * a.heads;
+  const uint32_t q1 = blockIdx.x / (uint32_t)fields;
+  const int bh = (int)(blockIdx.x - q1 * fields);
+  const int tg = (int)(q1 / (uint32_t)a.mparts), part = (int)q1 - tg * a.mparts;
   const int b = bh / a.heads;
-  const int len = seq_length(a, b);
-  const int tmax = limit_of(a, b, len, 0, a.n - 1);
+  const Sequence sq = load_sequence(a, b);
+  const int tmax = limit_of(a, sq, 0, a.n - 1);
   const int w0 = tg * 256;
   if (w0 >= tmax) return;
   // the row steps that see one of these tokens, this workgroup's part of them
-  const int64_t start = a.starts ? (int64_t)a.starts[b] : (int64_t)len - a.n;
-  const int64_t i0 = a.causal ? max((int64_t)w0 - start, (int64_t)0) : 0;
+  const int64_t i0 = a.causal ? max((int64_t)w0 - sq.start, (int64_t)0) : 0;
   const int steps = (a.rows + QT - 1) / QT;
   const int s_lo = (int)min(i0 * a.ratio / QT, (int64_t)steps);
-  const int s0 = s_lo + (int)((int64_t)(steps - s_lo) * part / a.mparts);
-  const int s1 = s_lo + (int)((int64_t)(steps - s_lo) * (part + 1) / a.mparts);
+  const int s0 = s_lo + split_begin(steps - s_lo, part, a.mparts), s1 = s_lo + split_begin(steps - s_lo, part + 1, a.mparts);
   const int t0 = w0 + 64 * wave;
 
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk;
   QueryRegs nx;
-  if (s0 < s1) fetch_queries(a, bh, b, len, s0, nx);
+  if (s0 < s1) fetch_queries(a, bh, sq, s0, nx);
   h8_t kc[2][8];
   float2 m[2][NB];
 #pragma unroll
@@ -99,12 +96,12 @@ __global__ __launch_bounds__(NTH, 2) void k_mass_many(const AttendArgs a) {
 #pragma unroll
     for (int k = 0; k < NB; k++) sum[u][k] = 0.0f;
   if (s0 < s1) put_queries(lds, nx);
-  if (s0 + 1 < s1) fetch_queries(a, bh, b, len, s0 + 1, nx);
+  if (s0 + 1 < s1) fetch_queries(a, bh, sq, s0 + 1, nx);
   for (int st = s0; st < s1; st++) {
     __syncthreads();
     const unsigned char *buf = lds + ((st - s0) & 1) * QSTEP;
     if (st + 1 < s1) put_queries(lds + ((st + 1 - s0) & 1) * QSTEP, nx);
-    if (st + 2 < s1) fetch_queries(a, bh, b, len, st + 2, nx);
+    if (st + 2 < s1) fetch_queries(a, bh, sq, st + 2, nx);
     const unsigned char *qb = buf + (row >> 4) * 8192 + 16 * n;
     f16_t z[2], zl[2];
 #pragma unroll
@@ -167,9 +164,10 @@ __global__ __launch_bounds__(NTH, 2) void k_mass_many(const AttendArgs a) {
 
 __global__ __launch_bounds__(NTH) void k_mass_add(const AttendArgs a) {
   const int fields = a.batch * a.heads;
-  const int64_t chunks = (a.nblk + NTH - 1) / NTH, blk = (blockIdx.x % chunks) * NTH + threadIdx.x;
+  const uint32_t chunks = (uint32_t)((a.nblk + NTH - 1) / NTH);
   const int bh = (int)(blockIdx.x / chunks), b = bh / a.heads;
-  if (blk >= a.nblk || (blk << a.bshift) >= limit_of(a, b, seq_length(a, b), 0, a.n - 1)) return;
+  const int64_t blk = (int64_t)(blockIdx.x - bh * chunks) * NTH + threadIdx.x;
+  if (blk >= a.nblk || (blk << a.bshift) >= limit_of(a, load_sequence(a, b), 0, a.n - 1)) return;
   float w = 0.0f;
 #pragma unroll 8
   for (int p = 0; p < a.mparts; p++) w += a.mpart[((int64_t)p * fields + bh) * a.nblk + blk];

@@ -3,7 +3,8 @@
 // the memory traffic of the codes.
 //
 // A workgroup takes one part of one field pair's tokens for one row tile; its
-// four waves take the part's 32-token units in turn and join at the end.  Per
+// waves (four, or eight where that saves the splits) take the part's 32-token
+// units in turn and join at the end.  Per
 // unit a wave computes S^T = K Q^T (tokens x rows), turns its scores into
 // weights in registers and feeds them as they lie to O^T = V^T P^T: lane
 // (row = lane % 16, grp = lane / 16) holds the scores of tokens 4 grp + 0..3
@@ -23,43 +24,49 @@
 
 namespace cga {
 
-struct RawUnit {
-  uint4 k[2][2];  // [tile][half row]: token 16 tile + lane % 16, codes 64 x + 16 grp ..
-  uint2 v[2][4];  // [tile][i]: token 16 tile + 4 grp + i, codes 8 (lane % 16) ..
-  float2 km[2], vm[2];
+// a unit's codes as they are loaded; the keys of the next unit are asked for as
+// soon as this one's are used, and so the values
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+struct RawKeys {
+  u4_t k[2][2];  // [tile][half row]: token 16 tile + lane % 16, codes 64 x + 16 grp ..
+  float2 m[2];
+};
+struct RawValues {
+  u2_t v[2][4];  // [tile][i]: token 16 tile + 4 grp + i, codes 8 (lane % 16) ..
+  float2 m[2];
 };
 
-__device__ __forceinline__ void load_unit(const AttendArgs &a, const uint8_t *kf, const uint8_t *vf,
-                                          const float2 *km, const float2 *vm, int t0, RawUnit &u) {
+// with 16-token blocks the capacity may end after the unit's first tile: its
+// second then repeats the first
+__device__ __forceinline__ void load_keys(const AttendArgs &a, const uint8_t *kf, const float2 *km, int t0, RawKeys &u) {
   const int lane = threadIdx.x & 63, n = lane & 15, grp = lane >> 4;
-  const uint8_t *kb = kf + (int64_t)t0 * D, *vb = vf + (int64_t)t0 * D;
-  if ((int64_t)t0 + UNIT <= a.tcap) {
+  const int second = (int64_t)t0 + UNIT <= a.tcap ? 16 : 0;
+  const uint8_t *k0 = kf + (int64_t)t0 * D, *k1 = k0 + second * D;
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-#pragma unroll
-      for (int x = 0; x < 2; x++) u.k[t][x] = *(const uint4 *)(kb + (16 * t + n) * D + 64 * x + 16 * grp);
-#pragma unroll
-      for (int i = 0; i < 4; i++) u.v[t][i] = *(const uint2 *)(vb + (16 * t + 4 * grp + i) * D + 8 * n);
-    }
-  } else {  // 16-token blocks: the capacity ends after the unit's first tile
-#pragma unroll
-    for (int t = 0; t < 2; t++) {
-#pragma unroll
-      for (int x = 0; x < 2; x++) u.k[t][x] = *(const uint4 *)(kb + n * D + 64 * x + 16 * grp);
-#pragma unroll
-      for (int i = 0; i < 4; i++) u.v[t][i] = *(const uint2 *)(vb + (4 * grp + i) * D + 8 * n);
-    }
+  for (int x = 0; x < 2; x++) {
+    u.k[0][x] = *(const u4_t *)(k0 + n * D + 64 * x + 16 * grp);
+    u.k[1][x] = *(const u4_t *)(k1 + n * D + 64 * x + 16 * grp);
   }
+  u.m[0] = km[(int64_t)t0 >> a.bshift];
+  u.m[1] = km[((int64_t)t0 + second) >> a.bshift];
+}
+
+__device__ __forceinline__ void load_values(const AttendArgs &a, const uint8_t *vf, const float2 *vm, int t0, RawValues &u) {
+  const int lane = threadIdx.x & 63, n = lane & 15, grp = lane >> 4;
+  const int second = (int64_t)t0 + UNIT <= a.tcap ? 16 : 0;
+  const uint8_t *v0 = vf + (int64_t)t0 * D, *v1 = v0 + second * D;
 #pragma unroll
-  for (int t = 0; t < 2; t++) {
-    const int64_t blk = min((int64_t)(t0 + 16 * t) >> a.bshift, a.nblk - 1);
-    u.km[t] = km[blk];
-    u.vm[t] = vm[blk];
+  for (int i = 0; i < 4; i++) {
+    u.v[0][i] = *(const u2_t *)(v0 + (4 * grp + i) * D + 8 * n);
+    u.v[1][i] = *(const u2_t *)(v1 + (4 * grp + i) * D + 8 * n);
   }
+  u.m[0] = vm[(int64_t)t0 >> a.bshift];
+  u.m[1] = vm[((int64_t)t0 + second) >> a.bshift];
 }
 
 template <int J>
-__device__ __forceinline__ h8_t value_frag(const RawUnit &u) {
+__device__ __forceinline__ h8_t value_frag(const RawValues &u) {
   constexpr int B = J & 3;
   uint32_t w[2][4];
 #pragma unroll
@@ -79,52 +86,82 @@ struct RowState {
 // fp32 storage: the weights in two fp16 parts, the keys' codes centred like the
 // values' (scores to 2^-22 of the sum of |q'| 255 step; uncentred 10 times
 // that).  bf16 storage: the weights are one fp16 part (2^-11 of a weight).
-template <bool BF16, bool MASS>
-__global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
-  __shared__ __align__(16) float lds[4 * ROWS * PITCH];
-  __shared__ float2 ml[4][ROWS];
+template <bool BF16, bool MASS, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
+  __shared__ __align__(16) float lds[NW * ROWS * PITCH];
+  __shared__ float2 ml[NW][ROWS];
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t id = blockIdx.x;
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  const int tile = (int)(id % a.tiles);
-  id /= a.tiles;
-  const int h = (int)(id % a.heads), b = (int)(id / a.heads);
-  const int bh = b * a.heads + h;
+  // 32-bit divisions: a 64-bit one takes longer than a unit of work
+  const uint32_t id = blockIdx.x, q1 = id / (uint32_t)a.splits;
+  const int split = (int)(id - q1 * a.splits);
+  const int bh = a.tiles == 1 ? (int)q1 : (int)(q1 / (uint32_t)a.tiles);
+  const int tile = (int)q1 - bh * a.tiles;
+  const int b = (int)((uint32_t)bh / (uint32_t)a.heads), h = bh - b * a.heads;
   const int r0 = tile * ROWS, nr = min(ROWS, a.rows - r0);
   // on their way first: what does not wait for the sequence's length
   const float *gk = a.gk + (int64_t)h * D * a.g;
-  const RowPart qp = load_row_part<BF16>(a, b, h, r0);
-  GaugeWeights gw;
-  load_gauge<false>(gk, a.g, 0, gw);
-  const int len = seq_length(a, b);
-  const int tmax = limit_of(a, b, len, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
+  const bool front = NW == 4 || wave < 4;  // the first four waves gauge the queries, and the outputs
+  RowPart qp;
+  GaugeFrag gw;
+  if (front) {
+    qp = load_row_part<BF16>(a, b, h, r0);
+    load_gauge<false>(gk, a.g, gw);
+  }
+  const Sequence sq = load_sequence(a, b);
+  const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
-  const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
+  const int u0 = split_begin(units, split, a.splits), u1 = split_begin(units, split + 1, a.splits);
 
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
 
-  RawUnit nx;
-  if (u0 + wave < u1) load_unit(a, kf, vf, km, vm, (u0 + wave) * UNIT, nx);
+  RawKeys uk;
+  RawValues uv;
+  if (u0 + wave < u1) {
+    load_keys(a, kf, km, (u0 + wave) * UNIT, uk);
+    load_values(a, vf, vm, (u0 + wave) * UNIT, uv);
+  }
 
   // gauged query rows
   float *xs = lds, *ys = lds + ROWS * PITCH;
-  put_row_part(xs, qp);
-  if (nr < ROWS)
-    for (int i = threadIdx.x; i < (ROWS - nr) * D; i += NTH) ys[(nr + (i >> 7)) * PITCH + (i & 127)] = 0.0f;
+  if (front) put_row_part(xs, qp);
   __syncthreads();
-  gauge_rows<false, ROWS>(xs, nr, gk, a.g, gw, [&](int r, int c, float v) { ys[r * PITCH + c] = v; });
-  __syncthreads();
+  if (a.g) {
+    if (front) gauge_tiles<1, false>(xs, ys, a.g, gw);
+    __syncthreads();
+  } else {
+    ys = xs;
+  }
+  // the operands, a step to a wave, and from LDS to all (each wave for itself:
+  // 400 vector instructions instead of 130)
   QueryFrags q;
-  make_frags<true, true>(ys, a.c, q);
-  q.ca *= BF16 ? kCodeUnit : kCentredUnit;
-  __syncthreads();
+  {
+    unsigned char *fs = (unsigned char *)(lds + 2 * ROWS * PITCH);  // [hi, lo][step][lane]
+    float *qs = (float *)(fs + 8192);  // [step][row] parts of the minimum's factor, then the score's factor
+    if (front) {
+      QueryFrags one;
+      make_frags<true, true, 1>(ys, a.c, wave, one);
+      *(h8_t *)(fs + wave * 1024 + lane * 16) = one.hi[0];
+      *(h8_t *)(fs + 4096 + wave * 1024 + lane * 16) = one.lo[0];
+      if (grp == 0) {
+        qs[wave * ROWS + row] = one.cq;
+        qs[(4 + wave) * ROWS + row] = one.ca;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      q.hi[s] = *(const h8_t *)(fs + s * 1024 + lane * 16);
+      q.lo[s] = *(const h8_t *)(fs + 4096 + s * 1024 + lane * 16);
+    }
+    q.cq = (qs[row] + qs[ROWS + row]) + (qs[2 * ROWS + row] + qs[3 * ROWS + row]);
+    q.ca = qs[4 * ROWS + row] * (BF16 ? kCodeUnit : kCentredUnit);
+  }
 
   // what this lane's row sees; rows that are not there see everything, and
   // are never stored
-  const int lim = row < nr ? query_limit(a, b, len, (r0 + row) / a.ratio) : tmax;
+  const int lim = row < nr ? query_limit(a, sq, (int)((uint32_t)(r0 + row) / (uint32_t)a.ratio)) : tmax;
   int all = lim;
 #pragma unroll
   for (int k = 1; k < 16; k <<= 1) all = min(all, __shfl_xor(all, k));
@@ -139,32 +176,32 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
 #pragma unroll
   for (int j = 0; j < 8; j++) acc[j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
-  for (int un = u0 + wave; un < u1; un += 4) {
-    const RawUnit u = nx;
+  for (int un = u0 + wave; un < u1; un += NW) {
     const int t0 = un * UNIT;
-    if (un + 4 < u1) load_unit(a, kf, vf, km, vm, t0 + 4 * UNIT, nx);
+    const bool more = un + NW < u1;
     float s[2][4];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
       f4_t z = f4_t{0.f, 0.f, 0.f, 0.f}, zl = z;
 #pragma unroll
       for (int x = 0; x < 2; x++) {
-        const h8_t c0 = codes8<!BF16>(u.k[t][x].x, u.k[t][x].y), c1 = codes8<!BF16>(u.k[t][x].z, u.k[t][x].w);
+        const h8_t c0 = codes8<!BF16>(uk.k[t][x].x, uk.k[t][x].y), c1 = codes8<!BF16>(uk.k[t][x].z, uk.k[t][x].w);
         z = mfma(c0, q.hi[2 * x], z);
         z = mfma(c1, q.hi[2 * x + 1], z);
         zl = mfma(c0, q.lo[2 * x], zl);
         zl = mfma(c1, q.lo[2 * x + 1], zl);
       }
       z += zl;
-      const float A = u.km[t].y * q.ca, Bm = (BF16 ? u.km[t].x : __builtin_fmaf(128.0f, u.km[t].y, u.km[t].x)) * q.cq;
+      const float A = uk.m[t].y * q.ca, Bm = (BF16 ? uk.m[t].x : __builtin_fmaf(128.0f, uk.m[t].y, uk.m[t].x)) * q.cq;
 #pragma unroll
       for (int r = 0; r < 4; r++) s[t][r] = __builtin_fmaf(z[r], A, Bm);
     }
+    if (more) load_keys(a, kf, km, t0 + NW * UNIT, uk);
     float vst[2], vmn[2];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      vst[t] = u.vm[t].y;
-      vmn[t] = __builtin_fmaf(128.0f, u.vm[t].y, u.vm[t].x);  // the value of code 128
+      vst[t] = uv.m[t].y;
+      vmn[t] = __builtin_fmaf(128.0f, uv.m[t].y, uv.m[t].x);  // the value of code 128
     }
     if (t0 + UNIT > all) {
 #pragma unroll
@@ -220,19 +257,14 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
         }
       }
     }
+    float bt[2];  // block sums over the row's lanes, relative to mu
+    float bmu = st.mu;
     if constexpr (MASS) {
       if (a.bshift == 4) {
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-          const float v = row_sum(bs[t]);
-          const int64_t e = (t0 >> 4) + t;
-          if (grp == 0 && row < nr && e < a.entries)
-            a.bsum[((int64_t)bh * a.entries + e) * a.rows + r0 + row] = make_float2(v, st.mu);
-        }
+        bt[0] = row_sum(bs[0]);
+        bt[1] = row_sum(bs[1]);
       } else {
-        const float v = row_sum(bs[0] + bs[1]);
-        if (grp == 0 && row < nr)
-          a.bsum[((int64_t)bh * a.entries + (t0 >> 5)) * a.rows + r0 + row] = make_float2(v, st.mu);
+        bt[0] = row_sum(bs[0] + bs[1]);
       }
     }
     const h8_t P = as_h8(ph[0][0], ph[0][1], ph[1][0], ph[1][1]);
@@ -240,98 +272,154 @@ __global__ __launch_bounds__(NTH) void k_attend_rows(const AttendArgs a) {
     if constexpr (!BF16) Pl = as_h8(pl[0][0], pl[0][1], pl[1][0], pl[1][1]);
 #define CG_PV(J)                                        \
   {                                                     \
-    const h8_t vj = value_frag<J>(u);                   \
+    const h8_t vj = value_frag<J>(uv);                   \
     acc[J] = mfma(vj, P, acc[J]);                       \
     if constexpr (!BF16) acc[J] = mfma(vj, Pl, acc[J]); \
   }
     CG_PV(0) CG_PV(1) CG_PV(2) CG_PV(3) CG_PV(4) CG_PV(5) CG_PV(6) CG_PV(7)
 #undef CG_PV
+    if (more) load_values(a, vf, vm, t0 + NW * UNIT, uv);
+    if constexpr (MASS) {  // behind the loads: waiting for those does not wait for a store
+      const int64_t e = t0 >> min(a.bshift, 5);
+      float2 *p = a.bsum + ((int64_t)bh * a.entries + e) * a.rows + r0 + row;
+      if (grp == 0 && row < nr) {
+        *p = make_float2(bt[0], bmu);
+        if (a.bshift == 4 && e + 1 < a.entries) p[a.rows] = make_float2(bt[1], bmu);
+      }
+    }
   }
 
-  // join the waves: rows' sums relative to the workgroup's maximum
+  const float *gv = a.gv + (int64_t)h * D * a.g;
+  if (a.splits == 1 && front) load_gauge<true>(gv, a.g, gw);
+  // join the waves: each leaves its sums relative to its own maximum
+  __syncthreads();  // the operands have been read
   const float l = row_sum(st.l), mv = row_sum(st.mv);
   if (grp == 0) ml[wave][row] = make_float2(st.m, l);
-  __syncthreads();
-  float M = -INFINITY, Lw = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; w++) M = fmaxf(M, ml[w][row].x);
-#pragma unroll
-  for (int w = 0; w < 4; w++) Lw += ml[w][row].x > -INFINITY ? ml[w][row].y * exp2_fast(ml[w][row].x - M) : 0.0f;
   {
-    const bool some = st.m > -INFINITY;
-    const float k = some ? exp2_fast(st.m - M) : 0.0f;
     // true sums: acc 2^9 / f (the codes' and the weights' scales)
-    const float ks = some ? k * exp2_fast(st.mo - st.m) : 0.0f;
+    const float ks = st.m > -INFINITY ? exp2_fast(st.mo - st.m) : 0.0f;
     float *o = lds + (wave * ROWS + row) * PITCH;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; j++) v[j] = acc[j][r] * ks + mv * k;
+      for (int j = 0; j < 8; j++) v[j] = __builtin_fmaf(acc[j][r], ks, mv);
       *(float4 *)(o + 8 * (4 * grp + r)) = make_float4(v[0], v[1], v[2], v[3]);
       *(float4 *)(o + 8 * (4 * grp + r) + 4) = make_float4(v[4], v[5], v[6], v[7]);
     }
   }
   __syncthreads();
-  if (wave == 0 && grp == 0 && row < nr) {
-    const int64_t pr = ((int64_t)bh * a.splits + split) * a.rows + r0 + row;
-    if (a.part_ml) a.part_ml[pr] = make_float2(M, Lw);
-    if (a.splits == 1 && a.lse) store_lse(a, b, h, r0 + row, M, Lw);
-    if (a.splits == 1 && a.lse2) a.lse2[(int64_t)bh * a.rows + r0 + row] = Lw > 0.0f ? M + __builtin_log2f(Lw) : INFINITY;
-    ml[0][row] = make_float2(M, Lw);
-  }
-  if (a.splits > 1) {
-    for (int i = threadIdx.x; i < nr * (D / 4); i += NTH) {
-      const int r = i / (D / 4), c = 4 * (i % (D / 4));
-      float4 v = *(const float4 *)(lds + r * PITCH + c);
-#pragma unroll
-      for (int w = 1; w < 4; w++) {
-        const float4 x = *(const float4 *)(lds + (w * ROWS + r) * PITCH + c);
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-      }
-      *(float4 *)(a.part_o + (((int64_t)bh * a.splits + split) * a.rows + r0 + r) * D + c) = v;
-    }
-    return;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nr * (D / 4); i += NTH) {
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * NW) {  // also rows that are not there: none is left undefined
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
-    const float ll = ml[0][r].y;
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-    float4 v = *(const float4 *)(lds + r * PITCH + c);
+    float M = -INFINITY;
 #pragma unroll
-    for (int w = 1; w < 4; w++) {
-      const float4 x = *(const float4 *)(lds + (w * ROWS + r) * PITCH + c);
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    for (int k = 0; k < NW; k++) M = fmaxf(M, ml[k][r].x);
+    float L = 0.0f;
+    f4_t v = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NW; k++) {
+      const float2 w = ml[k][r];
+      const float f = w.x > -INFINITY ? exp2_fast(w.x - M) : 0.0f;
+      L += w.y * f;
+      v += *(const f4_t *)(lds + (k * ROWS + r) * PITCH + c) * f;
     }
-    v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-    *(float4 *)(lds + r * PITCH + c) = v;  // this thread alone reads row r's channels c .. c + 3
+    const int64_t pr = ((int64_t)bh * a.splits + split) * a.rows + r0 + r;
+    if (c == 0 && r < nr) {
+      if (a.part_ml) a.part_ml[pr] = make_float2(M, L);
+      if (a.splits == 1 && a.lse) store_lse(a, b, h, r0 + r, M, L);
+    }
+    if (a.splits > 1) {
+      if (r < nr) *(f4_t *)(a.part_o + pr * D + c) = v;
+    } else {
+      *(f4_t *)(lds + r * PITCH + c) = v * (L > 0.0f ? 1.0f / L : 0.0f);  // this thread alone reads these channels of row r
+    }
   }
-  const float *gv = a.gv + (int64_t)h * D * a.g;
-  load_gauge<true>(gv, a.g, 0, gw);
+  if (a.splits > 1) return;
   __syncthreads();
-  gauge_rows<true, ROWS>(lds, nr, gv, a.g, gw, [&](int r, int c, float v) { store_out<BF16>(a, b, h, r0 + r, c, v); });
+  float *os = lds;
+  if (a.g) {
+    os = lds + ROWS * PITCH;
+    if (front) gauge_tiles<1, false>(lds, os, a.g, gw);
+    __syncthreads();
+  }
+  if (front) store_rows<BF16>(a, b, h, r0, nr, os);
 }
+
+// Block weights of few rows from the sums the attention left, 256 blocks to a
+// workgroup: mass[block] += sum over rows of sum_t 2^(s_t - m) 2^(m - log2 sum)
+__device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
+  __shared__ float lse2[ROWS];
+  const uint32_t chunks = (uint32_t)((a.nblk + NTH - 1) / NTH);
+  const int bh = (int)(id / chunks), b = bh / a.heads;
+  const int64_t blk = (int64_t)(id - bh * chunks) * NTH + threadIdx.x;
+  const int tmax = limit_of(a, load_sequence(a, b), 0, a.n - 1);
+  const int row = threadIdx.x >> 4, j = threadIdx.x & 15;  // 16 lanes to a row's splits
+  float M = -INFINITY, L = 0.0f;
+  if (row < a.rows) {
+    const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + row;
+    for (int s = j; s < a.splits; s += 16) {
+      const float2 x = pm[(int64_t)s * a.rows];
+      const float m = fmaxf(M, x.x);
+      if (m > -INFINITY) L = L * exp2_fast(M - m) + x.y * exp2_fast(x.x - m);
+      M = m;
+    }
+  }
+#pragma unroll
+  for (int k = 8; k >= 1; k >>= 1) {
+    const float m2 = __shfl_xor(M, k), l2 = __shfl_xor(L, k), m = fmaxf(M, m2);
+    if (m > -INFINITY) L = L * exp2_fast(M - m) + l2 * exp2_fast(m2 - m);
+    M = m;
+  }
+  if (j == 0) lse2[row] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
+  __syncthreads();
+  if (blk >= a.nblk || (blk << a.bshift) >= tmax) return;
+  const int per = a.bshift == 6 ? 2 : 1;
+  float w = 0.0f;
+  for (int k = 0; k < per; k++) {
+    const int64_t e = blk * per + k;
+    if (a.bshift != 4 && e * UNIT >= tmax) break;  // the unit was not visited
+    const float2 *p = a.bsum + ((int64_t)bh * a.entries + e) * a.rows;
+#pragma unroll 4
+    for (int r = 0; r < a.rows; r++) {
+      const float2 x = p[r];
+      if (x.x > 0.0f && lse2[r] < INFINITY) w += x.x * exp2_fast(x.y - lse2[r]);
+    }
+  }
+  a.mass[(int64_t)bh * a.nblk + blk] += w;
+}
+
+__global__ __launch_bounds__(NTH) void k_mass_finish(const AttendArgs a) { finish_mass(a, blockIdx.x); }
 
 // Joins the splits of one row, a workgroup to a row: 2^(m_s - M) of every
 // split, eight groups of 32 lanes adding every eighth split's sums, then the
-// inverse gauge.  For few rows with many splits.
-template <bool BF16>
+// inverse gauge.  For few rows with many splits; workgroups past the last row
+// finish the blocks' weights (MASS), which need no more than the rows do.
+template <bool BF16, bool MASS>
 __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   __shared__ __align__(16) float part[8][D];
   __shared__ __align__(16) float us[PITCH];
   __shared__ float wt[MERGE_SPLITS];
   __shared__ float2 red[4];
-  const int64_t id = blockIdx.x;
-  const int r = (int)(id % a.rows), bh = (int)(id / a.rows);
-  const int h = bh % a.heads, b = bh / a.heads;
+  const uint32_t id = blockIdx.x;
+  if constexpr (MASS) {
+    const uint32_t merging = (uint32_t)(a.batch * a.heads * a.rows);
+    if (id >= merging) {
+      finish_mass(a, id - merging);
+      return;
+    }
+  }
+  const int bh = (int)(id / (uint32_t)a.rows), r = (int)id - bh * a.rows;
+  const int b = (int)((uint32_t)bh / (uint32_t)a.heads), h = bh - b * a.heads;
   const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r;
   const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r) * D;
   const int S = a.splits, t = threadIdx.x;
   // this thread's part of G_V, on its way while the sums are joined
-  const float *gv = a.gv + (int64_t)h * D * a.g;
-  GaugeWeights gw;
-  load_gauge<true>(gv, a.g, 0, gw);
+  // (the two halves of the workgroup take half of a channel's chain each)
+  const int c = t & (D - 1), cg = c & (a.g - 1), gh = a.g >> 1, k0 = (t >> 7) * gh;
+  const float *gp = a.gv + (int64_t)h * D * a.g + (int64_t)(c - cg) * a.g + (int64_t)k0 * a.g + cg;
+  float gw[16];
+#pragma unroll
+  for (int k = 0; k < 16; k++) gw[k] = k < gh ? gp[(int64_t)k * a.g] : 0.0f;
   float M = -INFINITY;
   for (int s = t; s < S; s += NTH) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
 #pragma unroll
@@ -369,7 +457,20 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
     us[t] = L > 0.0f ? v / L : 0.0f;
   }
   __syncthreads();
-  gauge_rows<true, 2>(us, 1, gv, a.g, gw, [&](int, int cc, float v) { store_out<BF16>(a, b, h, r, cc, v); });
+  if (a.g == 0) {
+    if (t < D) store_out<BF16>(a, b, h, r, t, us[t]);
+    return;
+  }
+  const float *x = us + (c - cg) + k0;
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; k++)
+    if (k < gh) v = __builtin_fmaf(gw[k], x[k], v);
+#pragma unroll 16
+  for (int k = 16; k < gh; k++) v = __builtin_fmaf(gp[(int64_t)k * a.g], x[k], v);
+  part[t >> 7][c] = v;
+  __syncthreads();
+  if (t < D) store_out<BF16>(a, b, h, r, t, part[0][t] + part[1][t]);
 }
 
 // The same for many rows with few splits: 16 rows to a workgroup, a row to a
@@ -377,13 +478,13 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
 template <bool BF16>
 __global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
   __shared__ __align__(16) float us[ROWS * PITCH];
-  const int64_t id = blockIdx.x;
-  const int r0 = (int)(id % a.tiles) * ROWS, bh = (int)(id / a.tiles);
+  const uint32_t id = blockIdx.x;
+  const int bh = (int)(id / (uint32_t)a.tiles), r0 = (int)(id - bh * a.tiles) * ROWS;
   const int h = bh % a.heads, b = bh / a.heads, nr = min(ROWS, a.rows - r0);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float *gv = a.gv + (int64_t)h * D * a.g;
-  GaugeWeights gw;
-  load_gauge<true>(gv, a.g, 0, gw);
+  GaugeFrag gw;
+  load_gauge<true>(gv, a.g, gw);
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int rr = wave + 4 * i, r = min(r0 + rr, a.rows - 1);
@@ -408,64 +509,42 @@ __global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
     }
   }
   __syncthreads();
-  gauge_rows<true, ROWS>(us, nr, gv, a.g, gw, [&](int r, int cc, float v) { store_out<BF16>(a, b, h, r0 + r, cc, v); });
-}
-
-// Block weights of few rows from the sums the attention left: mass[block] +=
-// sum over rows of sum_t 2^(s_t - m) 2^(m - log2 sum)
-__global__ __launch_bounds__(NTH) void k_mass_finish(const AttendArgs a) {
-  __shared__ float lse2[ROWS];
-  const int chunks = (int)((a.nblk + NTH - 1) / NTH);
-  const int64_t id = blockIdx.x;
-  const int bh = (int)(id / chunks), b = bh / a.heads;
-  const int64_t blk = (id % chunks) * NTH + threadIdx.x;
-  const int len = seq_length(a, b);
-  const int tmax = limit_of(a, b, len, 0, a.n - 1);
-  if ((int)threadIdx.x < a.rows) {
-    const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + threadIdx.x;
-    float M = -INFINITY, L = 0.0f;
-    for (int s = 0; s < a.splits; s++) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
-    for (int s = 0; s < a.splits; s++) {
-      const float2 x = pm[(int64_t)s * a.rows];
-      L += x.x > -INFINITY ? x.y * exp2_fast(x.x - M) : 0.0f;
-    }
-    lse2[threadIdx.x] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
+  if (a.g) {
+    gauge_tiles<1, true>(us, us, a.g, gw);
+    __syncthreads();
   }
-  __syncthreads();
-  if (blk >= a.nblk || (blk << a.bshift) >= tmax) return;
-  const int per = a.bshift == 6 ? 2 : 1;
-  float w = 0.0f;
-  for (int k = 0; k < per; k++) {
-    const int64_t e = blk * per + k;
-    if (a.bshift != 4 && e * UNIT >= tmax) break;  // the unit was not visited
-    const float2 *p = a.bsum + ((int64_t)bh * a.entries + e) * a.rows;
-    for (int r = 0; r < a.rows; r++)
-      if (p[r].x > 0.0f && lse2[r] < INFINITY) w += p[r].x * exp2_fast(p[r].y - lse2[r]);
-  }
-  a.mass[(int64_t)bh * a.nblk + blk] += w;
+  store_rows<BF16>(a, b, h, r0, nr, us);
 }
 
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.tiles * a.splits)), block(NTH);
+  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.tiles * a.splits));
   const bool mass = a.mass && a.bsum;
-  if (bf16 && mass) hipLaunchKernelGGL((k_attend_rows<true, true>), grid, block, 0, s, a);
-  else if (bf16) hipLaunchKernelGGL((k_attend_rows<true, false>), grid, block, 0, s, a);
-  else if (mass) hipLaunchKernelGGL((k_attend_rows<false, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_attend_rows<false, false>), grid, block, 0, s, a);
-  return hipGetLastError();
+#define CG_R(BF, MA, NW)                                                                       \
+  if (bf16 == BF && mass == MA && a.waves == NW) {                                             \
+    hipLaunchKernelGGL((k_attend_rows<BF, MA, NW>), grid, dim3(64 * NW), 0, s, a);             \
+    return hipGetLastError();                                                                  \
+  }
+  CG_R(true, false, 4) CG_R(true, true, 4) CG_R(false, false, 4) CG_R(false, true, 4)
+  CG_R(true, false, 8) CG_R(true, true, 8) CG_R(false, false, 8) CG_R(false, true, 8)
+#undef CG_R
+  return hipErrorInvalidValue;
 }
 
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const int64_t fields = (int64_t)a.batch * a.heads;
+  const dim3 block(NTH);
   if (a.tiles > 1) {
-    const dim3 grid((unsigned)(fields * a.tiles)), block(NTH);
+    const dim3 grid((unsigned)(fields * a.tiles));
     if (bf16) hipLaunchKernelGGL(k_attend_merge_many<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(k_attend_merge_many<false>, grid, block, 0, s, a);
-  } else {
-    const dim3 grid((unsigned)(fields * a.rows)), block(NTH);
-    if (bf16) hipLaunchKernelGGL(k_attend_merge<true>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_attend_merge<false>, grid, block, 0, s, a);
+    return hipGetLastError();
   }
+  const bool mass = a.mass && a.bsum && a.tokens > 0;
+  const dim3 grid((unsigned)(fields * a.rows + (mass ? fields * ((a.nblk + NTH - 1) / NTH) : 0)));
+  if (bf16 && mass) hipLaunchKernelGGL((k_attend_merge<true, true>), grid, block, 0, s, a);
+  else if (bf16) hipLaunchKernelGGL((k_attend_merge<true, false>), grid, block, 0, s, a);
+  else if (mass) hipLaunchKernelGGL((k_attend_merge<false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_attend_merge<false, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -268,24 +268,23 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   const int lane = threadIdx.x & 63, row = lane & 31, half = lane >> 5, n = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fields = a.batch * a.heads, groups = (a.rows + TROWS - 1) / TROWS;
-  int64_t id = blockIdx.x;
-  const int bh = (int)(id % fields);  // a head's workgroups share an XCD's L2 where the heads are a multiple of 8
-  id /= fields;
-  const int split = (int)(id % a.splits);
+  const uint32_t q1 = blockIdx.x / (uint32_t)fields, q2 = q1 / (uint32_t)a.splits;
+  const int bh = (int)(blockIdx.x - q1 * fields);  // a head's workgroups share an XCD's L2 where the heads are a multiple of 8
+  const int split = (int)(q1 - q2 * a.splits);
   // the longest first; where all are resident at once (two to a compute unit) the
   // second half runs from the shortest up, beside the first half's longest
-  const int turn_of = (int)(id / a.splits), first = (groups + 1) / 2;
+  const int turn_of = (int)q2, first = (groups + 1) / 2;
   const bool paired = (int64_t)gridDim.x <= 512 && a.splits == 1;
   const int grpi = paired && turn_of >= first ? turn_of - first : groups - 1 - turn_of;
   const int h = bh % a.heads, b = bh / a.heads;
   const int r0 = grpi * TROWS, nr = min(TROWS, a.rows - r0);
-  const int len = seq_length(a, b);
+  const Sequence sq = load_sequence(a, b);
 
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
-  const int tmax = limit_of(a, b, len, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
+  const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
-  const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
+  const int u0 = split_begin(units, split, a.splits), u1 = split_begin(units, split + 1, a.splits);
   UnitRegs nx;
   if (u0 < u1) fetch_unit(a, kf, vf, km, vm, u0, nx);
 
@@ -307,7 +306,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
     }
   }
   // what the row sees; rows that are not there see everything
-  const int lim = wr < a.rows ? query_limit(a, b, len, wr / a.ratio) : tmax;
+  const int lim = wr < a.rows ? query_limit(a, sq, (int)((uint32_t)wr / (uint32_t)a.ratio)) : tmax;
   int all = lim;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) all = min(all, __shfl_xor(all, k));
@@ -364,8 +363,8 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
 
   // rows' sums, scaled as they stand, into LDS; then parts or outputs
   const float *gv = a.gv + (int64_t)h * D * a.g;
-  GaugeWeights gw;
-  load_gauge<true>(gv, a.g, 0, gw);
+  GaugeFrag gw;
+  load_gauge<true>(gv, a.g, gw);
   float *us = (float *)lds;
   {
     const int rr = wave * WROWS + row;
@@ -397,9 +396,11 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
       *(float4 *)(po + 4 * (int64_t)i) = *(const float4 *)(us + (i / (D / 4)) * PITCH + 4 * (i % (D / 4)));
     return;
   }
-  for (int t = 0; t < nr; t += 64)
-    gauge_rows<true, 64>(us + t * PITCH, min(64, nr - t), gv, a.g, gw,
-                         [&](int r, int c, float v) { store_out<BF16>(a, b, h, r0 + t + r, c, v); });
+  if (a.g) {
+    gauge_tiles<TROWS / ROWS, true>(us, us, a.g, gw);
+    __syncthreads();
+  }
+  store_rows<BF16>(a, b, h, r0, nr, us);
 }
 
 // One workgroup per four row tiles: gauge, split into the operands' parts and
@@ -407,31 +408,26 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
 template <bool BF16, bool LO>
 __global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
   __shared__ __align__(16) float xs[4 * ROWS * PITCH];
-  const int quads = (a.tiles + 3) / 4;
-  const int64_t id = blockIdx.x;
-  const int tile0 = (int)(id % quads) * 4, bh = (int)(id / quads);
+  const uint32_t quads = (uint32_t)(a.tiles + 3) / 4, id = blockIdx.x;
+  const int bh = (int)(id / quads), tile0 = (int)(id - bh * quads) * 4;
   const int h = bh % a.heads, b = bh / a.heads;
   const float *gk = a.gk + (int64_t)h * D * a.g;
-  GaugeWeights gw;
-  load_gauge<false>(gk, a.g, 0, gw);
+  GaugeFrag gw;
+  load_gauge<false>(gk, a.g, gw);
   RowPart p[4];
 #pragma unroll
   for (int t = 0; t < 4; t++) p[t] = load_row_part<BF16>(a, b, h, (tile0 + t) * ROWS);
 #pragma unroll
   for (int t = 0; t < 4; t++) put_row_part(xs + t * ROWS * PITCH, p[t]);
   __syncthreads();
-  if (a.g) {  // in place: every thread has its results before any is stored
-    float y[2 * ROWS];
-    gauge_rows<false, 4 * ROWS>(xs, 4 * ROWS, gk, a.g, gw, [&](int r, int c, float v) { y[r >> 1] = v; });
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 2 * ROWS; r++) xs[(2 * r + (threadIdx.x >> 7)) * PITCH + (threadIdx.x & (D - 1))] = y[r];
+  if (a.g) {
+    gauge_tiles<4, true>(xs, xs, a.g, gw);
     __syncthreads();
   }
   const int lane = threadIdx.x & 63, tile = tile0 + (int)(threadIdx.x >> 6);
   if (tile >= a.tiles) return;
   QueryFrags q;
-  make_frags<LO, false>(xs + (threadIdx.x >> 6) * ROWS * PITCH, a.c, q);
+  make_frags<LO, false, 4>(xs + (threadIdx.x >> 6) * ROWS * PITCH, a.c, 0, q);
   uint4 *d = a.qfrag + ((int64_t)bh * a.tiles + tile) * 8 * 64 + lane;
 #pragma unroll
   for (int s = 0; s < 4; s++) {
