@@ -33,6 +33,7 @@ struct EvictArgs {
   int64_t tokens, nblk, nblk_out;
   int32_t layers, batch, heads, block, budget, sink, recent;
   int32_t in_place;
+  int32_t pshift;          // log2 of a block's 16-byte pieces
 };
 hipError_t evict_launch(const EvictArgs &a, hipStream_t s);
 

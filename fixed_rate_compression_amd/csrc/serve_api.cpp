@@ -126,6 +126,7 @@ int cg_evict(const cg_shape *shape, const cg_codec *codec, int32_t budget, int32
   a.sink = sink;
   a.recent = recent;
   a.in_place = in_place ? 1 : 0;
+  a.pshift = codec->block_tokens == 16 ? 7 : codec->block_tokens == 32 ? 8 : 9;
   hipError_t e = cgs::evict_launch(a, (hipStream_t)stream);
   return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_evict launch");
 }

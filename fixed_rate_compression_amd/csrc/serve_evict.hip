@@ -10,7 +10,8 @@ namespace cgs {
 constexpr int ST = 1024;       // threads of a selecting workgroup
 constexpr int SW = ST / 64;
 constexpr int MT = 256;        // threads of a moving workgroup
-constexpr int STEP = 4;        // 16-byte pieces a moving thread holds
+constexpr int STEP = 8;        // 16-byte pieces a moving thread holds
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));  // an array of these stays in registers (of uint4 it did not)
 
 // weights in an unsigned order: NaN below everything, -0 equal to +0
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -23,17 +24,19 @@ __device__ __forceinline__ int lanes_below(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
 
-// One workgroup per (layer, sequence, head).  The smallest kept weight is
-// found eight bits at a time from the top (a radix selection: four counting
-// passes over the weights, which stay in the L2), then one ordered pass
-// writes the kept blocks' numbers and weights; blocks of that smallest weight
-// stay in index order until the budget is met.
+// One workgroup per (layer, sequence, head).  The smallest kept weight is found
+// eight bits at a time from the top: four counting passes over weights held in
+// registers (past 8192 blocks: read again).  Then one ordered pass writes the
+// kept blocks' numbers and weights; blocks of that smallest weight stay in index
+// order until the budget is met.  256 heads of 256 blocks: 8 us, 128 heads of
+// 2500: 12; counting every weight against every other from LDS took 11 and 51.
+constexpr int HELD = 8;
 __global__ __launch_bounds__(ST) void k_evict_select(const EvictArgs a) {
   __shared__ int hist[SW][256];
   __shared__ int cnt[SW][2];
   __shared__ int pick[2];
   const int64_t id = blockIdx.x;
-  const int b = (int)(id / a.heads % a.batch);
+  const int b = (int)(blockIdx.x / (uint32_t)a.heads % (uint32_t)a.batch);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t len = min(max(a.lengths ? (int64_t)a.lengths[b] : a.tokens, (int64_t)0), a.tokens);
   const int n = (int)((len + a.block - 1) / a.block);
@@ -45,13 +48,25 @@ __global__ __launch_bounds__(ST) void k_evict_select(const EvictArgs a) {
   uint32_t key = 0;
   int need = all ? 0 : a.budget - a.sink - a.recent;
   if (!all && need > 0) {
+    uint32_t held[HELD];
+#pragma unroll
+    for (int e = 0; e < HELD; e++) {
+      const int i = threadIdx.x + e * ST;
+      held[e] = i >= lo && i < hi ? order_key(mass[i]) : 0u;
+    }
     for (int sft = 24; sft >= 0; sft -= 8) {
       for (int i = threadIdx.x; i < SW * 256; i += ST) (&hist[0][0])[i] = 0;
       __syncthreads();
-      for (int i = lo + threadIdx.x; i < hi; i += ST) {
-        const uint32_t k = order_key(mass[i]);
+      const auto count = [&](uint32_t k) {
         if (sft == 24 || (k >> (sft + 8)) == (key >> (sft + 8))) atomicAdd(&hist[wave][(k >> sft) & 255], 1);
+      };
+#pragma unroll
+      for (int e = 0; e < HELD; e++) {
+        const int i = threadIdx.x + e * ST;
+        if (i >= lo && i < hi) count(held[e]);
       }
+      for (int i = threadIdx.x + HELD * ST; i < hi; i += ST)
+        if (i >= lo) count(order_key(mass[i]));
       __syncthreads();
       if (threadIdx.x < 256) {
         int c = 0;
@@ -132,49 +147,51 @@ __global__ __launch_bounds__(ST) void k_evict_select(const EvictArgs a) {
 // read by all threads everything up to it may be overwritten.  Into another
 // cache the field is cut into `chunks`.
 __global__ __launch_bounds__(MT) void k_evict_move(const EvictArgs a, int chunks) {
-  const int64_t f = blockIdx.x / chunks;  // (layer, kind, b, h)
-  const int chunk = (int)(blockIdx.x % chunks);
+  const uint32_t f32 = blockIdx.x / (uint32_t)chunks, heads = (uint32_t)(a.batch * a.heads);
+  const int chunk = (int)(blockIdx.x - f32 * chunks);
+  const int64_t f = f32;  // (layer, kind, b, h)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.batch; b += MT) {
       const int64_t len = min(max(a.lengths ? (int64_t)a.lengths[b] : a.tokens, (int64_t)0), a.tokens);
       const int64_t n = (len + a.block - 1) / a.block;
       a.lengths_out[b] = (int32_t)(n > a.budget ? len - (n - a.budget) * a.block : len);
     }
-  const int64_t bh = f % ((int64_t)a.batch * a.heads), layer = f / ((int64_t)2 * a.batch * a.heads);
-  const int32_t *kept = a.kept + (layer * a.batch * a.heads + bh) * a.budget;
+  const uint32_t layer = f32 / (2 * heads), bh = f32 % heads;
+  const int32_t *kept = a.kept + ((int64_t)layer * heads + bh) * a.budget;
   const float2 *ms = a.meta + f * a.nblk;
   float2 *md = a.meta_out + f * a.nblk_out;
-  const int64_t bytes = (int64_t)a.block * 128;
-  const uint8_t *src = a.payload + f * a.nblk * bytes;
-  uint8_t *dst = a.payload_out + f * a.nblk_out * bytes;
-  const int per = (int)(bytes / 16);  // 16-byte pieces of a block
-  const int b0 = (int)((int64_t)a.budget * chunk / chunks), b1 = (int)((int64_t)a.budget * (chunk + 1) / chunks);
+  const int sh = a.pshift, per = 1 << sh;  // 16-byte pieces of a block
+  const u4_t *src = (const u4_t *)a.payload + f * a.nblk * per;
+  u4_t *dst = (u4_t *)a.payload_out + f * a.nblk_out * per;
+  const int each = (a.budget + chunks - 1) / chunks, b0 = min(chunk * each, a.budget), b1 = min(b0 + each, a.budget);
+  __shared__ int32_t from[MT];  // former numbers of the blocks [j0, j0 + MT)
   for (int j0 = b0; j0 < b1; j0 += MT) {
     const int j = j0 + (int)threadIdx.x;
     const int s = j < b1 ? kept[j] : -1;
+    __syncthreads();
+    from[threadIdx.x] = s;
     float2 m = make_float2(0.f, 0.f);
     if (s >= 0) m = ms[s];
-    if (a.in_place) __syncthreads();
-    if (s >= 0) md[j] = m;
-    if (a.in_place) __syncthreads();
-  }
-  const int64_t p0 = (int64_t)b0 * per, p1 = (int64_t)b1 * per;
-  for (int64_t p = p0; p < p1; p += MT * STEP) {
-    uint4 v[STEP];
-    int s[STEP];
+    __syncthreads();
+    if (s >= 0) md[j] = m;  // in place: at or below any number that is still to be read
+    const int np = min(MT, b1 - j0) << sh;
+    for (int p = 0; p < np; p += MT * STEP) {
+      u4_t v[STEP];
+      int s[STEP];
 #pragma unroll
-    for (int k = 0; k < STEP; k++) {
-      const int64_t x = p + (int64_t)k * MT + threadIdx.x;
-      s[k] = x < p1 ? kept[x / per] : -1;
-      if (s[k] >= 0) v[k] = *(const uint4 *)(src + s[k] * bytes + (x % per) * 16);
-    }
-    if (a.in_place) __syncthreads();
+      for (int k = 0; k < STEP; k++) {
+        const int x = p + k * MT + (int)threadIdx.x;
+        s[k] = x < np ? from[x >> sh] : -1;
+        if (a.in_place && s[k] == j0 + (x >> sh)) s[k] = -1;  // stays where it is
+        if (s[k] >= 0) v[k] = src[(int64_t)s[k] * per + (x & (per - 1))];
+      }
+      if (a.in_place) __syncthreads();
 #pragma unroll
-    for (int k = 0; k < STEP; k++) {
-      const int64_t x = p + (int64_t)k * MT + threadIdx.x;
-      if (s[k] >= 0) *(uint4 *)(dst + x * 16) = v[k];
+      for (int k = 0; k < STEP; k++)
+        if (s[k] >= 0) __builtin_nontemporal_store(v[k], &dst[((int64_t)j0 << sh) + p + k * MT + (int)threadIdx.x]);
+      if (a.in_place) __syncthreads();
     }
-    if (a.in_place) __syncthreads();
+    if (np > 0 && from[0] < 0) return;  // blocks behind the last kept one
   }
 }
 
@@ -184,9 +201,9 @@ hipError_t evict_launch(const EvictArgs &a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   int64_t chunks = 1;
-  if (!a.in_place) {  // four workgroups a compute unit, 16 KB at least to each
+  if (!a.in_place) {  // eight workgroups a compute unit, 16 KB at least to each
     const int64_t bytes = (int64_t)a.budget * a.block * 128;
-    chunks = (1024 + 2 * heads - 1) / (2 * heads);
+    chunks = (2048 + 2 * heads - 1) / (2 * heads);
     if (chunks > (bytes + 16383) / 16384) chunks = (bytes + 16383) / 16384;
     if (chunks > a.budget) chunks = a.budget;
   }
