@@ -16,7 +16,7 @@ struct AppendArgs {
   const int32_t *lengths, *starts;
   const float *gauges;     // the layer's [kind][heads][128 g]
   int64_t tcap, tokens, nblk;
-  int32_t batch, heads, n, block, tiles;  // tiles: 64-row strips of a sequence at most
+  int32_t batch, heads, n, block, bshift, tiles;  // tiles: 64-row strips of a sequence at most
 };
 hipError_t append_launch(const AppendArgs &a, bool bf16, int g, hipStream_t s);
 

@@ -67,6 +67,7 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
   a.heads = shape->heads;
   a.n = n_new;
   a.block = codec->block_tokens;
+  a.bshift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
   a.tiles = (int32_t)tiles;
   hipError_t e = cgs::append_launch(a, shape->dtype == CG_DTYPE_BF16, gauge->group, (hipStream_t)stream);
   return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_append launch");

@@ -21,27 +21,26 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   __shared__ __align__(16) float xs[TILE_T * PITCH];
   __shared__ float red[8];
   constexpr size_t ESZ = BF16 ? 2 : 4;
-  int64_t id = blockIdx.x;
-  const int strip = (int)(id % a.tiles);
-  id /= a.tiles;
-  const int h = (int)(id % a.heads);
-  id /= a.heads;
-  const int b = (int)(id % a.batch), kind = (int)(id / a.batch);
-  const int64_t len = min(max(a.lengths ? (int64_t)a.lengths[b] : a.tokens, (int64_t)0), a.tokens);
-  const int64_t start = a.starts ? (int64_t)a.starts[b] : len - a.n;
+  const uint32_t q1 = blockIdx.x / (uint32_t)a.tiles, q2 = q1 / (uint32_t)a.heads;
+  const int strip = (int)(blockIdx.x - q1 * a.tiles), h = (int)(q1 - q2 * a.heads);
+  const int kind = (int)(q2 / (uint32_t)a.batch), b = (int)q2 - kind * a.batch;
+  const int64_t f = q1;  // (kind, b, h)
+  TileGauge<G, false> tg;  // on its way first
+  if constexpr (G != 0) tg.load(a.gauges + ((int64_t)kind * a.heads + h) * D * G);
+  const int32_t *any = (const int32_t *)a.k;  // both loads at once, from a place that is there where an array is not
+  const int32_t ln = *(a.lengths ? a.lengths + b : any), sn = *(a.starts ? a.starts + b : any);
+  const int64_t len = a.lengths ? min(max((int64_t)ln, (int64_t)0), a.tokens) : a.tokens;
+  const int64_t start = a.starts ? (int64_t)sn : len - a.n;
   const int64_t p0 = max(start, (int64_t)0), p1 = min(start + a.n, len);  // positions of the new rows
   if (p1 <= p0) return;
-  const int BT = a.block;
-  const int64_t head = p0 / BT * BT, end = (p1 + BT - 1) / BT * BT;  // whole blocks
+  const int BT = a.block;  // a power of two
+  const int64_t head = p0 & ~(int64_t)(BT - 1), end = (p1 + BT - 1) & ~(int64_t)(BT - 1);  // whole blocks
   const int64_t tb = head + (int64_t)strip * TILE_T;
   if (tb >= end) return;
   const int nrows = (int)min((int64_t)TILE_T, end - tb);
-  const int64_t f = ((int64_t)kind * a.batch + b) * a.heads + h;
   const uint8_t *src = (const uint8_t *)(kind ? a.v : a.k) + ((int64_t)b * a.batch_stride + (int64_t)h * D) * ESZ;
   uint8_t *tail = (uint8_t *)a.tail + f * BT * D * ESZ;
 
-  TileGauge<G, false> tg;
-  if constexpr (G != 0) tg.load(a.gauges + ((int64_t)kind * a.heads + h) * D * G);
   for (int i = threadIdx.x; i < nrows * 16; i += NT) {
     const int r = i >> 4, c = (i & 15) * 8;
     const int64_t p = tb + r;
@@ -62,11 +61,11 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   }
   __syncthreads();
   if (strip == 0) {  // the raw rows of the last block
-    const int64_t q0 = max(p0, (p1 - 1) / BT * BT);
-    const int per = (int)(D * ESZ / 16);
+    const int64_t q0 = max(p0, (p1 - 1) & ~(int64_t)(BT - 1));
+    constexpr int per = (int)(D * ESZ / 16);
     for (int i = threadIdx.x; i < (int)(p1 - q0) * per; i += NT) {
       const int64_t p = q0 + i / per;
-      *(uint4 *)(tail + (p % BT) * D * ESZ + 16 * (i % per)) =
+      *(uint4 *)(tail + (p & (BT - 1)) * D * ESZ + 16 * (i % per)) =
           *(const uint4 *)(src + (p - start) * a.row_stride * ESZ + 16 * (i % per));
     }
   }
@@ -94,7 +93,7 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   }
   __syncthreads();
   if (!active) return;
-  const int wpb = BT / 16, w0 = (t / BT) * wpb;
+  const int wpb = BT >> 4, w0 = (t & ~(BT - 1)) >> 4;
   mn = red[2 * w0];
   mx = red[2 * w0 + 1];
   for (int k = 1; k < wpb; k++) {
@@ -107,8 +106,8 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   for (int k = 0; k < 32; k++) q[k] = cgq::quant1(v[k], r, 255);
   cgq::pack32<8>(q, wd);
   cgq::store_words<8>(a.payload + (f * a.tcap + tb + t) * D + 32 * j, wd);
-  if (j == 0 && t % BT == 0) {
-    float *m = a.meta + 2 * (f * a.nblk + (tb + t) / BT);
+  if (j == 0 && (t & (BT - 1)) == 0) {
+    float *m = a.meta + 2 * (f * a.nblk + ((tb + t) >> a.bshift));
     m[0] = r.mn;
     m[1] = r.scale;
   }

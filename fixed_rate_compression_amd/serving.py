@@ -1,0 +1,93 @@
+"""An 8-bit block-uniform cache that is served from where it lies: new K/V rows
+go in token by token (cg_append), attention reads the codes (cg_attend), and the
+blocks that received the least attention leave (cg_evict).
+
+One step of a decoder, the same for prompts, chunks of them and single tokens:
+
+    cache.begin(n)                      # every sequence grows by n rows
+    for layer in range(layers):
+        cache.append(layer, k, v)       # k, v [batch, n, heads, 128] after RoPE
+        o = cache.attend(layer, q)      # q, o [batch, n, q_heads, 128]
+
+begin(n, valid) takes right-padded rows: sequence b gets the first valid[b] of
+them.  Sequences have their own lengths, on the device; nothing here waits for
+it, so a step may be recorded into a graph and replayed (the host's bound of the
+lengths, which refuses a step that cannot fit, does not see replays: rows past
+the capacity are dropped).
+
+All arithmetic runs in the HIP library; this class only owns buffers.
+"""
+from __future__ import annotations
+
+from . import binding as cg
+
+
+class ServingCache:
+    def __init__(self, layers, batch, heads, q_heads, capacity, gauge, block_tokens=32,
+                 dtype=cg.CG_DTYPE_BF16, head_dim=128, with_mass=False):
+        import torch
+
+        if capacity < 0 or block_tokens <= 0 or capacity % block_tokens:
+            raise ValueError("capacity must be a multiple of block_tokens")
+        self.codec = cg.make_codec(cg.CG_BACKEND_BLOCK_UNIFORM, 8, block_tokens)
+        self.shape = cg.make_shape(layers, 2, batch, heads, capacity, capacity, head_dim, dtype)
+        self.gauge, self.q_heads = gauge, q_heads
+        self.dtype = torch.bfloat16 if dtype == cg.CG_DTYPE_BF16 else torch.float32
+        pay, meta, _ = cg.cg_encoded_bytes(self.shape, self.codec)
+        dev = {"device": "cuda"}
+        self.payload = torch.zeros(pay, dtype=torch.uint8, **dev)
+        self.meta = torch.zeros(meta // 4, **dev)
+        self.tail = torch.zeros((layers, 2, batch, heads, block_tokens, head_dim), dtype=self.dtype, **dev)
+        self.mass = torch.zeros((layers, batch, heads, capacity // block_tokens), **dev) if with_mass else None
+        self.lengths = torch.zeros(batch, dtype=torch.int32, **dev)
+        self.starts = torch.zeros(batch, dtype=torch.int32, **dev)   # of the present step
+        self.n = 0                                                   # rows of the present step
+        self.most = 0                                                # no sequence is longer
+        self._work = {}                                              # workspace by queries a step
+
+    def begin(self, n, valid=None):
+        """A step of n rows a sequence; valid: device int32 [batch], rows that are there (or None: all)."""
+        if n < 0:
+            raise ValueError("n < 0")
+        if self.most + n > self.shape.token_capacity:
+            raise ValueError(f"{n} rows do not fit: up to {self.most} of {self.shape.token_capacity} are taken")
+        self.n = n
+        self.most += n
+        self.starts.copy_(self.lengths)
+        if valid is None:
+            self.lengths.add_(n)
+        else:
+            self.lengths.add_(valid.clamp(0, n))
+
+    def append(self, layer, k, v):
+        """The step's rows of one layer, before that layer's attend."""
+        cg.cg_append(self.shape, self.gauge, self.codec, layer, self.n, k, v, self.tail, self.payload, self.meta,
+                     self.lengths, self.starts)
+
+    def attend(self, layer, q, scale=None, causal=True, out=None, lse=None):
+        """Attention of the step's queries; gathers the blocks' weights where the cache has them."""
+        import torch
+
+        if out is None:
+            out = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+        at = cg.make_attn(layer, self.q_heads, self.n, self.shape.head_dim ** -0.5 if scale is None else scale, causal,
+                          self.lengths, self.starts, (q.stride(0), q.stride(1)))
+        ws = self._work.get(self.n)
+        if ws is None:
+            need = cg.cg_attend_workspace_bytes(self.shape, self.gauge, self.codec, at, self.mass is not None)
+            ws = self._work[self.n] = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        cg.cg_attend(self.shape, self.payload, self.meta, self.gauge, self.codec, at, q, out, lse, self.mass, ws)
+        return out
+
+    def evict(self, budget, sink=1, recent=1):
+        """Keep `budget` blocks of every (layer, sequence, head), in place; -> the kept blocks' former numbers."""
+        import torch
+
+        if self.mass is None:
+            raise ValueError("the cache was made without with_mass")
+        s = self.shape
+        kept = torch.empty((s.layers, s.batch, s.heads, max(budget, 0)), dtype=torch.int32, device="cuda")
+        cg.cg_evict(s, self.codec, budget, sink, recent, self.mass, self.payload, self.meta, s, self.payload, self.meta,
+                    self.mass, kept, self.lengths, self.lengths)
+        self.most = min(self.most, budget * self.codec.block_tokens)
+        return kept
