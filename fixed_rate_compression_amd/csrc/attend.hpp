@@ -36,6 +36,7 @@ using cgk::D;
 using cgk::PITCH;
 
 constexpr int ROWS = 16;  // query rows of a row tile (one matrix-core operand)
+constexpr int FEW_TILES = 3;  // at most of the few-row form
 constexpr int UNIT = 32;  // tokens of a unit of work
 constexpr int NTH = 256;  // threads of a workgroup
 constexpr int MERGE_SPLITS = 1024;  // splits at most
@@ -231,22 +232,22 @@ __device__ __forceinline__ void put_row_part(float *xs, const RowPart &p) {
 // use, beside other loads.  On the vector units the same for four rows and
 // groups of 16 took 2000 cycles, most of it waiting.
 struct GaugeFrag {
-  f4_t b[2][8];  // output block nb, terms 16 s + 4 (lane / 16) + 0 .. 3 for channel lane % 16
+  f4_t b[2][2];  // output block nb, terms 16 (s0 + s) + 4 (lane / 16) + 0 .. 3 for channel lane % 16
 };
 
 template <bool INV>
-__device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, GaugeFrag &f) {
+__device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, int s0, GaugeFrag &f) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, kr = lane >> 4, n = lane & 15;
   const int ge = max(g, 16);
   if (g == 0) return;
 #pragma unroll
-  for (int s = 0; s < 8; s++) {
-    if (16 * s < ge) {
+  for (int s = 0; s < 2; s++) {
+    if (16 * (s0 + s) < ge) {
 #pragma unroll
       for (int nb = 0; nb < 2; nb++) {
         const int col = 32 * wave + 16 * nb + n, base = col & ~(ge - 1);  // sizes are powers of two
-        const int c = col & (g - 1), k = base + 16 * s + 4 * kr, kk = k & (g - 1);
+        const int c = col & (g - 1), k = base + 16 * (s0 + s) + 4 * kr, kk = k & (g - 1);
         const float *gp = gh + (int64_t)(col - c) * g;
         f4_t w;
         if constexpr (INV) {
@@ -261,32 +262,39 @@ __device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, 
   }
 }
 
-// tiles [0, T) of xs -> ys, both [16 T][PITCH]; IN_PLACE: the workgroup meets
-// between the reads and the writes (ys == xs).  The caller's barriers stand
-// before and after.
-template <int T, bool IN_PLACE>
-__device__ __forceinline__ void gauge_tiles(const float *xs, float *ys, int g, const GaugeFrag &f) {
+// tiles [0, T) of xs -> ys, both [16 T][PITCH]; first: load_gauge's for s0 = 0.
+// IN_PLACE: the workgroup meets between the reads and the writes (ys == xs).
+// The caller's barriers stand before and after.
+template <bool INV, int T, bool IN_PLACE>
+__device__ __forceinline__ void gauge_tiles(const float *xs, float *ys, const float *__restrict__ gh, int g,
+                                            const GaugeFrag &first) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, kr = lane >> 4, n = lane & 15;
   const int ge = max(g, 16);
   f4_t acc[T][2];
 #pragma unroll
   for (int t = 0; t < T; t++) acc[t][0] = acc[t][1] = f4_t{0.f, 0.f, 0.f, 0.f};
+  GaugeFrag f = first, nx = first;
+#pragma unroll 1
+  for (int s0 = 0; 16 * s0 < ge; s0 += 2) {
+    if (16 * (s0 + 2) < ge) load_gauge<INV>(gh, g, s0 + 2, nx);
 #pragma unroll
-  for (int s = 0; s < 8; s++) {
-    if (16 * s < ge) {
+    for (int s = 0; s < 2; s++) {
+      if (16 * (s0 + s) < ge) {
 #pragma unroll
-      for (int t = 0; t < T; t++) {
-        const float *row = xs + (16 * t + n) * PITCH + 16 * s + 4 * kr;
+        for (int t = 0; t < T; t++) {
+          const float *row = xs + (16 * t + n) * PITCH + 16 * (s0 + s) + 4 * kr;
 #pragma unroll
-        for (int nb = 0; nb < 2; nb++) {
-          const f4_t x = *(const f4_t *)(row + ((32 * wave + 16 * nb) & ~(ge - 1)));
+          for (int nb = 0; nb < 2; nb++) {
+            const f4_t x = *(const f4_t *)(row + ((32 * wave + 16 * nb) & ~(ge - 1)));
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            acc[t][nb] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], f.b[nb][s][e], acc[t][nb], 0, 0, 0);
+            for (int e = 0; e < 4; e++)
+              acc[t][nb] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], f.b[nb][s][e], acc[t][nb], 0, 0, 0);
+          }
         }
       }
     }
+    f = nx;
   }
   if (IN_PLACE) __syncthreads();
 #pragma unroll

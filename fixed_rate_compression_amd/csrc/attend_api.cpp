@@ -14,7 +14,7 @@ using cgh::error;
 struct Plan {
   int64_t rows, tiles;
   int splits, mparts, waves;
-  bool few;  // one row tile: block sums come with the attention
+  bool few;  // few row tiles: block sums come with the attention
   int64_t entries;
   size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, mpart_bytes, qfrag_bytes, qrow_bytes;
   size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + mpart_bytes + qfrag_bytes + qrow_bytes; }
@@ -22,9 +22,12 @@ struct Plan {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workgroups that keep 256 compute units busy: four on each (their LDS),
-// with at least 256 tokens (two units a wave) to a workgroup.
-constexpr int64_t kTargetWorkgroups = 1024, kMinTokens = 256;
+// Workgroups of few rows: what 256 compute units hold at once, three on each
+// (two where block sums are gathered: more registers), with at least 256 tokens
+// (two units a wave) to each.  A multiple that does not fill the last round
+// costs: 131072 tokens with sums 54 us by 512 workgroups, 66 by 768; 262144
+// without 95 by 768, 103 by 640.
+constexpr int64_t kResident = 768, kResidentSums = 512, kMinTokens = 256;
 // 128-row tiles: two workgroups fit a compute unit
 constexpr int64_t kTargetTiles = 512;
 // weights of many rows: four workgroups to a compute unit, four row steps at least to each
@@ -34,10 +37,12 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   Plan p{};
   p.rows = (int64_t)t->n_queries * (t->q_heads / s->heads);
   p.tiles = (p.rows + cga::ROWS - 1) / cga::ROWS;
-  p.few = p.tiles <= 1;
+  // 8 sequences x 8 KV heads x 4096 tokens with 32, 48 and 64 rows a head: 25, 27
+  // and 43 us by row tiles of 16, by tiles of 128 and their layout 34, 35 and 37
+  p.few = p.tiles <= cga::FEW_TILES;
   const int64_t fields = (int64_t)s->batch * s->heads;
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
-  const int64_t target = p.few ? kTargetWorkgroups : kTargetTiles;
+  const int64_t target = !p.few ? kTargetTiles : mass ? kResidentSums : kResident;
   int64_t sp = work > 0 ? (p.few ? (target + work - 1) / work : target / work) : 1;
   const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
   if (sp > most) sp = most;
@@ -94,7 +99,7 @@ int check_attn(const cg_shape *s, const cg_attn *t) {
   if (rows > (int64_t)1 << 26 || (int64_t)s->batch * s->heads > (int64_t)1 << 22 ||
       (rows + 15) / 16 * s->batch * s->heads > (int64_t)1 << 27)
     return error(CG_E_SHAPE, "too many query rows");
-  if ((int64_t)s->batch * s->heads * ((s->tokens + 31) / 32) > (int64_t)1 << 31)
+  if ((int64_t)s->batch * s->heads * ((s->token_capacity + 31) / 32) > (int64_t)1 << 31)
     return error(CG_E_SHAPE, "too many tokens for one launch");
   return CG_OK;
 }

@@ -1,6 +1,7 @@
-// Attention of up to 16 query rows (a row tile) over the 8-bit cache, split
-// along the tokens: the form for single tokens and few drafted ones, bound by
-// the memory traffic of the codes.
+// Attention of few query rows (up to three row tiles of 16) over the 8-bit
+// cache, split along the tokens: the form for single tokens and few drafted
+// ones, bound by the memory traffic of the codes (of which the second and third
+// tile find most in the caches).
 //
 // A workgroup takes one part of one field pair's tokens for one row tile; its
 // waves (four, or eight where that saves the splits) take the part's 32-token
@@ -87,7 +88,7 @@ struct RowState {
 // values' (scores to 2^-22 of the sum of |q'| 255 step; uncentred 10 times
 // that).  bf16 storage: the weights are one fp16 part (2^-11 of a weight).
 template <bool BF16, bool MASS, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_rows(const AttendArgs a) {
   __shared__ __align__(16) float lds[NW * ROWS * PITCH];
   __shared__ float2 ml[NW][ROWS];
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
@@ -106,7 +107,7 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
   GaugeFrag gw;
   if (front) {
     qp = load_row_part<BF16>(a, b, h, r0);
-    load_gauge<false>(gk, a.g, gw);
+    load_gauge<false>(gk, a.g, 0, gw);
   }
   const Sequence sq = load_sequence(a, b);
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
   if (front) put_row_part(xs, qp);
   __syncthreads();
   if (a.g) {
-    if (front) gauge_tiles<1, false>(xs, ys, a.g, gw);
+    if (front) gauge_tiles<false, 1, false>(xs, ys, gk, a.g, gw);
     __syncthreads();
   } else {
     ys = xs;
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
   }
 
   const float *gv = a.gv + (int64_t)h * D * a.g;
-  if (a.splits == 1 && front) load_gauge<true>(gv, a.g, gw);
+  if (a.splits == 1 && front) load_gauge<true>(gv, a.g, 0, gw);
   // join the waves: each leaves its sums relative to its own maximum
   __syncthreads();  // the operands have been read
   const float l = row_sum(st.l), mv = row_sum(st.mv);
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
   float *os = lds;
   if (a.g) {
     os = lds + ROWS * PITCH;
-    if (front) gauge_tiles<1, false>(lds, os, a.g, gw);
+    if (front) gauge_tiles<true, 1, false>(lds, os, gv, a.g, gw);
     __syncthreads();
   }
   if (front) store_rows<BF16>(a, b, h, r0, nr, os);
@@ -348,41 +349,45 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttendArgs a) {
 // Block weights of few rows from the sums the attention left, 256 blocks to a
 // workgroup: mass[block] += sum over rows of sum_t 2^(s_t - m) 2^(m - log2 sum)
 __device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
-  __shared__ float lse2[ROWS];
+  __shared__ float lse2[FEW_TILES * ROWS];
+  __shared__ int lim[FEW_TILES * ROWS];
   const uint32_t chunks = (uint32_t)((a.nblk + NTH - 1) / NTH);
   const int bh = (int)(id / chunks), b = bh / a.heads;
   const int64_t blk = (int64_t)(id - bh * chunks) * NTH + threadIdx.x;
-  const int tmax = limit_of(a, load_sequence(a, b), 0, a.n - 1);
-  const int row = threadIdx.x >> 4, j = threadIdx.x & 15;  // 16 lanes to a row's splits
-  float M = -INFINITY, L = 0.0f;
-  if (row < a.rows) {
+  const Sequence sq = load_sequence(a, b);
+  const int j = threadIdx.x & 15;  // 16 lanes to a row's splits
+  for (int row = threadIdx.x >> 4; row < a.rows; row += NTH / 16) {
     const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + row;
+    float M = -INFINITY, L = 0.0f;
     for (int s = j; s < a.splits; s += 16) {
       const float2 x = pm[(int64_t)s * a.rows];
       const float m = fmaxf(M, x.x);
       if (m > -INFINITY) L = L * exp2_fast(M - m) + x.y * exp2_fast(x.x - m);
       M = m;
     }
-  }
 #pragma unroll
-  for (int k = 8; k >= 1; k >>= 1) {
-    const float m2 = __shfl_xor(M, k), l2 = __shfl_xor(L, k), m = fmaxf(M, m2);
-    if (m > -INFINITY) L = L * exp2_fast(M - m) + l2 * exp2_fast(m2 - m);
-    M = m;
+    for (int k = 8; k >= 1; k >>= 1) {
+      const float m2 = __shfl_xor(M, k), l2 = __shfl_xor(L, k), m = fmaxf(M, m2);
+      if (m > -INFINITY) L = L * exp2_fast(M - m) + l2 * exp2_fast(m2 - m);
+      M = m;
+    }
+    if (j == 0) {
+      lse2[row] = M + __builtin_log2f(L);
+      lim[row] = L > 0.0f ? query_limit(a, sq, (int)((uint32_t)row / (uint32_t)a.ratio)) : 0;
+    }
   }
-  if (j == 0) lse2[row] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
   __syncthreads();
-  if (blk >= a.nblk || (blk << a.bshift) >= tmax) return;
-  const int per = a.bshift == 6 ? 2 : 1;
+  if (blk >= a.nblk || (blk << a.bshift) >= limit_of(a, sq, 0, a.n - 1)) return;
+  const int per = a.bshift == 6 ? 2 : 1, esh = min(a.bshift, 5);
   float w = 0.0f;
   for (int k = 0; k < per; k++) {
     const int64_t e = blk * per + k;
-    if (a.bshift != 4 && e * UNIT >= tmax) break;  // the unit was not visited
     const float2 *p = a.bsum + ((int64_t)bh * a.entries + e) * a.rows;
 #pragma unroll 4
     for (int r = 0; r < a.rows; r++) {
+      if ((e << esh) >= lim[r]) continue;  // nothing for this row: perhaps nobody wrote its sum
       const float2 x = p[r];
-      if (x.x > 0.0f && lse2[r] < INFINITY) w += x.x * exp2_fast(x.y - lse2[r]);
+      if (x.x > 0.0f) w += x.x * exp2_fast(x.y - lse2[r]);
     }
   }
   a.mass[(int64_t)bh * a.nblk + blk] += w;
@@ -449,7 +454,10 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   }
   *(float4 *)&part[grp][c4] = u;
   __syncthreads();
-  if (t == 0 && a.lse) store_lse(a, b, h, r, M, L);
+  if (t == 0) {
+    if (a.lse) store_lse(a, b, h, r, M, L);
+    if (a.lse2) a.lse2[(int64_t)bh * a.rows + r] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
+  }
   if (t < D) {
     float v = 0.0f;
 #pragma unroll
@@ -484,33 +492,46 @@ __global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float *gv = a.gv + (int64_t)h * D * a.g;
   GaugeFrag gw;
-  load_gauge<true>(gv, a.g, gw);
+  load_gauge<true>(gv, a.g, 0, gw);
+  // four rows a wave, side by side
+  int r[4];
+  float M[4], L[4];
+  float2 u[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int rr = wave + 4 * i, r = min(r0 + rr, a.rows - 1);
-    const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r;
-    const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r) * D + 2 * lane;
-    float M = -INFINITY, L = 0.0f;
-    for (int s = 0; s < a.splits; s++) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
-    float2 u = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < a.splits; s++) {
-      const float2 x = pm[(int64_t)s * a.rows], y = *(const float2 *)(po + (int64_t)s * a.rows * D);
-      const float k = x.x > -INFINITY ? exp2_fast(x.x - M) : 0.0f;
-      L += x.y * k;
-      u.x += y.x * k;
-      u.y += y.y * k;
+    r[i] = min(r0 + wave + 4 * i, a.rows - 1);
+    M[i] = -INFINITY;
+    L[i] = 0.0f;
+    u[i] = make_float2(0.f, 0.f);
+  }
+  const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows;
+  const float *po = a.part_o + (int64_t)bh * a.splits * a.rows * D + 2 * lane;
+  for (int s = 0; s < a.splits; s++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) M[i] = fmaxf(M[i], pm[(int64_t)s * a.rows + r[i]].x);
+#pragma unroll 2
+  for (int s = 0; s < a.splits; s++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float2 x = pm[(int64_t)s * a.rows + r[i]], y = *(const float2 *)(po + ((int64_t)s * a.rows + r[i]) * D);
+      const float k = x.x > -INFINITY ? exp2_fast(x.x - M[i]) : 0.0f;
+      L[i] += x.y * k;
+      u[i].x += y.x * k;
+      u[i].y += y.y * k;
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    *(float2 *)(us + rr * PITCH + 2 * lane) = make_float2(u.x * inv, u.y * inv);
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int rr = wave + 4 * i;
+    const float inv = L[i] > 0.0f ? 1.0f / L[i] : 0.0f;
+    *(float2 *)(us + rr * PITCH + 2 * lane) = make_float2(u[i].x * inv, u[i].y * inv);
     if (lane == 0 && rr < nr) {
-      if (a.lse) store_lse(a, b, h, r, M, L);
-      if (a.lse2) a.lse2[(int64_t)bh * a.rows + r] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
+      if (a.lse) store_lse(a, b, h, r[i], M[i], L[i]);
+      if (a.lse2) a.lse2[(int64_t)bh * a.rows + r[i]] = L[i] > 0.0f ? M[i] + __builtin_log2f(L[i]) : INFINITY;
     }
   }
   __syncthreads();
   if (a.g) {
-    gauge_tiles<1, true>(us, us, a.g, gw);
+    gauge_tiles<true, 1, true>(us, us, gv, a.g, gw);
     __syncthreads();
   }
   store_rows<BF16>(a, b, h, r0, nr, us);
@@ -532,14 +553,17 @@ hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
 
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const int64_t fields = (int64_t)a.batch * a.heads;
+  const bool mass = a.mass && a.bsum && a.tokens > 0;
   const dim3 block(NTH);
-  if (a.tiles > 1) {
+  // a workgroup a row while they fit the machine twice over (1024 rows of 64
+  // splits: 8.6 us, by sixteens 58), else sixteen rows (9600 rows of 3: 13 and 26)
+  if (fields * a.rows > 4096) {
     const dim3 grid((unsigned)(fields * a.tiles));
     if (bf16) hipLaunchKernelGGL(k_attend_merge_many<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(k_attend_merge_many<false>, grid, block, 0, s, a);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && mass ? mass_finish_launch(a, s) : e;
   }
-  const bool mass = a.mass && a.bsum && a.tokens > 0;
   const dim3 grid((unsigned)(fields * a.rows + (mass ? fields * ((a.nblk + NTH - 1) / NTH) : 0)));
   if (bf16 && mass) hipLaunchKernelGGL((k_attend_merge<true, true>), grid, block, 0, s, a);
   else if (bf16) hipLaunchKernelGGL((k_attend_merge<true, false>), grid, block, 0, s, a);

@@ -364,7 +364,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   // rows' sums, scaled as they stand, into LDS; then parts or outputs
   const float *gv = a.gv + (int64_t)h * D * a.g;
   GaugeFrag gw;
-  load_gauge<true>(gv, a.g, gw);
+  load_gauge<true>(gv, a.g, 0, gw);
   float *us = (float *)lds;
   {
     const int rr = wave * WROWS + row;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
     return;
   }
   if (a.g) {
-    gauge_tiles<TROWS / ROWS, true>(us, us, a.g, gw);
+    gauge_tiles<true, TROWS / ROWS, true>(us, us, gv, a.g, gw);
     __syncthreads();
   }
   store_rows<BF16>(a, b, h, r0, nr, us);
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
   const int h = bh % a.heads, b = bh / a.heads;
   const float *gk = a.gk + (int64_t)h * D * a.g;
   GaugeFrag gw;
-  load_gauge<false>(gk, a.g, gw);
+  load_gauge<false>(gk, a.g, 0, gw);
   RowPart p[4];
 #pragma unroll
   for (int t = 0; t < 4; t++) p[t] = load_row_part<BF16>(a, b, h, (tile0 + t) * ROWS);
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
   for (int t = 0; t < 4; t++) put_row_part(xs + t * ROWS * PITCH, p[t]);
   __syncthreads();
   if (a.g) {
-    gauge_tiles<4, true>(xs, xs, a.g, gw);
+    gauge_tiles<false, 4, true>(xs, xs, gk, a.g, gw);
     __syncthreads();
   }
   const int lane = threadIdx.x & 63, tile = tile0 + (int)(threadIdx.x >> 6);
