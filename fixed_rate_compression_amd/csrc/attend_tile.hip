@@ -68,14 +68,16 @@ __device__ __forceinline__ void put_unit(unsigned char *lds, int un, int tmax, c
   if (i < 4) {
     const bool there = un * UNIT + 16 * (i & 1) < tmax;  // a block that holds no row yet is not looked at
     const float mid = LO || (i & 2) ? __builtin_fmaf(128.0f, s.m.y, s.m.x) : s.m.x;  // the value of code 128 (0)
-    *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * i) = make_float2(there ? mid : 0.0f, there ? s.m.y : 0.0f);
+    const float st = there ? s.m.y : 0.0f;
+    *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * i) =
+        make_float2(there ? mid : 0.0f, (i & 2) ? fmaxf(__builtin_amdgcn_logf(st), -200.0f) : st);  // values: log2 of the step
   }
 }
 
 // a lane's row (the same in lanes l and l + 32 but for l and mv), as in
 // attend_rows.hip, but mu is -inf while the row has seen nothing
 struct TileState {
-  float m, mu, mo, f, l, mv;
+  float m, mu, mo, f, l, mv;  // f: log2 of the values' scale
 };
 
 // the queries of a wave: channels 16 s + 8 half + 0 .. 7 of row lane % 32 at step s
@@ -84,12 +86,15 @@ struct TileQueries {
   float ca, cq;
 };
 
-// the weights of a unit and what goes with them; NB ranges to a unit (two
-// where blocks have 16 tokens)
+// the weights of a unit, p_t sv_b f, and what goes with them; NB ranges to a
+// unit (two where blocks have 16 tokens).  The values' factor is added to the
+// exponent: sums of p itself are those of the weights over the factor.  Where it
+// is below 2^-60 the weights vanish in fp16 either way and 2^-60 stands for it
+// (a constant block has factor 0, its rows still count).
 template <int NB>
 struct UnitWeights {
   float p[16];
-  float ps[NB], w[NB], mid[NB];  // sums of weights, value factors, values of code 128
+  float ps[NB], mid[NB];  // sums of p_t, values of code 128
 };
 
 // scores of a unit: z = K Q^T, z[r] that of token 8 (r / 4) + 4 half + r % 4,
@@ -110,18 +115,18 @@ __device__ __forceinline__ void unit_scores(const unsigned char *kb, const TileQ
 }
 
 template <int NB>
-__device__ __forceinline__ void sum_weights(UnitWeights<NB> &o) {
+__device__ __forceinline__ void sum_weights(const float (&p)[16], float (&ps)[NB]) {
   float h[2];
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    const float *p = o.p + 8 * u;
-    h[u] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    const float *x = p + 8 * u;
+    h[u] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
   }
   if constexpr (NB == 2) {
-    o.ps[0] = h[0];
-    o.ps[1] = h[1];
+    ps[0] = h[0];
+    ps[1] = h[1];
   } else {
-    o.ps[0] = h[0] + h[1];
+    ps[0] = h[0] + h[1];
   }
 }
 
@@ -131,12 +136,14 @@ __device__ __forceinline__ void sum_weights(UnitWeights<NB> &o) {
 template <bool MASKED, int NB>
 __device__ __forceinline__ bool unit_weights(const float2 *mt, const TileQueries &q, const f16_t &z, int vis,
                                              const TileState &st, UnitWeights<NB> &o) {
+  float iw[NB], sum[NB], over = 0.0f;
 #pragma unroll
   for (int u = 0; u < NB; u++) {
     const float2 mk = mt[u], mv = mt[2 + u];
     o.mid[u] = mv.x;
-    o.w[u] = mv.y * st.f;
-    const float A = mk.y * q.ca, B = __builtin_fmaf(mk.x, q.cq, -st.mu);
+    const float lw = fmaxf(mv.y + st.f, -60.0f);
+    iw[u] = exp2_fast(-lw);
+    const float A = mk.y * q.ca, B = __builtin_fmaf(mk.x, q.cq, lw - st.mu);
 #pragma unroll
     for (int k = 0; k < 16 / NB; k++) {
       const int r = 16 / NB * u + k;
@@ -144,11 +151,12 @@ __device__ __forceinline__ bool unit_weights(const float2 *mt, const TileQueries
       o.p[r] = exp2_fast(MASKED && 8 * (r >> 2) + (r & 3) >= vis ? -INFINITY : s);
     }
   }
-  sum_weights(o);
-  float over = o.ps[0] * 128.0f;
-  if constexpr (NB == 2) over = fmaxf(over, o.ps[1] * 128.0f);
+  sum_weights<NB>(o.p, sum);
 #pragma unroll
-  for (int u = 0; u < NB; u++) over = fmaxf(over, o.ps[u] * o.w[u]);
+  for (int u = 0; u < NB; u++) {
+    o.ps[u] = sum[u] * iw[u];
+    over = fmaxf(over, fmaxf(sum[u], o.ps[u] * 128.0f));
+  }
   return over > 32768.0f;
 }
 
@@ -177,7 +185,7 @@ __device__ __forceinline__ void raise(const unsigned char *kb, const unsigned ch
       t = fmaxf(t, o.p[r]);
     }
     mx = fmaxf(mx, t);
-    mv = fmaxf(mv, t + __builtin_amdgcn_logf(mt[2 + u].y));  // log2; -inf for a constant block
+    mv = fmaxf(mv, t + mt[2 + u].y);
   }
   const float mn = fmaxf(st.m, pair_max(mx));
   float on = fmaxf(st.mo, pair_max(mv));
@@ -191,15 +199,24 @@ __device__ __forceinline__ void raise(const unsigned char *kb, const unsigned ch
   for (int j = 0; j < 4; j++) acc[j] *= ao;
   st.m = st.mu = mn;
   st.mo = on;
-  st.f = some ? exp2_fast(mn - on + 9.0f) : 1.0f;
+  st.f = some ? mn - on + 9.0f : 0.0f;
   const float mu = some ? mn : 0.0f;
-#pragma unroll
-  for (int r = 0; r < 16; r++) o.p[r] = exp2_fast(o.p[r] - mu);
-  sum_weights(o);
+  float iw[NB], sum[NB];
 #pragma unroll
   for (int u = 0; u < NB; u++) {
+    const float lw = fmaxf(mt[2 + u].y + st.f, -60.0f);
+    iw[u] = exp2_fast(-lw);
+#pragma unroll
+    for (int k = 0; k < 16 / NB; k++) {
+      const int r = 16 / NB * u + k;
+      o.p[r] = exp2_fast(o.p[r] + (lw - mu));
+    }
+  }
+  sum_weights<NB>(o.p, sum);
+#pragma unroll
+  for (int u = 0; u < NB; u++) {
+    o.ps[u] = sum[u] * iw[u];
     o.mid[u] = mt[2 + u].x;
-    o.w[u] = mt[2 + u].y * st.f;
   }
 }
 
@@ -219,10 +236,9 @@ __device__ __forceinline__ void take_weights(const UnitWeights<NB> &o, TileState
 #pragma unroll
   for (int x = 0; x < 2; x++) {
     uint32_t ph[4], pl[4];
-    const float w = o.w[NB == 2 ? x : 0];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const float a = o.p[8 * x + 2 * k] * w, b = o.p[8 * x + 2 * k + 1] * w;
+      const float a = o.p[8 * x + 2 * k], b = o.p[8 * x + 2 * k + 1];
       ph[k] = pack_f16x2(a, b);
       if constexpr (!BF16) {
         const f2_t hh = unpack_f16x2(ph[k]);
@@ -315,7 +331,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   TileState st;
   st.m = st.mo = st.mu = -INFINITY;
   st.l = st.mv = 0.0f;
-  st.f = 1.0f;
+  st.f = 0.0f;
   f16_t acc[4];
 #pragma unroll
   for (int j = 0; j < 4; j++)
