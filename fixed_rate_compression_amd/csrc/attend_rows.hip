@@ -258,16 +258,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
         }
       }
     }
-    float bt[2];  // block sums over the row's lanes, relative to mu
-    float bmu = st.mu;
-    if constexpr (MASS) {
-      if (a.bshift == 4) {
-        bt[0] = row_sum(bs[0]);
-        bt[1] = row_sum(bs[1]);
-      } else {
-        bt[0] = row_sum(bs[0] + bs[1]);
-      }
-    }
     const h8_t P = as_h8(ph[0][0], ph[0][1], ph[1][0], ph[1][1]);
     h8_t Pl;
     if constexpr (!BF16) Pl = as_h8(pl[0][0], pl[0][1], pl[1][0], pl[1][1]);
@@ -280,12 +270,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     CG_PV(0) CG_PV(1) CG_PV(2) CG_PV(3) CG_PV(4) CG_PV(5) CG_PV(6) CG_PV(7)
 #undef CG_PV
     if (more) load_values(a, vf, vm, t0 + NW * UNIT, uv);
-    if constexpr (MASS) {  // behind the loads: waiting for those does not wait for a store
+    if constexpr (MASS) {  // block sums over the row's lanes; behind the loads: waiting for those does not wait for a store
       const int64_t e = t0 >> min(a.bshift, 5);
       float2 *p = a.bsum + ((int64_t)bh * a.entries + e) * a.rows + r0 + row;
+      const bool two = a.bshift == 4;
+      const float v0 = row_sum(two ? bs[0] : bs[0] + bs[1]), v1 = two ? row_sum(bs[1]) : 0.0f;
       if (grp == 0 && row < nr) {
-        *p = make_float2(bt[0], bmu);
-        if (a.bshift == 4 && e + 1 < a.entries) p[a.rows] = make_float2(bt[1], bmu);
+        *p = make_float2(v0, st.mu);
+        if (two && e + 1 < a.entries) p[a.rows] = make_float2(v1, st.mu);
       }
     }
   }
