@@ -120,6 +120,7 @@ __global__ __launch_bounds__(NTH, 2) void k_mass_many(const AttendArgs a) {
     }
     const float4 rp = *(const float4 *)(buf + QBYTES + 16 * row);
     const int lim = __float_as_int(rp.w) - t0 - 4 * half;
+    const bool masked = __any(lim < 64 - 4 * half);  // some row does not see all of the wave's tokens
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       z[u] += zl[u];
@@ -128,11 +129,16 @@ __global__ __launch_bounds__(NTH, 2) void k_mass_many(const AttendArgs a) {
         const float A = m[u][k].y * rp.x, B = __builtin_fmaf(m[u][k].x, rp.y, -rp.z);
         float p[16 / NB];
 #pragma unroll
-        for (int e = 0; e < 16 / NB; e++) {
-          const int r = 16 / NB * k + e;
-          const float s = __builtin_fmaf(z[u][r], A, B);
-          p[e] = exp2_fast(32 * u + 8 * (r >> 2) + (r & 3) < lim ? s : -INFINITY);
+        for (int e = 0; e < 16 / NB; e++) p[e] = __builtin_fmaf(z[u][16 / NB * k + e], A, B);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 16 / NB; e++) {
+            const int r = 16 / NB * k + e;
+            p[e] = 32 * u + 8 * (r >> 2) + (r & 3) < lim ? p[e] : -INFINITY;
+          }
         }
+#pragma unroll
+        for (int e = 0; e < 16 / NB; e++) p[e] = exp2_fast(p[e]);
 #pragma unroll
         for (int w = 8 / NB; w >= 1; w >>= 1)
 #pragma unroll
