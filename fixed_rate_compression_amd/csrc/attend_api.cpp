@@ -22,12 +22,37 @@ struct Plan {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workgroups of few rows: what 256 compute units hold at once, three on each
-// (two where block sums are gathered: more registers), with at least 256 tokens
-// (two units a wave) to each.  A multiple that does not fill the last round
-// costs: 131072 tokens with sums 54 us by 512 workgroups, 66 by 768; 262144
-// without 95 by 768, 103 by 640.
+// Splits of the few-row form.  256 compute units hold `kResident` of its
+// workgroups at once (three on each; two where block sums are gathered: more
+// registers).  A round of them takes about 6 us for what does not depend on the
+// tokens, plus each workgroup's tokens at its share of 5.5 TB/s, at best 10 ns a
+// token; a merge takes about 4.5 us.  The splits are the most that some number of
+// rounds holds, with at least 256 tokens (two units a wave) to a workgroup: 80
+// KV heads of 3000 tokens, 9 splits (one round) 16 us, 10 splits 23; 131072
+// tokens with sums 54 us by 512 workgroups, 66 by 768.
 constexpr int64_t kResident = 768, kResidentSums = 512, kMinTokens = 256;
+
+int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
+  const int64_t most = (tokens + kMinTokens - 1) / kMinTokens;
+  int64_t best = 1;
+  double best_us = 0.0;
+  for (int k = 0; k <= 4; k++) {
+    int64_t sp = k ? k * resident / work : 1;
+    if (sp > most) sp = most;
+    if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
+    if (sp < 1) sp = 1;
+    const int64_t groups = work * sp, rounds = (groups + resident - 1) / resident;
+    const double busy = groups < resident ? (double)groups / resident : 1.0;
+    const double share = resident * 256.0 / 5.5e6 * busy, token_us = share > 0.010 ? share : 0.010;
+    const double us = rounds * (6.0 + (double)tokens / sp * token_us) + (sp > 1 ? 4.5 : 0.0);
+    if (k == 0 || us < best_us) {
+      best = sp;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
 // 128-row tiles: two workgroups fit a compute unit
 constexpr int64_t kTargetTiles = 512;
 // weights of many rows: four workgroups to a compute unit, four row steps at least to each
@@ -42,12 +67,16 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   p.few = p.tiles <= cga::FEW_TILES;
   const int64_t fields = (int64_t)s->batch * s->heads;
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
-  const int64_t target = !p.few ? kTargetTiles : mass ? kResidentSums : kResident;
-  int64_t sp = work > 0 ? (p.few ? (target + work - 1) / work : target / work) : 1;
-  const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
-  if (sp > most) sp = most;
-  if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
-  if (sp < 1) sp = 1;
+  int64_t sp = 1;
+  if (work > 0 && p.few) {
+    sp = few_splits(work, s->tokens, mass ? kResidentSums : kResident);
+  } else if (work > 0) {
+    const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
+    sp = kTargetTiles / work;
+    if (sp > most) sp = most;
+    if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
+    if (sp < 1) sp = 1;
+  }
   // Short histories: eight waves to a workgroup in place of splits and their
   // merge.  8 KV heads x 4 query heads, one sequence of 512 / 1024 / 2048
   // tokens: 9.0 / 10.9 / 16.4 us, with splits 12.2 / 12.2 / 12.5; 32 sequences of
