@@ -392,9 +392,9 @@ __device__ __forceinline__ void store_rows(const AttendArgs &a, int b, int h, in
 
 __device__ __forceinline__ void store_lse(const AttendArgs &a, int b, int h, int r, float m, float l) {
   const int i = r / a.ratio, j = r - i * a.ratio;
-  // natural logarithm of the row's sum of exp(score)
+  // natural logarithm of the row's sum of exp(score); a NaN stays one
   a.lse[((int64_t)b * a.n + i) * a.heads * a.ratio + h * a.ratio + j] =
-      l > 0.0f ? (m + __builtin_log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      l != 0.0f ? (m + __builtin_log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace cga

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     if (t0 + UNIT > all) {
 #pragma unroll
       for (int t = 0; t < 2; t++) {
-        if (t0 + 16 * t >= tmax) vst[t] = vmn[t] = 0.0f;  // a block that holds no row yet
+        if (t0 + 16 * t >= lim) vst[t] = vmn[t] = 0.0f;  // nothing this row sees: perhaps not a number
 #pragma unroll
         for (int r = 0; r < 4; r++)
           s[t][r] = t0 + 16 * t + 4 * grp + r < lim ? s[t][r] : -INFINITY;
@@ -354,18 +354,18 @@ __device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
     for (int s = j; s < a.splits; s += 16) {
       const float2 x = pm[(int64_t)s * a.rows];
       const float m = fmaxf(M, x.x);
-      if (m > -INFINITY) L = L * exp2_fast(M - m) + x.y * exp2_fast(x.x - m);
+      L = m > -INFINITY ? L * exp2_fast(M - m) + x.y * exp2_fast(x.x - m) : L + x.y;
       M = m;
     }
 #pragma unroll
     for (int k = 8; k >= 1; k >>= 1) {
       const float m2 = __shfl_xor(M, k), l2 = __shfl_xor(L, k), m = fmaxf(M, m2);
-      if (m > -INFINITY) L = L * exp2_fast(M - m) + l2 * exp2_fast(m2 - m);
+      L = m > -INFINITY ? L * exp2_fast(M - m) + l2 * exp2_fast(m2 - m) : L + l2;
       M = m;
     }
     if (j == 0) {
       lse2[row] = M + __builtin_log2f(L);
-      lim[row] = L > 0.0f ? query_limit(a, sq, (int)((uint32_t)row / (uint32_t)a.ratio)) : 0;
+      lim[row] = L != 0.0f ? query_limit(a, sq, (int)((uint32_t)row / (uint32_t)a.ratio)) : 0;
     }
   }
   __syncthreads();
@@ -379,7 +379,7 @@ __device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
     for (int r = 0; r < a.rows; r++) {
       if ((e << esh) >= lim[r]) continue;  // nothing for this row: perhaps nobody wrote its sum
       const float2 x = p[r];
-      if (x.x > 0.0f) w += x.x * exp2_fast(x.y - lse2[r]);
+      if (x.x != 0.0f) w += x.x * exp2_fast(x.y - lse2[r]);
     }
   }
   a.mass[(int64_t)bh * a.nblk + blk] += w;
@@ -448,13 +448,13 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   __syncthreads();
   if (t == 0) {
     if (a.lse) store_lse(a, b, h, r, M, L);
-    if (a.lse2) a.lse2[(int64_t)bh * a.rows + r] = L > 0.0f ? M + __builtin_log2f(L) : INFINITY;
+    if (a.lse2) a.lse2[(int64_t)bh * a.rows + r] = L != 0.0f ? M + __builtin_log2f(L) : INFINITY;
   }
   if (t < D) {
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; k++) v += part[k][t];
-    us[t] = L > 0.0f ? v / L : 0.0f;
+    us[t] = L != 0.0f ? v / L : 0.0f;
   }
   __syncthreads();
   if (a.g == 0) {
@@ -518,7 +518,7 @@ __global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
     *(float2 *)(us + rr * PITCH + 2 * lane) = make_float2(u[i].x * inv, u[i].y * inv);
     if (lane == 0 && rr < nr) {
       if (a.lse) store_lse(a, b, h, r[i], M[i], L[i]);
-      if (a.lse2) a.lse2[(int64_t)bh * a.rows + r[i]] = L[i] > 0.0f ? M[i] + __builtin_log2f(L[i]) : INFINITY;
+      if (a.lse2) a.lse2[(int64_t)bh * a.rows + r[i]] = L[i] != 0.0f ? M[i] + __builtin_log2f(L[i]) : INFINITY;
     }
   }
   __syncthreads();

@@ -70,7 +70,7 @@ __device__ __forceinline__ void put_unit(unsigned char *lds, int un, int tmax, c
     const float mid = LO || (i & 2) ? __builtin_fmaf(128.0f, s.m.y, s.m.x) : s.m.x;  // the value of code 128 (0)
     const float st = there ? s.m.y : 0.0f;
     *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * i) =
-        make_float2(there ? mid : 0.0f, (i & 2) ? fmaxf(__builtin_amdgcn_logf(st), -200.0f) : st);  // values: log2 of the step
+        make_float2(there ? mid : 0.0f, (i & 2) ? fminf(fmaxf(__builtin_amdgcn_logf(st), -200.0f), 128.0f) : st);  // values: log2 of the step
   }
 }
 
@@ -130,6 +130,13 @@ __device__ __forceinline__ void sum_weights(const float (&p)[16], float (&ps)[NB
   }
 }
 
+// whether the lane's row sees none of range u's tokens: the values' range, which
+// may hold a NaN of a later token, is then left out
+template <int NB>
+__device__ __forceinline__ bool unseen(int u, int vis) {
+  return vis + (int)((threadIdx.x & 32) >> 3) <= (NB == 2 ? 16 * u : 0);
+}
+
 // weights of a unit; vis: tokens of the unit, less 4 half, that the lane's row
 // sees (MASKED).  Returns whether some weight is too large for its scale (or
 // infinite: a row that has seen nothing yet).
@@ -140,7 +147,7 @@ __device__ __forceinline__ bool unit_weights(const float2 *mt, const TileQueries
 #pragma unroll
   for (int u = 0; u < NB; u++) {
     const float2 mk = mt[u], mv = mt[2 + u];
-    o.mid[u] = mv.x;
+    o.mid[u] = MASKED && unseen<NB>(u, vis) ? 0.0f : mv.x;
     const float lw = fmaxf(mv.y + st.f, -60.0f);
     iw[u] = exp2_fast(-lw);
     const float A = mk.y * q.ca, B = __builtin_fmaf(mk.x, q.cq, lw - st.mu);
@@ -216,7 +223,7 @@ __device__ __forceinline__ void raise(const unsigned char *kb, const unsigned ch
 #pragma unroll
   for (int u = 0; u < NB; u++) {
     o.ps[u] = sum[u] * iw[u];
-    o.mid[u] = mt[2 + u].x;
+    o.mid[u] = unseen<NB>(u, vis) ? 0.0f : mt[2 + u].x;
   }
 }
 
@@ -401,7 +408,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
         a.part_ml[((int64_t)bh * a.splits + split) * a.rows + wr] = make_float2(st.m, L);
       } else {
         if (a.lse) store_lse(a, b, h, wr, st.m, L);
-        if (a.lse2) a.lse2[(int64_t)bh * a.rows + wr] = L > 0.0f ? st.m + __builtin_log2f(L) : INFINITY;
+        if (a.lse2) a.lse2[(int64_t)bh * a.rows + wr] = L != 0.0f ? st.m + __builtin_log2f(L) : INFINITY;
       }
     }
   }

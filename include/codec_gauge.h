@@ -444,9 +444,13 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  *         NULL: every block of the layer gains the sum of the weights that its
  *         rows received from all visible queries and all heads of the group
  * A query that sees nothing (padding, an empty sequence) gives zeros and an
- * lse of -inf, and no mass.  Scores, sums and weights of a sum are fp32; the
- * operands of the matrix products are fp16: queries in two parts (2^-22), for
- * fp32 storage the weights too, for bf16 storage one part (2^-11 of a weight).
+ * lse of -inf, and no mass.  A query with a NaN or an infinity has NaN for out,
+ * lse and the mass of what it sees, as has one that sees a key block whose range
+ * is NaN; a value block's NaN range reaches out alone.  Queries that see nothing
+ * of such a block are not touched by it.  Scores, sums and weights of a sum are fp32; the operands
+ * of the matrix products are fp16: queries in two parts (2^-22), in one (2^-11)
+ * for bf16 storage with more than 48 rows a KV head and neither lse nor mass;
+ * weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
  * The order of sums depends on the shape and the lengths only (deterministic).
  * The workspace belongs to one call at a time.  Asynchronous on stream.
  */
@@ -466,7 +470,9 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
  * Every block that receives a row is encoded again from its raw rows: gauge
  * (fp32 fmaf chains, any built group), range over the rows that are there,
  * codes as in cg_encode.  Codes of rows behind the last are left as they were.
- * The rows must continue the sequence (or rewrite rows of its last block).
+ * The rows must continue the sequence, or begin at one of its last block's rows;
+ * they are its last: rows behind them in their last block are taken as not
+ * there, also where lengths reaches past starts + n_new.
  */
 int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec, int32_t layer,
               int32_t n_new, const void *k_new, const void *v_new, int64_t batch_stride,
