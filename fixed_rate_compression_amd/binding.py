@@ -42,6 +42,7 @@ class CgShape(ctypes.Structure):
 
 
 class CgGauge(ctypes.Structure):
+    _keep = None    # the tensor G points into (make_gauge)
     _fields_ = [("group", ctypes.c_int32), ("G", ctypes.c_void_p)]
 
 
@@ -67,6 +68,7 @@ class CgStats(ctypes.Structure):
 
 
 class CgAttn(ctypes.Structure):
+    _keep = ()      # the tensors lengths and starts point into (make_attn)
     _fields_ = [("layer", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("n_queries", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("lengths", ctypes.c_void_p),
                 ("starts", ctypes.c_void_p), ("q_batch_stride", ctypes.c_int64),
@@ -396,6 +398,21 @@ def _sized(name, t, dtype, count):
     return t.data_ptr()
 
 
+def _here(*arrays):
+    """Kernels run on the current GPU: arrays elsewhere are refused before a launch."""
+    cur = None
+    for t in arrays:
+        if t is None or isinstance(t, int):
+            continue
+        if isinstance(t, np.ndarray) or not t.is_cuda:
+            raise ValueError("device tensors are needed, got one in host memory")
+        if cur is None:
+            import torch
+            cur = torch.cuda.current_device()
+        if t.device.index != cur:
+            raise ValueError(f"a tensor is on GPU {t.device.index}, the current one is {cur}")
+
+
 def _storage(shape):
     return "bfloat16" if shape.dtype == CG_DTYPE_BF16 else "float32"
 
@@ -434,8 +451,10 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
         if rows and ((batch > 1 and sb != (attn.q_batch_stride or n * heads * d)) or
                      (n > 1 and sn != (attn.q_token_stride or heads * d)) or (heads > 1 and sh != d) or sd != 1):
             raise ValueError(f"q of strides {q.stride()} does not lie as attn says")
+        _here(q)
         q = q.data_ptr()
     blk = codec.block_tokens
+    _here(out, payload, meta, lse, mass, workspace, gauge._keep, *attn._keep)
     rc = lib().cg_attend(
         shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, attn, q,
         _sized("out", out, st, rows * d), _sized("lse", lse, "float32", rows),
@@ -463,6 +482,7 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
             raise ValueError(f"{name}: rows of an expanded tensor")
         bs, rs = (sb if shape.batch > 1 else 0), (sr if n_new > 1 else 0)
         ptrs.append(t.data_ptr())
+    _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
     _check("cg_append", lib().cg_append(
         ctypes.byref(shape), ctypes.byref(gauge), ctypes.byref(codec), layer, n_new, *ptrs, bs, rs,
         _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
@@ -476,6 +496,7 @@ def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape,
     heads = shape.layers * shape.batch * shape.heads
     nblk, nout = (s.token_capacity // codec.block_tokens if codec.block_tokens > 0 else 0
                   for s in (shape, out_shape))
+    _here(mass, payload, meta, payload_out, meta_out, mass_out, kept, lengths_out, lengths)
     _check("cg_evict", lib().cg_evict(
         ctypes.byref(shape), ctypes.byref(codec), budget, sink, recent,
         _sized("mass", mass, "float32", heads * nblk), _ptr(payload), _nbytes(payload), _ptr(meta),

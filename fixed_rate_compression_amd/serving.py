@@ -10,7 +10,7 @@ One step of a decoder, the same for prompts, chunks of them and single tokens:
         o = cache.attend(layer, q)      # q, o [batch, n, q_heads, 128]
 
 begin(n, valid) takes right-padded rows: sequence b gets the first valid[b] of
-them.  Sequences have their own lengths, on the device; nothing here waits for
+them (the host's bound of the lengths counts all n).  Sequences have their own lengths, on the device; nothing here waits for
 it, so a step may be recorded into a graph and replayed (the host's bound of the
 lengths, which refuses a step that cannot fit, does not see replays: rows past
 the capacity are dropped).
@@ -71,7 +71,8 @@ class ServingCache:
         if out is None:
             out = torch.empty(q.shape, dtype=self.dtype, device=q.device)
         at = cg.make_attn(layer, self.q_heads, self.n, self.shape.head_dim ** -0.5 if scale is None else scale, causal,
-                          self.lengths, self.starts, (q.stride(0), q.stride(1)))
+                          self.lengths, self.starts,
+                          tuple(q.stride(d) if q.shape[d] > 1 else 0 for d in (0, 1)))   # of one row: any
         ws = self._work.get(self.n)
         if ws is None:
             need = cg.cg_attend_workspace_bytes(self.shape, self.gauge, self.codec, at, self.mass is not None)

@@ -177,3 +177,20 @@ def test_binding_checks_types_and_sizes():
         with pytest.raises(ValueError):
             cg.cg_evict(sh, co, 2, 0, 1, a["mass"], pay, meta, sh, pay.clone(), meta.clone(), a["wo"], a["kept"],
                         a["lo"], ln.clone(), stream=0)
+
+
+def test_host_tensors_are_refused():
+    """A tensor in host memory never reaches a kernel."""
+    import torch
+
+    sh, co, g = shape(), codec(), cg.make_gauge(0)
+    pay, meta = torch.zeros(16 * 64 * 128, dtype=torch.uint8), torch.zeros(16 * 2 * 2)
+    q = torch.zeros((2, 1, 4, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="host memory"):
+        cg.cg_attend(sh, pay, meta, g, co, attn(), q, torch.zeros_like(q), stream=0)
+    k, tail = torch.zeros((2, 1, 2, 128), dtype=torch.bfloat16), torch.zeros(2 * 2 * 2 * 2 * 32 * 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="host memory"):
+        cg.cg_append(sh, g, co, 0, 1, k, k, tail, pay, meta, stream=0)
+    mass, kept, ln = torch.zeros((2, 2, 2, 2)), torch.zeros((2, 2, 2, 1), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="host memory"):
+        cg.cg_evict(sh, co, 1, 0, 1, mass, pay, meta, sh, pay, meta, mass, kept, ln, stream=0)
