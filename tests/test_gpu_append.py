@@ -157,3 +157,21 @@ def test_captured_append():
         g.replay()
     t.cuda.synchronize()
     f.check()
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_new_rows_are_the_last(block):
+    """Rows of the last block are written again; lengths past the new rows' end bring none back."""
+    f = Filled(99 + block, [41, 35], block=block)
+    t = torch()
+    old = t.randn(f.x.shape, device="cuda").to(f.x.dtype)
+    f.put(old[0], old[1], 41, [41, 41], [0, 0])
+    f.put(f.x[0, :, :32], f.x[1, :, :32], 32, [32, 32], [0, 0])
+    new = t.stack([f.x[:, 0, 32:35], f.x[:, 1, 32:35]], 1)     # positions 32 .. 34 of both
+    f.put(new[0], new[1], 3, [41, 39], [32, 32])
+    pay, meta = f.pay.clone(), f.meta.clone()
+    f.put(new[0], new[1], 3, [35, 35], [32, 32])
+    assert t.equal(pay, f.pay) and t.equal(meta, f.meta)
+    f.pay[:, :, :, :, 35:] = FILL
+    f.meta[:, :, :, :, 35 // block + 1:] = 5.0
+    f.check(lengths=[35, 35])
