@@ -25,11 +25,13 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Splits of the few-row form.  256 compute units hold `kResident` of its
 // workgroups at once (three on each; two where block sums are gathered: more
 // registers).  A round of them takes about 6 us for what does not depend on the
-// tokens, plus each workgroup's tokens at its share of 5.5 TB/s, at best 10 ns a
-// token; a merge takes about 4.5 us.  The splits are the most that some number of
-// rounds holds, with at least 256 tokens (two units a wave) to a workgroup: 80
-// KV heads of 3000 tokens, 9 splits (one round) 16 us, 10 splits 23; 131072
-// tokens with sums 54 us by 512 workgroups, 66 by 768.
+// tokens, plus each workgroup's tokens at its share of 5.5 TB/s, at best 12.5 ns a
+// token; a merge takes about 4.5 us.  Of one split and the most that one, two,
+// three or four rounds hold the fastest by that sum is taken, with at least 256
+// tokens (two units a wave) to a workgroup.  80 KV heads of 3000 tokens: 9 splits
+// (one round) 19 us, 10 splits 24; 200 heads of 4000 tokens: one split 55 us, 3
+// splits and merge 49; 800 heads: 171 and 162; 300 heads of 8000 tokens: one split
+// 121, 2 splits 130; 131072 tokens with sums by 512 workgroups 54 us, by 768 66.
 constexpr int64_t kResident = 768, kResidentSums = 512, kMinTokens = 256;
 
 int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
@@ -41,10 +43,12 @@ int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
     if (sp > most) sp = most;
     if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
     if (sp < 1) sp = 1;
-    const int64_t groups = work * sp, rounds = (groups + resident - 1) / resident;
-    const double busy = groups < resident ? (double)groups / resident : 1.0;
-    const double share = resident * 256.0 / 5.5e6 * busy, token_us = share > 0.010 ? share : 0.010;
-    const double us = rounds * (6.0 + (double)tokens / sp * token_us) + (sp > 1 ? 4.5 : 0.0);
+    // whole rounds, then what is left, at its share of the bandwidth
+    const int64_t groups = work * sp, full = groups / resident, rest = groups % resident;
+    const double each = (double)tokens / sp, whole = resident * 256.0 / 5.5e6;
+    const double part = whole * rest / resident;
+    const double us = full * (6.0 + each * (whole > 0.0125 ? whole : 0.0125)) +
+                      (rest ? 6.0 + each * (part > 0.0125 ? part : 0.0125) : 0.0) + (sp > 1 ? 4.5 : 0.0);
     if (k == 0 || us < best_us) {
       best = sp;
       best_us = us;

@@ -156,6 +156,16 @@ def test_long_and_split(n, R):
     check(c, c.run())
 
 
+def test_more_workgroups_than_are_resident():
+    """522 row tiles of few rows, split all the same: 5742 rows are merged by sixteens
+    and the blocks' weights finished apart."""
+    rng = np.random.default_rng(545)
+    lengths = rng.integers(1, 700, 58).tolist()
+    lengths[7] = 2500
+    c = Case(545, B=58, H=3, R=11, n=3, T=2500, lengths=lengths).device()
+    check(c, c.run())
+
+
 def test_offsets_past_32_bits():
     """The second of two layers of a cache of more than 2^32 bytes."""
     t = torch()
