@@ -81,12 +81,14 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
     if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
     if (sp < 1) sp = 1;
   }
-  // Short histories: eight waves to a workgroup in place of splits and their
-  // merge.  8 KV heads x 4 query heads, one sequence of 512 / 1024 / 2048
-  // tokens: 9.0 / 10.9 / 16.4 us, with splits 12.2 / 12.2 / 12.5; 32 sequences of
-  // 1024: 15.6 and 23.2; 16 of 2048: 18.3 and 22.7.
+  // Short histories: eight waves to a workgroup, one to a compute unit, in place
+  // of splits and their merge.  8 KV heads x 4 query heads, one sequence of 512
+  // tokens: 9.3 us, by four waves 10.0; of 1000 and 2048: 11.7 and 16.4, with
+  // splits 12.2 and 12.5; 16 sequences of 2048: 19.2 and 20.4; 32 of 1024 and of
+  // 2048: 16.4 and 29.1, by four waves 17.7 and 33.1; 40 of 1024, past one to a
+  // unit: 25.7 and 21.0.
   p.waves = 4;
-  if (p.few && sp > 1 && s->tokens <= (fields >= 128 ? 2048 : 1024)) {
+  if (p.few && work <= 256 && s->tokens > kMinTokens && s->tokens <= (work >= 128 ? 2048 : 1024)) {
     p.waves = 8;
     sp = 1;
   }
