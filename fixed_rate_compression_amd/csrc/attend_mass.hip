@@ -3,6 +3,9 @@
 // that the attention left.  No row's state is carried, so the work splits over
 // tokens and rows alike; a workgroup's share of a block's sum goes to a slot of
 // its own and the slots are added in order (no atomics: the same bits every time).
+// Bound like the attention by matrix and vector work that hardly overlap: two
+// products and an exponential a score.  2048 queries x 4 heads over 8192 tokens of 8
+// KV heads 265 us, two prompts to 1000 tokens 34 us and 4.6 to add the slots.
 #include "attend.hpp"
 
 namespace cga {

@@ -21,6 +21,12 @@
 // unlike steps keep 11 significant bits each.  The largest weight lies between
 // 2^9 and 2^15: below 2^-14 a weight is rounded to multiples of 2^-24, which
 // is 2^-33 of the largest.
+//
+// 262144 tokens of 8 KV heads: 95 us, 5.6 TB/s of the 5.97 that a plain sum of the
+// same bytes reaches, the codes read once.  16 sequences to 8192 tokens 26 us (4.6 TB/s:
+// the longest end last), with block sums 8 sequences to 16384 37 us (3.8 TB/s: two
+// workgroups a compute unit for the registers, three spill and take 42), one
+// sequence of 1000 tokens 11.7 us, all of it latency.
 #include "attend.hpp"
 
 namespace cga {

@@ -14,6 +14,12 @@
 // The running maximum is not looked for: a lane's sum of weights tells whether
 // one of them has outgrown its scale, and only then (and where a row sees its
 // first token) the scores are formed again and the maximum raised.
+//
+// 2048 queries x 4 heads over 8192 tokens of 8 KV heads: the whole call 271 us,
+// 888 TFLOP/s; the matrix cores work 40 % of the cycles and the vector units 48 %,
+// hardly at once.  Two prompts to 1000 tokens with both query parts: 48 us, the last
+// rows' workgroups, which see all tokens, on their own at the end.  Value stores
+// free of the bank conflicts they have (8 bytes of two rows a thread) changed nothing.
 #include <type_traits>
 
 #include "attend.hpp"
