@@ -57,8 +57,29 @@ int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
   return best;
 }
 
-// 128-row tiles: two workgroups fit a compute unit
+// Splits of 128-row tiles.  A workgroup takes 24 ns a token on a compute unit of
+// its own and 36 beside another (512 at once), after about 6 us; a merge moves
+// every split's sums twice (5 us and 4.5 TB/s).  8 KV heads x 4 query heads, a
+// prompt of 300 / 500 / 1000 tokens: 14.6 / 19.4 / 32.2 us, in two splits 18.3 /
+// 22.5 / 36.9; 512 queries over 2048 and 8192 tokens: 54 and 191 us, in two splits 42
+// and 117, in four 40 and 100; 1024 over 8192: 206 and in two 175.
 constexpr int64_t kTargetTiles = 512;
+
+int64_t tile_splits(int64_t work, int64_t rows, int64_t tokens) {
+  const int64_t most = (tokens + kMinTokens - 1) / kMinTokens;
+  int64_t best = 1;
+  double best_us = 0.0;
+  for (int64_t sp = 1; sp == 1 || (sp <= most && work * sp <= kTargetTiles && sp <= cga::MERGE_SPLITS); sp *= 2) {
+    const double each = (double)tokens / sp * (work * sp <= kTargetTiles / 2 ? 0.024 : 0.036);
+    const double us = 6.0 + each + (sp > 1 ? 5.0 + (double)rows * sp * cga::D * 4 / 4.5e6 : 0.0);
+    if (sp == 1 || us < best_us) {
+      best = sp;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
 // weights of many rows: four workgroups to a compute unit, four row steps at least to
 // each (prompts of 2 x 1000 tokens, 1 x 2000: 34 and 49 us; half as many 36 and 65,
 // twice as many 39)
@@ -77,11 +98,7 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   if (work > 0 && p.few) {
     sp = few_splits(work, s->tokens, mass ? kResidentSums : kResident);
   } else if (work > 0) {
-    const int64_t most = (s->tokens + kMinTokens - 1) / kMinTokens;
-    sp = kTargetTiles / work;
-    if (sp > most) sp = most;
-    if (sp > cga::MERGE_SPLITS) sp = cga::MERGE_SPLITS;
-    if (sp < 1) sp = 1;
+    sp = tile_splits(work, fields * p.rows, s->tokens);
   }
   // Short histories: eight waves to a workgroup, one to a compute unit, in place
   // of splits and their merge.  8 KV heads x 4 query heads, one sequence of 512
