@@ -81,7 +81,9 @@ class ServingCache:
         return out
 
     def evict(self, budget, sink=1, recent=1):
-        """Keep `budget` blocks of every (layer, sequence, head), in place; -> the kept blocks' former numbers."""
+        """Keep `budget` blocks of every (layer, sequence, head), in place; -> the kept blocks' former numbers.
+
+        Between steps: the rows' positions change, so the present step ends here."""
         import torch
 
         if self.mass is None:
@@ -91,4 +93,5 @@ class ServingCache:
         cg.cg_evict(s, self.codec, budget, sink, recent, self.mass, self.payload, self.meta, s, self.payload, self.meta,
                     self.mass, kept, self.lengths, self.lengths)
         self.most = min(self.most, budget * self.codec.block_tokens)
+        self.n = 0
         return kept

@@ -188,3 +188,25 @@ def test_refusals():
         c.begin(1)
     with pytest.raises(ValueError):
         c.evict(1)
+
+
+def test_an_eviction_ends_the_step():
+    """Positions change: rows of the step before are refused, the next step goes on."""
+    t = torch()
+    c = ServingCache(1, 1, 1, 2, 64, cg.make_gauge(0), 16, with_mass=True)
+    k = t.ones((1, 40, 1, D), dtype=t.bfloat16, device="cuda")
+    q = t.ones((1, 40, 2, D), dtype=t.bfloat16, device="cuda")
+    c.begin(40)
+    c.append(0, k, k)
+    c.attend(0, q)
+    c.evict(2)
+    assert c.lengths.tolist() == [24]
+    with pytest.raises(ValueError):
+        c.append(0, k, k)
+    with pytest.raises(ValueError):
+        c.attend(0, q)
+    with pytest.raises(ValueError):
+        c.begin(40)                # the host's bound: a sequence of 32 rows would have kept them all
+    c.begin(32)
+    c.append(0, k[:, :32], k[:, :32])
+    assert bool((c.attend(0, q[:, :32]) == 1).all()) and c.lengths.tolist() == [56]
