@@ -413,6 +413,13 @@ def _here(*arrays):
             raise ValueError(f"a tensor is on GPU {t.device.index}, the current one is {cur}")
 
 
+def _gauge_sized(gauge, shape):
+    """The gauge's tensor holds what the C call reads of it."""
+    G, need = gauge._keep, shape.layers * 2 * shape.heads * shape.head_dim * gauge.group
+    if hasattr(G, "numel") and (G.dtype != _dtype("float32") or G.numel() < need):
+        raise ValueError(f"gauge: {need} values of float32 are needed, got {G.numel()} of {G.dtype}")
+
+
 def _storage(shape):
     return "bfloat16" if shape.dtype == CG_DTYPE_BF16 else "float32"
 
@@ -451,12 +458,14 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
         if rows and ((batch > 1 and sb != (attn.q_batch_stride or n * heads * d)) or
                      (n > 1 and sn != (attn.q_token_stride or heads * d)) or (heads > 1 and sh != d) or sd != 1):
             raise ValueError(f"q of strides {q.stride()} does not lie as attn says")
-        _here(q)
-        q = q.data_ptr()
     blk = codec.block_tokens
-    _here(out, payload, meta, lse, mass, workspace, gauge._keep, *attn._keep)
+    _gauge_sized(gauge, shape)
+    for name, t in zip(("lengths", "starts"), attn._keep):
+        _sized(name, t, "int32", batch)
+    _here(q, out, payload, meta, lse, mass, workspace, gauge._keep, *attn._keep)
     rc = lib().cg_attend(
-        shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, attn, q,
+        shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, attn,
+        q if isinstance(q, int) else q.data_ptr(),
         _sized("out", out, st, rows * d), _sized("lse", lse, "float32", rows),
         _sized("mass", mass, "float32", shape.layers * batch * shape.heads * (shape.token_capacity // blk if blk > 0 else 0)),
         _ptr(workspace), _nbytes(workspace), _stream(stream))
@@ -482,6 +491,7 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
             raise ValueError(f"{name}: rows of an expanded tensor")
         bs, rs = (sb if shape.batch > 1 else 0), (sr if n_new > 1 else 0)
         ptrs.append(t.data_ptr())
+    _gauge_sized(gauge, shape)
     _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
     _check("cg_append", lib().cg_append(
         ctypes.byref(shape), ctypes.byref(gauge), ctypes.byref(codec), layer, n_new, *ptrs, bs, rs,

@@ -194,3 +194,23 @@ def test_host_tensors_are_refused():
     mass, kept, ln = torch.zeros((2, 2, 2, 2)), torch.zeros((2, 2, 2, 1), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="host memory"):
         cg.cg_evict(sh, co, 1, 0, 1, mass, pay, meta, sh, pay, meta, mass, kept, ln, stream=0)
+
+
+def test_small_arrays_are_refused():
+    """Lengths, starts and gauges that hold less than a call reads of them."""
+    import torch
+
+    sh, co = shape(), codec()
+    pay, meta = torch.zeros(16 * 64 * 128, dtype=torch.uint8), torch.zeros(16 * 2 * 2)
+    q = torch.zeros((2, 1, 4, 128), dtype=torch.bfloat16)
+    one, g = torch.zeros(1, dtype=torch.int32), cg.make_gauge(0)
+    for kw in (dict(lengths=one), dict(starts=one)):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            cg.cg_attend(sh, pay, meta, g, co, cg.make_attn(0, 4, 1, 0.1, **kw), q, torch.zeros_like(q), stream=0)
+    k, tail = torch.zeros((2, 1, 2, 128), dtype=torch.bfloat16), torch.zeros(2 * 2 * 2 * 2 * 32 * 128, dtype=torch.bfloat16)
+    for G in (torch.zeros(2 * 2 * 2 * 128 * 16 - 1), torch.zeros(2 * 2 * 2 * 128 * 16, dtype=torch.float64)):
+        g = cg.make_gauge(16, G)
+        with pytest.raises(ValueError, match="gauge"):
+            cg.cg_attend(sh, pay, meta, g, co, cg.make_attn(0, 4, 1, 0.1), q, torch.zeros_like(q), stream=0)
+        with pytest.raises(ValueError, match="gauge"):
+            cg.cg_append(sh, g, co, 0, 1, k, k, tail, pay, meta, stream=0)
