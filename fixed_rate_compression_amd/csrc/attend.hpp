@@ -55,14 +55,14 @@ struct AttendArgs {
   float2 *part_ml;               // [b][h][split][rows] (maximum, sum of weights)
   float2 *bsum;                  // [b][h][entry][rows] (block sum, its maximum)
   float *lse2;                   // [b][h][rows] log2 of the row's sum (many rows with mass)
-  float *mpart;                  // [part][b][h][nblk] parts of the blocks' weights (many rows)
   uint4 *qfrag;                  // [b][h][tile][hi/lo][step][lane] fp16 query operands
   float2 *qrow;                  // [b][h][16 tiles] (score factor, minimum factor)
   int64_t tcap, tokens, nblk;
   int64_t q_bs, q_ts;            // query strides (elements)
   int64_t entries;               // block-sum entries of a field
   int32_t batch, heads, ratio, n, rows, tiles;  // rows = n ratio, tiles = ceil(rows / 16)
-  int32_t g, bshift, causal, splits, mparts;
+  int32_t n_all, first;          // queries of the call, the first of these n (q, out and lse point at it)
+  int32_t g, bshift, causal, splits, few;
   int32_t waves;  // of a few-row workgroup: 4 or 8
   float c;                       // scale log2(e)
 };
@@ -74,10 +74,9 @@ hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // after one that lays the gauged queries out (qfrag, qrow)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
-// block weights: few rows from the attention's block sums, many rows from a
-// second pass over the keys with the rows' sums known
+// block weights from the attention's block sums, of few rows and of many
 hipError_t mass_finish_launch(const AttendArgs &a, hipStream_t s);
-hipError_t mass_many_launch(const AttendArgs &a, hipStream_t s);
+hipError_t mass_rows_launch(const AttendArgs &a, hipStream_t s);
 
 // ---------------------------------------------------------------------------
 // device pieces
@@ -156,7 +155,7 @@ __device__ __forceinline__ float row_max(float v) {
   return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 
-// a sequence's length and the position of its first query, loaded once
+// a sequence's length and the position of the first of these queries, loaded once
 struct Sequence {
   int len;
   int64_t start;
@@ -167,7 +166,7 @@ __device__ __forceinline__ Sequence load_sequence(const AttendArgs &a, int b) {
   const int32_t n = *(a.lengths ? a.lengths + b : any), p = *(a.starts ? a.starts + b : any);
   Sequence s;
   s.len = a.lengths ? (int)min(max((int64_t)n, (int64_t)0), a.tokens) : (int)a.tokens;
-  s.start = a.starts ? (int64_t)p : (int64_t)s.len - a.n;
+  s.start = (a.starts ? (int64_t)p : (int64_t)s.len - a.n_all) + a.first;
   return s;
 }
 
@@ -366,7 +365,7 @@ __device__ __forceinline__ void make_frags(const float *xs, float c, int s0, Que
 template <bool BF16>
 __device__ __forceinline__ void store_out(const AttendArgs &a, int b, int h, int r, int c, float v) {
   const int i = r / a.ratio, j = r - i * a.ratio;
-  const int64_t off = (((int64_t)b * a.n + i) * a.heads * a.ratio + h * a.ratio + j) * D + c;
+  const int64_t off = (((int64_t)b * a.n_all + i) * a.heads * a.ratio + h * a.ratio + j) * D + c;
   if (BF16) ((uint16_t *)a.out)[off] = (uint16_t)cgk::bf16_rne(v);
   else ((float *)a.out)[off] = v;
 }
@@ -379,7 +378,7 @@ __device__ __forceinline__ void store_rows(const AttendArgs &a, int b, int h, in
     const float *y = ys + (x >> 4) * PITCH + c;
     const f4_t lo = *(const f4_t *)y, hi = *(const f4_t *)(y + 4);
     const int i = (int)((uint32_t)r / (uint32_t)a.ratio), j = r - i * a.ratio;
-    const int64_t off = (((int64_t)b * a.n + i) * a.heads * a.ratio + h * a.ratio + j) * D + c;
+    const int64_t off = (((int64_t)b * a.n_all + i) * a.heads * a.ratio + h * a.ratio + j) * D + c;
     if (BF16) {
       *(uint4 *)((uint16_t *)a.out + off) = make_uint4(cgk::pack_bf16x2(lo[0], lo[1]), cgk::pack_bf16x2(lo[2], lo[3]),
                                                        cgk::pack_bf16x2(hi[0], hi[1]), cgk::pack_bf16x2(hi[2], hi[3]));
@@ -393,7 +392,7 @@ __device__ __forceinline__ void store_rows(const AttendArgs &a, int b, int h, in
 __device__ __forceinline__ void store_lse(const AttendArgs &a, int b, int h, int r, float m, float l) {
   const int i = r / a.ratio, j = r - i * a.ratio;
   // natural logarithm of the row's sum of exp(score); a NaN stays one
-  a.lse[((int64_t)b * a.n + i) * a.heads * a.ratio + h * a.ratio + j] =
+  a.lse[((int64_t)b * a.n_all + i) * a.heads * a.ratio + h * a.ratio + j] =
       l != 0.0f ? (m + __builtin_log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 

@@ -13,11 +13,12 @@ using cgh::error;
 
 struct Plan {
   int64_t rows, tiles;
-  int splits, mparts, waves;
+  int n;  // queries of a sequence that are taken at once
+  int splits, waves;
   bool few;  // few row tiles: block sums come with the attention
   int64_t entries;
-  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, mpart_bytes, qfrag_bytes, qrow_bytes;
-  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + mpart_bytes + qfrag_bytes + qrow_bytes; }
+  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, qfrag_bytes, qrow_bytes;
+  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + qfrag_bytes + qrow_bytes; }
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -80,19 +81,28 @@ int64_t tile_splits(int64_t work, int64_t rows, int64_t tokens) {
   return best;
 }
 
-// weights of many rows: four workgroups to a compute unit, four row steps at least to
-// each (prompts of 2 x 1000 tokens, 1 x 2000: 34 and 49 us; half as many 36 and 65,
-// twice as many 39)
-constexpr int64_t kTargetMass = 1024;
+// Block weights of many rows need 8 bytes a row and 32 tokens of the capacity.
+// Where that would pass 1 GiB the queries are taken in turn, 128 rows a KV head
+// at least.
+constexpr uint64_t kMaxSums = (uint64_t)1 << 30;
 
 Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {
   Plan p{};
-  p.rows = (int64_t)t->n_queries * (t->q_heads / s->heads);
+  const int64_t fields = (int64_t)s->batch * s->heads, ratio = t->q_heads / s->heads;
+  const int64_t nblk = s->token_capacity / c->block_tokens;
+  p.entries = c->block_tokens == 64 ? 2 * nblk : nblk;
+  p.n = t->n_queries;
+  if (mass && p.n * ratio > (int64_t)cga::FEW_TILES * cga::ROWS) {
+    int64_t rows = p.entries ? (int64_t)(kMaxSums / 8) / (fields * p.entries) : p.n * ratio;
+    if (rows < 128) rows = 128;
+    const int64_t each = rows < ratio ? 1 : rows / ratio, turns = (p.n + each - 1) / each;
+    p.n = (int)((p.n + turns - 1) / turns);
+  }
+  p.rows = p.n * ratio;
   p.tiles = (p.rows + cga::ROWS - 1) / cga::ROWS;
   // 8 sequences x 8 KV heads x 4096 tokens with 32, 48 and 64 rows a head: 25, 27
   // and 43 us by row tiles of 16, by tiles of 128 and their layout 34, 35 and 37
   p.few = p.tiles <= cga::FEW_TILES;
-  const int64_t fields = (int64_t)s->batch * s->heads;
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
   int64_t sp = 1;
   if (work > 0 && p.few) {
@@ -112,21 +122,12 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
     sp = 1;
   }
   p.splits = (int)sp;
-  const int64_t nblk = s->token_capacity / c->block_tokens;
-  p.entries = c->block_tokens == 64 ? 2 * nblk : nblk;
   const bool parts = p.splits > 1;
   p.o_bytes = parts ? up256((size_t)(fields * p.splits * p.rows) * cga::D * 4) : 0;
   p.ml_bytes = parts || (mass && p.few) ? up256((size_t)(fields * p.splits * p.rows) * 8) : 0;
-  if (mass && p.few) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
+  if (mass) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
   if (!p.few) {
-    if (mass) {  // 256 tokens and a part of the rows to a workgroup
-      const int64_t groups = fields * ((s->tokens + 255) / 256), steps = (p.rows + 31) / 32;
-      int64_t mp = groups > 0 ? (kTargetMass + groups - 1) / groups : 1;
-      if (mp > (steps + 3) / 4) mp = (steps + 3) / 4;
-      p.mparts = (int)mp;
-      p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
-      p.mpart_bytes = up256((size_t)(mp * fields * nblk) * 4);
-    }
+    if (mass) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
     p.qfrag_bytes = up256((size_t)(fields * p.tiles) * 8 * 64 * 16);
     p.qrow_bytes = up256((size_t)(fields * p.tiles) * cga::ROWS * 8);
   }
@@ -153,7 +154,7 @@ int check_attn(const cg_shape *s, const cg_attn *t) {
   if (rows > (int64_t)1 << 26 || (int64_t)s->batch * s->heads > (int64_t)1 << 22 ||
       (rows + 15) / 16 * s->batch * s->heads > (int64_t)1 << 27)
     return error(CG_E_SHAPE, "too many query rows");
-  if ((int64_t)s->batch * s->heads * ((s->token_capacity + 31) / 32) > (int64_t)1 << 31)
+  if ((int64_t)s->batch * s->heads * ((s->token_capacity + 15) / 16) >= (int64_t)1 << 31)
     return error(CG_E_SHAPE, "too many tokens for one launch");
   return CG_OK;
 }
@@ -194,7 +195,8 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   const int64_t ts = attn->q_token_stride ? attn->q_token_stride : token;
   const int64_t bs = attn->q_batch_stride ? attn->q_batch_stride : token * attn->n_queries;
   const char *q0 = (const char *)q, *o0 = (const char *)out;
-  const int64_t qb = ((shape->batch - 1) * bs + (attn->n_queries - 1) * ts + token) * esz;
+  const int64_t qb = (int64_t)cgh::reach(shape->batch, bs, attn->n_queries, ts, token) * esz;
+  if (!qb) return error(CG_E_INVAL, "query strides reach too far");
   const int64_t ob = (int64_t)shape->batch * attn->n_queries * token * esz;
   if (q0 < o0 + ob && o0 < q0 + qb) return error(CG_E_INVAL, "q and out overlap");
   const Plan p = make_plan(shape, codec, attn, mass != nullptr);
@@ -216,21 +218,17 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.g = gauge->group;
   a.gk = gauge->group ? gauge->G + (int64_t)attn->layer * 2 * shape->heads * d * gauge->group : nullptr;
   a.gv = gauge->group ? a.gk + (int64_t)shape->heads * d * gauge->group : nullptr;
-  a.q = q;
-  a.out = out;
-  a.lse = lse;
   a.mass = mass ? mass + (int64_t)attn->layer * fields * a.nblk : nullptr;
   a.q_bs = bs;
   a.q_ts = ts;
   a.batch = shape->batch;
   a.heads = shape->heads;
   a.ratio = attn->q_heads / shape->heads;
-  a.n = attn->n_queries;
-  a.rows = (int32_t)p.rows;
-  a.tiles = (int32_t)p.tiles;
+  a.n_all = attn->n_queries;
   a.bshift = codec->block_tokens == 16 ? 4 : codec->block_tokens == 32 ? 5 : 6;
   a.causal = attn->causal;
   a.splits = p.splits;
+  a.few = p.few;
   a.waves = p.waves;
   a.entries = p.entries;
   a.c = (float)((double)attn->scale * 1.4426950408889634074);
@@ -240,21 +238,28 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.part_ml = (float2 *)take(p.ml_bytes);
   a.bsum = (float2 *)take(p.bsum_bytes);
   a.lse2 = (float *)take(p.lse2_bytes);
-  a.mpart = (float *)take(p.mpart_bytes);
-  a.mparts = p.mparts;
   a.qfrag = (uint4 *)take(p.qfrag_bytes);
   a.qrow = (float2 *)take(p.qrow_bytes);
 
   const bool bf16 = shape->dtype == CG_DTYPE_BF16;
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
-  if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
-  if (p.splits > 1 && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
-    return cgh::hip_error(e, "cg_attend merge launch");
-  if (mass && shape->tokens > 0) {
-    // with splits, the merge of few rows has finished the weights
-    e = !p.few ? cga::mass_many_launch(a, st) : p.splits > 1 ? hipSuccess : cga::mass_finish_launch(a, st);
-    if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
+  for (int32_t first = 0; first < attn->n_queries; first += p.n) {
+    a.first = first;
+    a.n = attn->n_queries - first < p.n ? attn->n_queries - first : p.n;
+    a.rows = a.n * a.ratio;
+    a.tiles = (a.rows + cga::ROWS - 1) / cga::ROWS;
+    a.q = (const char *)q + (int64_t)first * ts * esz;
+    a.out = (char *)out + (int64_t)first * token * esz;
+    a.lse = lse ? lse + (int64_t)first * attn->q_heads : nullptr;
+    hipError_t e = p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
+    if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
+    if (p.splits > 1 && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
+      return cgh::hip_error(e, "cg_attend merge launch");
+    if (mass && shape->tokens > 0) {
+      // with splits, the merge of few rows has finished the weights
+      e = !p.few ? cga::mass_rows_launch(a, st) : p.splits > 1 ? hipSuccess : cga::mass_finish_launch(a, st);
+      if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
+    }
   }
   return CG_OK;
 }

@@ -551,7 +551,7 @@ hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
 
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const int64_t fields = (int64_t)a.batch * a.heads;
-  const bool mass = a.mass && a.bsum && a.tokens > 0;
+  const bool mass = a.mass && a.bsum && a.tokens > 0 && a.few;
   const dim3 block(NTH);
   // a workgroup a row while they fit the machine twice over (1024 rows of 64
   // splits: 8.6 us, by sixteens 58), else sixteen rows (9600 rows of 3: 13 and 26)

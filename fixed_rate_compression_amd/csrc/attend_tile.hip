@@ -18,7 +18,8 @@
 // 2048 queries x 4 heads over 8192 tokens of 8 KV heads: the whole call 271 us,
 // 888 TFLOP/s; the matrix cores work 40 % of the cycles and the vector units 48 %,
 // hardly at once.  Two prompts to 1000 tokens with both query parts: 48 us, the last
-// rows' workgroups, which see all tokens, on their own at the end.  Value stores
+// rows' workgroups, which see all tokens, on their own at the end; keeping every
+// row's sum of every unit for the blocks' weights adds 1.5 us.  Value stores
 // free of the bank conflicts they have (8 bytes of two rows a thread) changed nothing.
 #include <type_traits>
 
@@ -286,10 +287,25 @@ __device__ __forceinline__ void unit_values(const unsigned char *vb, const UnitO
     }
 }
 
+// a row's sum of a unit's weights and the maximum it stands on, for the blocks' weights
+template <int NB>
+__device__ __forceinline__ void store_sums(const AttendArgs &a, int bh, int un, int wr, int half,
+                                           const UnitWeights<NB> &o, float mu) {
+  const int64_t e = (int64_t)un * NB;
+  float2 *p = a.bsum + ((int64_t)bh * a.entries + e) * a.rows + wr;
+#pragma unroll
+  for (int u = 0; u < NB; u++) {
+    const uint32_t x = __float_as_uint(o.ps[u]);
+    const auto y = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    const float v = __uint_as_float(y[0]) + __uint_as_float(y[1]);
+    if (half == 0 && wr < a.rows && (u == 0 || e + u < a.entries)) p[(int64_t)u * a.rows] = make_float2(v, mu);
+  }
+}
+
 // LO: the queries' second fp16 part takes part (fp32 storage, or where log-sums
 // or weights are asked for); else a query is rounded to 2^-11 of a channel.
-// NB: ranges to a unit of 32 tokens.
-template <bool BF16, bool LO, int NB>
+// NB: ranges to a unit of 32 tokens.  SUMS: the rows' sums of every unit are kept.
+template <bool BF16, bool LO, int NB, bool SUMS>
 __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   static_assert(BF16 || LO, "fp32 storage takes both parts");
   constexpr int LOOP_LDS = LOBUF + (LO ? 4 * 8192 : 0), END_LDS = TROWS * PITCH * 4;
@@ -368,6 +384,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
     fetch_unit(a, kf, vf, km, vm, u0 + 2, nx);
     __syncthreads();
     raise<LO, NB>(keys_at(u0), lo, ranges_at(u0), q, lim - u0 * UNIT - 4 * half, st, acc, o);
+    if constexpr (SUMS) store_sums<NB>(a, bh, u0, wr, half, o, st.mu);
     const auto turn = [&](int un, auto masked) {
       __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
       put_unit<LO>(lds, un + 2, tmax, nx);
@@ -380,6 +397,7 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
       unit_values<BF16>(values_at(un), P, acc);
       const bool up = unit_weights<decltype(masked)::value, NB>(mt, q, z, vis, st, o);
       if (__any(up)) raise<LO, NB>(keys_at(un + 1), lo, mt, q, vis, st, acc, o);
+      if constexpr (SUMS) store_sums<NB>(a, bh, un + 1, wr, half, o, st.mu);
     };
     // units that every row of the wave sees whole, then the others
     const int ua = min(u1 - 1, max(all / UNIT - 1, u0));
@@ -470,18 +488,19 @@ hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const int64_t groups = (a.rows + TROWS - 1) / TROWS;
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * groups * a.splits)), block(NTH);
   const dim3 pre((unsigned)((int64_t)a.batch * a.heads * ((a.tiles + 3) / 4)));
-  const bool two = a.bshift == 4;  // ranges to a unit
-#define CG_T(BF, LO)                                                                           \
-  {                                                                                            \
+#define CG_T(BF, LO, NB, SUMS)                                                                 \
+  if (bf16 == BF && lo == LO && nb == NB && sums == SUMS) {                                    \
     hipLaunchKernelGGL((k_attend_prepare<BF, LO>), pre, block, 0, s, a);                       \
-    if (two) hipLaunchKernelGGL((k_attend_tile<BF, LO, 2>), grid, block, 0, s, a);             \
-    else hipLaunchKernelGGL((k_attend_tile<BF, LO, 1>), grid, block, 0, s, a);                 \
+    hipLaunchKernelGGL((k_attend_tile<BF, LO, NB, SUMS>), grid, block, 0, s, a);               \
+    return hipGetLastError();                                                                  \
   }
-  if (!bf16) CG_T(false, true)
-  else if (a.lse || a.mass) CG_T(true, true)
-  else CG_T(true, false)
+  const bool lo = !bf16 || a.lse || a.mass, sums = a.bsum != nullptr;
+  const int nb = a.bshift == 4 ? 2 : 1;  // ranges to a unit
+  CG_T(true, false, 1, false) CG_T(true, false, 2, false)
+  CG_T(true, true, 1, false) CG_T(true, true, 2, false) CG_T(false, true, 1, false) CG_T(false, true, 2, false)
+  CG_T(true, true, 1, true) CG_T(true, true, 2, true) CG_T(false, true, 1, true) CG_T(false, true, 2, true)
 #undef CG_T
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 }  // namespace cga

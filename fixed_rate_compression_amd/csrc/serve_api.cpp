@@ -45,7 +45,8 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
   const int64_t tiles = ((int64_t)n_new + codec->block_tokens - 1 + 63) / 64;
   if (fields * tiles >= (int64_t)1 << 31) return error(CG_E_SHAPE, "too many rows for one launch");
   const uint64_t esz = shape->dtype == CG_DTYPE_BF16 ? 2 : 4;
-  const uint64_t in = (uint64_t)((shape->batch - 1) * bs + (n_new - 1) * rs + row) * esz;
+  const uint64_t in = cgh::reach(shape->batch, bs, n_new, rs, row) * esz;
+  if (!in) return error(CG_E_INVAL, "row strides reach too far");
   const uint64_t tb = (uint64_t)fields * codec->block_tokens * shape->head_dim * esz;
   char *t0 = (char *)tail + (uint64_t)layer * tb;
   if (overlap(k_new, in, t0, tb) || overlap(v_new, in, t0, tb))

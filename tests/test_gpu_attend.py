@@ -187,6 +187,32 @@ def test_offsets_past_32_bits():
     assert np.all(np.abs(m - ref["mass"]) <= ref["mass_tol"]) and not mass[0].any() and not mass[1, :, :, 16:].any()
 
 
+@pytest.mark.parametrize("T,n,block,causal,bf16", [(500, 150, 32, True, True), (500, 150, 64, False, True),
+                                                   (3001, 131, 16, True, False)])
+def test_block_weights_of_queries_taken_in_turn(T, n, block, causal, bf16):
+    """A capacity at which the rows' sums would pass 1 GiB: the queries go in turn, some of
+    them padding before the first position or behind the last."""
+    t = torch()
+    B, H, R, cap = 2, 4, 4, 1 << 20
+    used = -(-T // block) * block
+    c = Case(555 + n, B=B, H=H, R=R, n=n, T=T, cap=used, block=block, bf16=bf16, lengths=[T, 77], starts=[T - n + 3, -60],
+             causal=causal)
+    ref = c.reference()
+    c.device()
+    big = t.zeros((1, 2, B, H, cap, D), dtype=t.uint8, device="cuda")
+    meta = t.zeros((1, 2, B, H, cap // block, 2), device="cuda")
+    big[:, :, :, :, :used] = c.payd
+    meta[:, :, :, :, :used // block] = c.metad
+    c.payd, c.metad, c.cap = big, meta, cap
+    c.shape = cg.make_shape(1, 2, B, H, T, cap, D, cg.CG_DTYPE_BF16 if bf16 else cg.CG_DTYPE_F32)
+    need = cg.cg_attend_workspace_bytes(c.shape, c.gauge, c.codec, c.attn(), True)
+    assert need < 2 ** 30 < B * H * R * n * (cap // min(block, 32)) * 8
+    out, lse, mass = c.run()
+    check(c, (out, lse, None), ref)
+    m = to_host(mass).astype(np.float64)[0]
+    assert np.all(np.abs(m[..., :used // block] - ref["mass"]) <= ref["mass_tol"]) and not m[..., used // block:].any()
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_mass_accumulates_and_repeats_bit_for_bit(n):
     t = torch()

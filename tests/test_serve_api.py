@@ -214,3 +214,11 @@ def test_small_arrays_are_refused():
             cg.cg_attend(sh, pay, meta, g, co, cg.make_attn(0, 4, 1, 0.1), q, torch.zeros_like(q), stream=0)
         with pytest.raises(ValueError, match="gauge"):
             cg.cg_append(sh, g, co, 0, 1, k, k, tail, pay, meta, stream=0)
+
+
+def test_strides_that_reach_too_far_are_refused():
+    far = 1 << 40
+    assert attend(at=attn(n_queries=1 << 21, q_token_stride=far)) == cg.CG_E_INVAL
+    r = ctypes.byref
+    assert cg.lib().cg_append(r(shape()), r(cg.make_gauge(0)), r(codec()), 0, 1 << 21, P, P, 0, far, None, None, FAR, P,
+                              FAR, P, FAR, None) == cg.CG_E_INVAL
