@@ -36,7 +36,7 @@ using cgk::D;
 using cgk::PITCH;
 
 constexpr int ROWS = 16;  // query rows of a row tile (one matrix-core operand)
-constexpr int FEW_TILES = 3;  // at most of the few-row form
+constexpr int FEW_TILES = 4;  // at most of the few-row form
 constexpr int UNIT = 32;  // tokens of a unit of work
 constexpr int NTH = 256;  // threads of a workgroup
 constexpr int MERGE_SPLITS = 1024;  // splits at most
@@ -55,8 +55,6 @@ struct AttendArgs {
   float2 *part_ml;               // [b][h][split][rows] (maximum, sum of weights)
   float2 *bsum;                  // [b][h][entry][rows] (block sum, its maximum)
   float *lse2;                   // [b][h][rows] log2 of the row's sum (many rows with mass)
-  uint4 *qfrag;                  // [b][h][tile][hi/lo][step][lane] fp16 query operands
-  float2 *qrow;                  // [b][h][16 tiles] (score factor, minimum factor)
   int64_t tcap, tokens, nblk;
   int64_t q_bs, q_ts;            // query strides (elements)
   int64_t entries;               // block-sum entries of a field
@@ -70,8 +68,7 @@ struct AttendArgs {
 // rows [0, rows) of every field over its tokens, one workgroup per (field,
 // row tile, split); splits > 1 leaves parts for merge_launch
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
-// the same for many rows, one workgroup per (field, 128 rows, split),
-// after one that lays the gauged queries out (qfrag, qrow)
+// the same for many rows, one workgroup per (field, 128 rows, split)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // block weights from the attention's block sums, of few rows and of many
@@ -304,61 +301,66 @@ __device__ __forceinline__ void gauge_tiles(const float *xs, float *ys, const fl
       for (int j = 0; j < 4; j++) ys[(16 * t + 4 * kr + j) * PITCH + 32 * wave + 16 * nb + n] = acc[t][nb][j];
 }
 
-// The fp16 operands of 16 gauged rows xs [16][PITCH]: lane (row = lane % 16,
-// grp = lane / 16) holds 8 channels of its row at step s: BYTES: 64 (s / 2) +
-// 16 grp + 8 (s % 2) + 0 .. 7, the order in which 16-byte loads of key codes
-// arrive; else 32 s + 8 grp + 0 .. 7.
+// power-of-two factor that puts a row's largest magnitude into [2^13, 2^14), and back
+struct FragScale {
+  float up, un;
+};
+__device__ __forceinline__ FragScale frag_scale(float mx) {
+  const int ex = mx > 0.0f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
+  const int sh = min(max(13 - ex, -100), 100);
+  return FragScale{__uint_as_float((uint32_t)(127 + sh) << 23), __uint_as_float((uint32_t)(127 - sh) << 23)};
+}
+
+// 8 channels u, v of a row as fp16 operands, their sum added to `sum`.  TWO: two
+// fixed-point parts; else one, each channel rounded to 2^-11.
+template <bool TWO>
+__device__ __forceinline__ void frag_parts(f4_t u, f4_t v, float up, h8_t &hi, h8_t &lo, float &sum) {
+  constexpr float H = 1.5f * 134217728.0f, L = 1.5f * 65536.0f;  // x + H - H rounds to multiples of 2^4, L of 2^-7
+  uint32_t wh[4], wl[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const float x = (k < 2 ? u[2 * k] : v[2 * k - 4]) * up, y = (k < 2 ? u[2 * k + 1] : v[2 * k - 3]) * up;
+    if constexpr (TWO) {
+      const float xh = (x + H) - H, yh = (y + H) - H;
+      const float xl = ((x - xh) + L) - L, yl = ((y - yh) + L) - L;
+      wh[k] = pack_f16x2(xh, yh);  // both parts are exact in fp16
+      wl[k] = pack_f16x2(xl, yl);
+      sum += (xh + xl) + (yh + yl);
+    } else {
+      wh[k] = pack_f16x2(x, y);
+      wl[k] = 0u;
+      const f2_t h = unpack_f16x2(wh[k]);
+      sum += h.x + h.y;
+    }
+  }
+  hi = as_h8(wh[0], wh[1], wh[2], wh[3]);
+  lo = as_h8(wl[0], wl[1], wl[2], wl[3]);
+}
+
+// The fp16 operands, step s, of 16 gauged rows xs [16][PITCH]: lane (row = lane %
+// 16, grp = lane / 16) holds channels 64 (s / 2) + 16 grp + 8 (s % 2) + 0 .. 7 of its
+// row, the order in which 16-byte loads of key codes arrive.  cq is this step's
+// part of the minimum's factor.
 struct QueryFrags {
   h8_t hi[4], lo[4];
   float ca, cq;  // score = (sum of q' code) step ca + minimum cq
 };
 
-// TWO: two fixed-point parts; else one fp16 part, each channel rounded to 2^-11.
-// Steps [S0, S0 + NS) only; cq is then their part of it.
-template <bool TWO, bool BYTES, int NS>
-__device__ __forceinline__ void make_frags(const float *xs, float c, int s0, QueryFrags &f) {
+__device__ __forceinline__ void make_frags(const float *xs, float c, int s, h8_t &hi, h8_t &lo, float &ca, float &cq) {
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
   const float *rp = xs + row * PITCH;
   float mx = 0.0f;
 #pragma unroll
-  for (int s = 0; s < 8; s++) {  // the row's largest magnitude, a quarter of the row to a lane
-    const f4_t u = *(const f4_t *)(rp + 32 * grp + 4 * s);
+  for (int k = 0; k < 8; k++) {  // the row's largest magnitude, a quarter of the row to a lane
+    const f4_t u = *(const f4_t *)(rp + 32 * grp + 4 * k);
     mx = fmaxf(fmaxf(mx, fabsf(u[0])), fmaxf(fabsf(u[1]), fmaxf(fabsf(u[2]), fabsf(u[3]))));
   }
-  mx = row_max(mx);
-  // power-of-two factor that puts it into [2^13, 2^14)
-  const int ex = mx > 0.0f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
-  const int sh = min(max(13 - ex, -100), 100);
-  const float up = __uint_as_float((uint32_t)(127 + sh) << 23), un = __uint_as_float((uint32_t)(127 - sh) << 23);
-  constexpr float H = 1.5f * 134217728.0f, L = 1.5f * 65536.0f;  // x + H - H rounds to multiples of 2^4, L of 2^-7
+  const FragScale sc = frag_scale(row_max(mx));
+  const float *p = rp + 64 * (s >> 1) + 16 * grp + 8 * (s & 1);
   float sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < NS; e++) {
-    const int s = s0 + e;
-    const float *p = rp + (BYTES ? 64 * (s >> 1) + 16 * grp + 8 * (s & 1) : 32 * s + 8 * grp);
-    const f4_t u = *(const f4_t *)p, v = *(const f4_t *)(p + 4);
-    uint32_t wh[4], wl[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const float x = (k < 2 ? u[2 * k] : v[2 * k - 4]) * up, y = (k < 2 ? u[2 * k + 1] : v[2 * k - 3]) * up;
-      if constexpr (TWO) {
-        const float xh = (x + H) - H, yh = (y + H) - H;
-        const float xl = ((x - xh) + L) - L, yl = ((y - yh) + L) - L;
-        wh[k] = pack_f16x2(xh, yh);  // both parts are exact in fp16
-        wl[k] = pack_f16x2(xl, yl);
-        sum += (xh + xl) + (yh + yl);
-      } else {
-        wh[k] = pack_f16x2(x, y);
-        wl[k] = 0u;
-        const f2_t h = unpack_f16x2(wh[k]);
-        sum += h.x + h.y;
-      }
-    }
-    f.hi[e] = as_h8(wh[0], wh[1], wh[2], wh[3]);
-    f.lo[e] = as_h8(wl[0], wl[1], wl[2], wl[3]);
-  }
-  f.ca = c * un;
-  f.cq = f.ca * row_sum(sum);
+  frag_parts<true>(*(const f4_t *)p, *(const f4_t *)(p + 4), sc.up, hi, lo, sum);
+  ca = c * sc.un;
+  cq = ca * row_sum(sum);
 }
 
 // one output element (b, query row r of head h, channel c)

@@ -17,8 +17,8 @@ struct Plan {
   int splits, waves;
   bool few;  // few row tiles: block sums come with the attention
   int64_t entries;
-  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes, qfrag_bytes, qrow_bytes;
-  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes + qfrag_bytes + qrow_bytes; }
+  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes;
+  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes; }
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -100,8 +100,9 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   }
   p.rows = p.n * ratio;
   p.tiles = (p.rows + cga::ROWS - 1) / cga::ROWS;
-  // 8 sequences x 8 KV heads x 4096 tokens with 32, 48 and 64 rows a head: 25, 27
-  // and 43 us by row tiles of 16, by tiles of 128 and their layout 34, 35 and 37
+  // 8 KV heads x 4096 tokens with 32, 48 and 64 rows a head: one sequence 14, 17 and 17
+  // us by row tiles of 16, 21, 22 and 23 by tiles of 128 (merges with them), 8
+  // sequences 31, 37 and 45 against 40, 45 and 47
   p.few = p.tiles <= cga::FEW_TILES;
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
   int64_t sp = 1;
@@ -126,11 +127,7 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   p.o_bytes = parts ? up256((size_t)(fields * p.splits * p.rows) * cga::D * 4) : 0;
   p.ml_bytes = parts || (mass && p.few) ? up256((size_t)(fields * p.splits * p.rows) * 8) : 0;
   if (mass) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
-  if (!p.few) {
-    if (mass) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
-    p.qfrag_bytes = up256((size_t)(fields * p.tiles) * 8 * 64 * 16);
-    p.qrow_bytes = up256((size_t)(fields * p.tiles) * cga::ROWS * 8);
-  }
+  if (mass && !p.few) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
   return p;
 }
 
@@ -238,8 +235,6 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.part_ml = (float2 *)take(p.ml_bytes);
   a.bsum = (float2 *)take(p.bsum_bytes);
   a.lse2 = (float *)take(p.lse2_bytes);
-  a.qfrag = (uint4 *)take(p.qfrag_bytes);
-  a.qrow = (float2 *)take(p.qrow_bytes);
 
   const bool bf16 = shape->dtype == CG_DTYPE_BF16;
   hipStream_t st = (hipStream_t)stream;

@@ -1,7 +1,7 @@
-// Attention of few query rows (up to three row tiles of 16) over the 8-bit
+// Attention of few query rows (up to four row tiles of 16) over the 8-bit
 // cache, split along the tokens: the form for single tokens and few drafted
-// ones, bound by the memory traffic of the codes (of which the second and third
-// tile find most in the caches).
+// ones, bound by the memory traffic of the codes (of which the other
+// tiles find most in the caches).
 //
 // A workgroup takes one part of one field pair's tokens for one row tile; its
 // waves (four, or eight where that saves the splits) take the part's 32-token
@@ -147,13 +147,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     unsigned char *fs = (unsigned char *)(lds + 2 * ROWS * PITCH);  // [hi, lo][step][lane]
     float *qs = (float *)(fs + 8192);  // [step][row] parts of the minimum's factor, then the score's factor
     if (front) {
-      QueryFrags one;
-      make_frags<true, true, 1>(ys, a.c, wave, one);
-      *(h8_t *)(fs + wave * 1024 + lane * 16) = one.hi[0];
-      *(h8_t *)(fs + 4096 + wave * 1024 + lane * 16) = one.lo[0];
+      h8_t hi, lo;
+      float ca, cq;
+      make_frags(ys, a.c, wave, hi, lo, ca, cq);
+      *(h8_t *)(fs + wave * 1024 + lane * 16) = hi;
+      *(h8_t *)(fs + 4096 + wave * 1024 + lane * 16) = lo;
       if (grp == 0) {
-        qs[wave * ROWS + row] = one.cq;
-        qs[(4 + wave) * ROWS + row] = one.ca;
+        qs[wave * ROWS + row] = cq;
+        qs[(4 + wave) * ROWS + row] = ca;
       }
     }
     __syncthreads();

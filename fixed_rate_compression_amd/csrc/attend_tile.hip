@@ -2,7 +2,8 @@
 // and drafted tokens, bound by the vector units that make the weights.
 //
 // A workgroup takes 128 query rows of one KV head, 32 to each of its four
-// waves, and walks the tokens 32 at a time: a unit's codes go
+// waves, gauges them in LDS (in a launch of their own, through memory, 13 us for
+// 64000 rows and 5 more here), and walks the tokens 32 at a time: a unit's codes go
 // through registers, are widened to centred fp16 once for the four waves and
 // laid in LDS while another unit is worked on, one barrier a unit.  Widening
 // at the use, from codes in LDS, took 96 of 244 vector instructions a wave
@@ -15,12 +16,12 @@
 // one of them has outgrown its scale, and only then (and where a row sees its
 // first token) the scores are formed again and the maximum raised.
 //
-// 2048 queries x 4 heads over 8192 tokens of 8 KV heads: the whole call 271 us,
-// 888 TFLOP/s; the matrix cores work 40 % of the cycles and the vector units 48 %,
-// hardly at once.  Two prompts to 1000 tokens with both query parts: 48 us, the last
-// rows' workgroups, which see all tokens, on their own at the end; keeping every
-// row's sum of every unit for the blocks' weights adds 1.5 us.  Value stores
-// free of the bank conflicts they have (8 bytes of two rows a thread) changed nothing.
+// 2048 queries x 4 heads over 8192 tokens of 8 KV heads: the whole call 270 us,
+// 891 TFLOP/s; the matrix cores work 40 % of the cycles and the vector units 48 %,
+// hardly at once.  Two prompts to 1000 tokens with both query parts and every row's
+// sum of every unit kept for the blocks' weights (1.5 us): 55 us, the last rows'
+// workgroups, which see all tokens, on their own at the end.  Value stores free of
+// the bank conflicts they have (8 bytes of two rows a thread) changed nothing.
 #include <type_traits>
 
 #include "attend.hpp"
@@ -92,6 +93,27 @@ struct TileQueries {
   h8_t hi[8];
   float ca, cq;
 };
+
+// The fp16 operands of a wave's 32 gauged rows xs [32][PITCH]: the scale and the two
+// fixed-point parts of make_frags, or one part (a channel rounded to 2^-11).
+template <bool TWO>
+__device__ __forceinline__ void tile_queries(const float *xs, float c, TileQueries &q, h8_t (&lo)[8]) {
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const float *rp = xs + (lane & 31) * PITCH + 8 * half;
+  f4_t x[16];
+  float mx = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; k++) {
+    x[k] = *(const f4_t *)(rp + 16 * (k >> 1) + 4 * (k & 1));
+    mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x[k][0]), fabsf(x[k][1]))), fmaxf(fabsf(x[k][2]), fabsf(x[k][3])));
+  }
+  const FragScale sc = frag_scale(fmaxf(mx, __shfl_xor(mx, 32)));
+  float sum = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 8; s++) frag_parts<TWO>(x[2 * s], x[2 * s + 1], sc.up, q.hi[s], lo[s], sum);
+  q.ca = c * sc.un;
+  q.cq = q.ca * (sum + __shfl_xor(sum, 32));
+}
 
 // the weights of a unit, p_t sv_b f, and what goes with them; NB ranges to a
 // unit (two where blocks have 16 tokens).  The values' factor is added to the
@@ -333,22 +355,32 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   UnitRegs nx;
   if (u0 < u1) fetch_unit(a, kf, vf, km, vm, u0, nx);
 
-  // gauged queries as operands (a wave past the last row tile takes the last one's)
+  // gauged queries as operands
   TileQueries q;
-  const unsigned char *lo = lds + LOBUF + wave * 8192 + lane * 16;
+  unsigned char *const lo = lds + LOBUF + wave * 8192 + lane * 16;
   const int wr = r0 + wave * WROWS + row;  // the lane's row
   {
-    const int64_t tile = (int64_t)bh * a.tiles + min(wr >> 4, a.tiles - 1);
-    const uint4 *f = a.qfrag + tile * 8 * 64;
-    const float2 x = a.qrow[tile * ROWS + n];
-    q.ca = x.x * (LO ? kCentredUnit : kCodeUnit);
-    q.cq = x.y;
+    float *xs = (float *)lds;
+    const float *gk = a.gk + (int64_t)h * D * a.g;
+    GaugeFrag gw;
+    load_gauge<false>(gk, a.g, 0, gw);
+    RowPart p[TROWS / ROWS];
 #pragma unroll
-    for (int s = 0; s < 8; s++) {
-      const int c = 2 * s + half, at = (c >> 2) * 64 + (c & 3) * 16 + n;  // the 8 channels from 8 c on
-      q.hi[s] = __builtin_bit_cast(h8_t, f[at]);
-      if constexpr (LO) *(uint4 *)(lds + LOBUF + wave * 8192 + s * 1024 + lane * 16) = f[4 * 64 + at];
+    for (int t = 0; t < TROWS / ROWS; t++) p[t] = load_row_part<BF16>(a, b, h, r0 + t * ROWS);
+#pragma unroll
+    for (int t = 0; t < TROWS / ROWS; t++) put_row_part(xs + t * ROWS * PITCH, p[t]);
+    __syncthreads();
+    if (a.g) {
+      gauge_tiles<false, TROWS / ROWS, true>(xs, xs, gk, a.g, gw);
+      __syncthreads();
     }
+    h8_t part[8];
+    tile_queries<LO>(xs + wave * WROWS * PITCH, a.c, q, part);
+    __syncthreads();  // the rows have been read
+    q.ca *= LO ? kCentredUnit : kCodeUnit;
+    if constexpr (LO)
+#pragma unroll
+      for (int s = 0; s < 8; s++) *(h8_t *)(lo + s * 1024) = part[s];
   }
   // what the row sees; rows that are not there see everything
   const int lim = wr < a.rows ? query_limit(a, sq, (int)((uint32_t)wr / (uint32_t)a.ratio)) : tmax;
@@ -450,47 +482,11 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   store_rows<BF16>(a, b, h, r0, nr, us);
 }
 
-// One workgroup per four row tiles: gauge, split into the operands' parts and
-// store in operand order, with each row's factors.
-template <bool BF16, bool LO>
-__global__ __launch_bounds__(NTH) void k_attend_prepare(const AttendArgs a) {
-  __shared__ __align__(16) float xs[4 * ROWS * PITCH];
-  const uint32_t quads = (uint32_t)(a.tiles + 3) / 4, id = blockIdx.x;
-  const int bh = (int)(id / quads), tile0 = (int)(id - bh * quads) * 4;
-  const int h = bh % a.heads, b = bh / a.heads;
-  const float *gk = a.gk + (int64_t)h * D * a.g;
-  GaugeFrag gw;
-  load_gauge<false>(gk, a.g, 0, gw);
-  RowPart p[4];
-#pragma unroll
-  for (int t = 0; t < 4; t++) p[t] = load_row_part<BF16>(a, b, h, (tile0 + t) * ROWS);
-#pragma unroll
-  for (int t = 0; t < 4; t++) put_row_part(xs + t * ROWS * PITCH, p[t]);
-  __syncthreads();
-  if (a.g) {
-    gauge_tiles<false, 4, true>(xs, xs, gk, a.g, gw);
-    __syncthreads();
-  }
-  const int lane = threadIdx.x & 63, tile = tile0 + (int)(threadIdx.x >> 6);
-  if (tile >= a.tiles) return;
-  QueryFrags q;
-  make_frags<LO, false, 4>(xs + (threadIdx.x >> 6) * ROWS * PITCH, a.c, 0, q);
-  uint4 *d = a.qfrag + ((int64_t)bh * a.tiles + tile) * 8 * 64 + lane;
-#pragma unroll
-  for (int s = 0; s < 4; s++) {
-    d[s * 64] = __builtin_bit_cast(uint4, q.hi[s]);
-    if constexpr (LO) d[(4 + s) * 64] = __builtin_bit_cast(uint4, q.lo[s]);
-  }
-  if (lane < ROWS) a.qrow[((int64_t)bh * a.tiles + tile) * ROWS + lane] = make_float2(q.ca, q.cq);
-}
-
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const int64_t groups = (a.rows + TROWS - 1) / TROWS;
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * groups * a.splits)), block(NTH);
-  const dim3 pre((unsigned)((int64_t)a.batch * a.heads * ((a.tiles + 3) / 4)));
 #define CG_T(BF, LO, NB, SUMS)                                                                 \
   if (bf16 == BF && lo == LO && nb == NB && sums == SUMS) {                                    \
-    hipLaunchKernelGGL((k_attend_prepare<BF, LO>), pre, block, 0, s, a);                       \
     hipLaunchKernelGGL((k_attend_tile<BF, LO, NB, SUMS>), grid, block, 0, s, a);               \
     return hipGetLastError();                                                                  \
   }
