@@ -394,9 +394,31 @@ __device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
 
 __global__ __launch_bounds__(NTH) void k_mass_finish(const AttendArgs a) { finish_mass(a, blockIdx.x); }
 
+// sum / maximum over a wave's 64 lanes, without LDS
+template <int N>
+__device__ __forceinline__ float ror16(float v) {  // from the lane N further round in its 16
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += ror16<8>(v);
+  v += ror16<4>(v);
+  v += ror16<2>(v);
+  v += ror16<1>(v);
+  return row_sum(v);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, ror16<8>(v));
+  v = fmaxf(v, ror16<4>(v));
+  v = fmaxf(v, ror16<2>(v));
+  v = fmaxf(v, ror16<1>(v));
+  return row_max(v);
+}
+
 // Joins the splits of one row, a workgroup to a row: 2^(m_s - M) of every
 // split, eight groups of 32 lanes adding every eighth split's sums, then the
-// inverse gauge.  For few rows with many splits; workgroups past the last row
+// inverse gauge.  Up to 64 splits each wave forms all factors for itself, beside
+// the loads of the sums: 32 rows of 32 splits 4.0 us, through LDS and two more
+// barriers 5.0; 3200 rows of 3 splits 8.5 and 10.0.  For few rows with many splits; workgroups past the last row
 // finish the blocks' weights (MASS), which need no more than the rows do.
 template <bool BF16, bool MASS>
 __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
@@ -417,41 +439,58 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r;
   const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r) * D;
   const int S = a.splits, t = threadIdx.x;
-  // this thread's part of G_V, on its way while the sums are joined
-  // (the two halves of the workgroup take half of a channel's chain each)
+  const int lane = t & 63, grp = t >> 5, c4 = 4 * (t & 31);
+  // on their way first, in the order of their use: the splits' maxima and sums, the
+  // first rows of sums, this thread's part of G_V (the two halves of the
+  // workgroup take half of a channel's chain each)
+  constexpr int HEAD = 4;
+  float2 ml = make_float2(-INFINITY, 0.0f);
+  f4_t head[HEAD];
+  if (S <= 64) {
+    if (lane < S) ml = pm[(int64_t)lane * a.rows];
+#pragma unroll
+    for (int k = 0; k < HEAD; k++)
+      head[k] = grp + 8 * k < S ? *(const f4_t *)(po + (int64_t)(grp + 8 * k) * a.rows * D + c4) : f4_t{0.f, 0.f, 0.f, 0.f};
+  }
   const int c = t & (D - 1), cg = c & (a.g - 1), gh = a.g >> 1, k0 = (t >> 7) * gh;
   const float *gp = a.gv + (int64_t)h * D * a.g + (int64_t)(c - cg) * a.g + (int64_t)k0 * a.g + cg;
   float gw[16];
 #pragma unroll
   for (int k = 0; k < 16; k++) gw[k] = k < gh ? gp[(int64_t)k * a.g] : 0.0f;
-  float M = -INFINITY;
-  for (int s = t; s < S; s += NTH) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
+  float M = -INFINITY, L = 0.0f;
+  f4_t u = f4_t{0.f, 0.f, 0.f, 0.f};
+  if (S <= 64) {
+    M = wave_max(ml.x);
+    const float w = ml.x > -INFINITY ? exp2_fast(ml.x - M) : 0.0f;
+    L = wave_sum(ml.y * w);
 #pragma unroll
-  for (int k = 32; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor(M, k));
-  if ((t & 63) == 0) red[t >> 6].x = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
-  float L = 0.0f;
-  for (int s = t; s < S; s += NTH) {
-    const float2 x = pm[(int64_t)s * a.rows];
-    const float k = x.x > -INFINITY ? exp2_fast(x.x - M) : 0.0f;
-    wt[s] = k;
-    L += x.y * k;
-  }
+    for (int k = 0; k < HEAD; k++) u += head[k] * __shfl(w, grp + 8 * k);
 #pragma unroll
-  for (int k = 32; k >= 1; k >>= 1) L += __shfl_xor(L, k);
-  if ((t & 63) == 0) red[t >> 6].y = L;
-  __syncthreads();
-  L = (red[0].y + red[1].y) + (red[2].y + red[3].y);
-  const int grp = t >> 5, c4 = 4 * (t & 31);
-  float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = HEAD; k < 8; k++) {
+      if (8 * k >= S) break;
+      const float f = __shfl(w, grp + 8 * k);
+      if (grp + 8 * k < S) u += *(const f4_t *)(po + (int64_t)(grp + 8 * k) * a.rows * D + c4) * f;
+    }
+  } else {
+    for (int s = t; s < S; s += NTH) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
+    M = wave_max(M);
+    if (lane == 0) red[t >> 6].x = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
+    for (int s = t; s < S; s += NTH) {
+      const float2 x = pm[(int64_t)s * a.rows];
+      const float k = x.x > -INFINITY ? exp2_fast(x.x - M) : 0.0f;
+      wt[s] = k;
+      L += x.y * k;
+    }
+    L = wave_sum(L);
+    if (lane == 0) red[t >> 6].y = L;
+    __syncthreads();
+    L = (red[0].y + red[1].y) + (red[2].y + red[3].y);
 #pragma unroll 4
-  for (int s = grp; s < S; s += 8) {
-    const float k = wt[s];
-    const float4 x = *(const float4 *)(po + (int64_t)s * a.rows * D + c4);
-    u.x += x.x * k; u.y += x.y * k; u.z += x.z * k; u.w += x.w * k;
+    for (int s = grp; s < S; s += 8) u += *(const f4_t *)(po + (int64_t)s * a.rows * D + c4) * wt[s];
   }
-  *(float4 *)&part[grp][c4] = u;
+  *(f4_t *)&part[grp][c4] = u;
   __syncthreads();
   if (t == 0) {
     if (a.lse) store_lse(a, b, h, r, M, L);
