@@ -53,6 +53,7 @@ struct AttendArgs {
   float *mass;                   // the layer's [b][h][nblk] or null
   float *part_o;                 // [b][h][split][rows][128] sums of a split
   float2 *part_ml;               // [b][h][split][rows] (maximum, sum of weights)
+  int2 *dealt;                   // [b] (first slot, slots) of sequences of unlike lengths
   float2 *bsum;                  // [b][h][entry][rows] (block sum, its maximum)
   float *lse2;                   // [b][h][rows] log2 of the row's sum (many rows with mass)
   int64_t tcap, tokens, nblk;
@@ -62,6 +63,7 @@ struct AttendArgs {
   int32_t n_all, first;          // queries of the call, the first of these n (q, out and lse point at it)
   int32_t g, bshift, causal, splits, few;
   int32_t waves;  // of a few-row workgroup: 4 or 8
+  int32_t ragged, slots, least;  // few rows of sequences of unlike lengths: see Slot
   float c;                       // scale log2(e)
 };
 
@@ -165,6 +167,53 @@ __device__ __forceinline__ Sequence load_sequence(const AttendArgs &a, int b) {
   s.len = a.lengths ? (int)min(max((int64_t)n, (int64_t)0), a.tokens) : (int)a.tokens;
   s.start = (a.starts ? (int64_t)p : (int64_t)s.len - a.n_all) + a.first;
   return s;
+}
+
+// Few rows of sequences of unlike lengths: `slots` workgroups a head and row tile are
+// dealt to the sequences by their lengths, a sequence of u units has max(ceil(u / t),
+// 1) of them.  t is the first of five growing sizes (at least `least`) with which they
+// suffice: ceil(sum u / (slots - k batch / 4)), k = 0 .. 4; with the last, the
+// sum of u / t + 1 over the sequences is no more than slots.  Equal lengths take the
+// first, a whole number of slots each.  Parts are laid out by slot, [head][slot][rows].
+struct Slot {
+  int b, first, count;  // sequence (batch: none), its first slot and how many it has
+};
+
+// sum over the lanes up to this one
+template <int N>
+__device__ __forceinline__ int shr16(int v) {  // from the lane N before it in its 16, else 0
+  return __builtin_amdgcn_update_dpp(0, v, 0x110 + N, 0xf, 0xf, true);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v += shr16<1>(v);
+  v += shr16<2>(v);
+  v += shr16<4>(v);
+  v += shr16<8>(v);
+  const int lane = threadIdx.x & 63;
+  const int s0 = __builtin_amdgcn_readlane(v, 15), s1 = __builtin_amdgcn_readlane(v, 31), s2 = __builtin_amdgcn_readlane(v, 47);
+  return v + (lane >= 16 ? s0 : 0) + (lane >= 32 ? s1 : 0) + (lane >= 48 ? s2 : 0);
+}
+
+// the sequence that slot j belongs to; a wave's lanes are the sequences (at most 64,
+// with fewer than 2^31 units in all)
+__device__ __forceinline__ Slot find_slot(const AttendArgs &a, int j) {
+  const int lane = threadIdx.x & 63;
+  const bool there = lane < a.batch;
+  const int len = there ? a.lengths[lane] : 0;
+  const uint32_t u = there ? (uint32_t)((min(max((int64_t)len, (int64_t)0), a.tokens) + UNIT - 1) / UNIT) : 0u;
+  const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)u), 63);
+  int n, end;
+  for (int k = 0; k < 5; k++) {
+    const uint32_t shares = (uint32_t)(a.slots - k * a.batch / 4);
+    const uint32_t t = max((sum + (shares - 1)) / shares, (uint32_t)a.least);
+    n = there ? max((int)((u + t - 1) / t), 1) : 0;
+    end = wave_scan(n);  // slots up to this sequence's last
+    if (__builtin_amdgcn_readlane(end, 63) <= a.slots) break;
+  }
+  const int l = __popcll(__ballot(end <= j));
+  if (l >= a.batch) return Slot{a.batch, 0, 0};
+  const int count = __builtin_amdgcn_readlane(n, l);
+  return Slot{l, __builtin_amdgcn_readlane(end, l) - count, count};
 }
 
 // tokens query i sees: none unless it stands inside the sequence

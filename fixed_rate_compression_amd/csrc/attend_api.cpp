@@ -14,11 +14,12 @@ using cgh::error;
 struct Plan {
   int64_t rows, tiles;
   int n;  // queries of a sequence that are taken at once
-  int splits, waves;
+  int splits, waves, ragged, slots, least;
+  bool merge;
   bool few;  // few row tiles: block sums come with the attention
   int64_t entries;
-  size_t o_bytes, ml_bytes, bsum_bytes, lse2_bytes;
-  size_t total() const { return o_bytes + ml_bytes + bsum_bytes + lse2_bytes; }
+  size_t o_bytes, ml_bytes, dealt_bytes, bsum_bytes, lse2_bytes;
+  size_t total() const { return o_bytes + ml_bytes + dealt_bytes + bsum_bytes + lse2_bytes; }
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -123,9 +124,22 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
     sp = 1;
   }
   p.splits = (int)sp;
-  const bool parts = p.splits > 1;
-  p.o_bytes = parts ? up256((size_t)(fields * p.splits * p.rows) * cga::D * 4) : 0;
-  p.ml_bytes = parts || (mass && p.few) ? up256((size_t)(fields * p.splits * p.rows) * 8) : 0;
+  // Sequences of unlike lengths: splits dealt by length (see Slot), with one split
+  // half as many more for the longest.  8 KV heads, 8 sequences of 0 .. 16384 tokens
+  // with sums 31 us, equal splits 37; 16 of 0 .. 8192 23 and 26 (all of 8192: 53 and 51);
+  // 32 sequences of 2000 tokens but one of 131072: the whole call 72 and 428; 64 of
+  // 16000 in one split each, with a merge that finds nothing to do: 390 and 389.
+  p.ragged = p.few && p.waves == 4 && t->lengths && s->batch > 1 && s->batch <= 64 &&
+             s->tokens > (p.splits > 1 ? 2048 : 16384) && s->tokens < (int64_t)1 << 30;
+  const int64_t slots = (int64_t)s->batch * p.splits + (p.ragged && p.splits == 1 ? s->batch / 2 : 0);
+  p.slots = (int)slots;
+  p.least = (int)((s->tokens + cga::UNIT - 1) / cga::UNIT / cga::MERGE_SPLITS + 1);
+  if (p.least < kMinTokens / cga::UNIT) p.least = kMinTokens / cga::UNIT;
+  const int64_t parts = slots * s->heads * p.rows;
+  p.merge = p.splits > 1 || p.ragged;
+  p.o_bytes = p.merge ? up256((size_t)parts * cga::D * 4) : 0;
+  p.ml_bytes = p.merge || (mass && p.few) ? up256((size_t)parts * 8) : 0;
+  if (p.ragged) p.dealt_bytes = up256((size_t)s->batch * 8);
   if (mass) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
   if (mass && !p.few) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
   return p;
@@ -226,6 +240,9 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.causal = attn->causal;
   a.splits = p.splits;
   a.few = p.few;
+  a.ragged = p.ragged;
+  a.slots = p.slots;
+  a.least = p.least;
   a.waves = p.waves;
   a.entries = p.entries;
   a.c = (float)((double)attn->scale * 1.4426950408889634074);
@@ -233,6 +250,7 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   auto take = [&w](size_t n) { char *r = n ? w : nullptr; w += n; return r; };
   a.part_o = (float *)take(p.o_bytes);
   a.part_ml = (float2 *)take(p.ml_bytes);
+  a.dealt = (int2 *)take(p.dealt_bytes);
   a.bsum = (float2 *)take(p.bsum_bytes);
   a.lse2 = (float *)take(p.lse2_bytes);
 
@@ -248,11 +266,11 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
     a.lse = lse ? lse + (int64_t)first * attn->q_heads : nullptr;
     hipError_t e = p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
     if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
-    if (p.splits > 1 && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
+    if (p.merge && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
       return cgh::hip_error(e, "cg_attend merge launch");
     if (mass && shape->tokens > 0) {
-      // with splits, the merge of few rows has finished the weights
-      e = !p.few ? cga::mass_rows_launch(a, st) : p.splits > 1 ? hipSuccess : cga::mass_finish_launch(a, st);
+      // the merge of few rows has finished the weights
+      e = !p.few ? cga::mass_rows_launch(a, st) : p.merge ? hipSuccess : cga::mass_finish_launch(a, st);
       if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
     }
   }

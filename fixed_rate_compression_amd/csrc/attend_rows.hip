@@ -23,10 +23,10 @@
 // is 2^-33 of the largest.
 //
 // 262144 tokens of 8 KV heads: 95 us, 5.6 TB/s of the 5.97 that a plain sum of the
-// same bytes reaches, the codes read once.  16 sequences to 8192 tokens 26 us (4.6 TB/s:
-// the longest end last), with block sums 8 sequences to 16384 37 us (3.8 TB/s: two
-// workgroups a compute unit for the registers, three spill and take 42), one
-// sequence of 1000 tokens 11.7 us, all of it latency.
+// same bytes reaches, the codes read once.  16 sequences of 0 .. 8192 tokens 23 us
+// (5.2 TB/s), with block sums 8 sequences of 0 .. 16384 31 us (4.5 TB/s: two
+// workgroups a compute unit for the registers, three spill), one sequence of 1000
+// tokens 11.7 us, all of it latency.
 #include "attend.hpp"
 
 namespace cga {
@@ -100,11 +100,30 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
   const int lane = threadIdx.x & 63, row = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // 32-bit divisions: a 64-bit one takes longer than a unit of work
-  const uint32_t id = blockIdx.x, q1 = id / (uint32_t)a.splits;
-  const int split = (int)(id - q1 * a.splits);
-  const int bh = a.tiles == 1 ? (int)q1 : (int)(q1 / (uint32_t)a.tiles);
-  const int tile = (int)q1 - bh * a.tiles;
-  const int b = (int)((uint32_t)bh / (uint32_t)a.heads), h = bh - b * a.heads;
+  const uint32_t id = blockIdx.x;
+  int b, h, tile, split, splits;
+  int64_t part;  // where this part's row 0 goes
+  if (a.ragged) {  // row tiles of a slot and head on one XCD where the heads are a multiple of 8
+    const uint32_t q1 = id / (uint32_t)a.heads, q2 = q1 / (uint32_t)a.tiles;
+    h = (int)(id - q1 * a.heads);
+    tile = (int)(q1 - q2 * a.tiles);
+    const Slot sl = find_slot(a, (int)q2);
+    if (sl.b >= a.batch) return;
+    b = __builtin_amdgcn_readfirstlane(sl.b);
+    split = __builtin_amdgcn_readfirstlane((int)q2 - sl.first);
+    splits = __builtin_amdgcn_readfirstlane(sl.count);
+    part = ((int64_t)h * a.slots + (int)q2) * a.rows;
+  } else {
+    const uint32_t q1 = id / (uint32_t)a.splits;
+    split = (int)(id - q1 * a.splits);
+    splits = a.splits;
+    const int f = a.tiles == 1 ? (int)q1 : (int)(q1 / (uint32_t)a.tiles);
+    tile = (int)q1 - f * a.tiles;
+    b = (int)((uint32_t)f / (uint32_t)a.heads);
+    h = f - b * a.heads;
+    part = ((int64_t)f * a.splits + split) * a.rows;
+  }
+  const int bh = b * a.heads + h;
   const int r0 = tile * ROWS, nr = min(ROWS, a.rows - r0);
   // on their way first: what does not wait for the sequence's length
   const float *gk = a.gk + (int64_t)h * D * a.g;
@@ -118,7 +137,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
   const Sequence sq = load_sequence(a, b);
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
-  const int u0 = split_begin(units, split, a.splits), u1 = split_begin(units, split + 1, a.splits);
+  const int u0 = split_begin(units, split, splits), u1 = split_begin(units, split + 1, splits);
 
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
@@ -290,7 +309,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
   }
 
   const float *gv = a.gv + (int64_t)h * D * a.g;
-  if (a.splits == 1 && front) load_gauge<true>(gv, a.g, 0, gw);
+  if (splits == 1 && front) load_gauge<true>(gv, a.g, 0, gw);
   // join the waves: each leaves its sums relative to its own maximum
   __syncthreads();  // the operands have been read
   const float l = row_sum(st.l), mv = row_sum(st.mv);
@@ -309,6 +328,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     }
   }
   __syncthreads();
+  // for the merge (a store before the loop turns its scalar loads into vector ones)
+  if (a.ragged && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0)
+    a.dealt[b] = make_int2((int)(id / (uint32_t)(a.heads * a.tiles)), splits);
   for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * NW) {  // also rows that are not there: none is left undefined
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
     float M = -INFINITY;
@@ -323,18 +345,18 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
       L += w.y * f;
       v += *(const f4_t *)(lds + (k * ROWS + r) * PITCH + c) * f;
     }
-    const int64_t pr = ((int64_t)bh * a.splits + split) * a.rows + r0 + r;
+    const int64_t pr = part + r0 + r;
     if (c == 0 && r < nr) {
       if (a.part_ml) a.part_ml[pr] = make_float2(M, L);
-      if (a.splits == 1 && a.lse) store_lse(a, b, h, r0 + r, M, L);
+      if (splits == 1 && a.lse) store_lse(a, b, h, r0 + r, M, L);
     }
-    if (a.splits > 1) {
+    if (splits > 1) {
       if (r < nr) *(f4_t *)(a.part_o + pr * D + c) = v;
     } else {
       *(f4_t *)(lds + r * PITCH + c) = v * (L > 0.0f ? 1.0f / L : 0.0f);  // this thread alone reads these channels of row r
     }
   }
-  if (a.splits > 1) return;
+  if (splits > 1) return;
   __syncthreads();
   float *os = lds;
   if (a.g) {
@@ -343,6 +365,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     __syncthreads();
   }
   if (front) store_rows<BF16>(a, b, h, r0, nr, os);
+}
+
+// the parts of (b, h): the first one's number and how many there are
+struct Parts {
+  int64_t first;
+  int count;
+};
+__device__ __forceinline__ Parts parts_of(const AttendArgs &a, int b, int h) {
+  if (!a.ragged) return Parts{((int64_t)b * a.heads + h) * a.splits, a.splits};
+  const int2 x = a.dealt[b];
+  return Parts{(int64_t)h * a.slots + x.x, x.y};
 }
 
 // Block weights of few rows from the sums the attention left, 256 blocks to a
@@ -355,10 +388,11 @@ __device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
   const int64_t blk = (int64_t)(id - bh * chunks) * NTH + threadIdx.x;
   const Sequence sq = load_sequence(a, b);
   const int j = threadIdx.x & 15;  // 16 lanes to a row's splits
+  const Parts ps = parts_of(a, b, bh - b * a.heads);
   for (int row = threadIdx.x >> 4; row < a.rows; row += NTH / 16) {
-    const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + row;
+    const float2 *pm = a.part_ml + ps.first * a.rows + row;
     float M = -INFINITY, L = 0.0f;
-    for (int s = j; s < a.splits; s += 16) {
+    for (int s = j; s < ps.count; s += 16) {
       const float2 x = pm[(int64_t)s * a.rows];
       const float m = fmaxf(M, x.x);
       L = m > -INFINITY ? L * exp2_fast(M - m) + x.y * exp2_fast(x.x - m) : L + x.y;
@@ -436,9 +470,11 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   }
   const int bh = (int)(id / (uint32_t)a.rows), r = (int)id - bh * a.rows;
   const int b = (int)((uint32_t)bh / (uint32_t)a.heads), h = bh - b * a.heads;
-  const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows + r;
-  const float *po = a.part_o + ((int64_t)bh * a.splits * a.rows + r) * D;
-  const int S = a.splits, t = threadIdx.x;
+  const Parts ps = parts_of(a, b, h);
+  if (a.ragged && ps.count == 1) return;  // the attention has stored the row
+  const float2 *pm = a.part_ml + ps.first * a.rows + r;
+  const float *po = a.part_o + (ps.first * a.rows + r) * D;
+  const int S = ps.count, t = threadIdx.x;
   const int lane = t & 63, grp = t >> 5, c4 = 4 * (t & 31);
   // on their way first, in the order of their use: the splits' maxima and sums, the
   // first rows of sums, this thread's part of G_V (the two halves of the
@@ -542,13 +578,15 @@ __global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
     L[i] = 0.0f;
     u[i] = make_float2(0.f, 0.f);
   }
-  const float2 *pm = a.part_ml + (int64_t)bh * a.splits * a.rows;
-  const float *po = a.part_o + (int64_t)bh * a.splits * a.rows * D + 2 * lane;
-  for (int s = 0; s < a.splits; s++)
+  const Parts ps = parts_of(a, b, h);
+  if (a.ragged && ps.count == 1) return;
+  const float2 *pm = a.part_ml + ps.first * a.rows;
+  const float *po = a.part_o + ps.first * a.rows * D + 2 * lane;
+  for (int s = 0; s < ps.count; s++)
 #pragma unroll
     for (int i = 0; i < 4; i++) M[i] = fmaxf(M[i], pm[(int64_t)s * a.rows + r[i]].x);
 #pragma unroll 2
-  for (int s = 0; s < a.splits; s++)
+  for (int s = 0; s < ps.count; s++)
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const float2 x = pm[(int64_t)s * a.rows + r[i]], y = *(const float2 *)(po + ((int64_t)s * a.rows + r[i]) * D);
@@ -576,7 +614,7 @@ __global__ __launch_bounds__(NTH) void k_attend_merge_many(const AttendArgs a) {
 }
 
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.tiles * a.splits));
+  const dim3 grid((unsigned)((int64_t)a.heads * a.tiles * a.slots));
   const bool mass = a.mass && a.bsum;
 #define CG_R(BF, MA, NW)                                                                       \
   if (bf16 == BF && mass == MA && a.waves == NW) {                                             \

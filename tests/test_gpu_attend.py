@@ -156,6 +156,49 @@ def test_long_and_split(n, R):
     check(c, c.run())
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("lengths", [
+    [2600, 1], [0, 0, 0, 2500], [0] * 5, [2049] * 3, [5000, 37, 0, 1200, 256, 4999, 31], [100] * 15 + [6000] + [900],
+    [(37 * i) % 300 for i in range(69)] + [4000], [4000] + [0] * 66, [33] * 130,
+])
+def test_unlike_lengths(lengths, bf16):
+    """Splits are dealt by length: one long sequence among short and empty ones, more
+    sequences than a wave has lanes, equal ones."""
+    c = Case(546 + len(lengths), B=len(lengths), H=1, R=3, n=1, T=6016, block=32, lengths=lengths, bf16=bf16).device()
+    ref = c.reference()
+    check(c, c.run(), ref)
+    check(c, c.run(lse=False, mass=False), ref)
+
+
+@pytest.mark.parametrize("n", [2, 15])
+def test_unlike_lengths_with_row_tiles_and_padding(n):
+    c = Case(547 + n, B=6, H=3, R=4, n=n, T=3000, block=16, lengths=[3000, 2, 0, 700, 1500, 64],
+             starts=[2999 - n, 0, 0, 695, 1000, -1]).device()
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("n", [1, 6])
+def test_replay_of_unlike_lengths(n):
+    """The dealing follows the lengths on the device."""
+    t = torch()
+    c = Case(548, B=5, T=4000, n=n).device()
+    L, B, H, R, _, T, block, g = c.dims
+    at = c.attn()
+    out, mass = t.empty_like(c.q), t.zeros((L, B, H, c.cap // block), device="cuda")
+    ws = empty_u8(cg.cg_attend_workspace_bytes(c.shape, c.gauge, c.codec, at, True))
+    cg.cg_attend(c.shape, c.payd, c.metad, c.gauge, c.codec, at, c.q, out, None, mass, ws)
+    gr = t.cuda.CUDAGraph()
+    with t.cuda.graph(gr):
+        cg.cg_attend(c.shape, c.payd, c.metad, c.gauge, c.codec, at, c.q, out, None, mass, ws)
+    for ln in ([4000] * 5, [1, 4000, 0, 77, 2000], [0, 0, 0, 0, 9], [3999, 3000, 2000, 1000, 500]):
+        c.len_d.copy_(t.tensor(ln, dtype=t.int32))
+        mass.zero_()
+        gr.replay()
+        t.cuda.synchronize()
+        want = c.run()
+        assert t.equal(out, want[0]) and t.equal(mass, want[2]), ln
+
+
 def test_more_workgroups_than_are_resident():
     """522 row tiles of few rows, split all the same: 5742 rows are merged by sixteens
     and the blocks' weights finished apart."""
