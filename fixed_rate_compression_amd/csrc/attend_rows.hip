@@ -450,9 +450,9 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // Joins the splits of one row, a workgroup to a row: 2^(m_s - M) of every
 // split, eight groups of 32 lanes adding every eighth split's sums, then the
-// inverse gauge.  Up to 64 splits each wave forms all factors for itself, beside
+// inverse gauge.  Up to 128 splits each wave forms all factors for itself, beside
 // the loads of the sums: 32 rows of 32 splits 4.0 us, through LDS and two more
-// barriers 5.0; 3200 rows of 3 splits 8.5 and 10.0.  For few rows with many splits; workgroups past the last row
+// barriers 5.0; 3200 rows of 3 splits 8.5 and 10.0; 32 rows of 96 5.3 and 8.0.  For few rows with many splits; workgroups past the last row
 // finish the blocks' weights (MASS), which need no more than the rows do.
 template <bool BF16, bool MASS>
 __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
@@ -480,10 +480,11 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   // first rows of sums, this thread's part of G_V (the two halves of the
   // workgroup take half of a channel's chain each)
   constexpr int HEAD = 4;
-  float2 ml = make_float2(-INFINITY, 0.0f);
+  float2 ml = make_float2(-INFINITY, 0.0f), mh = ml;
   f4_t head[HEAD];
-  if (S <= 64) {
+  if (S <= 128) {
     if (lane < S) ml = pm[(int64_t)lane * a.rows];
+    if (lane + 64 < S) mh = pm[(int64_t)(lane + 64) * a.rows];
 #pragma unroll
     for (int k = 0; k < HEAD; k++)
       head[k] = grp + 8 * k < S ? *(const f4_t *)(po + (int64_t)(grp + 8 * k) * a.rows * D + c4) : f4_t{0.f, 0.f, 0.f, 0.f};
@@ -495,18 +496,25 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
   for (int k = 0; k < 16; k++) gw[k] = k < gh ? gp[(int64_t)k * a.g] : 0.0f;
   float M = -INFINITY, L = 0.0f;
   f4_t u = f4_t{0.f, 0.f, 0.f, 0.f};
-  if (S <= 64) {
-    M = wave_max(ml.x);
-    const float w = ml.x > -INFINITY ? exp2_fast(ml.x - M) : 0.0f;
-    L = wave_sum(ml.y * w);
+  if (S <= 128) {
+    M = wave_max(fmaxf(ml.x, mh.x));
+    const float w = ml.x > -INFINITY ? exp2_fast(ml.x - M) : 0.0f, wh = mh.x > -INFINITY ? exp2_fast(mh.x - M) : 0.0f;
+    L = wave_sum(__builtin_fmaf(mh.y, wh, ml.y * w));
 #pragma unroll
     for (int k = 0; k < HEAD; k++) u += head[k] * __shfl(w, grp + 8 * k);
+    const auto more = [&](float f, int first) {  // four more, side by side
+      f4_t v[4];
 #pragma unroll
-    for (int k = HEAD; k < 8; k++) {
-      if (8 * k >= S) break;
-      const float f = __shfl(w, grp + 8 * k);
-      if (grp + 8 * k < S) u += *(const f4_t *)(po + (int64_t)(grp + 8 * k) * a.rows * D + c4) * f;
-    }
+      for (int k = 0; k < 4; k++) {
+        const int x = first + grp + 8 * k;
+        v[k] = x < S ? *(const f4_t *)(po + (int64_t)x * a.rows * D + c4) : f4_t{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k++) u += v[k] * __shfl(f, (first + grp + 8 * k) & 63);
+    };
+    if (S > 32) more(w, 32);
+    if (S > 64) more(wh, 64);
+    if (S > 96) more(wh, 96);
   } else {
     for (int s = t; s < S; s += NTH) M = fmaxf(M, pm[(int64_t)s * a.rows].x);
     M = wave_max(M);
@@ -523,8 +531,14 @@ __global__ __launch_bounds__(NTH) void k_attend_merge(const AttendArgs a) {
     if (lane == 0) red[t >> 6].y = L;
     __syncthreads();
     L = (red[0].y + red[1].y) + (red[2].y + red[3].y);
-#pragma unroll 4
-    for (int s = grp; s < S; s += 8) u += *(const f4_t *)(po + (int64_t)s * a.rows * D + c4) * wt[s];
+    for (int s = grp; s < S; s += 64) {
+      f4_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+        v[k] = s + 8 * k < S ? *(const f4_t *)(po + (int64_t)(s + 8 * k) * a.rows * D + c4) : f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 8; k++) u += v[k] * (s + 8 * k < S ? wt[s + 8 * k] : 0.0f);
+    }
   }
   *(f4_t *)&part[grp][c4] = u;
   __syncthreads();
