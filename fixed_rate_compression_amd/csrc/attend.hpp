@@ -29,6 +29,7 @@
 #include <stdint.h>
 
 #include "cg_tile.hpp"
+#include "cg_wave.hpp"
 
 namespace cga {
 
@@ -179,21 +180,6 @@ struct Slot {
   int b, first, count;  // sequence (batch: none), its first slot and how many it has
 };
 
-// sum over the lanes up to this one
-template <int N>
-__device__ __forceinline__ int shr16(int v) {  // from the lane N before it in its 16, else 0
-  return __builtin_amdgcn_update_dpp(0, v, 0x110 + N, 0xf, 0xf, true);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-  v += shr16<1>(v);
-  v += shr16<2>(v);
-  v += shr16<4>(v);
-  v += shr16<8>(v);
-  const int lane = threadIdx.x & 63;
-  const int s0 = __builtin_amdgcn_readlane(v, 15), s1 = __builtin_amdgcn_readlane(v, 31), s2 = __builtin_amdgcn_readlane(v, 47);
-  return v + (lane >= 16 ? s0 : 0) + (lane >= 32 ? s1 : 0) + (lane >= 48 ? s2 : 0);
-}
-
 // the sequence that slot j belongs to; a wave's lanes are the sequences (at most 64,
 // with fewer than 2^31 units in all)
 __device__ __forceinline__ Slot find_slot(const AttendArgs &a, int j) {
@@ -201,13 +187,13 @@ __device__ __forceinline__ Slot find_slot(const AttendArgs &a, int j) {
   const bool there = lane < a.batch;
   const int len = there ? a.lengths[lane] : 0;
   const uint32_t u = there ? (uint32_t)((min(max((int64_t)len, (int64_t)0), a.tokens) + UNIT - 1) / UNIT) : 0u;
-  const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)u), 63);
+  const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane(cgw::wave_scan((int)u), 63);
   int n, end;
   for (int k = 0; k < 5; k++) {
     const uint32_t shares = (uint32_t)(a.slots - k * a.batch / 4);
     const uint32_t t = max((sum + (shares - 1)) / shares, (uint32_t)a.least);
     n = there ? max((int)((u + t - 1) / t), 1) : 0;
-    end = wave_scan(n);  // slots up to this sequence's last
+    end = cgw::wave_scan(n);  // slots up to this sequence's last
     if (__builtin_amdgcn_readlane(end, 63) <= a.slots) break;
   }
   const int l = __popcll(__ballot(end <= j));

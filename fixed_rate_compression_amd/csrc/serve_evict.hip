@@ -3,6 +3,7 @@
 //
 // Blocks, not tokens, leave: a block's codes share one range, so whole blocks
 // move as they are and nothing is quantized a second time.
+#include "cg_wave.hpp"
 #include "serve.hpp"
 
 namespace cgs {
@@ -24,12 +25,111 @@ __device__ __forceinline__ int lanes_below(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
 
-// One workgroup per (layer, sequence, head).  The smallest kept weight is found
+// Up to 4096 blocks a head: their weights stay in registers, K to a thread, block e
+// 256 + thread.  The smallest kept weight is built from its top bit down, each bit
+// by a count of the weights at or above it, until the count is the number to keep
+// or the bits end; then one ordered pass writes the kept blocks' numbers and
+// weights, blocks of that smallest weight in index order until the budget is met.
+// 256 heads of 256 blocks 5.6 us, by the four counting passes below 8.5; 128 heads of
+// 2500 10.9 and 11.8, of 4096 12.9 and 14.8.
+constexpr int PT = 256, PW = PT / 64;
+template <int K>
+__global__ __launch_bounds__(PT) void k_evict_pick(const EvictArgs a) {
+  __shared__ int cnt[2][PW];
+  __shared__ int part[2][K * PW > 64 ? K * PW : 64];  // ties, kept blocks of (e, wave)
+  const int64_t id = blockIdx.x;
+  const int b = (int)(blockIdx.x / (uint32_t)a.heads % (uint32_t)a.batch);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t len = min(max(a.lengths ? (int64_t)a.lengths[b] : a.tokens, (int64_t)0), a.tokens);
+  const int n = (int)((len + a.block - 1) / a.block);
+  const float *mass = a.mass + id * a.nblk;
+  float *mo = a.mass_out + id * a.nblk_out;
+  int32_t *kept = a.kept + id * a.budget;
+  const bool all = n <= a.budget;
+  const int lo = a.sink, hi = n - a.recent;  // blocks that compete
+  float x[K];
+  uint32_t key[K];  // 0: not competing, or NaN
+#pragma unroll
+  for (int e = 0; e < K; e++) {
+    const int i = e * PT + (int)threadIdx.x;
+    x[e] = i < n ? mass[i] : 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < K; e++) {
+    const int i = e * PT + (int)threadIdx.x;
+    key[e] = i >= lo && i < hi ? order_key(x[e]) : 0u;
+  }
+  const int want = all ? 0 : a.budget - a.sink - a.recent;
+  // count of the competing weights of at least c (> 0); one barrier, `turn` alternates
+  const auto at_least = [&](uint32_t c, int turn) {
+    int m = 0;
+#pragma unroll
+    for (int e = 0; e < K; e++) m += __popcll(__ballot(key[e] >= c));
+    if (lane == 0) cnt[turn & 1][wave] = m;
+    __syncthreads();
+    return (cnt[turn & 1][0] + cnt[turn & 1][1]) + (cnt[turn & 1][2] + cnt[turn & 1][3]);
+  };
+  // the largest `least` that `want` weights reach; `above`: how many pass it for certain
+  uint32_t least = 0;
+  int above = 0;
+  bool exact = want == 0;  // all that reach `least` stay
+  if (want > 0) {
+    for (int bit = 31; bit >= 0; bit--) {
+      const uint32_t c = least | 1u << bit;
+      const int m = at_least(c, bit);
+      if (m >= want) least = c;
+      else above = m;
+      if (m == want) {
+        exact = true;
+        break;
+      }
+    }
+  }
+  const int need = want - above;  // how many of weight `least` stay (where not exact)
+  uint64_t stay[K], tie[K];
+#pragma unroll
+  for (int e = 0; e < K; e++) {
+    const int i = e * PT + (int)threadIdx.x;
+    const bool mid = i >= lo && i < hi && !all;
+    stay[e] = __ballot(i < n && (!mid || (want > 0 && (exact ? key[e] >= least : key[e] > least))));
+    tie[e] = exact ? 0ull : __ballot(mid && key[e] == least);
+  }
+  // positions: entry (e, wave) of part begins where the entries before it end
+  if (!exact) {
+#pragma unroll
+    for (int e = 0; e < K; e++)
+      if (lane == e) part[0][e * PW + wave] = __popcll(tie[e]);
+    __syncthreads();
+    const int v = lane < K * PW ? part[0][lane] : 0, end = cgw::wave_scan(v);
+#pragma unroll
+    for (int e = 0; e < K; e++) {
+      const int before = __builtin_amdgcn_readlane(end - v, e * PW + wave);
+      const bool mine = (tie[e] >> lane & 1) && before + lanes_below(tie[e]) < need;
+      stay[e] |= __ballot(mine);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < K; e++)
+    if (lane == e) part[1][e * PW + wave] = __popcll(stay[e]);
+  __syncthreads();  // every weight has been read: mass_out may be mass
+  const int v = lane < K * PW ? part[1][lane] : 0, end = cgw::wave_scan(v);
+  const int out = __builtin_amdgcn_readlane(end, 63);
+#pragma unroll
+  for (int e = 0; e < K; e++) {
+    const int at = __builtin_amdgcn_readlane(end - v, e * PW + wave) + lanes_below(stay[e]);
+    if (stay[e] >> lane & 1) {
+      kept[at] = e * PT + (int)threadIdx.x;
+      mo[at] = x[e];
+    }
+  }
+  for (int i = out + (int)threadIdx.x; i < a.budget; i += PT) kept[i] = -1;
+  for (int64_t i = out + (int)threadIdx.x; i < a.nblk_out; i += PT) mo[i] = 0.0f;
+}
+
+// More: one workgroup per (layer, sequence, head).  The smallest kept weight is found
 // eight bits at a time from the top: four counting passes over weights held in
-// registers (past 8192 blocks: read again).  Then one ordered pass writes the
-// kept blocks' numbers and weights; blocks of that smallest weight stay in index
-// order until the budget is met.  256 heads of 256 blocks: 8 us, 128 heads of
-// 2500: 12; counting every weight against every other from LDS took 11 and 51.
+// registers (past 8192 blocks: read again).  Then the ordered pass, as above.  128
+// heads of 8192 blocks 21 us.
 constexpr int HELD = 8;
 __global__ __launch_bounds__(ST) void k_evict_select(const EvictArgs a) {
   __shared__ int hist[SW][256];
@@ -198,7 +298,12 @@ __global__ __launch_bounds__(MT) void k_evict_move(const EvictArgs a, int chunks
 
 hipError_t evict_launch(const EvictArgs &a, hipStream_t s) {
   const int64_t heads = (int64_t)a.layers * a.batch * a.heads;
-  hipLaunchKernelGGL(k_evict_select, dim3((unsigned)heads), dim3(ST), 0, s, a);
+  const int64_t blocks = (a.tokens + a.block - 1) / a.block;
+  const dim3 grid((unsigned)heads);
+  if (blocks <= PT) hipLaunchKernelGGL(k_evict_pick<1>, grid, dim3(PT), 0, s, a);
+  else if (blocks <= 4 * PT) hipLaunchKernelGGL(k_evict_pick<4>, grid, dim3(PT), 0, s, a);
+  else if (blocks <= 16 * PT) hipLaunchKernelGGL(k_evict_pick<16>, grid, dim3(PT), 0, s, a);
+  else hipLaunchKernelGGL(k_evict_select, grid, dim3(ST), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   int64_t chunks = 1;

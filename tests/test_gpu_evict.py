@@ -124,3 +124,15 @@ def test_captured_in_place():
     t.cuda.synchronize()
     assert ln.tolist() == [192, 100] and t.equal(p0, pd)
     assert kept[0, 0, 0].tolist() == list(range(6))
+
+
+@pytest.mark.parametrize("nb", [1, 64, 255, 256, 257, 1023, 1025, 4096, 4097, 8193, 9001])
+@pytest.mark.parametrize("kind", ["ties", "spread", "nan"])
+def test_every_number_of_blocks(nb, kind):
+    """The forms of the selection, at both sides of their borders."""
+    rng = np.random.default_rng(nb)
+    m = {"ties": rng.integers(0, 4, (1, 1, 3, nb)), "spread": np.exp(rng.uniform(-80, 80, (1, 1, 3, nb))),
+         "nan": np.where(rng.random((1, 1, 3, nb)) < 0.6, np.nan, rng.integers(-2, 2, (1, 1, 3, nb)))}[kind].astype(np.float32)
+    budget = max(1, nb // 3)
+    run(nb, 1, 1, 3, nb * 16, 16, budget, min(2, budget - 1), 1, [nb * 16 - 7], mass=m, in_place=nb % 2 == 0)
+    run(nb + 1, 1, 1, 3, nb * 16, 16, max(1, nb - 1), 0, 1, [nb * 16], mass=m, in_place=nb % 2 == 1)
