@@ -134,17 +134,21 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     qp = load_row_part<BF16>(a, b, h, r0);
     load_gauge<false>(gk, a.g, 0, gw);
   }
+  const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
+  const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
+  RawKeys uk;
+  RawValues uv;
+  // nor do the first units of a sequence that is not split (rows of the capacity, used
+  // or not; 200 tokens 8.3 us, behind the length 8.6)
+  if (splits == 1 && wave * UNIT < a.tcap) {
+    load_keys(a, kf, km, wave * UNIT, uk);
+    load_values(a, vf, vm, wave * UNIT, uv);
+  }
   const Sequence sq = load_sequence(a, b);
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
   const int u0 = split_begin(units, split, splits), u1 = split_begin(units, split + 1, splits);
-
-  const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
-  const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
-
-  RawKeys uk;
-  RawValues uv;
-  if (u0 + wave < u1) {
+  if (splits > 1 && u0 + wave < u1) {
     load_keys(a, kf, km, (u0 + wave) * UNIT, uk);
     load_values(a, vf, vm, (u0 + wave) * UNIT, uv);
   }
