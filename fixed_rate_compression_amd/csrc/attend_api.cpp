@@ -129,17 +129,19 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   // with sums 31 us, equal splits 37; 16 of 0 .. 8192 23 and 26 (all of 8192: 53 and 51);
   // 32 sequences of 2000 tokens but one of 131072: the whole call 72 and 428; 64 of
   // 16000 in one split each, with a merge that finds nothing to do: 390 and 389.
-  p.ragged = p.few && p.waves == 4 && t->lengths && s->batch > 1 && s->batch <= 64 &&
-             s->tokens > (p.splits > 1 ? 2048 : 16384) && s->tokens < (int64_t)1 << 30;
-  const int64_t slots = (int64_t)s->batch * p.splits + (p.ragged && p.splits == 1 ? s->batch / 2 : 0);
-  p.slots = (int)slots;
+  // (The workspace is the same with and without lengths.)
+  const bool may = p.few && p.waves == 4 && s->batch > 1 && s->batch <= 64 &&
+                   s->tokens > (p.splits > 1 ? 2048 : 16384) && s->tokens < (int64_t)1 << 30;
+  p.ragged = may && t->lengths;
+  const int64_t more = may && p.splits == 1 ? s->batch / 2 : 0, slots = (int64_t)s->batch * p.splits;
+  p.slots = (int)(slots + (p.ragged ? more : 0));
   p.least = (int)((s->tokens + cga::UNIT - 1) / cga::UNIT / cga::MERGE_SPLITS + 1);
   if (p.least < kMinTokens / cga::UNIT) p.least = kMinTokens / cga::UNIT;
-  const int64_t parts = slots * s->heads * p.rows;
+  const int64_t parts = (slots + more) * s->heads * p.rows;
   p.merge = p.splits > 1 || p.ragged;
-  p.o_bytes = p.merge ? up256((size_t)parts * cga::D * 4) : 0;
-  p.ml_bytes = p.merge || (mass && p.few) ? up256((size_t)parts * 8) : 0;
-  if (p.ragged) p.dealt_bytes = up256((size_t)s->batch * 8);
+  p.o_bytes = p.merge || may ? up256((size_t)parts * cga::D * 4) : 0;
+  p.ml_bytes = p.merge || may || (mass && p.few) ? up256((size_t)parts * 8) : 0;
+  if (may) p.dealt_bytes = up256((size_t)s->batch * 8);
   if (mass) p.bsum_bytes = up256((size_t)(fields * p.entries * p.rows) * 8);
   if (mass && !p.few) p.lse2_bytes = up256((size_t)(fields * p.rows) * 4);
   return p;

@@ -14,18 +14,18 @@
 namespace cga {
 
 template <int W>
-__global__ __launch_bounds__(NTH) void k_mass_rows(const AttendArgs a) {
+__global__ __launch_bounds__(NTH) void k_mass_rows(const AttendArgs a, int groups) {
   __shared__ float red[NTH / 64];
   constexpr int PER = NTH / 64 / W;  // blocks to a workgroup
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t groups = (uint32_t)((a.nblk + PER - 1) / PER);
-  const int bh = (int)(blockIdx.x / groups), b = bh / a.heads;
-  const int64_t blk = (int64_t)(blockIdx.x - bh * groups) * PER + wave / W;
+  const int bh = (int)(blockIdx.x / (uint32_t)groups), b = bh / a.heads;
   const Sequence sq = load_sequence(a, b);
-  const int64_t t0 = blk << a.bshift;
   const int tmax = limit_of(a, sq, 0, a.n - 1);
-  float w = 0.0f;
-  if (t0 < tmax) {
+  // the same number of turns for all waves of a block
+  for (int64_t blk = (int64_t)((int)blockIdx.x - bh * groups) * PER + wave / W; blk << a.bshift < tmax;
+       blk += (int64_t)groups * PER) {
+    const int64_t t0 = blk << a.bshift;
+    float w = 0.0f;
     const int per = a.bshift == 6 ? 2 : 1, esh = min(a.bshift, 5);
     for (int k = 0; k < per; k++) {
       const int64_t te = t0 + ((int64_t)k << esh);
@@ -41,21 +41,27 @@ __global__ __launch_bounds__(NTH) void k_mass_rows(const AttendArgs a) {
         w = __builtin_fmaf(x.x, exp2_fast(x.y - ls[r]), w);
       }
     }
-  }
 #pragma unroll
-  for (int k = 32; k >= 1; k >>= 1) w += __shfl_xor(w, k);
-  if constexpr (W > 1) {
-    if (lane == 0) red[wave] = w;
-    __syncthreads();
-    w = (red[0] + red[1]) + (red[2] + red[3]);
+    for (int k = 32; k >= 1; k >>= 1) w += __shfl_xor(w, k);
+    if constexpr (W > 1) {
+      if (lane == 0) red[wave] = w;
+      __syncthreads();
+      w = (red[0] + red[1]) + (red[2] + red[3]);
+      __syncthreads();
+    }
+    if (lane == 0 && wave % W == 0) a.mass[(int64_t)bh * a.nblk + blk] += w;
   }
-  if (lane == 0 && wave % W == 0 && t0 < tmax) a.mass[(int64_t)bh * a.nblk + blk] += w;
 }
 
 hipError_t mass_rows_launch(const AttendArgs &a, hipStream_t s) {
-  const int64_t fields = (int64_t)a.batch * a.heads;
-  if (a.rows <= 512) hipLaunchKernelGGL(k_mass_rows<1>, dim3((unsigned)(fields * ((a.nblk + 3) / 4))), dim3(NTH), 0, s, a);
-  else hipLaunchKernelGGL(k_mass_rows<4>, dim3((unsigned)(fields * a.nblk)), dim3(NTH), 0, s, a);
+  // a wave to a block of few rows; 16 workgroups a compute unit at most, which take a
+  // field's blocks in turn: the capacity may be far beyond what is there
+  const int64_t fields = (int64_t)a.batch * a.heads, per = a.rows <= 512 ? 4 : 1;
+  const int64_t most = (((a.tokens - 1) >> a.bshift) + per) / per, fit = (4096 + fields - 1) / fields;
+  const int groups = (int)(most < fit ? most : fit);
+  const dim3 grid((unsigned)(fields * groups));
+  if (per == 4) hipLaunchKernelGGL(k_mass_rows<1>, grid, dim3(NTH), 0, s, a, groups);
+  else hipLaunchKernelGGL(k_mass_rows<4>, grid, dim3(NTH), 0, s, a, groups);
   return hipGetLastError();
 }
 

@@ -15,7 +15,8 @@ it, so a step may be recorded into a graph and replayed (the host's bound of the
 lengths, which refuses a step that cannot fit, does not see replays: rows past
 the capacity are dropped).
 
-All arithmetic runs in the HIP library; this class only owns buffers.
+All arithmetic runs in the HIP library; this class only owns buffers.  A cache
+belongs to one stream at a time.
 """
 from __future__ import annotations
 
@@ -43,7 +44,9 @@ class ServingCache:
         self.starts = torch.zeros(batch, dtype=torch.int32, **dev)   # of the present step
         self.n = 0                                                   # rows of the present step
         self.most = 0                                                # no sequence is longer
-        self._work = {}                                              # workspace by queries a step
+        self._need = {}                                              # workspace bytes by queries a step
+        self._work = []                                              # workspaces, growing; none is freed: a
+                                                                     # recorded step may use it
 
     def begin(self, n, valid=None):
         """A step of n rows a sequence; valid: device int32 [batch], rows that are there (or None: all)."""
@@ -73,11 +76,15 @@ class ServingCache:
         at = cg.make_attn(layer, self.q_heads, self.n, self.shape.head_dim ** -0.5 if scale is None else scale, causal,
                           self.lengths, self.starts,
                           tuple(q.stride(d) if q.shape[d] > 1 else 0 for d in (0, 1)))   # of one row: any
-        ws = self._work.get(self.n)
-        if ws is None:
-            need = cg.cg_attend_workspace_bytes(self.shape, self.gauge, self.codec, at, self.mass is not None)
-            ws = self._work[self.n] = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
-        cg.cg_attend(self.shape, self.payload, self.meta, self.gauge, self.codec, at, q, out, lse, self.mass, ws)
+        need = self._need.get(self.n)
+        if need is None:
+            need = self._need[self.n] = cg.cg_attend_workspace_bytes(self.shape, self.gauge, self.codec, at,
+                                                                     self.mass is not None)
+        if not self._work or self._work[-1].numel() < need:
+            size = max(need, 16, self._work[-1].numel() * 3 // 2 if self._work else 0)
+            self._work.append(torch.empty(size, dtype=torch.uint8, device="cuda"))
+        cg.cg_attend(self.shape, self.payload, self.meta, self.gauge, self.codec, at, q, out, lse, self.mass,
+                     self._work[-1])
         return out
 
     def evict(self, budget, sink=1, recent=1):

@@ -210,3 +210,18 @@ def test_an_eviction_ends_the_step():
     c.begin(32)
     c.append(0, k[:, :32], k[:, :32])
     assert bool((c.attend(0, q[:, :32]) == 1).all()) and c.lengths.tolist() == [56]
+
+
+def test_workspaces_do_not_pile_up():
+    """Prompts of many lengths share one workspace that grows; an older one outlives what recorded it."""
+    t = torch()
+    c = ServingCache(1, 2, 2, 8, 4096, cg.make_gauge(0), 32, with_mass=True)
+    k = t.randn((2, 40, 2, D), device="cuda").bfloat16()
+    q = t.randn((2, 40, 8, D), device="cuda").bfloat16()
+    outs = []
+    for n in list(range(40, 0, -1)) + list(range(1, 41)):
+        c.begin(n)
+        c.append(0, k[:, :n], k[:, :n])
+        outs.append(c.attend(0, q[:, :n]))
+    assert len(c._work) <= 3
+    assert all(bool(t.isfinite(o.float()).all()) for o in outs)

@@ -222,3 +222,13 @@ def test_strides_that_reach_too_far_are_refused():
     r = ctypes.byref
     assert cg.lib().cg_append(r(shape()), r(cg.make_gauge(0)), r(codec()), 0, 1 << 21, P, P, 0, far, None, None, FAR, P,
                               FAR, P, FAR, None) == cg.CG_E_INVAL
+
+
+@pytest.mark.parametrize("tokens", [64, 2048, 4096, 32768])
+@pytest.mark.parametrize("batch,n", [(1, 1), (2, 1), (64, 1), (8, 20), (3, 300)])
+def test_workspace_does_not_depend_on_the_arrays(tokens, batch, n):
+    """A size asked for without lengths serves calls with them."""
+    sh = shape(batch=batch, heads=8, tokens=tokens, token_capacity=tokens)
+    need = [cg.cg_attend_workspace_bytes(sh, cg.make_gauge(0), codec(), attn(q_heads=32, n_queries=n, lengths=a, starts=b), m)
+            for m in (False, True) for a in (None, P) for b in (None, P)]
+    assert len(set(need[:4])) == 1 and len(set(need[4:])) == 1
