@@ -10,10 +10,10 @@ One step of a decoder, the same for prompts, chunks of them and single tokens:
         o = cache.attend(layer, q)      # q, o [batch, n, q_heads, 128]
 
 begin(n, valid) takes right-padded rows: sequence b gets the first valid[b] of
-them (the host's bound of the lengths counts all n).  Sequences have their own lengths, on the device; nothing here waits for
-it, so a step may be recorded into a graph and replayed (the host's bound of the
-lengths, which refuses a step that cannot fit, does not see replays: rows past
-the capacity are dropped).
+them (the host's bound of the lengths counts all n).  Sequences have their own
+lengths, on the device; nothing here waits for them, so a step may be recorded
+into a graph and replayed (the host's bound, which refuses a step that cannot
+fit, does not see replays: rows past the capacity are dropped).
 
 All arithmetic runs in the HIP library; this class only owns buffers.  A cache
 belongs to one stream at a time.

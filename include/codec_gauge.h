@@ -427,7 +427,12 @@ typedef struct cg_attn {
   int64_t q_token_stride; /* multiples of 16 bytes; a query's heads are contiguous */
 } cg_attn;
 
-/* Device scratch of cg_attend (host only).  with_mass: nonzero if mass is given. */
+/*
+ * Device scratch of cg_attend (host only).  with_mass: nonzero if mass is given;
+ * that takes 8 bytes for every row (query and head of a group) of a KV head and 32
+ * tokens of the capacity, of many rows about 1 GiB at most (queries in turn).
+ * The size does not depend on which arrays attn gives.
+ */
 int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec,
                               const cg_attn *attn, int32_t with_mass, size_t *bytes);
 
@@ -447,10 +452,11 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  * lse of -inf, and no mass.  A query with a NaN or an infinity has NaN for out,
  * lse and the mass of what it sees, as has one that sees a key block whose range
  * is NaN; a value block's NaN range reaches out alone.  Queries that see nothing
- * of such a block are not touched by it.  Scores, sums and weights of a sum are fp32; the operands
- * of the matrix products are fp16: queries in two parts (2^-22), in one (2^-11)
- * for bf16 storage with more than 64 rows a KV head and neither lse nor mass;
- * weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
+ * of such a block are not touched by it.
+ * Scores, sums and weights of a sum are fp32; the operands of the matrix products
+ * are fp16: queries in two parts (2^-22), in one (2^-11) for bf16 storage with more
+ * than 64 rows a KV head and neither lse nor mass; weights for fp32 storage in two
+ * parts, for bf16 storage in one (2^-11).
  * The order of sums depends on the shape and the lengths only (deterministic).
  * The workspace belongs to one call at a time.  Asynchronous on stream.
  */
