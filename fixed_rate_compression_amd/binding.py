@@ -399,18 +399,38 @@ def _sized(name, t, dtype, count):
 
 
 def _here(*arrays):
-    """Kernels run on the current GPU: arrays elsewhere are refused before a launch."""
+    """Kernels run on the current GPU: arrays elsewhere are refused before a launch.
+    -> its number (None if no array was a tensor)."""
     cur = None
     for t in arrays:
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             continue
-        if isinstance(t, np.ndarray) or not t.is_cuda:
+        dev = -1 if isinstance(t, np.ndarray) else t.get_device()
+        if dev == cur:
+            continue
+        if dev < 0:
             raise ValueError("device tensors are needed, got one in host memory")
         if cur is None:
             import torch
             cur = torch.cuda.current_device()
-        if t.device.index != cur:
-            raise ValueError(f"a tensor is on GPU {t.device.index}, the current one is {cur}")
+        if dev != cur:
+            raise ValueError(f"a tensor is on GPU {dev}, the current one is {cur}")
+    return cur
+
+
+_raw_stream = None
+
+
+def _stream_on(stream, device):
+    """_stream for a device that is known to be the current one: torch.cuda.current_stream
+    makes an object and takes 3 us, a third of a small call."""
+    global _raw_stream
+    if stream is not None or device is None:
+        return _stream(stream)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 def _gauge_sized(gauge, shape):
@@ -462,13 +482,13 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
     _gauge_sized(gauge, shape)
     for name, t in zip(("lengths", "starts"), attn._keep):
         _sized(name, t, "int32", batch)
-    _here(q, out, payload, meta, lse, mass, workspace, gauge._keep, *attn._keep)
+    dev = _here(q, out, payload, meta, lse, mass, workspace, gauge._keep, *attn._keep)
     rc = lib().cg_attend(
         shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, attn,
         q if isinstance(q, int) else q.data_ptr(),
         _sized("out", out, st, rows * d), _sized("lse", lse, "float32", rows),
         _sized("mass", mass, "float32", shape.layers * batch * shape.heads * (shape.token_capacity // blk if blk > 0 else 0)),
-        _ptr(workspace), _nbytes(workspace), _stream(stream))
+        _ptr(workspace), _nbytes(workspace), _stream_on(stream, dev))
     if rc != CG_OK:
         _check("cg_attend", rc)
 
@@ -492,12 +512,12 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
         bs, rs = (sb if shape.batch > 1 else 0), (sr if n_new > 1 else 0)
         ptrs.append(t.data_ptr())
     _gauge_sized(gauge, shape)
-    _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
+    dev = _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
     _check("cg_append", lib().cg_append(
         ctypes.byref(shape), ctypes.byref(gauge), ctypes.byref(codec), layer, n_new, *ptrs, bs, rs,
         _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
         _sized("tail", tail, st, shape.layers * 2 * shape.batch * row * codec.block_tokens),
-        _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream(stream)))
+        _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream_on(stream, dev)))
 
 
 def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape, payload_out, meta_out,
@@ -506,7 +526,7 @@ def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape,
     heads = shape.layers * shape.batch * shape.heads
     nblk, nout = (s.token_capacity // codec.block_tokens if codec.block_tokens > 0 else 0
                   for s in (shape, out_shape))
-    _here(mass, payload, meta, payload_out, meta_out, mass_out, kept, lengths_out, lengths)
+    dev = _here(mass, payload, meta, payload_out, meta_out, mass_out, kept, lengths_out, lengths)
     _check("cg_evict", lib().cg_evict(
         ctypes.byref(shape), ctypes.byref(codec), budget, sink, recent,
         _sized("mass", mass, "float32", heads * nblk), _ptr(payload), _nbytes(payload), _ptr(meta),
@@ -514,7 +534,7 @@ def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape,
         _ptr(payload_out), _nbytes(payload_out), _ptr(meta_out), _nbytes(meta_out),
         _sized("mass_out", mass_out, "float32", heads * nout),
         _sized("kept", kept, "int32", heads * max(budget, 0)),
-        _sized("lengths_out", lengths_out, "int32", shape.batch), _stream(stream)))
+        _sized("lengths_out", lengths_out, "int32", shape.batch), _stream_on(stream, dev)))
 
 
 def cg_last_error() -> str:
