@@ -160,14 +160,19 @@ struct Sequence {
   int len;
   int64_t start;
 };
-__device__ __forceinline__ Sequence load_sequence(const AttendArgs &a, int b) {
-  // both loads at once, from a place that is there where an array is not
-  const int32_t *any = (const int32_t *)a.q;
-  const int32_t n = *(a.lengths ? a.lengths + b : any), p = *(a.starts ? a.starts + b : any);
+// from what the arrays hold (anything where there is none)
+__device__ __forceinline__ Sequence sequence_of(const AttendArgs &a, int32_t n, int32_t p) {
   Sequence s;
   s.len = a.lengths ? (int)min(max((int64_t)n, (int64_t)0), a.tokens) : (int)a.tokens;
   s.start = (a.starts ? (int64_t)p : (int64_t)s.len - a.n_all) + a.first;
   return s;
+}
+
+__device__ __forceinline__ Sequence load_sequence(const AttendArgs &a, int b) {
+  // both loads at once, from a place that is there where an array is not
+  const int32_t *any = (const int32_t *)a.q;
+  const int32_t n = *(a.lengths ? a.lengths + b : any), p = *(a.starts ? a.starts + b : any);
+  return sequence_of(a, n, p);
 }
 
 // Few rows of sequences of unlike lengths: `slots` workgroups a head and row tile are
@@ -178,6 +183,7 @@ __device__ __forceinline__ Sequence load_sequence(const AttendArgs &a, int b) {
 // first, a whole number of slots each.  Parts are laid out by slot, [head][slot][rows].
 struct Slot {
   int b, first, count;  // sequence (batch: none), its first slot and how many it has
+  int32_t n, p;         // what lengths and starts hold for it
 };
 
 // the sequence that slot j belongs to; a wave's lanes are the sequences (at most 64,
@@ -185,7 +191,7 @@ struct Slot {
 __device__ __forceinline__ Slot find_slot(const AttendArgs &a, int j) {
   const int lane = threadIdx.x & 63;
   const bool there = lane < a.batch;
-  const int len = there ? a.lengths[lane] : 0;
+  const int32_t len = there ? a.lengths[lane] : 0, start = there && a.starts ? a.starts[lane] : 0;
   const uint32_t u = there ? (uint32_t)((min(max((int64_t)len, (int64_t)0), a.tokens) + UNIT - 1) / UNIT) : 0u;
   const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane(cgw::wave_scan((int)u), 63);
   int n, end;
@@ -197,9 +203,10 @@ __device__ __forceinline__ Slot find_slot(const AttendArgs &a, int j) {
     if (__builtin_amdgcn_readlane(end, 63) <= a.slots) break;
   }
   const int l = __popcll(__ballot(end <= j));
-  if (l >= a.batch) return Slot{a.batch, 0, 0};
+  if (l >= a.batch) return Slot{a.batch, 0, 0, 0, 0};
   const int count = __builtin_amdgcn_readlane(n, l);
-  return Slot{l, __builtin_amdgcn_readlane(end, l) - count, count};
+  return Slot{l, __builtin_amdgcn_readlane(end, l) - count, count, __builtin_amdgcn_readlane(len, l),
+              __builtin_amdgcn_readlane(start, l)};
 }
 
 // tokens query i sees: none unless it stands inside the sequence

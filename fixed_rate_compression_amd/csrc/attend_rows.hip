@@ -101,29 +101,24 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // 32-bit divisions: a 64-bit one takes longer than a unit of work
   const uint32_t id = blockIdx.x;
-  int b, h, tile, split, splits;
+  int b, h, tile, slot = 0, split = 0, splits = a.splits;
   int64_t part;  // where this part's row 0 goes
   if (a.ragged) {  // row tiles of a slot and head on one XCD where the heads are a multiple of 8
     const uint32_t q1 = id / (uint32_t)a.heads, q2 = q1 / (uint32_t)a.tiles;
     h = (int)(id - q1 * a.heads);
     tile = (int)(q1 - q2 * a.tiles);
-    const Slot sl = find_slot(a, (int)q2);
-    if (sl.b >= a.batch) return;
-    b = __builtin_amdgcn_readfirstlane(sl.b);
-    split = __builtin_amdgcn_readfirstlane((int)q2 - sl.first);
-    splits = __builtin_amdgcn_readfirstlane(sl.count);
-    part = ((int64_t)h * a.slots + (int)q2) * a.rows;
+    slot = (int)q2;
+    b = (int)(q2 * (uint32_t)a.batch / (uint32_t)a.slots);  // with equal lengths; found out below
+    part = ((int64_t)h * a.slots + slot) * a.rows;
   } else {
-    const uint32_t q1 = id / (uint32_t)a.splits;
-    split = (int)(id - q1 * a.splits);
-    splits = a.splits;
+    const uint32_t q1 = id / (uint32_t)splits;
+    split = (int)(id - q1 * splits);
     const int f = a.tiles == 1 ? (int)q1 : (int)(q1 / (uint32_t)a.tiles);
     tile = (int)q1 - f * a.tiles;
     b = (int)((uint32_t)f / (uint32_t)a.heads);
     h = f - b * a.heads;
-    part = ((int64_t)f * a.splits + split) * a.rows;
+    part = ((int64_t)f * splits + split) * a.rows;
   }
-  const int bh = b * a.heads + h;
   const int r0 = tile * ROWS, nr = min(ROWS, a.rows - r0);
   // on their way first: what does not wait for the sequence's length
   const float *gk = a.gk + (int64_t)h * D * a.g;
@@ -134,6 +129,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     qp = load_row_part<BF16>(a, b, h, r0);
     load_gauge<false>(gk, a.g, 0, gw);
   }
+  Sequence sq;
+  if (a.ragged) {
+    const Slot sl = find_slot(a, slot);
+    if (sl.b >= a.batch) return;
+    if (front && sl.b != b) qp = load_row_part<BF16>(a, sl.b, h, r0);
+    b = sl.b;
+    split = slot - sl.first;
+    splits = sl.count;
+    sq = sequence_of(a, sl.n, sl.p);
+  }
+  const int bh = b * a.heads + h;
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
   RawKeys uk;
@@ -144,7 +150,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     load_keys(a, kf, km, wave * UNIT, uk);
     load_values(a, vf, vm, wave * UNIT, uv);
   }
-  const Sequence sq = load_sequence(a, b);
+  if (!a.ragged) sq = load_sequence(a, b);
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
   const int u0 = split_begin(units, split, splits), u1 = split_begin(units, split + 1, splits);
@@ -334,7 +340,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
   __syncthreads();
   // for the merge (a store before the loop turns its scalar loads into vector ones)
   if (a.ragged && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0)
-    a.dealt[b] = make_int2((int)(id / (uint32_t)(a.heads * a.tiles)), splits);
+    a.dealt[b] = make_int2(slot, splits);
   for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * NW) {  // also rows that are not there: none is left undefined
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
     float M = -INFINITY;
