@@ -111,6 +111,9 @@ __device__ __forceinline__ void tile_queries(const float *xs, float c, TileQueri
   float sum = 0.0f;
 #pragma unroll
   for (int s = 0; s < 8; s++) frag_parts<TWO>(x[2 * s], x[2 * s + 1], sc.up, q.hi[s], lo[s], sum);
+  // an infinity: NaN for the row, as its difference from its first part is with two (alone it
+  // can make every score -inf, whose weights would all be 0)
+  if constexpr (!TWO) sum = __builtin_fmaf(mx, 0.0f, sum);
   q.ca = c * sc.un;
   q.cq = q.ca * (sum + __shfl_xor(sum, 32));
 }

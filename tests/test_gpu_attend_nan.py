@@ -75,3 +75,27 @@ def test_a_range_that_is_not_finite(form, bf16, block, kind, at, value):
     assert np.isnan(ls[bad]).all() == (kind == 0)
     plain = c.run(lse=False, mass=False)[0]
     compare(c, (plain, got[1] if kind else got[1].nan_to_num(0.0), None), ref, bad)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("value", [float("-inf"), float("inf")])
+@pytest.mark.parametrize("T,n,R", [(20, 1, 2), (300, 5, 2), (9, 9, 8), (100, 100, 2), (70, 33, 3)])
+def test_a_query_whose_scores_are_all_infinite(T, n, R, value, bf16):
+    """No gauge, positive minima and codes: one infinite channel gives every visible key the
+    same infinite score (all -inf: no weight is a number, and none is zero)."""
+    c = Case(860 + T, T=T, n=n, R=R, g=0, bf16=bf16)
+    c.meta[:, 0, ..., 0] = np.abs(c.meta[:, 0, ..., 0]) + np.float32(0.1)
+    c.pay[:, 0, ..., 5] = np.maximum(c.pay[:, 0, ..., 5], 1)
+    ref = c.reference()
+    c.device()
+    i = min(n - 1, 3)                       # in the prompts: a query that sees few tokens
+    c.q[0, i, 1, 5] = value
+    bad = np.zeros(c.q.shape[:3], bool)
+    bad[0, i, 1] = True
+    got = c.run()
+    assert np.isnan(compare(c, got, ref, bad)[bad]).all()
+    for lse in (False, True):
+        out, ls, _ = c.run(lse=lse, mass=False)
+        compare(c, (out, ls if lse else got[1], None), ref, bad)
+        if lse:
+            assert np.isnan(to_host(ls)[bad]).all()
