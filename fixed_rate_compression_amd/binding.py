@@ -495,9 +495,10 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
 
 def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, meta, lengths=None,
               starts=None, stream=None):
-    """k_new, v_new [batch, n_new, heads, 128] with contiguous heads and the same strides."""
+    """k_new, v_new [batch, n_new, heads, 128] with contiguous heads and the same strides
+    between sequences and between rows (of one sequence, or one row each: any)."""
     st = _storage(shape)
-    row, bs, rs = shape.heads * shape.head_dim, 0, 0
+    row, at = shape.heads * shape.head_dim, None
     ptrs = []
     for name, t in (("k_new", k_new), ("v_new", v_new)):
         if t.dtype != _dtype(st):
@@ -505,12 +506,14 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
         if t.shape != (shape.batch, n_new, shape.heads, shape.head_dim):
             raise ValueError(f"{name} must be [batch, n_new, heads, head_dim], got {tuple(t.shape)}")
         sb, sr, sh, sd = t.stride()
-        if (sh != shape.head_dim and shape.heads > 1) or sd != 1 or t.stride() != k_new.stride():
-            raise ValueError(f"{name} of strides {t.stride()}: contiguous heads and equal strides are needed")
         if (shape.batch > 1 and sb == 0) or (n_new > 1 and sr == 0):
             raise ValueError(f"{name}: rows of an expanded tensor")
-        bs, rs = (sb if shape.batch > 1 else 0), (sr if n_new > 1 else 0)
+        lie = (sb if shape.batch > 1 else 0, sr if n_new > 1 else 0)
+        if (sh != shape.head_dim and shape.heads > 1) or sd != 1 or lie != (at or lie):
+            raise ValueError(f"{name} of strides {t.stride()}: contiguous heads and equal strides are needed")
+        at = lie
         ptrs.append(t.data_ptr())
+    bs, rs = at
     _gauge_sized(gauge, shape)
     dev = _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
     _check("cg_append", lib().cg_append(

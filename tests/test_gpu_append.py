@@ -175,3 +175,16 @@ def test_new_rows_are_the_last(block):
     f.pay[:, :, :, :, 35:] = FILL
     f.meta[:, :, :, :, 35 // block + 1:] = 5.0
     f.check(lengths=[35, 35])
+
+
+def test_single_rows_that_lie_differently():
+    """One row of one sequence: k and v may come from tensors of unlike strides."""
+    t = torch()
+    f, z = (Filled(120, [40]) for _ in range(2))
+    f.put(f.x[0], f.x[1], 40, [40])
+    wide = t.zeros((1, 40, 6, D), dtype=z.x.dtype, device="cuda")
+    wide[:, :, 4:6] = z.x[1]
+    for i in range(40):
+        z.put(z.x[0, :, i:i + 1].contiguous(), wide[:, i:i + 1, 4:6], 1, [i + 1])
+    z.check()
+    assert t.equal(f.tail[:, :, :, :, :8], z.tail[:, :, :, :, :8]) and t.equal(f.pay, z.pay)

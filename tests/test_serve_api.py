@@ -232,3 +232,24 @@ def test_workspace_does_not_depend_on_the_arrays(tokens, batch, n):
     need = [cg.cg_attend_workspace_bytes(sh, cg.make_gauge(0), codec(), attn(q_heads=32, n_queries=n, lengths=a, starts=b), m)
             for m in (False, True) for a in (None, P) for b in (None, P)]
     assert len(set(need[:4])) == 1 and len(set(need[4:])) == 1
+
+
+def test_strides_of_single_rows_are_free():
+    """One sequence, or one row a sequence: torch leaves any stride there, and k and v may
+    differ in it (a rotated key beside a slice of a fused projection)."""
+    import torch
+
+    wide = torch.zeros((2, 1, 6, 128), dtype=torch.bfloat16)
+    tails = torch.zeros(2 * 2 * 2 * 2 * 32 * 128, dtype=torch.bfloat16)
+    for batch, n, k, v in ((1, 1, wide[:1, :, 2:4].contiguous(), wide[:1, :, 4:6]),
+                           (1, 2, wide[:, 0, 2:4].unsqueeze(0), wide.transpose(0, 1)[:, :, 4:6]),
+                           (2, 1, wide[:, :, 2:4], wide.as_strided((2, 1, 2, 128), (768, 128, 128, 1), 512))):
+        sh = shape(batch=batch)
+        pay, meta = torch.zeros(8 * batch * 64 * 128, dtype=torch.uint8), torch.zeros(8 * batch * 2 * 2)
+        # past the checks of the strides: what is left to refuse is that these are in host memory
+        with pytest.raises(ValueError, match="host memory"):
+            cg.cg_append(sh, cg.make_gauge(0), codec(), 0, n, k, v, tails, pay, meta, stream=0)
+    k = wide[:, :, 2:4].contiguous()
+    pay, meta = torch.zeros(16 * 64 * 128, dtype=torch.uint8), torch.zeros(16 * 2 * 2)
+    with pytest.raises(ValueError, match="strides"):            # two sequences that do lie apart differently
+        cg.cg_append(shape(), cg.make_gauge(0), codec(), 0, 1, k, wide[:, :, 4:6], tails, pay, meta, stream=0)
