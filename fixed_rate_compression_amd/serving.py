@@ -42,6 +42,7 @@ class ServingCache:
         self.mass = torch.zeros((layers, batch, heads, capacity // block_tokens), **dev) if with_mass else None
         self.lengths = torch.zeros(batch, dtype=torch.int32, **dev)
         self.starts = torch.zeros(batch, dtype=torch.int32, **dev)   # of the present step
+        self._counts = (torch.int32, torch.int64)                    # types of a step's valid rows
         self.n = 0                                                   # rows of the present step
         self.most = 0                                                # no sequence is longer
         self._need = {}                                              # workspace bytes by queries a step
@@ -54,13 +55,19 @@ class ServingCache:
             raise ValueError("n < 0")
         if self.most + n > self.shape.token_capacity:
             raise ValueError(f"{n} rows do not fit: up to {self.most} of {self.shape.token_capacity} are taken")
+        if valid is not None:     # before anything changes: a refused step has not begun
+            at = self.lengths
+            if getattr(valid, "dtype", None) not in self._counts or valid.shape != at.shape or \
+                    valid.device != at.device:
+                raise ValueError("valid must be int32 [batch] beside the cache")
+            valid = valid.clamp(0, n)
         self.n = n
         self.most += n
         self.starts.copy_(self.lengths)
         if valid is None:
             self.lengths.add_(n)
         else:
-            self.lengths.add_(valid.clamp(0, n))
+            self.lengths.add_(valid)
 
     def append(self, layer, k, v):
         """The step's rows of one layer, before that layer's attend."""

@@ -225,3 +225,18 @@ def test_workspaces_do_not_pile_up():
         outs.append(c.attend(0, q[:, :n]))
     assert len(c._work) <= 3
     assert all(bool(t.isfinite(o.float()).all()) for o in outs)
+
+
+def test_a_refused_step_leaves_the_cache_as_it_was():
+    """Counts of valid rows that are not there for every sequence, or are no whole numbers on
+    the GPU, are refused before the step begins."""
+    t = torch()
+    c = ServingCache(1, 3, 1, 2, 64, cg.make_gauge(0), 32)
+    c.begin(20, t.tensor([20, 5, 0], dtype=t.int32, device="cuda"))
+    for bad in (t.tensor([4], dtype=t.int32, device="cuda"), t.tensor([1, 2], dtype=t.int32, device="cuda"),
+                t.tensor([1, 2, 3], dtype=t.int32), t.tensor([1.0, 2.0, 3.0], device="cuda"), [1, 2, 3]):
+        with pytest.raises(ValueError):
+            c.begin(40, bad)
+        assert (c.n, c.most) == (20, 20) and c.lengths.tolist() == [20, 5, 0] and c.starts.tolist() == [0, 0, 0]
+    c.begin(44, t.tensor([44, -3, 90], dtype=t.int64, device="cuda"))
+    assert c.lengths.tolist() == [64, 5, 44] and c.starts.tolist() == [20, 5, 0]
