@@ -44,6 +44,7 @@ class ServingCache:
         self.starts = torch.zeros(batch, dtype=torch.int32, **dev)   # of the present step
         self._counts = (torch.int32, torch.int64)                    # types of a step's valid rows
         self.n = 0                                                   # rows of the present step
+        self._put = set()                                            # layers that have them
         self.most = 0                                                # no sequence is longer
         self._need = {}                                              # workspace bytes by queries a step
         self._work = []                                              # workspaces, growing; none is freed: a
@@ -62,6 +63,7 @@ class ServingCache:
                 raise ValueError("valid must be int32 [batch] beside the cache")
             valid = valid.clamp(0, n)
         self.n = n
+        self._put.clear()
         self.most += n
         self.starts.copy_(self.lengths)
         if valid is None:
@@ -70,9 +72,13 @@ class ServingCache:
             self.lengths.add_(valid)
 
     def append(self, layer, k, v):
-        """The step's rows of one layer, before that layer's attend."""
+        """The step's rows of one layer, before that layer's attend; every layer once a step (only
+        the raw rows of a sequence's last block are kept, which may be another by then)."""
+        if layer in self._put:
+            raise ValueError(f"layer {layer} has the step's rows")
         cg.cg_append(self.shape, self.gauge, self.codec, layer, self.n, k, v, self.tail, self.payload, self.meta,
                      self.lengths, self.starts)
+        self._put.add(layer)
 
     def attend(self, layer, q, scale=None, causal=True, out=None, lse=None):
         """Attention of the step's queries; gathers the blocks' weights where the cache has them."""

@@ -240,3 +240,24 @@ def test_a_refused_step_leaves_the_cache_as_it_was():
         assert (c.n, c.most) == (20, 20) and c.lengths.tolist() == [20, 5, 0] and c.starts.tolist() == [0, 0, 0]
     c.begin(44, t.tensor([44, -3, 90], dtype=t.int64, device="cuda"))
     assert c.lengths.tolist() == [64, 5, 44] and c.starts.tolist() == [20, 5, 0]
+
+
+def test_a_layers_rows_go_in_once_a_step():
+    """Rows put in again after they have passed the end of a block would be encoded beside the
+    raw rows of a later one: refused, and the cache is as it was."""
+    t = torch()
+    c, want = (ServingCache(2, 1, 1, 2, 64, cg.make_gauge(0), 16) for _ in range(2))
+    k = t.randn((1, 30, 1, D), device="cuda", generator=t.Generator("cuda").manual_seed(3)).bfloat16()
+    for x in (c, want):
+        for lo, n in ((0, 10), (10, 20)):
+            x.begin(n)
+            for layer in range(2):
+                x.append(layer, k[:, lo:lo + n], k[:, lo:lo + n])
+            if x is c:
+                with pytest.raises(ValueError):
+                    x.append(1, k[:, lo:lo + n], k[:, lo:lo + n])
+    assert t.equal(c.payload, want.payload) and t.equal(c.meta, want.meta) and t.equal(c.tail, want.tail)
+    c.begin(1)
+    with pytest.raises(ValueError):
+        c.append(0, k[:, :2], k[:, :2])      # a refused call has put nothing in
+    c.append(0, k[:, :1], k[:, :1])
