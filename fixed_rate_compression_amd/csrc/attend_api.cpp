@@ -147,13 +147,16 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   return p;
 }
 
+// factor of the scores, which are powers of two
+float log2_scale(const cg_attn *t) { return (float)((double)t->scale * 1.4426950408889634074); }
+
 int check_attn(const cg_shape *s, const cg_attn *t) {
   if (!t) return error(CG_E_INVAL, "attn is NULL");
   if (t->layer < 0 || t->layer >= s->layers) return error(CG_E_SHAPE, "layer outside the cache shape");
   if (t->q_heads <= 0 || t->q_heads % s->heads) return error(CG_E_SHAPE, "q_heads must be a positive multiple of heads");
   if (t->n_queries < 0) return error(CG_E_SHAPE, "n_queries < 0");
   if (t->causal != 0 && t->causal != 1) return error(CG_E_INVAL, "causal must be 0 or 1");
-  if (!isfinite(t->scale)) return error(CG_E_INVAL, "scale is not finite");
+  if (!isfinite(t->scale) || !isfinite(log2_scale(t))) return error(CG_E_INVAL, "scale or scale log2(e) is not finite");
   if (((uintptr_t)t->lengths | (uintptr_t)t->starts) & 3u)
     return error(CG_E_INVAL, "lengths and starts must be 4-byte aligned");
   const int64_t token = (int64_t)t->q_heads * s->head_dim;
@@ -247,7 +250,7 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.least = p.least;
   a.waves = p.waves;
   a.entries = p.entries;
-  a.c = (float)((double)attn->scale * 1.4426950408889634074);
+  a.c = log2_scale(attn);
   char *w = (char *)workspace;
   auto take = [&w](size_t n) { char *r = n ? w : nullptr; w += n; return r; };
   a.part_o = (float *)take(p.o_bytes);

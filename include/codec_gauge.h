@@ -420,7 +420,8 @@ typedef struct cg_attn {
   int32_t n_queries;      /* queries of each sequence, n >= 0 (0: nothing is done) */
   int32_t causal;         /* 1: a query sees positions up to its own; 0: the
                              whole sequence */
-  float scale;            /* factor of the scores, e.g. 1 / sqrt(head_dim); finite */
+  float scale;            /* factor of the scores, e.g. 1 / sqrt(head_dim); finite,
+                             and so scale log2(e) in fp32 */
   const int32_t *lengths;
   const int32_t *starts;
   int64_t q_batch_stride; /* elements between sequences / queries of q (0: dense), */

@@ -253,3 +253,11 @@ def test_strides_of_single_rows_are_free():
     pay, meta = torch.zeros(16 * 64 * 128, dtype=torch.uint8), torch.zeros(16 * 2 * 2)
     with pytest.raises(ValueError, match="strides"):            # two sequences that do lie apart differently
         cg.cg_append(shape(), cg.make_gauge(0), codec(), 0, 1, k, wide[:, :, 4:6], tails, pay, meta, stream=0)
+
+
+@pytest.mark.parametrize("scale", [2.5e38, -2.5e38, 3.4e38])
+def test_scales_whose_factor_is_not_finite_are_refused(scale):
+    """Scores are formed in units of log2: scale log2(e) has to be an fp32 number."""
+    assert np.isfinite(np.float32(scale))
+    assert attend(at=attn(scale=scale, n_queries=0)) == cg.CG_E_INVAL
+    assert attend(at=attn(scale=scale / 2, n_queries=0)) == cg.CG_OK
