@@ -84,7 +84,8 @@ int64_t tile_splits(int64_t work, int64_t rows, int64_t tokens) {
 
 // Block weights of many rows need 8 bytes a row and 32 tokens of the capacity.
 // Where that would pass 1 GiB the queries are taken in turn, 128 rows a KV head
-// at least.
+// at least (a full tile: fewer would leave waves without rows), so a large batch and
+// capacity pass it all the same.
 constexpr uint64_t kMaxSums = (uint64_t)1 << 30;
 
 Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {

@@ -408,8 +408,10 @@ int cg_write_header(const cg_shape *shape, const cg_codec *codec, int32_t layer,
  *            (cg_attend) or new row (cg_append); NULL: lengths - n, the last n
  *            positions.  Query or row i stands at starts + i; positions below
  *            0 or at lengths and above are padding.
- * shape->tokens only bounds the lengths (and sizes launches and workspaces),
- * so calls recorded into a graph may be replayed as the lengths grow.
+ * shape->tokens only bounds the lengths (and sizes launches and workspaces, but
+ * for the sums behind `mass`), so calls recorded into a graph may be replayed as
+ * the lengths grow.  A launch is planned for sequences of that many rows: a bound
+ * far above the lengths costs splits and a merge that they do not need.
  * Codes and ranges of rows behind a sequence's end are never looked at (a
  * block's codes past its last row are read and left out).
  */
@@ -431,7 +433,11 @@ typedef struct cg_attn {
 /*
  * Device scratch of cg_attend (host only).  with_mass: nonzero if mass is given;
  * that takes 8 bytes for every row (query and head of a group) of a KV head and 32
- * tokens of the capacity, of many rows about 1 GiB at most (queries in turn).
+ * tokens of token_capacity (16, in blocks of 16), whatever shape->tokens is.  With
+ * more than 64 rows a KV head the queries are taken in turn where that passes 1 GiB,
+ * 128 rows a KV head (or one query's) at least: 1 KiB for every KV head of the batch
+ * and 32 tokens, 2 GiB for 64 sequences of 8 KV heads and 131072 tokens.  Fewer rows
+ * are never taken in turn: 512 bytes at most.
  * The size does not depend on which arrays attn gives.
  */
 int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec,

@@ -261,3 +261,30 @@ def test_scales_whose_factor_is_not_finite_are_refused(scale):
     assert np.isfinite(np.float32(scale))
     assert attend(at=attn(scale=scale, n_queries=0)) == cg.CG_E_INVAL
     assert attend(at=attn(scale=scale / 2, n_queries=0)) == cg.CG_OK
+
+
+@pytest.mark.parametrize("batch,heads,q_heads,capacity,block,n", [
+    (64, 8, 32, 131072, 32, 2000), (64, 8, 32, 131072, 16, 2000), (128, 8, 8, 131072, 64, 300),
+    (64, 8, 2048, 65536, 32, 9), (8, 8, 32, 131072, 32, 2000), (1, 8, 32, 131072, 32, 4096), (2, 4, 16, 8192, 64, 700),
+    (256, 8, 32, 65536, 32, 16)])
+def test_workspace_of_the_block_weights_is_what_the_header_says(batch, heads, q_heads, capacity, block, n):
+    """8 bytes a row and 32 tokens of the capacity; past 64 rows a KV head queries go in turn
+    above 1 GiB, 128 rows (or a query's) at least."""
+    sh = shape(layers=1, batch=batch, heads=heads, tokens=capacity, token_capacity=capacity)
+    at = attn(q_heads=q_heads, n_queries=n)
+    need = cg.cg_attend_workspace_bytes(sh, cg.make_gauge(0), codec(block=block), at, True)
+    ratio, entries = q_heads // heads, capacity // min(block, 32)
+    each = 8 * batch * heads * entries
+    rows = n * ratio
+    if rows > 64:
+        rows = min(rows, max((1 << 30) // each, 128, ratio))
+    # the parts of split rows and the rows' log-sums come on top: 512 + 8 + 4 bytes a row and split
+    splits = max(1, 768 // (batch * heads)) if rows <= 64 else 512
+    rest = batch * heads * rows * 524 * splits + 4 * 256 + 8 * batch
+    assert each * min(rows, 64) <= need <= each * rows + rest
+
+
+def test_workspace_of_the_block_weights_past_the_limit():
+    sh = shape(layers=1, batch=64, heads=8, tokens=131072, token_capacity=131072)
+    need = cg.cg_attend_workspace_bytes(sh, cg.make_gauge(0), codec(), attn(q_heads=32, n_queries=2048), True)
+    assert need == 512 * 4096 * 1024 + 512 * 128 * 4      # 2 GiB of sums, 128 rows at a time
