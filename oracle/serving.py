@@ -29,7 +29,7 @@ def _rows(payload, meta, T, block):
         return mm[:, :1], mm[:, 1:], payload[:T].astype(np.float64)
 
 
-def attend(q, payload, meta, G, layer, block, scale, causal, lengths, starts=None, fp32=False):
+def attend(q, payload, meta, G, layer, block, scale, causal, lengths, starts=None, fp32=False, one_part=False):
     """q [B, n, Hq, 128] fp64 -> dict of out, lse, mass (this layer's gain) and
     bounds out_tol, lse_tol, mass_tol of the kernels' unrounded results.
 
@@ -43,7 +43,21 @@ def attend(q, payload, meta, G, layer, block, scale, causal, lengths, starts=Non
     rounding.  A weight is off by 2 ds + 2^-21 (exp2 and its argument's
     rounding, |s| u at most), plus the rounding of the weight to fp16 (2^-11, in
     two parts 2^-21) in the sum over the codes, plus 2^-33 of the largest for
-    weights below 2^-23 of it."""
+    weights below 2^-23 of it.
+
+    one_part: the bounds of queries in one fp16 part, where only out is asked for.  A
+    channel of q' is rounded by 2^-11 of itself (below 2^-14 of the operands, 2^-27 of
+    the row's largest, by 2^-25 of them, which is below the other terms), in the products
+    with the codes and in the sum beside the minima alike, so a score moves by that of
+    the channels' products with the key.  Codes are fp16 subnormals there: the matrix
+    cores align products by exponent fields, and a subnormal's field is up to 2^10 above
+    a code's own (2^-24 a code, field 2^-14), so each of the 128 products loses up to
+    2^-23 2^10 of the largest channel in units of a code, 2^-6 of it in all; the sums in
+    fp32, cut instead of rounded, 2^-15 S.  In units of log2 the score of token t is off by
+      ds_t = scale log2(e) (2^-11 sum_c |q'_c k_tc| + 2^-6 max_c |q'_c| step_t + 2^-15 S + g u S_g)
+    and by the roundings of large scores as above.  With weights w_t = p_t 2^e_t,
+    |e_t| <= ds_t, the mean moves by sum_t p_t (2^e_t - 1) (v_t - out) over sum_t p_t 2^e_t.
+    """
     B, n, Hq, _ = q.shape
     H = payload.shape[3]
     R = Hq // H
@@ -85,12 +99,19 @@ def attend(q, payload, meta, G, layer, block, scale, causal, lengths, starts=Non
                     qs, qsg = np.abs(qg).sum(), (np.abs(GK) @ np.abs(x)).sum()
                     ds = scale * kmag * (2.0 ** -16 * qs + g * u * qsg)
                     ds += np.abs(s).max() * 8 * u
+                    moved = 0.0
+                    if one_part:
+                        d1 = 2.0 ** -11 * (np.abs(K[:vis]) @ np.abs(qg)) + 2.0 ** -6 * np.abs(qg).max() * kst[:vis, 0]
+                        d1 += kmag * (2.0 ** -15 * qs + g * u * qsg)
+                        d1 = scale * d1 + np.abs(s).max() * 8 * u          # of exp, so without log2(e)
+                        moved = (p * np.expm1(d1)) @ np.abs(V[:vis] - o) * np.exp(d1.max())
+                        ds = d1.max()
                     dw = 2 * ds + 2.0 ** -21
                     lse_tol[b, i, h * R + j] = ds + 2.0 ** -20 + 4 * u * abs(m)
                     cw = p @ (vst[:vis] * vc[:vis])      # sum of p step code
                     ab = (np.abs(p[:, None] * vmn[:vis])).sum() + (p[:, None] * 255 * vst[:vis]).sum()
                     big = (p[:, None] * vst[:vis]).max()
-                    et = wr * cw + (dw + 2.0 ** -18) * ab + 255 * vis * 2.0 ** -33 * big
+                    et = wr * cw + ((2.0 ** -21 if one_part else dw) + 2.0 ** -18) * ab + 255 * vis * 2.0 ** -33 * big + moved
                     tol[b, i, h * R + j] = np.abs(GV).T @ et + g * u * (np.abs(GV).T @ np.abs(o))
                     full = np.zeros(nblk * block)
                     full[:vis] = p

@@ -32,11 +32,11 @@ class Case:
         self.lengths = [T] * B if lengths is None else list(lengths)
         self.starts = starts
 
-    def reference(self):
+    def reference(self, one_part=False):
         L, B, H, R, n, T, block, g = self.dims
         q = oracle.to_f32(self.qh).astype(np.float64)
         return oracle.serving.attend(q, self.pay, self.meta, self.G, self.layer, block, np.float64(np.float32(self.scale)),
-                                     self.causal, self.lengths, self.starts, fp32=not self.bf16)
+                                     self.causal, self.lengths, self.starts, fp32=not self.bf16, one_part=one_part)
 
     def device(self):
         t = __import__("torch")
@@ -68,6 +68,45 @@ class Case:
         cg.cg_attend(self.shape, self.payd, self.metad, self.gauge, self.codec, at, self.q if q is None else q, out,
                      ls, ms, ws, stream)
         return out, ls, ms
+
+
+FEW = 64         # rows (queries times heads of a group) of the few-row form at most
+
+
+def form(case, mass):
+    """(rows of a KV head, whether the few-row form takes them, splits) of a case with one
+    sequence, read off the workspace it asks for."""
+    L, B, H, R, n, T, block, g = case.dims
+    assert B == 1
+    at = case.attn()
+    need = cg.cg_attend_workspace_bytes(case.shape, case.gauge, case.codec, at, mass)
+    rows = n * R
+    up = lambda x: -(-x // 256) * 256
+    if mass:
+        need -= up(H * rows * 8 * (case.cap // min(block, 32)))
+    found = set()
+    for few in (True, False):
+        for splits in range(1, 1025):
+            parts = H * rows * splits
+            size = up(parts * 512) + up(parts * 8) if splits > 1 else up(parts * 8) if few and mass else 0
+            if not few and mass:
+                size += up(H * rows * 4)
+            if size == need and few == (rows <= FEW):
+                found.add((rows, few, splits))
+    assert len(found) == 1, (need, found)
+    return found.pop()
+
+
+def check_outputs(case):
+    """The case with no optional output, the log-sums, and those with the blocks' weights,
+    each within the bounds of the variant that then runs."""
+    L, B, H, R, n, T, block, g = case.dims
+    two = case.reference()
+    one = case.reference(one_part=True) if case.bf16 and n * R > FEW else two
+    check(case, case.run(lse=False, mass=False), one, "out")
+    check(case, case.run(lse=True, mass=False), two, "out, lse")
+    check(case, case.run(lse=True, mass=True), two, "out, lse, mass")
+    return two
 
 
 def check(case, got, ref=None, where=None):

@@ -66,3 +66,26 @@ def test_keep_blocks_brute_force():
                 for j in range(sink, n - recent):
                     if j not in mid:
                         assert (w[i], -i) > (w[j], -j)
+
+
+def test_bounds_of_queries_in_one_part():
+    """Attention of queries whose gauged channels are rounded to fp16, formed in 64 bits, stays
+    within the one-part bound."""
+    for seed, g, qscale in ((5, 16, 1.0), (6, 128, 8.0), (7, 8, 0.01)):
+        c = Case(seed, B=1, H=1, R=2, n=5, T=90, block=16, g=g, qscale=qscale)
+        ref = c.reference(one_part=True)
+        K, V = (np.repeat(c.meta[0, kind, 0, 0], 16, 0)[:90].astype(np.float64) for kind in (0, 1))
+        K, V = (m[:, :1] + m[:, 1:] * c.pay[0, kind, 0, 0, :90] for kind, m in ((0, K), (1, V)))
+        GK, GV = (oracle.serving.dense(c.G[0, kind, 0]) for kind in (0, 1))
+        worst = 0.0
+        for i in range(5):
+            for j in range(2):
+                x = GK @ oracle.to_f32(c.qh)[0, i, j].astype(np.float64)
+                up = 2.0 ** (13 - np.floor(np.log2(np.abs(x).max())))
+                x = (x * up).astype(np.float16).astype(np.float64) / up
+                s = (K[:86 + i] @ x) * np.float64(np.float32(c.scale))
+                p = np.exp(s - s.max())
+                err = np.abs((p / p.sum()) @ V[:86 + i] @ GV - ref["out"][0, i, j])
+                assert np.all(err <= ref["out_tol"][0, i, j])
+                worst = max(worst, float((err / ref["out_tol"][0, i, j]).max()))
+        assert worst > 0                    # the rounding was there
