@@ -121,13 +121,6 @@ def attend(q, payload, meta, G, layer, block, scale, causal, lengths, starts=Non
     return dict(out=out, out_tol=tol, lse=lse, lse_tol=lse_tol, mass=mass, mass_tol=mass_tol)
 
 
-def append_rows(raw_old, new, T_old, block):
-    """Raw rows of one field after an append, for the blocks it touches:
-    (first block's number, rows from that block's start to the end)."""
-    head = T_old // block * block
-    return head // block, np.concatenate([raw_old[head:T_old], new], 0)
-
-
 def quantize(x, block):
     """Gauged fp32 rows from a block's start on -> (codes, [(min, step)]), the
     encoder's fp32 operations."""
