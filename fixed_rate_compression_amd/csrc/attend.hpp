@@ -16,13 +16,15 @@
 //
 // Query rows: a KV head's rows are (query i, head j of the group), row
 // i ratio + j; a row tile is 16 of them.  q' is scaled by a power of two that
-// puts the row's largest magnitude in [2^13, 2^14) and held in two fixed-point
-// parts, hi a multiple of 2^4 and lo of 2^-7 (2^-22 of the largest): each
-// part's sum over 128 centred codes is a whole number of at most 2^24 units,
-// so the matrix cores, which round their fp32 sums towards zero, add it
-// without a rounding (as two floating parts in one sum, fp32 outputs were off
-// by 1e-5, now by 1e-6).  sum q' is that of the parts, so a rounding of q'
-// perturbs the query and not the balance of the two terms of s_t.
+// puts the row's largest magnitude in [2^13, 2^14) and held in two fp16 parts: hi, a
+// multiple of 2^3, and lo, what is left of it (2^2 at most, so off by 2^-10: 2^-23 of
+// the largest; a channel below 2^-11 of that by 2^-12 of itself).  The sum of hi over 128
+// centred codes is a whole number of units, at most 2^25 and hardly ever beyond 2^24, so
+// the matrix cores, which round their fp32 sums towards zero, add it without a
+// rounding; that of lo is 2^-11 of it (as two floating parts in one sum, fp32 outputs
+// were off by 1e-5; with lo in fixed point, 2^-21 of the largest, log-sums of 45 and 5
+// tokens by 1.3e-7 and 3.0e-7, now by 0.6e-7 and 1.2e-7).  sum q' is that of the parts,
+// so a rounding of q' perturbs the query and not the balance of the two terms of s_t.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -354,20 +356,20 @@ __device__ __forceinline__ FragScale frag_scale(float mx) {
 }
 
 // 8 channels u, v of a row as fp16 operands, their sum added to `sum`.  TWO: two
-// fixed-point parts; else one, each channel rounded to 2^-11.
+// parts as above; else one, each channel rounded to 2^-11.
 template <bool TWO>
 __device__ __forceinline__ void frag_parts(f4_t u, f4_t v, float up, h8_t &hi, h8_t &lo, float &sum) {
-  constexpr float H = 1.5f * 134217728.0f, L = 1.5f * 65536.0f;  // x + H - H rounds to multiples of 2^4, L of 2^-7
+  constexpr float H = 1.5f * 67108864.0f;  // x + H - H rounds to multiples of 2^3
   uint32_t wh[4], wl[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) {
     const float x = (k < 2 ? u[2 * k] : v[2 * k - 4]) * up, y = (k < 2 ? u[2 * k + 1] : v[2 * k - 3]) * up;
     if constexpr (TWO) {
       const float xh = (x + H) - H, yh = (y + H) - H;
-      const float xl = ((x - xh) + L) - L, yl = ((y - yh) + L) - L;
-      wh[k] = pack_f16x2(xh, yh);  // both parts are exact in fp16
-      wl[k] = pack_f16x2(xl, yl);
-      sum += (xh + xl) + (yh + yl);
+      wh[k] = pack_f16x2(xh, yh);  // exact
+      wl[k] = pack_f16x2(x - xh, y - yh);
+      const f2_t l = unpack_f16x2(wl[k]);
+      sum += (xh + l.x) + (yh + l.y);
     } else {
       wh[k] = pack_f16x2(x, y);
       wl[k] = 0u;

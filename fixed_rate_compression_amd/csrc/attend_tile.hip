@@ -95,7 +95,7 @@ struct TileQueries {
 };
 
 // The fp16 operands of a wave's 32 gauged rows xs [32][PITCH]: the scale and the two
-// fixed-point parts of make_frags, or one part (a channel rounded to 2^-11).
+// parts of make_frags, or one part (a channel rounded to 2^-11).
 template <bool TWO>
 __device__ __forceinline__ void tile_queries(const float *xs, float c, TileQueries &q, h8_t (&lo)[8]) {
   const int lane = threadIdx.x & 63, half = lane >> 5;

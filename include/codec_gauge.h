@@ -461,9 +461,9 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  * is NaN; a value block's NaN range reaches out alone.  Queries that see nothing
  * of such a block are not touched by it.
  * Scores, sums and weights of a sum are fp32; the operands of the matrix products
- * are fp16: queries in two parts (2^-22), in one (2^-11) for bf16 storage with more
- * than 64 rows a KV head and neither lse nor mass; weights for fp32 storage in two
- * parts, for bf16 storage in one (2^-11).
+ * are fp16: queries in two parts (2^-23 of a row's largest channel), in one (2^-11
+ * of a channel) for bf16 storage with more than 64 rows a KV head and neither lse nor
+ * mass; weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
  * The order of sums depends on the shape and the lengths only (deterministic).
  * The workspace belongs to one call at a time.  Asynchronous on stream.
  */

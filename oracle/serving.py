@@ -35,7 +35,7 @@ def attend(q, payload, meta, G, layer, block, scale, causal, lengths, starts=Non
 
     Bounds, with u = 2^-24 and per row S = max_t sum_c |q'_c| (|mn_t| + 255 st_t):
     q' is an fp32 chain over g channels (g u sum |G| |q| a channel), split into
-    two fp16 parts (2^-22 of the row's largest |q'| at most, each), its product
+    two fp16 parts (2^-23 of the row's largest |q'| at most), its product
     with the codes a sum of 256 terms in fp32 and two more operations, so a
     score in units of log2 is off by at most
       ds = scale log2(e) (2^-16 S + g u S_g),
