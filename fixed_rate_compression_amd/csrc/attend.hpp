@@ -7,10 +7,12 @@
 //   u   = sum_t p_t v'_t = sum_t (p_t sv_b) code_t + sum_t p_t mv_b,  p_t = 2^(s_t - m)
 //   out = G_V^T u / sum_t p_t
 // so both products run on the codes themselves and the ranges are applied to
-// scores and weights.  For the values the code is taken less 128 and the
-// minimum plus 128 sv_b: the matrix cores' fp32 sums then hold the values'
-// deviations and not 128 times the sum of the weights, against which a mean
-// over many tokens is small (uncentred, 262144 tokens lose 2^-9 of the output).  A code c = 0 .. 255 placed in the low byte of an fp16
+// scores and weights.  For the values the code is taken less a centre z and the
+// minimum plus z sv_b: the matrix cores' fp32 sums then hold the values'
+// deviations and not z times the sum of the weights, against which a mean
+// over many tokens is small (uncentred, 262144 tokens lose 2^-9 of the output).  z is
+// 128 for bf16 storage and the code of the value 0 for fp32 storage, there for the keys
+// as well (see Centre).  A code c = 0 .. 255 placed in the low byte of an fp16
 // is the subnormal c 2^-24, which the matrix cores multiply exactly: widening
 // a dword of codes costs two byte permutes and no conversion.
 //
@@ -19,7 +21,7 @@
 // puts the row's largest magnitude in [2^13, 2^14) and held in two fp16 parts: hi, a
 // multiple of 2^3, and lo, what is left of it (2^2 at most, so off by 2^-10: 2^-23 of
 // the largest; a channel below 2^-11 of that by 2^-12 of itself).  The sum of hi over 128
-// centred codes is a whole number of units, at most 2^25 and hardly ever beyond 2^24, so
+// centred codes is a whole number of units, 2^26 at most and hardly ever beyond 2^24, so
 // the matrix cores, which round their fp32 sums towards zero, add it without a
 // rounding; that of lo is 2^-11 of it (as two floating parts in one sum, fp32 outputs
 // were off by 1e-5; with lo in fixed point, 2^-21 of the largest, log-sums of 45 and 5
@@ -117,18 +119,34 @@ __device__ __forceinline__ uint32_t bytes2(uint32_t w) {
 // matrix cores align the products of a sum by their exponent fields and cut
 // what lies below: with subnormal operands, whose significands begin with
 // zeros, sums of weights of unlike sizes kept 17 bits, with these 24.
-__device__ __forceinline__ uint32_t centred(uint32_t w) {
-  const h2_t up = {(_Float16)32768.0f, (_Float16)32768.0f}, c = {(_Float16)-0.25f, (_Float16)-0.25f};
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(h2_t, w), up, c));
+// c: the centre times -2^-9, in both halves.
+constexpr uint32_t kMiddle = 0xb400b400u;  // 128
+__device__ __forceinline__ uint32_t centred(uint32_t w, uint32_t c) {
+  const h2_t up = {(_Float16)32768.0f, (_Float16)32768.0f};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(h2_t, w), up, __builtin_bit_cast(h2_t, c)));
 }
 constexpr float kCodeUnit = 16777216.0f;  // 2^24: codes as they are
 constexpr float kCentredUnit = 512.0f;    // 2^9: centred codes
 
-// 8 consecutive codes (two dwords) as fp16 subnormals, CENTRED: less 128
+// fp32 storage: a block's codes less the one nearest to the value 0, so that products are
+// with the values themselves.  Around the middle of a range that lies to one side of 0 the
+// two terms of a score or an output nearly cancel, and the larger one's rounding stays:
+// equal weights over 58 values of ranges around 0 were off by 2.5e-6, by fp32 products
+// 0.25e-6.  The differences, at most 255, have 9 bits.
+struct Centre {
+  float mid;   // the value of the centre: half a step from 0, or the end of the range
+  uint32_t c;
+};
+__device__ __forceinline__ Centre centre_of(float2 m) {  // of a (minimum, step), whatever they are: 0 .. 255
+  const float z = fminf(fmaxf(rintf(-m.x * __builtin_amdgcn_rcpf(m.y)), 0.0f), 255.0f);
+  return Centre{__builtin_fmaf(z, m.y, m.x), pack_f16x2(z * -0x1p-9f, z * -0x1p-9f)};
+}
+
+// 8 consecutive codes (two dwords) as fp16 subnormals, CENTRED: less a centre
 template <bool CENTRED>
-__device__ __forceinline__ h8_t codes8(uint32_t a, uint32_t b) {
+__device__ __forceinline__ h8_t codes8(uint32_t a, uint32_t b, uint32_t c = kMiddle) {
   if constexpr (CENTRED)
-    return as_h8(centred(bytes2<0>(a)), centred(bytes2<2>(a)), centred(bytes2<0>(b)), centred(bytes2<2>(b)));
+    return as_h8(centred(bytes2<0>(a), c), centred(bytes2<2>(a), c), centred(bytes2<0>(b), c), centred(bytes2<2>(b), c));
   else
     return as_h8(bytes2<0>(a), bytes2<2>(a), bytes2<0>(b), bytes2<2>(b));
 }

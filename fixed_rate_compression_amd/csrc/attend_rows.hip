@@ -72,16 +72,17 @@ __device__ __forceinline__ void load_values(const AttendArgs &a, const uint8_t *
   u.m[1] = vm[((int64_t)t0 + second) >> a.bshift];
 }
 
+// c: the centres of the two tiles
 template <int J>
-__device__ __forceinline__ h8_t value_frag(const RawValues &u) {
+__device__ __forceinline__ h8_t value_frag(const RawValues &u, const uint32_t (&c)[2]) {
   constexpr int B = J & 3;
   uint32_t w[2][4];
 #pragma unroll
   for (int t = 0; t < 2; t++)
 #pragma unroll
     for (int i = 0; i < 4; i++) w[t][i] = J < 4 ? u.v[t][i].x : u.v[t][i].y;
-  return as_h8(centred(byte_pair<B>(w[0][0], w[0][1])), centred(byte_pair<B>(w[0][2], w[0][3])),
-               centred(byte_pair<B>(w[1][0], w[1][1])), centred(byte_pair<B>(w[1][2], w[1][3])));
+  return as_h8(centred(byte_pair<B>(w[0][0], w[0][1]), c[0]), centred(byte_pair<B>(w[0][2], w[0][3]), c[0]),
+               centred(byte_pair<B>(w[1][0], w[1][1]), c[1]), centred(byte_pair<B>(w[1][2], w[1][3]), c[1]));
 }
 
 // a row's running state, the same in its four lanes but for l and mv
@@ -90,9 +91,10 @@ struct RowState {
   float l, mv;          // this lane's part of the sums of p and of p mv_b
 };
 
-// fp32 storage: the weights in two fp16 parts, the keys' codes centred like the
-// values' (scores to 2^-22 of the sum of |q'| 255 step; uncentred 10 times
-// that).  bf16 storage: the weights are one fp16 part (2^-11 of a weight).
+// fp32 storage: the weights in two fp16 parts, keys' and values' codes around the value 0
+// (scores to 2^-22 of the sum of |q' k'|; with codes as they are 10 times that of
+// |q'| 255 step).  bf16 storage: the weights are one fp16 part (2^-11 of a weight),
+// the values' codes less 128.
 template <bool BF16, bool MASS, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_rows(const AttendArgs a) {
   __shared__ __align__(16) float lds[NW * ROWS * PITCH];
@@ -220,25 +222,31 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
 #pragma unroll
     for (int t = 0; t < 2; t++) {
       f4_t z = f4_t{0.f, 0.f, 0.f, 0.f}, zl = z;
+      Centre ck{uk.m[t].x, 0u};
+      if constexpr (!BF16) ck = centre_of(uk.m[t]);
 #pragma unroll
       for (int x = 0; x < 2; x++) {
-        const h8_t c0 = codes8<!BF16>(uk.k[t][x].x, uk.k[t][x].y), c1 = codes8<!BF16>(uk.k[t][x].z, uk.k[t][x].w);
+        const h8_t c0 = codes8<!BF16>(uk.k[t][x].x, uk.k[t][x].y, ck.c), c1 = codes8<!BF16>(uk.k[t][x].z, uk.k[t][x].w, ck.c);
         z = mfma(c0, q.hi[2 * x], z);
         z = mfma(c1, q.hi[2 * x + 1], z);
         zl = mfma(c0, q.lo[2 * x], zl);
         zl = mfma(c1, q.lo[2 * x + 1], zl);
       }
       z += zl;
-      const float A = uk.m[t].y * q.ca, Bm = (BF16 ? uk.m[t].x : __builtin_fmaf(128.0f, uk.m[t].y, uk.m[t].x)) * q.cq;
+      const float A = uk.m[t].y * q.ca, Bm = ck.mid * q.cq;
 #pragma unroll
       for (int r = 0; r < 4; r++) s[t][r] = __builtin_fmaf(z[r], A, Bm);
     }
     if (more) load_keys(a, kf, km, t0 + NW * UNIT, uk);
     float vst[2], vmn[2];
+    uint32_t vc[2];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
+      Centre cv{__builtin_fmaf(128.0f, uv.m[t].y, uv.m[t].x), kMiddle};
+      if constexpr (!BF16) cv = centre_of(uv.m[t]);
       vst[t] = uv.m[t].y;
-      vmn[t] = __builtin_fmaf(128.0f, uv.m[t].y, uv.m[t].x);  // the value of code 128
+      vmn[t] = cv.mid;  // the value of the centre
+      vc[t] = cv.c;
     }
     if (t0 + UNIT > all) {
 #pragma unroll
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     if constexpr (!BF16) Pl = as_h8(pl[0][0], pl[0][1], pl[1][0], pl[1][1]);
 #define CG_PV(J)                                        \
   {                                                     \
-    const h8_t vj = value_frag<J>(uv);                   \
+    const h8_t vj = value_frag<J>(uv, vc);              \
     acc[J] = mfma(vj, P, acc[J]);                       \
     if constexpr (!BF16) acc[J] = mfma(vj, Pl, acc[J]); \
   }

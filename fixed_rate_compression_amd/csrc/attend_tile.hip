@@ -44,41 +44,68 @@ __device__ __forceinline__ f16_t mfma32(h8_t a, h8_t b, f16_t c) {
 
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));  // stays in registers through a loop (a uint4 member did not)
 
+template <bool BF16>
 struct UnitRegs {
   u4_t k, v;
-  float2 m;
+  float2 m[BF16 ? 1 : 2];
 };
 
 // a unit's codes into registers: 16 bytes of a key and a value row to a thread;
 // tokens past the capacity repeat its last row
+template <bool BF16>
 __device__ __forceinline__ void fetch_unit(const AttendArgs &a, const uint8_t *kf, const uint8_t *vf,
-                                           const float2 *km, const float2 *vm, int un, UnitRegs &s) {
+                                           const float2 *km, const float2 *vm, int un, UnitRegs<BF16> &s) {
   const int i = threadIdx.x;
   const int64_t t = min((int64_t)un * UNIT + (i >> 3), a.tcap - 1);
   s.k = *(const u4_t *)(kf + t * D + 16 * (i & 7));
   s.v = *(const u4_t *)(vf + t * D + 16 * (i & 7));
-  // two 16-token tiles: key ranges, value ranges (lanes 0 .. 3 store them)
-  const int64_t blk = min(((int64_t)un * UNIT + 16 * (i & 1)) >> a.bshift, a.nblk - 1);
-  s.m = ((i & 2) ? vm : km)[blk];
+  // two 16-token tiles: key ranges, value ranges (lanes 0 .. 3 store them); fp32
+  // storage: those of the thread's token, whose codes they centre
+  const int64_t blk = min(((int64_t)un * UNIT + (BF16 ? 16 * (i & 1) : (i >> 3) & 16)) >> a.bshift, a.nblk - 1);
+  if constexpr (BF16) {
+    s.m[0] = ((i & 2) ? vm : km)[blk];
+  } else {
+    s.m[0] = km[blk];
+    s.m[1] = vm[blk];
+  }
 }
 
 // widened into LDS, once for the four waves (keys centred where both query
-// parts take part: then their sums are exact)
-template <bool LO>
-__device__ __forceinline__ void put_unit(unsigned char *lds, int un, int tmax, const UnitRegs &s) {
+// parts take part; around the value 0 for fp32 storage)
+template <bool BF16, bool LO>
+__device__ __forceinline__ void put_unit(unsigned char *lds, int un, int tmax, const UnitRegs<BF16> &s) {
   const int i = threadIdx.x;
   unsigned char *k = lds + KBUF + (un & 1) * KBYTES + (i >> 3) * KP + 32 * (i & 7);
   unsigned char *v = lds + VBUF + (un % 3) * VBYTES + (i >> 3) * VP + 32 * (i & 7);
-  *(h8_t *)k = codes8<LO>(s.k.x, s.k.y);
-  *(h8_t *)(k + 16) = codes8<LO>(s.k.z, s.k.w);
-  *(h8_t *)v = codes8<true>(s.v.x, s.v.y);
-  *(h8_t *)(v + 16) = codes8<true>(s.v.z, s.v.w);
-  if (i < 4) {
-    const bool there = un * UNIT + 16 * (i & 1) < tmax;  // a block that holds no row yet is not looked at
-    const float mid = LO || (i & 2) ? __builtin_fmaf(128.0f, s.m.y, s.m.x) : s.m.x;  // the value of code 128 (0)
-    const float st = there ? s.m.y : 0.0f;
-    *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * i) =
-        make_float2(there ? mid : 0.0f, (i & 2) ? fminf(fmaxf(__builtin_amdgcn_logf(st), -200.0f), 128.0f) : st);  // values: log2 of the step
+  // the range that this thread stores (entries: keys of both tiles, values of both) and
+  // the value of its centre
+  Centre ck{0.0f, kMiddle}, cv = ck;
+  int e;
+  float2 m;
+  float mid;
+  bool mine;
+  if constexpr (BF16) {
+    e = i;
+    mine = i < 4;
+    m = s.m[0];
+    mid = LO || (i & 2) ? __builtin_fmaf(128.0f, m.y, m.x) : m.x;
+  } else {
+    ck = centre_of(s.m[0]);
+    cv = centre_of(s.m[1]);
+    e = 2 * (i & 1) + (i >> 7);
+    mine = (i & 127) < 2;
+    m = i & 1 ? s.m[1] : s.m[0];
+    mid = i & 1 ? cv.mid : ck.mid;
+  }
+  *(h8_t *)k = codes8<LO>(s.k.x, s.k.y, ck.c);
+  *(h8_t *)(k + 16) = codes8<LO>(s.k.z, s.k.w, ck.c);
+  *(h8_t *)v = codes8<true>(s.v.x, s.v.y, cv.c);
+  *(h8_t *)(v + 16) = codes8<true>(s.v.z, s.v.w, cv.c);
+  if (mine) {
+    const bool there = un * UNIT + 16 * (e & 1) < tmax;  // a block that holds no row yet is not looked at
+    const float st = there ? m.y : 0.0f;
+    *(float2 *)(lds + MBUF + (un % 3) * 32 + 8 * e) =
+        make_float2(there ? mid : 0.0f, (e & 2) ? fminf(fmaxf(__builtin_amdgcn_logf(st), -200.0f), 128.0f) : st);  // values: log2 of the step
   }
 }
 
@@ -126,7 +153,7 @@ __device__ __forceinline__ void tile_queries(const float *xs, float c, TileQueri
 template <int NB>
 struct UnitWeights {
   float p[16];
-  float ps[NB], mid[NB];  // sums of p_t, values of code 128
+  float ps[NB], mid[NB];  // sums of p_t, values of the centres
 };
 
 // scores of a unit: z = K Q^T, z[r] that of token 8 (r / 4) + 4 half + r % 4,
@@ -355,8 +382,8 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
   const int u0 = split_begin(units, split, a.splits), u1 = split_begin(units, split + 1, a.splits);
-  UnitRegs nx;
-  if (u0 < u1) fetch_unit(a, kf, vf, km, vm, u0, nx);
+  UnitRegs<BF16> nx;
+  if (u0 < u1) fetch_unit<BF16>(a, kf, vf, km, vm, u0, nx);
 
   // gauged queries as operands
   TileQueries q;
@@ -413,17 +440,17 @@ __global__ __launch_bounds__(NTH, 2) void k_attend_tile(const AttendArgs a) {
   if (u0 < u1) {
     UnitWeights<NB> o;
     UnitOperands<BF16> P;
-    put_unit<LO>(lds, u0, tmax, nx);
-    fetch_unit(a, kf, vf, km, vm, u0 + 1, nx);  // units past the last are fetched (rows that exist) and not used
-    put_unit<LO>(lds, u0 + 1, tmax, nx);
-    fetch_unit(a, kf, vf, km, vm, u0 + 2, nx);
+    put_unit<BF16, LO>(lds, u0, tmax, nx);
+    fetch_unit<BF16>(a, kf, vf, km, vm, u0 + 1, nx);  // units past the last are fetched (rows that exist) and not used
+    put_unit<BF16, LO>(lds, u0 + 1, tmax, nx);
+    fetch_unit<BF16>(a, kf, vf, km, vm, u0 + 2, nx);
     __syncthreads();
     raise<LO, NB>(keys_at(u0), lo, ranges_at(u0), q, lim - u0 * UNIT - 4 * half, st, acc, o);
     if constexpr (SUMS) store_sums<NB>(a, bh, u0, wr, half, o, st.mu);
     const auto turn = [&](int un, auto masked) {
       __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
-      put_unit<LO>(lds, un + 2, tmax, nx);
-      fetch_unit(a, kf, vf, km, vm, un + 3, nx);
+      put_unit<BF16, LO>(lds, un + 2, tmax, nx);
+      fetch_unit<BF16>(a, kf, vf, km, vm, un + 3, nx);
       const float2 *mt = ranges_at(un + 1);
       const int vis = lim - (un + 1) * UNIT - 4 * half;
       take_weights<BF16, NB>(o, st, P);

@@ -32,3 +32,44 @@ def test_small_channels_of_a_query(T, n):
     for mass in (False, True):
         got = to_host(c.run(lse=True, mass=mass)[1]).astype(np.float64)
         assert np.all(np.abs(got - ref["lse"]) <= 2.0 ** -12 + 2.0 ** -20), float(np.abs(got - ref["lse"]).max())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("T,n", FORMS)
+def test_values_of_zero_beside_wide_ranges(T, n, block, causal):
+    """Channels whose cached values are all 0, in blocks whose range reaches far to one side of 0
+    for other channels: every product is with 0, so any weights give 0 exactly."""
+    rng = np.random.default_rng(T + n + block)
+    c = Case(920 + n, T=T, n=n, B=1, H=2, R=4, g=0, block=block, bf16=False, causal=causal)
+    zero = rng.integers(0, 256, c.meta[0, 1, ..., 0].shape)              # the code of 0 in each block
+    zero[..., ::5] = 0
+    zero[..., 1::5] = 255
+    step = np.exp2(rng.integers(-6, 7, zero.shape)).astype(np.float32)
+    c.meta[0, 1, ..., 0], c.meta[0, 1, ..., 1] = -step * zero, step      # exact
+    at = np.repeat(zero, block, -1)[..., None]
+    c.pay[0, 1] = np.where(np.arange(D) % 3 == 0, at, c.pay[0, 1])
+    c.device()
+    for lse, mass in ((False, False), (True, True)):
+        out = to_host(c.run(lse=lse, mass=mass)[0])
+        assert not out[..., ::3].any(), float(np.abs(out[..., ::3]).max())
+        assert out[..., 1::3].all()
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("T,n", FORMS)
+def test_keys_of_zero_beside_wide_ranges(T, n, block):
+    """Keys of 0 in blocks whose range reaches far: scores are 0 exactly, the log-sum that of the
+    number of visible tokens: 2^-22 of it for log2 and its factor, 2^-22 for a power of two and
+    its reciprocal that each weight may carry (a unit in the last place each)."""
+    rng = np.random.default_rng(T + n + block + 1)
+    c = Case(940 + n, T=T, n=n, B=1, H=2, R=4, g=0, block=block, bf16=False, scale=1000.0)
+    zero = rng.integers(0, 256, c.meta[0, 0, ..., 0].shape)
+    step = np.exp2(rng.integers(-3, 4, zero.shape)).astype(np.float32)
+    c.meta[0, 0, ..., 0], c.meta[0, 0, ..., 1] = -step * zero, step
+    c.pay[0, 0] = np.repeat(zero, block, -1)[..., None]
+    c.device()
+    want = np.log(np.arange(T - n + 1, T + 1, dtype=np.float64))[None, :, None]
+    for mass in (False, True):
+        got = to_host(c.run(lse=True, mass=mass)[1]).astype(np.float64)
+        assert np.all(np.abs(got - want) <= 2.0 ** -22 * want + 2.0 ** -22), float(np.abs(got - want).max())
