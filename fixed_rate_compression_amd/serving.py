@@ -95,7 +95,7 @@ class ServingCache:
                                                                      self.mass is not None)
         if not self._work or self._work[-1].numel() < need:
             size = max(need, 16, self._work[-1].numel() * 3 // 2 if self._work else 0)
-            self._work.append(torch.empty(size, dtype=torch.uint8, device="cuda"))
+            self._work.append(torch.empty(size, dtype=torch.uint8, device=self.payload.device))
         cg.cg_attend(self.shape, self.payload, self.meta, self.gauge, self.codec, at, q, out, lse, self.mass,
                      self._work[-1])
         return out
@@ -109,7 +109,7 @@ class ServingCache:
         if self.mass is None:
             raise ValueError("the cache was made without with_mass")
         s = self.shape
-        kept = torch.empty((s.layers, s.batch, s.heads, max(budget, 0)), dtype=torch.int32, device="cuda")
+        kept = torch.empty((s.layers, s.batch, s.heads, max(budget, 0)), dtype=torch.int32, device=self.payload.device)
         cg.cg_evict(s, self.codec, budget, sink, recent, self.mass, self.payload, self.meta, s, self.payload, self.meta,
                     self.mass, kept, self.lengths, self.lengths)
         self.most = min(self.most, budget * self.codec.block_tokens)

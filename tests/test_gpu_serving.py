@@ -261,3 +261,23 @@ def test_a_layers_rows_go_in_once_a_step():
     with pytest.raises(ValueError):
         c.append(0, k[:, :2], k[:, :2])      # a refused call has put nothing in
     c.append(0, k[:, :1], k[:, :1])
+
+
+def test_buffers_are_made_where_the_cache_lies(monkeypatch):
+    """Workspaces and results name the cache's GPU, not the current one: a workspace made
+    elsewhere by a call that is refused for it would be kept and refused from then on."""
+    t = torch()
+    c = ServingCache(1, 1, 1, 2, 64, cg.make_gauge(0), 16, with_mass=True)
+    k = t.zeros((1, 20, 1, D), dtype=t.bfloat16, device="cuda")
+    made, empty = [], t.empty
+
+    def record(*a, **kw):
+        made.append(t.device(kw["device"]))
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(t, "empty", record)
+    c.begin(20)
+    c.append(0, k, k)
+    c.attend(0, t.zeros((1, 20, 2, D), dtype=t.bfloat16, device="cuda"))
+    c.evict(2)
+    assert len(made) >= 3 and all(d == c.payload.device for d in made), made      # "cuda" alone is the current one
