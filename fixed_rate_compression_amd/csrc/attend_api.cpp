@@ -61,10 +61,10 @@ int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
 
 // Splits of 128-row tiles.  A workgroup takes 24 ns a token on a compute unit of
 // its own and 36 beside another (512 at once), after about 6 us; a merge moves
-// every split's sums twice (5 us and 4.5 TB/s).  8 KV heads x 4 query heads, a
-// prompt of 300 / 500 / 1000 tokens: 14.6 / 19.4 / 32.2 us, in two splits 18.3 /
-// 22.5 / 36.9; 512 queries over 2048 and 8192 tokens: 54 and 191 us, in two splits 42
-// and 117, in four 40 and 100; 1024 over 8192: 206 and in two 175.
+// every split's sums twice (5 us and 4.5 TB/s).  8 KV heads x 4 query heads, whole
+// calls: a prompt of 300 / 500 / 1000 tokens 18.7 / 23 / 35 us, in two splits 25 / 31 /
+// 45, in four 32 / 38 / 60; 512 queries over 2048 and 8192 tokens: 56 and 183 us, in two
+// splits 49 and 113, in four 49 and 100; 1024 over 8192: 186, in two 169, in four 181.
 constexpr int64_t kTargetTiles = 512;
 
 int64_t tile_splits(int64_t work, int64_t rows, int64_t tokens) {

@@ -25,8 +25,8 @@
 // 262144 tokens of 8 KV heads: 95 us, 5.6 TB/s of the 5.97 that a plain sum of the
 // same bytes reaches, the codes read once.  16 sequences of 0 .. 8192 tokens 23 us
 // (5.2 TB/s), with block sums 8 sequences of 0 .. 16384 31 us (4.5 TB/s: two
-// workgroups a compute unit for the registers, three spill), one sequence of 1000
-// tokens 11.7 us, all of it latency.
+// workgroups a compute unit for the registers, three spill), one sequence of 1024
+// tokens 11.3 us, all of it latency.
 #include "attend.hpp"
 
 namespace cga {
