@@ -369,7 +369,7 @@ struct FragScale {
 };
 __device__ __forceinline__ FragScale frag_scale(float mx) {
   const int ex = mx > 0.0f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
-  const int sh = min(max(13 - ex, -100), 100);
+  const int sh = min(13 - ex, 126);  // -115 (an infinity) at least; both factors are normal numbers
   return FragScale{__uint_as_float((uint32_t)(127 + sh) << 23), __uint_as_float((uint32_t)(127 - sh) << 23)};
 }
 

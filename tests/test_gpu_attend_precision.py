@@ -73,3 +73,23 @@ def test_keys_of_zero_beside_wide_ranges(T, n, block):
     for mass in (False, True):
         got = to_host(c.run(lse=True, mass=mass)[1]).astype(np.float64)
         assert np.all(np.abs(got - want) <= 2.0 ** -22 * want + 2.0 ** -22), float(np.abs(got - want).max())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,n", FORMS)
+@pytest.mark.parametrize("e", [-100, -90, 90, 116])
+def test_powers_of_two_between_queries_and_keys(e, T, n, bf16):
+    """Queries 2^e times as large on keys 2^e times as small: the same products and the same
+    roundings, so the same bits.  (2^-13 of a row's largest channel times scale log2(e), 2^-120
+    at -100, is a normal number; at -112 it would have 17 bits.)"""
+    t = __import__("torch")
+    c = Case(960 + n, T=T, n=n, B=1, H=2, R=4, block=32, bf16=bf16, spread=0.5, scale=2.0 ** -8)
+    c.meta[:, 0] *= 2.0 ** 5
+    c.device()
+    kinds = ((False, False), (True, False), (True, True))
+    want = [c.run(lse=a, mass=b) for a, b in kinds]
+    c.q = (c.q.float() * 2.0 ** e).to(c.q.dtype)
+    c.metad[:, 0] *= 2.0 ** -e
+    for (a, b), w in zip(kinds, want):
+        for x, y in zip(c.run(lse=a, mass=b), w):
+            assert x is None or t.equal(x, y), (a, b)
