@@ -26,7 +26,7 @@ EXPORTED = ["cg_encoded_bytes", "cg_encode", "cg_decode", "cg_decode_gauged", "c
             "cg_gauge_apply", "cg_write_header", "cg_decode_error_workspace_bytes",
             "cg_decode_error", "cg_decode_error_noalloc", "cg_cache_error_summary", "cg_adamw_update", "cg_gauge_control",
             "cg_second_moment_workspace_bytes", "cg_second_moment", "cg_gauge_grad", "cg_gauge_heads",
-            "cg_attend_workspace_bytes", "cg_attend", "cg_append", "cg_evict",
+            "cg_attend_workspace_bytes", "cg_attend", "cg_append", "cg_evict", "cg_read", "cg_rotate",
             "cg_last_error"]
 
 CG_KEEP_KEYS, CG_KEEP_VALUES = 1, 2
@@ -75,6 +75,18 @@ class CgAttn(ctypes.Structure):
                 ("q_token_stride", ctypes.c_int64)]
 
 
+class CgRotary(ctypes.Structure):
+    _keep = ()      # the tensors freq and the weights point into (make_rotary)
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("dealt", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("eps", ctypes.c_float),
+                ("magnitude", ctypes.c_float), ("freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+class CgRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
 class CodecGaugeError(RuntimeError):
     def __init__(self, fn, code, msg):
         super().__init__(f"{fn} failed with {code}: {msg}")
@@ -98,7 +110,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
         SP, GP, CP = ctypes.POINTER(CgShape), ctypes.POINTER(CgGauge), ctypes.POINTER(CgCodec)
-        U64P, AP = ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(CgAttn)
+        U64P, AP, RP = ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(CgAttn), ctypes.POINTER(CgRows)
         sig = {
             "cg_encoded_bytes": [SP, CP, U64P, U64P, U64P],
             "cg_encode": [SP, P, GP, CP, I64, I64, P, U64, P, U64, P],
@@ -128,6 +140,8 @@ def lib():
             "cg_attend": [SP, P, U64, P, U64, GP, CP, AP, P, P, P, P, P, ctypes.c_size_t, P],
             "cg_append": [SP, GP, CP, I32, I32, P, P, I64, I64, P, P, P, P, U64, P, U64, P],
             "cg_evict": [SP, CP, I32, I32, I32, P, P, U64, P, U64, P, SP, P, U64, P, U64, P, P, P, P],
+            "cg_read": [SP, P, U64, P, U64, GP, CP, I32, I32, P, P, P, P, I64, I64, P],
+            "cg_rotate": [SP, ctypes.POINTER(CgRotary), I32, I32, P, P, P, RP, RP, RP, RP, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -493,27 +507,35 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
         _check("cg_attend", rc)
 
 
-def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, meta, lengths=None,
-              starts=None, stream=None):
-    """k_new, v_new [batch, n_new, heads, 128] with contiguous heads and the same strides
-    between sequences and between rows (of one sequence, or one row each: any)."""
-    st = _storage(shape)
-    row, at = shape.heads * shape.head_dim, None
-    ptrs = []
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
+def _kv_rows(shape, n, named):
+    """Rows [batch, n, heads, head_dim] of the storage format with contiguous heads, all lying alike
+    -> their addresses and (strides between sequences, between rows)."""
+    st, at, ptrs = _storage(shape), None, []
+    for name, t in named:
+        if t is None:
+            ptrs.append(None)
+            continue
         if t.dtype != _dtype(st):
             raise ValueError(f"{name} must be {st}, got {t.dtype}")
-        if t.shape != (shape.batch, n_new, shape.heads, shape.head_dim):
-            raise ValueError(f"{name} must be [batch, n_new, heads, head_dim], got {tuple(t.shape)}")
+        if t.shape != (shape.batch, n, shape.heads, shape.head_dim):
+            raise ValueError(f"{name} must be [batch, {n}, heads, head_dim], got {tuple(t.shape)}")
         sb, sr, sh, sd = t.stride()
-        if (shape.batch > 1 and sb == 0) or (n_new > 1 and sr == 0):
+        if (shape.batch > 1 and sb == 0) or (n > 1 and sr == 0):
             raise ValueError(f"{name}: rows of an expanded tensor")
-        lie = (sb if shape.batch > 1 else 0, sr if n_new > 1 else 0)
+        lie = (sb if shape.batch > 1 else 0, sr if n > 1 else 0)
         if (sh != shape.head_dim and shape.heads > 1) or sd != 1 or lie != (at or lie):
             raise ValueError(f"{name} of strides {t.stride()}: contiguous heads and equal strides are needed")
         at = lie
         ptrs.append(t.data_ptr())
-    bs, rs = at
+    return ptrs, at or (0, 0)
+
+
+def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, meta, lengths=None,
+              starts=None, stream=None):
+    """k_new, v_new [batch, n_new, heads, 128] with contiguous heads and the same strides
+    between sequences and between rows (of one sequence, or one row each: any)."""
+    st, row = _storage(shape), shape.heads * shape.head_dim
+    ptrs, (bs, rs) = _kv_rows(shape, n_new, (("k_new", k_new), ("v_new", v_new)))
     _gauge_sized(gauge, shape)
     dev = _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
     _check("cg_append", lib().cg_append(
@@ -521,6 +543,79 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
         _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
         _sized("tail", tail, st, shape.layers * 2 * shape.batch * row * codec.block_tokens),
         _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream_on(stream, dev)))
+
+
+def cg_read(shape, payload, meta, gauge, codec, layer, k_out, v_out, lengths=None, starts=None, stream=None):
+    """Rows starts .. of every sequence of the layer into k_out and v_out [batch, n, heads, 128] (contiguous
+    heads, equal strides; either may be None); rows that a sequence does not have are left as they were."""
+    if k_out is None and v_out is None:
+        raise ValueError("k_out and v_out are None")
+    n = (v_out if k_out is None else k_out).shape[1]
+    ptrs, (bs, rs) = _kv_rows(shape, n, (("k_out", k_out), ("v_out", v_out)))
+    _gauge_sized(gauge, shape)
+    dev = _here(k_out, v_out, payload, meta, lengths, starts, gauge._keep)
+    rc = lib().cg_read(
+        shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, layer, n,
+        _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch), *ptrs, bs, rs,
+        _stream_on(stream, dev))
+    if rc != CG_OK:
+        _check("cg_read", rc)
+
+
+def make_rotary(freq, sections=None, interleaved=False, dealt=False, q_weight=None, k_weight=None, eps=1e-6,
+                magnitude=1.0) -> CgRotary:
+    """freq: device float32 [dim / 2], radians a position; sections: pairs of each axis (None: one axis);
+    q_weight, k_weight: device float32 [head_dim] of the heads' norms (None: no norm)."""
+    sec = list(sections) if sections is not None and len(sections) > 1 else []
+    if len(sec) > 4:
+        raise ValueError(f"{len(sec)} axes: four at most")
+    for name, t in (("freq", freq), ("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None and (t.dtype != _dtype("float32") or not t.is_contiguous() or t.dim() != 1):
+            raise ValueError(f"{name} must be contiguous float32 of one axis")
+    r = CgRotary(2 * freq.numel(), 1 if interleaved else 0, max(1, len(sec)), 1 if dealt else 0,
+                 (ctypes.c_int32 * 4)(*sec), eps, magnitude, _ptr(freq), _ptr(q_weight), _ptr(k_weight))
+    r._keep = (freq, q_weight, k_weight)
+    return r
+
+
+def _rows(name, t, shape, heads=None):
+    """[batch, n, heads, head_dim] of the storage format -> CgRows."""
+    st = _storage(shape)
+    if t.dtype != _dtype(st):
+        raise ValueError(f"{name} must be {st}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[0] != shape.batch or t.shape[3] != shape.head_dim or (heads is not None and t.shape[2] != heads):
+        raise ValueError(f"{name} must be [batch, n, {heads or 'q_heads'}, head_dim], got {tuple(t.shape)}")
+    b, n, h, d = t.shape
+    sb, sr, sh, sd = t.stride()
+    if t.numel() and ((b > 1 and sb == 0) or (n > 1 and sr == 0) or (h > 1 and sh != d) or sd != 1):
+        raise ValueError(f"{name} of strides {t.stride()}: contiguous heads are needed, and rows of their own")
+    return CgRows(t.data_ptr(), sb if b > 1 else 0, sr if n > 1 else 0)
+
+
+def cg_rotate(shape, rotary, q, k, q_out, k_out, lengths=None, starts=None, positions=None, stream=None):
+    """Norm and rotation of q [batch, n, q_heads, 128] and k [batch, n, heads, 128] into q_out and k_out, which
+    may be q and k themselves; either pair may be None.  positions: device int32 [axes, batch, n] or None."""
+    pairs = [(q, q_out), (k, k_out)]
+    if any((x is None) != (y is None) for x, y in pairs) or (q is None and k is None):
+        raise ValueError("queries or keys, each with its output, are needed")
+    n, q_heads = (k if q is None else q).shape[1], 0 if q is None else q.shape[2]
+    rows = []
+    for name, x, heads in (("q", q, None), ("k", k, shape.heads), ("q_out", q_out, q_heads), ("k_out", k_out, shape.heads)):
+        if x is not None and x.dim() == 4 and x.shape[1] != n:
+            raise ValueError(f"{name} has {x.shape[1]} rows a sequence, not {n}")
+        rows.append(None if x is None else _rows(name, x, shape, heads))
+    for name, w in zip(("freq", "q_weight", "k_weight"), rotary._keep):
+        if w is not None and name != "freq" and w.numel() != shape.head_dim:
+            raise ValueError(f"{name}: {shape.head_dim} values are needed, got {w.numel()}")
+    if positions is not None and not isinstance(positions, int) and positions.shape != (rotary.axes, shape.batch, n):
+        raise ValueError(f"positions must be [axes, batch, n], got {tuple(positions.shape)}")
+    dev = _here(q, k, q_out, k_out, lengths, starts, positions, *rotary._keep)
+    rc = lib().cg_rotate(
+        shape, rotary, q_heads, n, _sized("positions", positions, "int32", rotary.axes * shape.batch * n),
+        _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
+        *rows, _stream_on(stream, dev))
+    if rc != CG_OK:
+        _check("cg_rotate", rc)
 
 
 def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape, payload_out, meta_out,

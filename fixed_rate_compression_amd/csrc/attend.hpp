@@ -1,5 +1,7 @@
-// Attention over the 8-bit block-uniform cache: launch interface and the
-// device pieces its kernels share.  Not part of the public ABI.
+// Attention over the serving caches (8-bit block-uniform, 4-bit KIVI-style): launch
+// interface and the device pieces its kernels share.  Not part of the public ABI.
+//
+// 8 bits:
 //
 // With k'_t = mk_b + sk_b code_t and v'_t = mv_b + sv_b code_t (block b of
 // token t), a gauged query row q' = G_K q and c = scale log2(e):
@@ -48,7 +50,9 @@ constexpr int MERGE_SPLITS = 1024;  // splits at most
 
 struct AttendArgs {
   const uint8_t *kpay, *vpay;    // codes of the layer's key / value fields, field (b, h) at (b heads + h) tcap 128
-  const float2 *kmeta, *vmeta;   // (minimum, step) of the layer's blocks, [b][h][nblk]
+                                 // (4 bits: tcap 64)
+  const float2 *kmeta, *vmeta;   // (minimum, step) of the layer's blocks, [b][h][nblk]; 4 bits: of keys
+                                 // [b][h][nblk][128], of values [b][h][tcap][4]
   const int32_t *lengths;        // [batch] or null (tokens)
   const int32_t *starts;         // [batch] or null (lengths - n)
   const float *gk, *gv;          // the layer's gauges [heads][128 g], ignored when g == 0
@@ -75,6 +79,8 @@ struct AttendArgs {
 // rows [0, rows) of every field over its tokens, one workgroup per (field,
 // row tile, split); splits > 1 leaves parts for merge_launch
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
+// the same over the 4-bit cache, of any number of rows
+hipError_t rows4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // the same for many rows, one workgroup per (field, 128 rows, split)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
@@ -173,6 +179,26 @@ __device__ __forceinline__ float row_max(float v) {
   const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
   const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
   return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+
+// sum / maximum over a wave's 64 lanes, without LDS
+template <int N>
+__device__ __forceinline__ float ror16(float v) {  // from the lane N further round in its 16
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += ror16<8>(v);
+  v += ror16<4>(v);
+  v += ror16<2>(v);
+  v += ror16<1>(v);
+  return row_sum(v);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, ror16<8>(v));
+  v = fmaxf(v, ror16<4>(v));
+  v = fmaxf(v, ror16<2>(v));
+  v = fmaxf(v, ror16<1>(v));
+  return row_max(v);
 }
 
 // a sequence's length and the position of the first of these queries, loaded once

@@ -186,7 +186,7 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
   if (!bytes) return error(CG_E_INVAL, "bytes is NULL");
   if (!gauge) return error(CG_E_INVAL, "gauge is NULL");
   alignas(16) static const char any[16] = {};
-  int rc = cgh::check_cache8(shape, gauge, codec, any, UINT64_MAX, any, UINT64_MAX);
+  int rc = cgh::check_cache(shape, gauge, codec, any, UINT64_MAX, any, UINT64_MAX);
   if (rc) return rc;
   if ((rc = check_attn(shape, attn))) return rc;
   *bytes = make_plan(shape, codec, attn, with_mass != 0).total();
@@ -199,7 +199,7 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
               void *stream) {
   cgh::set_error("");
   if (!gauge) return error(CG_E_INVAL, "gauge is NULL");
-  int rc = cgh::check_cache8(shape, gauge, codec, payload, payload_cap, meta, meta_cap);
+  int rc = cgh::check_cache(shape, gauge, codec, payload, payload_cap, meta, meta_cap);
   if (rc) return rc;
   if ((rc = check_attn(shape, attn))) return rc;
   if (attn->n_queries == 0) return CG_OK;
@@ -226,10 +226,12 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.tcap = shape->token_capacity;
   a.tokens = shape->tokens;
   a.nblk = a.tcap / codec->block_tokens;
-  a.kpay = (const uint8_t *)payload + kf * a.tcap * d;
-  a.vpay = (const uint8_t *)payload + vf * a.tcap * d;
-  a.kmeta = (const float2 *)meta + kf * a.nblk;
-  a.vmeta = (const float2 *)meta + vf * a.nblk;
+  const bool kivi = cgh::is_kivi4(codec);
+  const int64_t pf = cgh::payload_field(codec, a.tcap), mf = cgh::meta_field(codec, a.tcap);
+  a.kpay = (const uint8_t *)payload + kf * pf;
+  a.vpay = (const uint8_t *)payload + vf * pf;
+  a.kmeta = (const float2 *)((const char *)meta + kf * mf);
+  a.vmeta = (const float2 *)((const char *)meta + vf * mf);
   a.lengths = attn->lengths;
   a.starts = attn->starts;
   a.g = gauge->group;
@@ -270,7 +272,7 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
     a.q = (const char *)q + (int64_t)first * ts * esz;
     a.out = (char *)out + (int64_t)first * token * esz;
     a.lse = lse ? lse + (int64_t)first * attn->q_heads : nullptr;
-    hipError_t e = p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
+    hipError_t e = kivi ? cga::rows4_launch(a, bf16, st) : p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
     if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
     if (p.merge && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
       return cgh::hip_error(e, "cg_attend merge launch");

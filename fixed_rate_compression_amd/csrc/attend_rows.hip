@@ -28,6 +28,7 @@
 // workgroups a compute unit for the registers, three spill), one sequence of 1024
 // tokens 11.3 us, all of it latency.
 #include "attend.hpp"
+#include "attend_few.hpp"
 
 namespace cga {
 
@@ -141,6 +142,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
     splits = sl.count;
     sq = sequence_of(a, sl.n, sl.p);
   }
+  const FewPlace fp{b, h, tile, slot, split, splits, part, r0, nr};
   const int bh = b * a.heads + h;
   const uint8_t *kf = a.kpay + (int64_t)bh * a.tcap * D, *vf = a.vpay + (int64_t)bh * a.tcap * D;
   const float2 *km = a.kmeta + (int64_t)bh * a.nblk, *vm = a.vmeta + (int64_t)bh * a.nblk;
@@ -328,61 +330,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend_ro
 
   const float *gv = a.gv + (int64_t)h * D * a.g;
   if (splits == 1 && front) load_gauge<true>(gv, a.g, 0, gw);
-  // join the waves: each leaves its sums relative to its own maximum
-  __syncthreads();  // the operands have been read
-  const float l = row_sum(st.l), mv = row_sum(st.mv);
-  if (grp == 0) ml[wave][row] = make_float2(st.m, l);
-  {
-    // true sums: acc 2^9 / f (the codes' and the weights' scales)
-    const float ks = st.m > -INFINITY ? exp2_fast(st.mo - st.m) : 0.0f;
-    float *o = lds + (wave * ROWS + row) * PITCH;
-#pragma unroll
-    for (int r = 0; r < 4; r++) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[j] = __builtin_fmaf(acc[j][r], ks, mv);
-      *(float4 *)(o + 8 * (4 * grp + r)) = make_float4(v[0], v[1], v[2], v[3]);
-      *(float4 *)(o + 8 * (4 * grp + r) + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  }
-  __syncthreads();
-  // for the merge (a store before the loop turns its scalar loads into vector ones)
-  if (a.ragged && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0)
-    a.dealt[b] = make_int2(slot, splits);
-  for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * NW) {  // also rows that are not there: none is left undefined
-    const int r = i / (D / 4), c = 4 * (i % (D / 4));
-    float M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < NW; k++) M = fmaxf(M, ml[k][r].x);
-    float L = 0.0f;
-    f4_t v = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NW; k++) {
-      const float2 w = ml[k][r];
-      const float f = w.x > -INFINITY ? exp2_fast(w.x - M) : 0.0f;
-      L += w.y * f;
-      v += *(const f4_t *)(lds + (k * ROWS + r) * PITCH + c) * f;
-    }
-    const int64_t pr = part + r0 + r;
-    if (c == 0 && r < nr) {
-      if (a.part_ml) a.part_ml[pr] = make_float2(M, L);
-      if (splits == 1 && a.lse) store_lse(a, b, h, r0 + r, M, L);
-    }
-    if (splits > 1) {
-      if (r < nr) *(f4_t *)(a.part_o + pr * D + c) = v;
-    } else {
-      *(f4_t *)(lds + r * PITCH + c) = v * (L > 0.0f ? 1.0f / L : 0.0f);  // this thread alone reads these channels of row r
-    }
-  }
-  if (splits > 1) return;
-  __syncthreads();
-  float *os = lds;
-  if (a.g) {
-    os = lds + ROWS * PITCH;
-    if (front) gauge_tiles<true, 1, false>(lds, os, gv, a.g, gw);
-    __syncthreads();
-  }
-  if (front) store_rows<BF16>(a, b, h, r0, nr, os);
+  const float mv = row_sum(st.mv);
+  // true sums: acc 2^9 / f (the codes' and the weights' scales)
+  const float ks = st.m > -INFINITY ? exp2_fast(st.mo - st.m) : 0.0f;
+  finish_few<BF16, NW>(a, fp, lds, ml, gv, gw, front, st.m, st.l, ks, mv, acc);
 }
 
 // the parts of (b, h): the first one's number and how many there are
@@ -445,26 +396,6 @@ __device__ __forceinline__ void finish_mass(const AttendArgs &a, uint32_t id) {
 }
 
 __global__ __launch_bounds__(NTH) void k_mass_finish(const AttendArgs a) { finish_mass(a, blockIdx.x); }
-
-// sum / maximum over a wave's 64 lanes, without LDS
-template <int N>
-__device__ __forceinline__ float ror16(float v) {  // from the lane N further round in its 16
-  return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + N, 0xf, 0xf, false));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  v += ror16<8>(v);
-  v += ror16<4>(v);
-  v += ror16<2>(v);
-  v += ror16<1>(v);
-  return row_sum(v);
-}
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, ror16<8>(v));
-  v = fmaxf(v, ror16<4>(v));
-  v = fmaxf(v, ror16<2>(v));
-  v = fmaxf(v, ror16<1>(v));
-  return row_max(v);
-}
 
 // Joins the splits of one row, a workgroup to a row: 2^(m_s - M) of every
 // split, eight groups of 32 lanes adding every eighth split's sums, then the

@@ -1,4 +1,4 @@
-// Host-side checks and error reporting shared by the entry points of the 8-bit
+// Host-side checks and error reporting shared by the entry points of the
 // serving operators (defined in codec_gauge_api.cpp).  Not part of the public ABI.
 #pragma once
 
@@ -18,9 +18,15 @@ inline uint64_t reach(int64_t batch, int64_t bs, int64_t n, int64_t rs, int64_t 
   const unsigned __int128 e = (unsigned __int128)(batch - 1) * bs + (unsigned __int128)(n - 1) * rs + row;
   return e >> 60 ? 0 : (uint64_t)e;
 }
-// a K/V cache in 8-bit block-uniform form with its buffers (gauge may be NULL:
-// not looked at)
-int check_cache8(const cg_shape *s, const cg_gauge *g, const cg_codec *c, const void *payload,
+int check_shape_of(const cg_shape *s);
+// a K/V cache in 8-bit block-uniform or 4-bit KIVI-style form with its buffers (gauge
+// may be NULL: not looked at)
+int check_cache(const cg_shape *s, const cg_gauge *g, const cg_codec *c, const void *payload,
                  uint64_t payload_cap, const void *meta, uint64_t meta_cap);
+
+inline bool is_kivi4(const cg_codec *c) { return c->backend == CG_BACKEND_KIVI; }  // of a cache that passed
+// bytes of a field of tcap rows: codes, (minimum, step) pairs
+inline int64_t payload_field(const cg_codec *c, int64_t tcap) { return is_kivi4(c) ? tcap * 64 : tcap * 128; }
+inline int64_t meta_field(const cg_codec *c, int64_t tcap) { return is_kivi4(c) ? tcap * 32 : tcap / c->block_tokens * 8; }
 
 }  // namespace cgh

@@ -359,13 +359,22 @@ bool expm_frechet(int n, const double *M, const double *D, double *R, double *L)
 void set_error(const char *msg) { g_err = msg; }
 int error(int code, const char *msg) { return fail(code, "%s", msg); }
 int hip_error(hipError_t e, const char *what) { return hip_fail(e, what); }
-int check_cache8(const cg_shape *s, const cg_gauge *g, const cg_codec *c, const void *payload,
-                 uint64_t payload_cap, const void *meta, uint64_t meta_cap) {
+int check_shape_of(const cg_shape *s) { return check_shape(s); }
+
+int check_cache(const cg_shape *s, const cg_gauge *g, const cg_codec *c, const void *payload,
+                uint64_t payload_cap, const void *meta, uint64_t meta_cap) {
   int rc;
   if ((rc = check_shape(s))) return rc;
-  if ((rc = check_codec(c, s))) return rc;
-  if (c->backend != CG_BACKEND_BLOCK_UNIFORM || c->bits != 8)
-    return fail(CG_E_UNSUPPORTED, "this operator reads block-uniform caches of 8 bits");
+  if (c && c->backend == CG_BACKEND_KIVI) {
+    // `tokens` bounds the lengths here and need not fill a key range; the capacity does
+    if (c->bits != 4 || c->block_tokens != 32 || c->residual_tokens != 0)
+      return fail(CG_E_UNSUPPORTED, "this operator reads KIVI-style caches of 4 bits, groups of 32 and no residual");
+    if (s->token_capacity % 32) return fail(CG_E_SHAPE, "token_capacity must be a multiple of 32");
+  } else {
+    if ((rc = check_codec(c, s))) return rc;
+    if (c->backend != CG_BACKEND_BLOCK_UNIFORM || c->bits != 8)
+      return fail(CG_E_UNSUPPORTED, "this operator reads block-uniform caches of 8 bits and KIVI-style ones of 4");
+  }
   if (g && (rc = check_gauge(g, s, c))) return rc;
   if (s->kv != 2) return fail(CG_E_SHAPE, "the cache needs keys and values (kv = 2)");
   if (s->token_capacity > (int64_t)0x7fffff00) return fail(CG_E_SHAPE, "token_capacity is over 2^31 - 256");

@@ -1,4 +1,4 @@
-// cg_append and cg_evict: argument checks and launches.
+// cg_append, cg_read and cg_evict: argument checks and launches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -24,7 +24,7 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
               void *payload, uint64_t payload_cap, void *meta, uint64_t meta_cap, void *stream) {
   cgh::set_error("");
   if (!gauge) return error(CG_E_INVAL, "gauge is NULL");
-  int rc = cgh::check_cache8(shape, gauge, codec, payload, payload_cap, meta, meta_cap);
+  int rc = cgh::check_cache(shape, gauge, codec, payload, payload_cap, meta, meta_cap);
   if (rc) return rc;
   if (layer < 0 || layer >= shape->layers) return error(CG_E_SHAPE, "layer outside the cache shape");
   if (n_new < 0) return error(CG_E_SHAPE, "n_new < 0");
@@ -54,8 +54,8 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
   a.tcap = shape->token_capacity;
   a.tokens = shape->tokens;
   a.nblk = a.tcap / codec->block_tokens;
-  a.payload = (uint8_t *)payload + f0 * a.tcap * shape->head_dim;
-  a.meta = (float *)meta + 2 * f0 * a.nblk;
+  a.payload = (uint8_t *)payload + f0 * cgh::payload_field(codec, a.tcap);
+  a.meta = (float *)((char *)meta + f0 * cgh::meta_field(codec, a.tcap));
   a.tail = t0;
   a.k = k_new;
   a.v = v_new;
@@ -70,8 +70,74 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
   a.block = codec->block_tokens;
   a.bshift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
   a.tiles = (int32_t)tiles;
-  hipError_t e = cgs::append_launch(a, shape->dtype == CG_DTYPE_BF16, gauge->group, (hipStream_t)stream);
+  hipError_t e = cgs::append_launch(a, shape->dtype == CG_DTYPE_BF16, gauge->group, cgh::is_kivi4(codec), (hipStream_t)stream);
   return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_append launch");
+}
+
+int cg_read(const cg_shape *shape, const void *payload, uint64_t payload_cap, const void *meta,
+            uint64_t meta_cap, const cg_gauge *gauge, const cg_codec *codec, int32_t layer, int32_t n,
+            const int32_t *lengths, const int32_t *starts, void *k_out, void *v_out, int64_t batch_stride,
+            int64_t row_stride, void *stream) {
+  cgh::set_error("");
+  if (!gauge) return error(CG_E_INVAL, "gauge is NULL");
+  int rc = cgh::check_cache(shape, gauge, codec, payload, payload_cap, meta, meta_cap);
+  if (rc) return rc;
+  if (layer < 0 || layer >= shape->layers) return error(CG_E_SHAPE, "layer outside the cache shape");
+  if (n < 0) return error(CG_E_SHAPE, "n < 0");
+  if (n == 0) return CG_OK;
+  if (!k_out && !v_out) return error(CG_E_INVAL, "k_out and v_out are NULL");
+  if (((uintptr_t)k_out | (uintptr_t)v_out) & 15u) return error(CG_E_INVAL, "k_out and v_out must be 16-byte aligned");
+  if (((uintptr_t)lengths | (uintptr_t)starts) & 3u)
+    return error(CG_E_INVAL, "lengths and starts must be 4-byte aligned");
+  const int64_t fields = (int64_t)2 * shape->batch * shape->heads, f0 = layer * fields;
+  const int64_t tiles = ((int64_t)n + 63) / 64;
+  if (fields * tiles >= (int64_t)1 << 31) return error(CG_E_SHAPE, "too many rows for one launch");
+  const int64_t row = (int64_t)shape->heads * shape->head_dim;
+  int64_t rs = row_stride ? row_stride : row, bs = batch_stride ? batch_stride : row * n;
+  const int64_t unit = shape->dtype == CG_DTYPE_BF16 ? 8 : 4, far = (int64_t)1 << 40;
+  if (rs < 0 || bs < 0 || rs % unit || bs % unit || rs > far || bs > far)
+    return error(CG_E_INVAL, "row strides must be multiples of 16 bytes and not negative");
+  const uint64_t esz = shape->dtype == CG_DTYPE_BF16 ? 2 : 4;
+  const uint64_t span = cgh::reach(shape->batch, bs, n, rs, row) * esz;
+  if (!span) return error(CG_E_INVAL, "row strides reach too far");
+  // one row a sequence: the sequences are the rows; one sequence: it has no next
+  if (n == 1 && shape->batch > 1) rs = bs;
+  if (shape->batch == 1) bs = rs * n;
+  // rows that lie in one another would be written by several workgroups
+  if (rs < row || (shape->batch > 1 && bs < (rs * (n - 1) + row) && rs < bs * (shape->batch - 1) + row))
+    return error(CG_E_INVAL, "rows of the output overlap");
+  cgs::ReadArgs a{};
+  const uint64_t pb = (uint64_t)shape->layers * fields * cgh::payload_field(codec, shape->token_capacity),
+                 mb = (uint64_t)shape->layers * fields * cgh::meta_field(codec, shape->token_capacity);
+  for (const void *o : {k_out, v_out})
+    if (o && (overlap(o, span, payload, pb) || overlap(o, span, meta, mb)))
+      return error(CG_E_INVAL, "the rows overlap the cache");
+  // keys and values may be parts of the same rows, side by side
+  if (k_out && v_out && overlap(k_out, span, v_out, span)) {
+    const int64_t d = ((const char *)v_out - (const char *)k_out) % (int64_t)(rs * esz);
+    const uint64_t m = (uint64_t)(d < 0 ? d + rs * (int64_t)esz : d);
+    if (bs % rs || m < row * esz || m + row * esz > rs * esz) return error(CG_E_INVAL, "k_out and v_out overlap");
+  }
+  if (shape->tokens == 0) return CG_OK;
+  a.tcap = shape->token_capacity;
+  a.tokens = shape->tokens;
+  a.nblk = a.tcap / codec->block_tokens;
+  a.payload = (const uint8_t *)payload + f0 * cgh::payload_field(codec, a.tcap);
+  a.meta = (const float2 *)((const char *)meta + f0 * cgh::meta_field(codec, a.tcap));
+  a.k = k_out;
+  a.v = v_out;
+  a.batch_stride = bs;
+  a.row_stride = rs;
+  a.lengths = lengths;
+  a.starts = starts;
+  a.gauges = gauge->group ? gauge->G + (int64_t)layer * 2 * shape->heads * shape->head_dim * gauge->group : nullptr;
+  a.batch = shape->batch;
+  a.heads = shape->heads;
+  a.n = n;
+  a.bshift = codec->block_tokens == 16 ? 4 : codec->block_tokens == 32 ? 5 : 6;
+  a.tiles = (int32_t)tiles;
+  hipError_t e = cgs::read_launch(a, shape->dtype == CG_DTYPE_BF16, gauge->group, cgh::is_kivi4(codec), (hipStream_t)stream);
+  return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_read launch");
 }
 
 int cg_evict(const cg_shape *shape, const cg_codec *codec, int32_t budget, int32_t sink, int32_t recent,
@@ -80,9 +146,9 @@ int cg_evict(const cg_shape *shape, const cg_codec *codec, int32_t budget, int32
              uint64_t payload_out_cap, void *meta_out, uint64_t meta_out_cap, float *mass_out,
              int32_t *kept, int32_t *lengths_out, void *stream) {
   cgh::set_error("");
-  int rc = cgh::check_cache8(shape, nullptr, codec, payload, payload_cap, meta, meta_cap);
+  int rc = cgh::check_cache(shape, nullptr, codec, payload, payload_cap, meta, meta_cap);
   if (rc) return rc;
-  if ((rc = cgh::check_cache8(out_shape, nullptr, codec, payload_out, payload_out_cap, meta_out, meta_out_cap)))
+  if ((rc = cgh::check_cache(out_shape, nullptr, codec, payload_out, payload_out_cap, meta_out, meta_out_cap)))
     return rc;
   if (out_shape->layers != shape->layers || out_shape->batch != shape->batch || out_shape->heads != shape->heads)
     return error(CG_E_SHAPE, "the caches differ in layers, batch or heads");
@@ -95,8 +161,10 @@ int cg_evict(const cg_shape *shape, const cg_codec *codec, int32_t budget, int32
     return error(CG_E_INVAL, "mass, kept and lengths must be 4-byte aligned");
   const int64_t heads = (int64_t)shape->layers * shape->batch * shape->heads;
   if (2 * heads * (int64_t)1024 >= (int64_t)1 << 31) return error(CG_E_SHAPE, "too many heads for one launch");
-  const uint64_t pb = (uint64_t)2 * heads * shape->token_capacity * shape->head_dim, mb = (uint64_t)2 * heads * nblk * 8;
-  const uint64_t po = (uint64_t)2 * heads * out_shape->token_capacity * shape->head_dim, mo = (uint64_t)2 * heads * nout * 8;
+  const uint64_t pb = (uint64_t)2 * heads * cgh::payload_field(codec, shape->token_capacity),
+                 mb = (uint64_t)2 * heads * cgh::meta_field(codec, shape->token_capacity);
+  const uint64_t po = (uint64_t)2 * heads * cgh::payload_field(codec, out_shape->token_capacity),
+                 mo = (uint64_t)2 * heads * cgh::meta_field(codec, out_shape->token_capacity);
   const uint64_t wb = (uint64_t)heads * nblk * 4, wo = (uint64_t)heads * nout * 4;
   const bool in_place = payload_out == payload;
   if (in_place) {
@@ -128,7 +196,9 @@ int cg_evict(const cg_shape *shape, const cg_codec *codec, int32_t budget, int32
   a.sink = sink;
   a.recent = recent;
   a.in_place = in_place ? 1 : 0;
-  a.pshift = codec->block_tokens == 16 ? 7 : codec->block_tokens == 32 ? 8 : 9;
+  const bool kivi = cgh::is_kivi4(codec);
+  a.pshift = codec->block_tokens == 16 || kivi ? 7 : codec->block_tokens == 32 ? 8 : 9;
+  a.mshift = kivi ? 6 : -1;
   hipError_t e = cgs::evict_launch(a, (hipStream_t)stream);
   return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_evict launch");
 }

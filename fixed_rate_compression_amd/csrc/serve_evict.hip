@@ -247,6 +247,8 @@ __global__ __launch_bounds__(ST) void k_evict_select(const EvictArgs a) {
 // read by all threads everything up to it may be overwritten.  Into another
 // cache the field is cut into `chunks`.  Half of 32 layers x 8 heads x 8192 tokens
 // (269 MB each way): 106 us, 4.9 TB/s, a large copy's 5.1.
+// KIVI: a block's ranges move as its codes do.
+template <bool KIVI>
 __global__ __launch_bounds__(MT) void k_evict_move(const EvictArgs a, int chunks) {
   const uint32_t f32 = blockIdx.x / (uint32_t)chunks, heads = (uint32_t)(a.batch * a.heads);
   const int chunk = (int)(blockIdx.x - f32 * chunks);
@@ -259,11 +261,6 @@ __global__ __launch_bounds__(MT) void k_evict_move(const EvictArgs a, int chunks
     }
   const uint32_t layer = f32 / (2 * heads), bh = f32 % heads;
   const int32_t *kept = a.kept + ((int64_t)layer * heads + bh) * a.budget;
-  const float2 *ms = a.meta + f * a.nblk;
-  float2 *md = a.meta_out + f * a.nblk_out;
-  const int sh = a.pshift, per = 1 << sh;  // 16-byte pieces of a block
-  const u4_t *src = (const u4_t *)a.payload + f * a.nblk * per;
-  u4_t *dst = (u4_t *)a.payload_out + f * a.nblk_out * per;
   const int each = (a.budget + chunks - 1) / chunks, b0 = min(chunk * each, a.budget), b1 = min(b0 + each, a.budget);
   __shared__ int32_t from[MT];  // former numbers of the blocks [j0, j0 + MT)
   for (int j0 = b0; j0 < b1; j0 += MT) {
@@ -271,28 +268,41 @@ __global__ __launch_bounds__(MT) void k_evict_move(const EvictArgs a, int chunks
     const int s = j < b1 ? kept[j] : -1;
     __syncthreads();
     from[threadIdx.x] = s;
-    float2 m = make_float2(0.f, 0.f);
-    if (s >= 0) m = ms[s];
-    __syncthreads();
-    if (s >= 0) md[j] = m;  // in place: at or below any number that is still to be read
-    const int np = min(MT, b1 - j0) << sh;
-    for (int p = 0; p < np; p += MT * STEP) {
-      u4_t v[STEP];
-      int s[STEP];
-#pragma unroll
-      for (int k = 0; k < STEP; k++) {
-        const int x = p + k * MT + (int)threadIdx.x;
-        s[k] = x < np ? from[x >> sh] : -1;
-        if (a.in_place && s[k] == j0 + (x >> sh)) s[k] = -1;  // stays where it is
-        if (s[k] >= 0) v[k] = src[(int64_t)s[k] * per + (x & (per - 1))];
-      }
-      if (a.in_place) __syncthreads();
-#pragma unroll
-      for (int k = 0; k < STEP; k++)
-        if (s[k] >= 0) __builtin_nontemporal_store(v[k], &dst[((int64_t)j0 << sh) + p + k * MT + (int)threadIdx.x]);
-      if (a.in_place) __syncthreads();
+    if constexpr (KIVI) {
+      __syncthreads();
+    } else {
+      const float2 *ms = a.meta + f * a.nblk;
+      float2 *md = a.meta_out + f * a.nblk_out;
+      float2 m = make_float2(0.f, 0.f);
+      if (s >= 0) m = ms[s];
+      __syncthreads();
+      if (s >= 0) md[j] = m;  // in place: at or below any number that is still to be read
     }
-    if (np > 0 && from[0] < 0) return;  // blocks behind the last kept one
+    // blocks of 1 << sh pieces
+    const auto move = [&](const void *from_field, void *to_field, int sh) {
+      const int per = 1 << sh, np = min(MT, b1 - j0) << sh;
+      const u4_t *src = (const u4_t *)from_field + f * a.nblk * per;
+      u4_t *dst = (u4_t *)to_field + f * a.nblk_out * per;
+      for (int p = 0; p < np; p += MT * STEP) {
+        u4_t v[STEP];
+        int s[STEP];
+#pragma unroll
+        for (int k = 0; k < STEP; k++) {
+          const int x = p + k * MT + (int)threadIdx.x;
+          s[k] = x < np ? from[x >> sh] : -1;
+          if (a.in_place && s[k] == j0 + (x >> sh)) s[k] = -1;  // stays where it is
+          if (s[k] >= 0) v[k] = src[(int64_t)s[k] * per + (x & (per - 1))];
+        }
+        if (a.in_place) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < STEP; k++)
+          if (s[k] >= 0) __builtin_nontemporal_store(v[k], &dst[((int64_t)j0 << sh) + p + k * MT + (int)threadIdx.x]);
+        if (a.in_place) __syncthreads();
+      }
+    };
+    move(a.payload, a.payload_out, a.pshift);
+    if constexpr (KIVI) move(a.meta, a.meta_out, a.mshift);
+    if (from[0] < 0) return;  // blocks behind the last kept one
   }
 }
 
@@ -308,12 +318,14 @@ hipError_t evict_launch(const EvictArgs &a, hipStream_t s) {
   if (e != hipSuccess) return e;
   int64_t chunks = 1;
   if (!a.in_place) {  // eight workgroups a compute unit, 16 KB at least to each
-    const int64_t bytes = (int64_t)a.budget * a.block * 128;
+    const int64_t bytes = (int64_t)a.budget * 16 * ((1 << a.pshift) + (a.mshift < 0 ? 0 : 1 << a.mshift));
     chunks = (2048 + 2 * heads - 1) / (2 * heads);
     if (chunks > (bytes + 16383) / 16384) chunks = (bytes + 16383) / 16384;
     if (chunks > a.budget) chunks = a.budget;
   }
-  hipLaunchKernelGGL(k_evict_move, dim3((unsigned)(2 * heads * chunks)), dim3(MT), 0, s, a, (int)chunks);
+  const dim3 moves((unsigned)(2 * heads * chunks));
+  if (a.mshift < 0) hipLaunchKernelGGL(k_evict_move<false>, moves, dim3(MT), 0, s, a, (int)chunks);
+  else hipLaunchKernelGGL(k_evict_move<true>, moves, dim3(MT), 0, s, a, (int)chunks);
   return hipGetLastError();
 }
 

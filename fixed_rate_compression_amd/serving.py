@@ -1,13 +1,19 @@
-"""An 8-bit block-uniform cache that is served from where it lies: new K/V rows
-go in token by token (cg_append), attention reads the codes (cg_attend), and the
-blocks that received the least attention leave (cg_evict).
+"""A cache of 8 bits (block-uniform) or 4 (KIVI-style) that is served from where it lies:
+new K/V rows go in token by token (cg_append), attention reads the codes (cg_attend),
+rows come back for other consumers (cg_read), and the blocks that received the least
+attention leave (cg_evict).
 
 One step of a decoder, the same for prompts, chunks of them and single tokens:
 
     cache.begin(n)                      # every sequence grows by n rows
     for layer in range(layers):
+        cache.rotate(q, k, rotary)      # in place: the heads' norms and RoPE, where the model's own code
+                                        # has not done it (rotary: binding.make_rotary)
         cache.append(layer, k, v)       # k, v [batch, n, heads, 128] after RoPE, of the same strides
         o = cache.attend(layer, q)      # q, o [batch, n, q_heads, 128]
+
+4 bits take 192 bytes a token and KV head, codes and ranges, 8 bits 256 and a block's
+range; block_tokens is 32 there.
 
 begin(n, valid) takes right-padded rows: sequence b gets the first valid[b] of
 them (the host's bound of the lengths counts all n).  Sequences have their own
@@ -36,19 +42,21 @@ from . import binding as cg
 
 class ServingCache:
     def __init__(self, layers, batch, heads, q_heads, capacity, gauge, block_tokens=32,
-                 dtype=cg.CG_DTYPE_BF16, head_dim=128, with_mass=False):
+                 dtype=cg.CG_DTYPE_BF16, head_dim=128, with_mass=False, bits=8):
         import torch
 
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8")
         if capacity < 0 or block_tokens <= 0 or capacity % block_tokens:
             raise ValueError("capacity must be a multiple of block_tokens")
-        self.codec = cg.make_codec(cg.CG_BACKEND_BLOCK_UNIFORM, 8, block_tokens)
+        self.codec = cg.make_codec(cg.CG_BACKEND_BLOCK_UNIFORM if bits == 8 else cg.CG_BACKEND_KIVI, bits, block_tokens)
         self.shape = cg.make_shape(layers, 2, batch, heads, capacity, capacity, head_dim, dtype)
         self.gauge, self.q_heads = gauge, q_heads
         self.dtype = torch.bfloat16 if dtype == cg.CG_DTYPE_BF16 else torch.float32
         pay, meta, _ = cg.cg_encoded_bytes(self.shape, self.codec)
         dev = {"device": "cuda"}
         self.payload = torch.zeros(pay, dtype=torch.uint8, **dev)
-        self.meta = torch.zeros(meta // 4, **dev)
+        self.meta = torch.zeros(meta // 4, **dev)   # (minimum, step) pairs
         self.tail = torch.zeros((layers, 2, batch, heads, block_tokens, head_dim), dtype=self.dtype, **dev)
         self.mass = torch.zeros((layers, batch, heads, capacity // block_tokens), **dev) if with_mass else None
         self.lengths = torch.zeros(batch, dtype=torch.int32, **dev)
@@ -82,6 +90,13 @@ class ServingCache:
         else:
             self.lengths.add_(valid)
 
+    def rotate(self, q, k, rotary, positions=None, q_out=None, k_out=None):
+        """Norms and rotation of the step's queries and keys, in place or into q_out and k_out, at the rows' places
+        in the cache or at positions [axes, batch, n]; padding rows are left as they were.  -> (q, k) as rotated."""
+        q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+        cg.cg_rotate(self.shape, rotary, q, k, q_out, k_out, self.lengths, self.starts, positions)
+        return q_out, k_out
+
     def append(self, layer, k, v):
         """The step's rows of one layer, before that layer's attend; every layer once a step (only
         the raw rows of a sequence's last block are kept, which may be another by then)."""
@@ -110,6 +125,17 @@ class ServingCache:
         cg.cg_attend(self.shape, self.payload, self.meta, self.gauge, self.codec, at, q, out, lse, self.mass,
                      self._work[-1])
         return out
+
+    def read(self, layer, n, starts=None, k_out=None, v_out=None):
+        """n rows of every sequence from starts (device int32 [batch]; None: its last n) on, decoded
+        -> (k, v) [batch, n, heads, 128]; rows that a sequence does not have are left as they were, zeros in new arrays."""
+        import torch
+
+        s = self.shape
+        if k_out is None and v_out is None:
+            k_out, v_out = torch.zeros((2, s.batch, n, s.heads, s.head_dim), dtype=self.dtype, device=self.payload.device)
+        cg.cg_read(s, self.payload, self.meta, self.gauge, self.codec, layer, k_out, v_out, self.lengths, starts)
+        return k_out, v_out
 
     def evict(self, budget, sink=1, recent=1):
         """Keep `budget` blocks of every (layer, sequence, head), in place; -> the kept blocks' former numbers.

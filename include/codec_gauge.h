@@ -395,19 +395,25 @@ int cg_write_header(const cg_shape *shape, const cg_codec *codec, int32_t layer,
                     void *header_host, uint64_t cap);
 
 /*
- * Serving on the encoded cache: append, attend, evict.
+ * Serving on the encoded cache: rotate, append, attend, read, evict.
  *
- * These read and write a BLOCK_UNIFORM cache of 8 bits (block_tokens 16, 32 or
- * 64; shape->kv == 2) where it lies: payload and meta as cg_encode lays them
- * out, values x' = minimum + step * code in gauged coordinates.  Sequences of
- * a batch have their own lengths:
+ * These read and write a cache where it lies (shape->kv == 2), payload and meta as
+ * cg_encode lays them out, values x' = minimum + step * code in gauged coordinates,
+ * in one of two forms:
+ *   8 bits  BLOCK_UNIFORM, block_tokens 16, 32 or 64: 1 byte a value
+ *   4 bits  KIVI, block_tokens 32, residual_tokens 0, token_capacity a multiple of
+ *           32: half a byte a value and 8 bytes of range for 32 (keys: of a
+ *           channel's 32 tokens; values: of a token's 32 channels).  Its blocks
+ *           are the 32 tokens of a key range; shape->tokens need not fill one
+ *           (cg_encoded_bytes: a shape with tokens = token_capacity).
+ * Others give CG_E_UNSUPPORTED.  Sequences of a batch have their own lengths:
  *   lengths  device int32 [batch], valid rows of each sequence, with the rows
  *            of the present step; NULL: shape->tokens.  Values outside
  *            [0, tokens] count as the nearest of the two.
  *   starts   device int32 [batch], position of each sequence's first query
- *            (cg_attend) or new row (cg_append); NULL: lengths - n, the last n
- *            positions.  Query or row i stands at starts + i; positions below
- *            0 or at lengths and above are padding.
+ *            (cg_attend) or row (cg_append, cg_read, cg_rotate); NULL: lengths - n,
+ *            the last n positions.  Query or row i stands at starts + i;
+ *            positions below 0 or at lengths and above are padding.
  * shape->tokens only bounds the lengths (and sizes launches and workspaces, but
  * for the sums behind `mass`), so calls recorded into a graph may be replayed as
  * the lengths grow.  A launch is planned for sequences of that many rows: a bound
@@ -457,13 +463,18 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  *         rows received from all visible queries and all heads of the group
  * A query that sees nothing (padding, an empty sequence) gives zeros and an
  * lse of -inf, and no mass.  A query with a NaN or an infinity has NaN for out,
- * lse and the mass of what it sees, as has one that sees a key block whose range
- * is NaN; a value block's NaN range reaches out alone.  Queries that see nothing
- * of such a block are not touched by it.
+ * lse and the mass of what it sees, as has one that sees a key block with a range that
+ * is NaN; a value block's NaN range reaches out alone (4 bits: a NaN or infinity in
+ * a token's range, the 32 channels of that range before the inverse gauge).
+ * Queries that see nothing of such a block (4-bit values: token) are not touched by it.
  * Scores, sums and weights of a sum are fp32; the operands of the matrix products
- * are fp16: queries in two parts (2^-23 of a row's largest channel), in one (2^-11
+ * are fp16.  8 bits: queries in two parts (2^-23 of a row's largest channel), in one (2^-11
  * of a channel) for bf16 storage with more than 64 rows a KV head and neither lse nor
  * mass; weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
+ * 4 bits: queries times key steps in two parts (2^-23 of the largest channel times the
+ * block's largest key), in three (2^-34) for fp32 storage and with lse or mass; weights
+ * and the values themselves for fp32 storage in two parts, for bf16 storage in one (2^-11, and 2^-34 of
+ * a block's largest value).
  * The order of sums depends on the shape and the lengths only (deterministic).
  * The workspace belongs to one call at a time.  Asynchronous on stream.
  */
@@ -482,7 +493,8 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
  *                 row's block that stand before it, and updated
  * Every block that receives a row is encoded again from its raw rows: gauge
  * (fp32 fmaf chains, any built group), range over the rows that are there,
- * codes as in cg_encode.  Codes of rows behind the last are left as they were.
+ * codes as in cg_encode.  Codes (4-bit values: and ranges) of rows behind the last are
+ * left as they were.
  * The rows must continue the sequence, or begin at one of its last block's rows;
  * they are its last: rows behind them in their last block are taken as not
  * there, also where lengths reaches past starts + n_new.
@@ -491,6 +503,63 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
               int32_t n_new, const void *k_new, const void *v_new, int64_t batch_stride,
               int64_t row_stride, const int32_t *lengths, const int32_t *starts, void *tail,
               void *payload, uint64_t payload_cap, void *meta, uint64_t meta_cap, void *stream);
+
+/*
+ * Rows of one layer read back, for a consumer of plain rows: decoded as cg_decode does,
+ * inverse gauge, storage format.
+ *   k_out, v_out  device [batch][n][heads][head_dim] with the given strides in
+ *                 elements (0: dense; multiples of 16 bytes; rows must not overlap);
+ *                 either may be NULL.  Both may be parts of the same rows.
+ * Row i of a sequence is the one at starts + i; rows that are padding are left as they
+ * were.  Inverse gauge: fp32 fmaf chains, or split bf16 products for bf16 storage and
+ * groups of 16 and 32 (2^-13 of sum |G| |x'|).
+ */
+int cg_read(const cg_shape *shape, const void *payload, uint64_t payload_cap, const void *meta,
+            uint64_t meta_cap, const cg_gauge *gauge, const cg_codec *codec, int32_t layer, int32_t n,
+            const int32_t *lengths, const int32_t *starts, void *k_out, void *v_out, int64_t batch_stride,
+            int64_t row_stride, void *stream);
+
+/*
+ * Norm and rotation of query and key heads, before cg_append and cg_attend.
+ *   x <- weight x / sqrt(mean x^2 + eps)        over a head's head_dim channels (weight NULL: not)
+ *   (x_a, x_b) <- magnitude (x_a cos - x_b sin, x_b cos + x_a sin)    for each pair i < dim / 2
+ * with cos and sin of position freq[i]: the position on the pair's axis.  Channels from dim on
+ * are not turned.
+ */
+typedef struct cg_rotary {
+  int32_t dim;            /* channels that turn, the first of a head: a multiple of 16 */
+  int32_t interleaved;    /* pair i: 0: channels i and i + dim / 2; 1: 2 i and 2 i + 1 */
+  int32_t axes;           /* 1 .. 4 positions a row */
+  int32_t dealt;          /* 0: the first sections[0] pairs turn by axis 0, the next
+                             sections[1] by axis 1, ..; 1: pair i by axis x = i % axes
+                             while i < axes sections[x], else by axis 0 */
+  int32_t sections[4];    /* pairs of each axis, dim / 2 in all (axes 1: ignored) */
+  float eps, magnitude;
+  const float *freq;      /* device fp32 [dim / 2], radians a position */
+  const float *q_weight;  /* device fp32 [head_dim], 16-byte aligned, or NULL */
+  const float *k_weight;
+} cg_rotary;
+
+typedef struct cg_rows {  /* device, storage format, [batch][n][heads][head_dim], heads contiguous */
+  void *data;
+  int64_t batch_stride;   /* elements; 0: dense; multiples of 16 bytes */
+  int64_t row_stride;
+} cg_rows;
+
+/*
+ *   q, k          rows of q_heads and shape->heads heads, each with its output; either
+ *                 pair may be NULL
+ *   q_out, k_out  apart from all others, or in place (same address and strides);
+ *                 queries and keys in place may be parts of the same rows
+ *   positions     device int32 [axes][batch][n], or NULL (axes 1): the rows' places,
+ *                 starts + i
+ * Rows that are padding are left as they were.  Angles are taken in fp64 and their whole turns
+ * left out; norms, products and sums are fp32, rounded to the storage format once.
+ * Asynchronous on stream.
+ */
+int cg_rotate(const cg_shape *shape, const cg_rotary *rotary, int32_t q_heads, int32_t n,
+              const int32_t *positions, const int32_t *lengths, const int32_t *starts, const cg_rows *q,
+              const cg_rows *k, const cg_rows *q_out, const cg_rows *k_out, void *stream);
 
 /*
  * Eviction by accumulated attention weight, all layers: a (layer, sequence,

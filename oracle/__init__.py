@@ -16,6 +16,8 @@ Parts:
   * ``spectral.py``: fp64 token-channel DCT statistics and their gradient.
   * ``serving.py``: fp64 attention over the 8-bit cache, the append's
     quantizer and the eviction's choice.
+  * ``serving4.py``: the same over the 4-bit cache, and the rotation of queries
+    and keys.
 
 Every function here is pinned by the ``-m "not gpu"`` tests (closed forms,
 library routines that are independent of this code, brute force,
@@ -32,6 +34,7 @@ import numpy as np
 from .linalg import expm, expm_frechet, gauge_from_skew  # noqa: F401
 from .spectral import dct_matrix, radius_matrix, dct_stats_field  # noqa: F401
 from . import serving  # noqa: F401
+from . import serving4  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _SRC = os.path.join(_HERE, "oracle_codec.c")
