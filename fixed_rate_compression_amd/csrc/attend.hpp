@@ -83,6 +83,8 @@ hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t rows4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // the same for many rows, one workgroup per (field, 128 rows, split)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
+// and over the 4-bit cache, one per (field, 128 or 256 rows, split)
+hipError_t tile4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // block weights from the attention's block sums, of few rows and of many
 hipError_t mass_finish_launch(const AttendArgs &a, hipStream_t s);
@@ -276,14 +278,14 @@ __device__ __forceinline__ int limit_of(const AttendArgs &a, const Sequence &q, 
 }
 
 // this thread's 8 channels of one of the query rows [r0, r0 + 16) of (b, h) as
-// fp32; rows past the last one are zero
+// fp32, four waves to the 16; rows past the last one are zero
 struct RowPart {
   f4_t lo, hi;
 };
 
 template <bool BF16>
 __device__ __forceinline__ RowPart load_row_part(const AttendArgs &a, int b, int h, int r0) {
-  const int r = r0 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;
+  const int r = r0 + ((threadIdx.x >> 4) & 15), c = (threadIdx.x & 15) * 8;
   RowPart p;
   p.lo = p.hi = f4_t{0.f, 0.f, 0.f, 0.f};
   if (r < a.rows) {
@@ -304,7 +306,7 @@ __device__ __forceinline__ RowPart load_row_part(const AttendArgs &a, int b, int
 
 // into xs [16][PITCH]
 __device__ __forceinline__ void put_row_part(float *xs, const RowPart &p) {
-  float *d = xs + (threadIdx.x >> 4) * PITCH + (threadIdx.x & 15) * 8;
+  float *d = xs + ((threadIdx.x >> 4) & 15) * PITCH + (threadIdx.x & 15) * 8;
   *(f4_t *)d = p.lo;
   *(f4_t *)(d + 4) = p.hi;
 }
@@ -321,7 +323,7 @@ struct GaugeFrag {
 
 template <bool INV>
 __device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, int s0, GaugeFrag &f) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
   const int lane = threadIdx.x & 63, kr = lane >> 4, n = lane & 15;
   const int ge = max(g, 16);
   if (g == 0) return;
@@ -352,7 +354,7 @@ __device__ __forceinline__ void load_gauge(const float *__restrict__ gh, int g, 
 template <bool INV, int T, bool IN_PLACE>
 __device__ __forceinline__ void gauge_tiles(const float *xs, float *ys, const float *__restrict__ gh, int g,
                                             const GaugeFrag &first) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
   const int lane = threadIdx.x & 63, kr = lane >> 4, n = lane & 15;
   const int ge = max(g, 16);
   f4_t acc[T][2];
@@ -461,9 +463,9 @@ __device__ __forceinline__ void store_out(const AttendArgs &a, int b, int h, int
 }
 
 // rows [r0, r0 + nr) of (b, h) from LDS [][PITCH], 16 bytes (8 values) a thread
-template <bool BF16>
+template <bool BF16, int NT = NTH>
 __device__ __forceinline__ void store_rows(const AttendArgs &a, int b, int h, int r0, int nr, const float *ys) {
-  for (int x = threadIdx.x; x < nr * 16; x += NTH) {
+  for (int x = threadIdx.x; x < nr * 16; x += NT) {
     const int r = r0 + (x >> 4), c = 8 * (x & 15);
     const float *y = ys + (x >> 4) * PITCH + c;
     const f4_t lo = *(const f4_t *)y, hi = *(const f4_t *)(y + 4);

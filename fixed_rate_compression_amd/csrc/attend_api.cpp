@@ -272,7 +272,7 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
     a.q = (const char *)q + (int64_t)first * ts * esz;
     a.out = (char *)out + (int64_t)first * token * esz;
     a.lse = lse ? lse + (int64_t)first * attn->q_heads : nullptr;
-    hipError_t e = kivi ? cga::rows4_launch(a, bf16, st) : p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
+    hipError_t e = kivi ? (p.few ? cga::rows4_launch(a, bf16, st) : cga::tile4_launch(a, bf16, st)) : p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
     if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
     if (p.merge && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
       return cgh::hip_error(e, "cg_attend merge launch");
