@@ -4,11 +4,11 @@
 // next unit beside the value product of the present one.
 //
 // Keys and values are widened to what they stand for, since their ranges differ along the
-// contraction (keys: by channel) or along both axes (values): one multiply-add a code in
-// fp32, rounded to fp16 once for all rows, in two parts where log-sums or
-// weights are asked for or the storage is fp32.  A power of two a unit keeps either in fp16's
-// range; it is found from the unit's 256 ranges two turns before the codes are
-// widened, a range to a thread.
+// contraction (keys: by channel) or along both axes (values): two packed fp16
+// multiply-adds a pair of codes, once for all rows, or in fp32 and in two parts (keys where
+// log-sums or weights are asked for, both for fp32 storage).  Where a unit's values leave
+// fp16's range a power of two brings them back; the units' largest magnitudes are found
+// from their ranges every fourth turn, a unit to a wave, four to seven turns ahead.
 #include <type_traits>
 
 #include "attend.hpp"
@@ -19,16 +19,24 @@ namespace cga {
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 
 constexpr int HALF_D = D / 2;  // bytes of a row of codes
-constexpr int kTop = 14;       // widened keys and values are below 2^14
+constexpr int kTop = 9;        // widened keys and values are below 2^9
 
 // LDS of a workgroup's token loop; two parts of the keys (P2), of the values (V2)
 template <bool P2, bool V2, int NW>
 struct Lds4 {
   static constexpr int K = 0, KLO = 2 * KBYTES, V = KLO + (P2 ? 2 * KBYTES : 0), VLO = V + 3 * VBYTES;
-  static constexpr int TOPS = VLO + (V2 ? 3 * VBYTES : 0);  // [4][4]: largest magnitudes, of the keys by waves 0 and 1, of the values by 2 and 3
-  static constexpr int BAD = TOPS + 64;                     // [4][2]: value ranges that are not numbers, bit 4 token + group
-  static constexpr int QLO = BAD + 64, LOOP = QLO + (P2 ? NW * 8192 : 0);
+  static constexpr int TOPS = VLO + (V2 ? 3 * VBYTES : 0);  // [8]: Unit4 of units that come
+  static constexpr int QLO = TOPS + 8 * 32, LOOP = QLO + (P2 ? NW * 8192 : 0);
   static constexpr int END = NW * WROWS * PITCH * 4, SIZE = LOOP > END ? LOOP : END;
+};
+
+// What a unit's ranges say: powers of two that keys and values are below, value ranges that are
+// not numbers (bit 2 token + group / 2 of groups 0 and 2, of groups 1 and 3)
+struct Unit4 {
+  int ek;
+  int ev;
+  uint32_t some, none;  // whether there is such a range
+  uint64_t bad0, bad1;
 };
 
 // A unit's codes and ranges on their way: N = 16 or 8 values of the keys and of the values to a thread.
@@ -38,10 +46,8 @@ struct Regs4 {
   uint32_t k[N / 8], v[N / 8];
   f4_t mk[4];
   float2 mv;
-  float2 top;  // one of the 256 ranges of the unit two further
 };
 
-template <int N>
 struct Place4 {
   const uint8_t *kf, *vf;
   const float2 *km, *vm;
@@ -49,25 +55,19 @@ struct Place4 {
 };
 
 template <int N>
-__device__ __forceinline__ void fetch4(const Place4<N> &p, int un, Regs4<N> &s) {
-  const int i = threadIdx.x;
-  const int64_t t0 = (int64_t)min(un, p.last) * UNIT;
-  constexpr int VT = D / N;  // threads to a token's values
+__device__ __forceinline__ void fetch4(const Place4 &p, int un, Regs4<N> &s) {
+  const uint32_t i = threadIdx.x;
+  const int64_t u = min(un, p.last);
+  constexpr uint32_t VT = D / N;  // threads to a token's values
+  const uint8_t *kc = p.kf + u * (UNIT * HALF_D), *vc = p.vf + u * (UNIT * HALF_D);
+  const uint8_t *km = (const uint8_t *)(p.km + u * 128), *vm = (const uint8_t *)(p.vm + u * 128);
 #pragma unroll
-  for (int x = 0; x < N / 8; x++) s.k[x] = *(const uint32_t *)(p.kf + (t0 + (i >> 4) + 16 * x) * HALF_D + 4 * (i & 15));
-  const uint32_t *v = (const uint32_t *)(p.vf + (t0 + i / VT) * HALF_D + N / 2 * (i % VT));
+  for (uint32_t x = 0; x < N / 8; x++) s.k[x] = *(const uint32_t *)(kc + ((i >> 4) * HALF_D + 4 * (i & 15)) + x * 16 * HALF_D);
 #pragma unroll
-  for (int x = 0; x < N / 8; x++) s.v[x] = v[x];
-  const f4_t *m = (const f4_t *)(p.km + t0 * 4 + 8 * (i & 15));
+  for (uint32_t x = 0; x < N / 8; x++) s.v[x] = *(const uint32_t *)(vc + ((i / VT) * HALF_D + N / 2 * (i % VT)) + 4 * x);
 #pragma unroll
-  for (int x = 0; x < 4; x++) s.mk[x] = m[x];
-  s.mv = p.vm[(t0 + i / VT) * 4 + N * (i % VT) / 32];
-}
-
-template <int N>
-__device__ __forceinline__ void fetch_top(const Place4<N> &p, int un, Regs4<N> &s) {
-  const int i = threadIdx.x & 255;  // the same for both halves of eight waves
-  s.top = (i < 128 ? p.km : p.vm - 128)[(int64_t)min(un, p.last) * 128 + i];
+  for (uint32_t x = 0; x < 4; x++) s.mk[x] = *(const f4_t *)(km + 64 * (i & 15) + 16 * x);
+  s.mv = *(const float2 *)(vm + (i / VT) * 32 + 8 * (N * (i % VT) / 32));
 }
 
 __device__ __forceinline__ float range_top(float2 m) { return fmaxf(fabsf(m.x), fabsf(__builtin_fmaf(15.0f, m.y, m.x))); }
@@ -75,94 +75,135 @@ __device__ __forceinline__ float range_top(float2 m) { return fmaxf(fabsf(m.x), 
 __device__ __forceinline__ bool bad_range(float2 m) {
   return !(range_top(m) + fabsf(m.x) < INFINITY && m.y < INFINITY);
 }
-// smallest E with |x| < 2^E
-__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 126; }
-
-// the unit's largest magnitudes, and its value ranges that are not numbers; `len`: rows of the
-// sequence, `tmax`: tokens that some row of the workgroup sees
-template <typename L, int N>
-__device__ __forceinline__ void put_top(unsigned char *lds, int un, int len, int tmax, const Regs4<N> &s) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (wave >= 4) return;
-  const bool there = wave < 2 ? un * UNIT < tmax : un * UNIT + 16 * (wave & 1) + (lane >> 2) < len;
-  const float2 m = there ? s.top : make_float2(0.f, 0.f);
-  const bool bad = wave >= 2 && bad_range(m);
-  const uint64_t all = __ballot(bad);
-  const float t = wave_max(bad ? 0.0f : range_top(m));
-  if (lane == 0) {
-    *(float *)(lds + L::TOPS + 16 * (un & 3) + 4 * wave) = t;
-    if (wave >= 2) *(uint64_t *)(lds + L::BAD + 16 * (un & 3) + 8 * (wave & 1)) = all;
-  }
+// A power of two above x: 2^9, which asks for no scaling, where x is in [2^-3, 2^8), so that small values keep
+// 2^-22 of the largest; else the smallest
+__device__ __forceinline__ int exponent_of(float x) {
+  const int e = (int)(__float_as_uint(x) >> 23) - 126;
+  return e >= -2 && e <= 8 ? kTop : e;
 }
 
-struct Exponents {
-  int k, v;
+// a wave's unit: two ranges of keys and of values to a lane
+struct Tops4 {
+  f4_t k, v;
 };
-template <typename L>
-__device__ __forceinline__ Exponents exponents_at(const unsigned char *lds, int un) {
-  const f4_t t = *(const f4_t *)(lds + L::TOPS + 16 * (un & 3));
-  return Exponents{exponent_of(fmaxf(t[0], t[1])), exponent_of(fmaxf(t[2], t[3]))};
+__device__ __forceinline__ void fetch_tops(const Place4 &p, int un, Tops4 &s) {
+  const int lane = threadIdx.x & 63;
+  const int64_t u = min(un, p.last);
+  s.k = *(const f4_t *)((const uint8_t *)(p.km + u * 128) + 16u * lane);
+  s.v = *(const f4_t *)((const uint8_t *)(p.vm + u * 128) + 16u * lane);
 }
-
-// eight codes as floats
-__device__ __forceinline__ void codes_f32(uint32_t w, float (&c)[8]) {
-  const uint32_t e = w & 0x0f0f0f0fu, o = (w >> 4) & 0x0f0f0f0fu;
-#pragma unroll
-  for (int k = 0; k < 4; k++) {
-    c[2 * k] = (float)((e >> 8 * k) & 0xffu);
-    c[2 * k + 1] = (float)((o >> 8 * k) & 0xffu);
+template <typename L>
+__device__ __forceinline__ void put_tops(unsigned char *lds, int un, int len, const Tops4 &s) {
+  const int lane = threadIdx.x & 63;
+  const float tk = wave_max(fmaxf(range_top(make_float2(s.k[0], s.k[1])), range_top(make_float2(s.k[2], s.k[3]))));
+  const bool there = un * UNIT + (lane >> 1) < len;  // ranges behind the sequence's end are whatever they are
+  const float2 m0 = make_float2(s.v[0], s.v[1]), m1 = make_float2(s.v[2], s.v[3]);
+  const bool bad0 = there && bad_range(m0), bad1 = there && bad_range(m1);
+  const uint64_t b0 = __ballot(bad0), b1 = __ballot(bad1);
+  const float tv = wave_max(fmaxf(there && !bad0 ? range_top(m0) : 0.0f, there && !bad1 ? range_top(m1) : 0.0f));
+  if (lane == 0) {
+    Unit4 *u = (Unit4 *)(lds + L::TOPS) + (un & 7);
+    *u = Unit4{exponent_of(tk), exponent_of(tv), (b0 | b1) ? 1u : 0u, 0u, b0, b1};
   }
 }
 
-// 8 values as fp16, what is left of them in `lo` (TWO)
-template <bool TWO>
-__device__ __forceinline__ void put8(unsigned char *p, int lo, const float (&x)[8]) {
+// Eight codes as halves, less 8 and times 2^-9: pairs (0, 4), (1, 5), (2, 6), (3, 7).  The low ones of
+// a byte's are multiples of 2^-24 as they stand, the high ones of 2^-20.
+__device__ __forceinline__ void centred8(uint32_t w, h2_t (&c)[4]) {
+  const h2_t up = {(_Float16)32768.0f, (_Float16)32768.0f}, up16 = {(_Float16)2048.0f, (_Float16)2048.0f};
+  const h2_t mid = {(_Float16)-0x1p-6f, (_Float16)-0x1p-6f};
+  const uint32_t x = w >> 8;
+  c[0] = __builtin_elementwise_fma(__builtin_bit_cast(h2_t, w & 0x000f000fu), up, mid);
+  c[1] = __builtin_elementwise_fma(__builtin_bit_cast(h2_t, w & 0x00f000f0u), up16, mid);
+  c[2] = __builtin_elementwise_fma(__builtin_bit_cast(h2_t, x & 0x000f000fu), up, mid);
+  c[3] = __builtin_elementwise_fma(__builtin_bit_cast(h2_t, x & 0x00f000f0u), up16, mid);
+}
+
+__device__ __forceinline__ h2_t pack2(float a, float b) {
+  const f2_t v = {a, b};
+  return __builtin_convertvector(v, h2_t);
+}
+
+// the values themselves, in the order of centred8, from a step (times 2^9) and a centre a pair
+__device__ __forceinline__ void put_centred(unsigned char *p, uint32_t w, const h2_t (&st)[4], const h2_t (&mid)[4]) {
+  h2_t c[4];
+  centred8(w, c);
+#pragma unroll
+  for (int k = 0; k < 4; k++) c[k] = __builtin_elementwise_fma(c[k], st[k], mid[k]);
+  *(h8_t *)p = as_h8(__builtin_bit_cast(uint32_t, c[0]), __builtin_bit_cast(uint32_t, c[1]), __builtin_bit_cast(uint32_t, c[2]),
+                     __builtin_bit_cast(uint32_t, c[3]));
+}
+
+// in two parts, formed in fp32, in the order of the channels
+__device__ __forceinline__ void put_two(unsigned char *p, int lo, uint32_t w, const float (&st)[8], const float (&m)[8]) {
+  const uint32_t e = w & 0x0f0f0f0fu, o = (w >> 4) & 0x0f0f0f0fu;
   uint32_t h[4], l[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) {
-    h[k] = pack_f16x2(x[2 * k], x[2 * k + 1]);
-    if constexpr (TWO) {
-      const f2_t hh = unpack_f16x2(h[k]);
-      l[k] = pack_f16x2(x[2 * k] - hh.x, x[2 * k + 1] - hh.y);
-    }
+    const float x = __builtin_fmaf((float)((e >> 8 * k) & 0xffu), st[2 * k], m[2 * k]);
+    const float y = __builtin_fmaf((float)((o >> 8 * k) & 0xffu), st[2 * k + 1], m[2 * k + 1]);
+    h[k] = pack_f16x2(x, y);
+    const f2_t hh = unpack_f16x2(h[k]);
+    l[k] = pack_f16x2(x - hh.x, y - hh.y);
   }
   *(h8_t *)p = as_h8(h[0], h[1], h[2], h[3]);
-  if constexpr (TWO) *(h8_t *)(p + lo) = as_h8(l[0], l[1], l[2], l[3]);
+  *(h8_t *)(p + lo) = as_h8(l[0], l[1], l[2], l[3]);
 }
 
 template <typename L, bool P2, bool V2, int N>
-__device__ __forceinline__ void put4(unsigned char *lds, int un, int len, int tmax, const Regs4<N> &s) {
+__device__ __forceinline__ void put4(unsigned char *lds, int un, int len, const Regs4<N> &s) {
   const int i = threadIdx.x;
   constexpr int VT = D / N;
-  const Exponents e = exponents_at<L>(lds, un);
-  float c[8], x[8];
+  const Unit4 *u = (const Unit4 *)(lds + L::TOPS) + (un & 7);
+  const int sk = kTop - __builtin_amdgcn_readfirstlane(u->ek), sv = kTop - __builtin_amdgcn_readfirstlane(u->ev);
   {
-    const bool there = un * UNIT < tmax;  // a block that holds no row yet is not looked at
     float m[8], st[8];
 #pragma unroll
     for (int k = 0; k < 8; k++) {
-      m[k] = there ? __builtin_ldexpf(s.mk[k >> 1][2 * (k & 1)], kTop - e.k) : 0.0f;
-      st[k] = there ? __builtin_ldexpf(s.mk[k >> 1][2 * (k & 1) + 1], kTop - e.k) : 0.0f;
+      m[k] = s.mk[k >> 1][2 * (k & 1)];
+      st[k] = s.mk[k >> 1][2 * (k & 1) + 1];
+    }
+    if (sk != 0) {
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        m[k] = __builtin_ldexpf(m[k], sk);
+        st[k] = __builtin_ldexpf(st[k], sk);
+      }
     }
     unsigned char *k = lds + L::K + (un & 1) * KBYTES + (i >> 4) * KP + 16 * (i & 15);
+    if constexpr (P2) {
 #pragma unroll
-    for (int t = 0; t < N / 8; t++) {
-      codes_f32(s.k[t], c);
+      for (int t = 0; t < N / 8; t++) put_two(k + 16 * t * KP, L::KLO - L::K, s.k[t], st, m);
+    } else {
+      h2_t hs[4], hm[4];
 #pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = __builtin_fmaf(c[j], st[j], m[j]);
-      put8<P2>(k + 16 * t * KP, L::KLO - L::K, x);
+      for (int x = 0; x < 4; x++) {
+        hs[x] = pack2(st[x], st[x + 4]) * (_Float16)512.0f;  // 35000 at most
+        hm[x] = pack2(__builtin_fmaf(8.0f, st[x], m[x]), __builtin_fmaf(8.0f, st[x + 4], m[x + 4]));
+      }
+#pragma unroll
+      for (int t = 0; t < N / 8; t++) put_centred(k + 16 * t * KP, s.k[t], hs, hm);
     }
   }
   {
     const bool there = un * UNIT + i / VT < len && !bad_range(s.mv);
-    const float m = there ? __builtin_ldexpf(s.mv.x, kTop - e.v) : 0.0f, st = there ? __builtin_ldexpf(s.mv.y, kTop - e.v) : 0.0f;
+    const float m = there ? __builtin_ldexpf(s.mv.x, sv) : 0.0f, st = there ? __builtin_ldexpf(s.mv.y, sv) : 0.0f;
     unsigned char *v = lds + L::V + (un % 3) * VBYTES + (i / VT) * VP + 2 * N * (i % VT);
+    if constexpr (V2) {
+      float ms[8], sts[8];
 #pragma unroll
-    for (int t = 0; t < N / 8; t++) {
-      codes_f32(s.v[t], c);
+      for (int k = 0; k < 8; k++) {
+        ms[k] = m;
+        sts[k] = st;
+      }
 #pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = __builtin_fmaf(c[j], st, m);
-      put8<V2>(v + 16 * t, L::VLO - L::V, x);
+      for (int t = 0; t < N / 8; t++) put_two(v + 16 * t, L::VLO - L::V, s.v[t], sts, ms);
+    } else {
+      const float c = __builtin_fmaf(8.0f, st, m);
+      const h2_t a = pack2(st, st) * (_Float16)512.0f, z = pack2(c, c);
+      const h2_t hs[4] = {a, a, a, a}, hm[4] = {z, z, z, z};
+#pragma unroll
+      for (int t = 0; t < N / 8; t++) put_centred(v + 16 * t, s.v[t], hs, hm);
     }
   }
 }
@@ -197,7 +238,9 @@ __device__ __forceinline__ void tile_queries4(const float *xs, float c, Queries4
     uint32_t h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const float u = x[2 * s + (k >> 1)][2 * (k & 1)] * sc.up, v = x[2 * s + (k >> 1)][2 * (k & 1) + 1] * sc.up;
+      // one part: in the order of centred8
+      const float u = (TWO ? x[2 * s + (k >> 1)][2 * (k & 1)] : x[2 * s][k]) * sc.up;
+      const float v = (TWO ? x[2 * s + (k >> 1)][2 * (k & 1) + 1] : x[2 * s + 1][k]) * sc.up;
       h[k] = pack_f16x2(u, v);
       if constexpr (TWO) {
         const f2_t hh = unpack_f16x2(h[k]);
@@ -326,16 +369,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
   const int h = bh % a.heads, b = bh / a.heads;
   const int r0 = grpi * TROWS, nr = min(TROWS, a.rows - r0);
   const Sequence sq = load_sequence(a, b);
-  const Place4<N> place{a.kpay + (int64_t)bh * a.tcap * HALF_D, a.vpay + (int64_t)bh * a.tcap * HALF_D,
-                        a.kmeta + (int64_t)bh * a.tcap * 4, a.vmeta + (int64_t)bh * a.tcap * 4, (int)a.nblk - 1};
+  const Place4 place{a.kpay + (int64_t)bh * a.tcap * HALF_D, a.vpay + (int64_t)bh * a.tcap * HALF_D,
+                     a.kmeta + (int64_t)bh * a.tcap * 4, a.vmeta + (int64_t)bh * a.tcap * 4, (int)a.nblk - 1};
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
   const int u0 = split_begin(units, split, a.splits), u1 = split_begin(units, split + 1, a.splits);
-  Regs4<N> nx, ny;
+  Regs4<N> nx;
+  Tops4 tops;  // a wave's own of four units: a workgroup's first four waves find them every fourth turn
   if (u0 < u1) {
     fetch4(place, u0, nx);
-    fetch_top(place, u0, nx);
-    fetch_top(place, u0 + 1, ny);
+    if (wave < 4) fetch_tops(place, u0 + wave, tops);
   }
 
   // gauged queries as operands
@@ -388,33 +431,31 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
   // the row's factor of a unit's scores and the log2 of its values' power of two; marks the rows that see
   // a value that is not a number
   const auto factors = [&](int un, float &A, float &lv) {
-    const Exponents e = exponents_at<L>(lds, un);
-    A = __builtin_ldexpf(q.ca, e.k - kTop);
-    lv = (float)e.v;
-    const uint64_t *bad = (const uint64_t *)(lds + L::BAD + 16 * (un & 3));
-    const uint64_t b0 = bad[0], b1 = bad[1];
-    if (__builtin_amdgcn_readfirstlane((uint32_t)(b0 | b0 >> 32 | b1 | b1 >> 32))) {
-      const int vis = min(max(lim - un * UNIT, 0), UNIT), v0 = min(vis, 16), v1 = vis - v0;
-      uint64_t x = (v0 < 16 ? b0 & ((1ull << 4 * v0) - 1) : b0) | (v1 < 16 ? b1 & ((1ull << 4 * v1) - 1) : b1);
-#pragma unroll
-      for (int k = 32; k >= 4; k >>= 1) x |= x >> k;
-      st.poison |= (uint32_t)x & 15u;
+    const Unit4 *u = (const Unit4 *)(lds + L::TOPS) + (un & 7);
+    const int4 e = *(const int4 *)u;
+    A = __builtin_ldexpf(q.ca, e.x - kTop);
+    lv = (float)e.y;
+    if (__builtin_amdgcn_readfirstlane(e.z)) {
+      const int vis = min(max(lim - un * UNIT, 0), UNIT);
+      const uint64_t see = vis < 32 ? (1ull << 2 * vis) - 1 : ~0ull;
+      const uint64_t b0 = u->bad0 & see, b1 = u->bad1 & see;
+      constexpr uint64_t EVEN = 0x5555555555555555ull;
+      st.poison |= (b0 & EVEN ? 1u : 0u) | (b1 & EVEN ? 2u : 0u) | (b0 & ~EVEN ? 4u : 0u) | (b1 & ~EVEN ? 8u : 0u);
     }
   };
 
   if (u0 < u1) {
     Weights4 o;
     UnitOperands<BF16> P;
-    put_top<L>(lds, u0, sq.len, tmax, nx);
-    put_top<L>(lds, u0 + 1, sq.len, tmax, ny);
-    fetch_top(place, u0 + 2, nx);
+    if (wave < 4) {
+      put_tops<L>(lds, u0 + wave, sq.len, tops);
+      fetch_tops(place, u0 + 4 + wave, tops);
+    }
     __syncthreads();
-    put4<L, P2, V2>(lds, u0, sq.len, tmax, nx);
+    put4<L, P2, V2>(lds, u0, sq.len, nx);
     fetch4(place, u0 + 1, nx);  // units past the last are fetched (rows that exist) and not used
-    put_top<L>(lds, u0 + 2, sq.len, tmax, nx);
-    put4<L, P2, V2>(lds, u0 + 1, sq.len, tmax, nx);
+    if (u0 + 1 < u1) put4<L, P2, V2>(lds, u0 + 1, sq.len, nx);
     fetch4(place, u0 + 2, nx);
-    fetch_top(place, u0 + 3, nx);
     __syncthreads();
     float A, lv;
     factors(u0, A, lv);
@@ -428,10 +469,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
     if constexpr (SUMS) store_sum(u0);
     const auto turn = [&](int un, auto masked) {
       __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
-      put4<L, P2, V2>(lds, un + 2, sq.len, tmax, nx);
-      put_top<L>(lds, un + 3, sq.len, tmax, nx);
+      if (un + 2 < u1) put4<L, P2, V2>(lds, un + 2, sq.len, nx);
       fetch4(place, un + 3, nx);
-      fetch_top(place, un + 4, nx);
+      if (((un - u0) & 3) == 0 && wave < 4) {
+        put_tops<L>(lds, un + 4 + wave, sq.len, tops);
+        fetch_tops(place, un + 8 + wave, tops);
+      }
       const int vis = lim - (un + 1) * UNIT - 4 * half;
       st.l += o.ps;
       pack_weights<BF16>(o.p, P);
@@ -472,8 +515,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
       for (int r = 0; r < 16; r += 4) {
         f4_t v;
 #pragma unroll
-        for (int x = 0; x < 4; x++) v[x] = __builtin_fmaf(acc[j][r + x] * 0x1p-23f, ks, k);  // 2^14 of the values, 2^9 of f
-        *(f4_t *)(us + rr * PITCH + 32 * j + 2 * r + 4 * half) = v;
+        for (int x = 0; x < 4; x++) v[x] = __builtin_fmaf(acc[j][r + x] * 0x1p-18f, ks, k);  // 2^9 of the values, 2^9 of f
+        float *o = us + rr * PITCH + 32 * j + 2 * r;
+        if constexpr (V2) {
+          *(f4_t *)(o + 4 * half) = v;
+        } else {  // the order of centred8
+          *(float2 *)(o + 2 * half) = make_float2(v[0], v[2]);
+          *(float2 *)(o + 2 * half + 4) = make_float2(v[1], v[3]);
+        }
       }
     }
     if (half == 0 && rr < nr) {
@@ -502,7 +551,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
 
 hipError_t tile4_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const bool p2 = !bf16 || a.lse || a.mass, sums = a.bsum != nullptr;
-  const int nw = p2 || a.rows > 128 ? 8 : 4;
+  const int nw = p2 ? 8 : 4;
   const int64_t groups = (a.rows + nw * WROWS - 1) / (nw * WROWS);
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * groups * a.splits)), block(64 * nw);
 #define CG_T(BF, P2, SUMS, NW)                                                             \
