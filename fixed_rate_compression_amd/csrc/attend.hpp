@@ -74,6 +74,10 @@ struct AttendArgs {
   int32_t waves;  // of a few-row workgroup: 4 or 8
   int32_t ragged, slots, least;  // few rows of sequences of unlike lengths: see Slot
   float c;                       // scale log2(e)
+  // many rows over the 4-bit cache: what ranges4_launch leaves of every block of the tokens' bound
+  uint8_t *ranges;               // [b][h][block] scaled ranges
+  void *units;                   // [b][h][block] powers of two
+  int32_t two;                   // keys in two parts
 };
 
 // rows [0, rows) of every field over its tokens, one workgroup per (field,
@@ -83,7 +87,10 @@ hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t rows4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // the same for many rows, one workgroup per (field, 128 rows, split)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
-// and over the 4-bit cache, one per (field, 128 or 256 rows, split)
+// and over the 4-bit cache, one per (field, 128 or 256 rows, split), after ranges4_launch
+int ranges4_bytes(bool bf16, bool two);  // of a block
+int units4_bytes();
+hipError_t ranges4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t tile4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t merge_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // block weights from the attention's block sums, of few rows and of many

@@ -7,8 +7,9 @@
 // contraction (keys: by channel) or along both axes (values): two packed fp16
 // multiply-adds a pair of codes, once for all rows, or in fp32 and in two parts (keys where
 // log-sums or weights are asked for, both for fp32 storage).  Where a unit's values leave
-// fp16's range a power of two brings them back; the units' largest magnitudes are found
-// from their ranges every fourth turn, a unit to a wave, four to seven turns ahead.
+// fp16's range a power of two brings them back.  That and the ranges in the form in which they are
+// used come from a launch before (k_ranges4): the vector units bound this kernel, and forming
+// them at every use took 64 of its 235 vector instructions a wave and unit.
 #include <type_traits>
 
 #include "attend.hpp"
@@ -25,86 +26,127 @@ constexpr int kTop = 9;        // widened keys and values are below 2^9
 template <bool P2, bool V2, int NW>
 struct Lds4 {
   static constexpr int K = 0, KLO = 2 * KBYTES, V = KLO + (P2 ? 2 * KBYTES : 0), VLO = V + 3 * VBYTES;
-  static constexpr int TOPS = VLO + (V2 ? 3 * VBYTES : 0);  // [8]: Unit4 of units that come
-  static constexpr int QLO = TOPS + 8 * 32, LOOP = QLO + (P2 ? NW * 8192 : 0);
+  static constexpr int QLO = VLO + (V2 ? 3 * VBYTES : 0), LOOP = QLO + (P2 ? NW * 8192 : 0);
   static constexpr int END = NW * WROWS * PITCH * 4, SIZE = LOOP > END ? LOOP : END;
 };
 
-// What a unit's ranges say: powers of two that keys and values are below, value ranges that are
-// not numbers (bit 2 token + group / 2 of groups 0 and 2, of groups 1 and 3)
+// What the tiles need of a block's ranges, formed once for all of them (k_ranges4): powers of
+// two that keys and values are below, value ranges that are not numbers (bit 4 token + group, of the first and
+// the last 16 tokens), and the ranges themselves, scaled, as they are used.  Keys in one part: for 8
+// channels the steps times 2^9, then the centres, as halves in the order of centred8; in two parts:
+// (minimum, step) in fp32.  Values likewise, a pair a token and group.
 struct Unit4 {
-  int ek;
-  int ev;
-  uint32_t some, none;  // whether there is such a range
+  int ek, ev;
+  uint32_t bad, none;  // whether there is such a range
   uint64_t bad0, bad1;
 };
+template <bool P2, bool V2>
+struct Ranges4 {
+  static constexpr int K = P2 ? 1024 : 512, V = V2 ? 1024 : 512, BYTES = K + V;
+};
+
+// the largest bit pattern over a wave, of magnitudes
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+  const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(x[0], x[1]);
+  const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(y[0], y[1]);
+}
+__device__ __forceinline__ uint32_t range_bits(float2 m) {  // of the larger end of a range; a NaN is the largest
+  const uint32_t a = __float_as_uint(m.x) & 0x7fffffffu, b = __float_as_uint(__builtin_fmaf(15.0f, m.y, m.x)) & 0x7fffffffu;
+  return max(a, b);
+}
+// A power of two above x: 2^9, which asks for no scaling, where x is in [2^-3, 2^8), so that small values keep
+// 2^-22 of the largest; else the smallest
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  const int e = (int)(bits >> 23) - 126;
+  return e >= -2 && e <= 8 ? kTop : e;
+}
+
+// One wave to a block of a sequence's tokens.
+template <bool P2, bool V2>
+__global__ __launch_bounds__(NTH) void k_ranges4(const AttendArgs a, int blocks) {
+  using R = Ranges4<P2, V2>;
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * (NTH / 64) + (threadIdx.x >> 6);  // (b, h, block)
+  const int64_t bh = at / blocks;
+  const int blk = (int)(at - bh * blocks);
+  if (bh >= (int64_t)a.batch * a.heads) return;
+  const Sequence sq = load_sequence(a, (int)(bh / a.heads));
+  if (blk * UNIT >= sq.len) return;
+  const float2 *km = a.kmeta + (bh * a.tcap + (int64_t)blk * UNIT) * 4, *vm = a.vmeta + (bh * a.tcap + (int64_t)blk * UNIT) * 4;
+  const int c0 = 8 * (lane >> 2) + (lane & 3);  // this lane's channels: c0 and c0 + 4
+  float2 k[2] = {km[c0], km[c0 + 4]}, v[2] = {vm[lane], vm[lane + 64]};  // values: token, group of entry 4 token + group
+  // ranges behind the sequence's end are whatever they are; one that gives a NaN or an infinity for some
+  // code (15 steps alone may) counts as zeros and is marked
+  constexpr uint32_t INF = 0x7f800000u;
+  uint64_t bad[2];
+#pragma unroll
+  for (int x = 0; x < 2; x++) {
+    const bool there = blk * UNIT + 16 * x + (lane >> 2) < sq.len;
+    const bool b = there && max(range_bits(v[x]), __float_as_uint(v[x].y) & 0x7fffffffu) >= INF;
+    bad[x] = __ballot(b);
+    if (!there || b) v[x] = make_float2(0.f, 0.f);
+  }
+  const int ek = exponent_of(wave_umax(max(range_bits(k[0]), range_bits(k[1]))));
+  const int ev = exponent_of(wave_umax(max(range_bits(v[0]), range_bits(v[1]))));
+  if (lane == 0) ((Unit4 *)a.units)[at] = Unit4{ek, ev, bad[0] | bad[1] ? 1u : 0u, 0u, bad[0], bad[1]};
+  uint8_t *o = a.ranges + at * R::BYTES;
+#pragma unroll
+  for (int x = 0; x < 2; x++) {
+    k[x] = make_float2(__builtin_ldexpf(k[x].x, kTop - ek), __builtin_ldexpf(k[x].y, kTop - ek));
+    v[x] = make_float2(__builtin_ldexpf(v[x].x, kTop - ev), __builtin_ldexpf(v[x].y, kTop - ev));
+  }
+  if constexpr (P2) {
+    ((float2 *)o)[c0] = k[0];
+    ((float2 *)o)[c0 + 4] = k[1];
+  } else {
+    uint32_t *p = (uint32_t *)(o + 32 * (lane >> 2)) + (lane & 3);
+    p[0] = pack_f16x2(512.0f * k[0].y, 512.0f * k[1].y);  // 35000 at most
+    p[4] = pack_f16x2(__builtin_fmaf(8.0f, k[0].y, k[0].x), __builtin_fmaf(8.0f, k[1].y, k[1].x));
+  }
+#pragma unroll
+  for (int x = 0; x < 2; x++) {
+    if constexpr (V2) ((float2 *)(o + R::K))[lane + 64 * x] = v[x];
+    else ((uint32_t *)(o + R::K))[lane + 64 * x] = pack_f16x2(512.0f * v[x].y, __builtin_fmaf(8.0f, v[x].y, v[x].x));
+  }
+}
 
 // A unit's codes and ranges on their way: N = 16 or 8 values of the keys and of the values to a thread.
 // Keys: channels 8 (i % 16) .. + 7 of tokens i / 16, + 16; values: N channels of a token.
-template <int N>
+template <bool P2, bool V2, int N>
 struct Regs4 {
   uint32_t k[N / 8], v[N / 8];
-  f4_t mk[4];
-  float2 mv;
+  u4_t mk[P2 ? 4 : 2];
+  uint32_t mv[V2 ? 2 : 1];
 };
 
 struct Place4 {
-  const uint8_t *kf, *vf;
-  const float2 *km, *vm;
-  int last;  // block of the capacity
+  const uint8_t *kf, *vf, *ranges;
+  const Unit4 *units;
+  int last;  // of the blocks that the tokens' bound has
 };
 
-template <int N>
-__device__ __forceinline__ void fetch4(const Place4 &p, int un, Regs4<N> &s) {
+template <bool P2, bool V2, int N>
+__device__ __forceinline__ void fetch4(const Place4 &p, int un, Regs4<P2, V2, N> &s) {
+  using R = Ranges4<P2, V2>;
   const uint32_t i = threadIdx.x;
   const int64_t u = min(un, p.last);
   constexpr uint32_t VT = D / N;  // threads to a token's values
-  const uint8_t *kc = p.kf + u * (UNIT * HALF_D), *vc = p.vf + u * (UNIT * HALF_D);
-  const uint8_t *km = (const uint8_t *)(p.km + u * 128), *vm = (const uint8_t *)(p.vm + u * 128);
+  const uint8_t *kc = p.kf + u * (UNIT * HALF_D), *vc = p.vf + u * (UNIT * HALF_D), *r = p.ranges + u * R::BYTES;
 #pragma unroll
   for (uint32_t x = 0; x < N / 8; x++) s.k[x] = *(const uint32_t *)(kc + ((i >> 4) * HALF_D + 4 * (i & 15)) + x * 16 * HALF_D);
 #pragma unroll
   for (uint32_t x = 0; x < N / 8; x++) s.v[x] = *(const uint32_t *)(vc + ((i / VT) * HALF_D + N / 2 * (i % VT)) + 4 * x);
 #pragma unroll
-  for (uint32_t x = 0; x < 4; x++) s.mk[x] = *(const f4_t *)(km + 64 * (i & 15) + 16 * x);
-  s.mv = *(const float2 *)(vm + (i / VT) * 32 + 8 * (N * (i % VT) / 32));
-}
-
-__device__ __forceinline__ float range_top(float2 m) { return fmaxf(fabsf(m.x), fabsf(__builtin_fmaf(15.0f, m.y, m.x))); }
-// whether a value range gives no number for some code
-__device__ __forceinline__ bool bad_range(float2 m) {
-  return !(range_top(m) + fabsf(m.x) < INFINITY && m.y < INFINITY);
-}
-// A power of two above x: 2^9, which asks for no scaling, where x is in [2^-3, 2^8), so that small values keep
-// 2^-22 of the largest; else the smallest
-__device__ __forceinline__ int exponent_of(float x) {
-  const int e = (int)(__float_as_uint(x) >> 23) - 126;
-  return e >= -2 && e <= 8 ? kTop : e;
-}
-
-// a wave's unit: two ranges of keys and of values to a lane
-struct Tops4 {
-  f4_t k, v;
-};
-__device__ __forceinline__ void fetch_tops(const Place4 &p, int un, Tops4 &s) {
-  const int lane = threadIdx.x & 63;
-  const int64_t u = min(un, p.last);
-  s.k = *(const f4_t *)((const uint8_t *)(p.km + u * 128) + 16u * lane);
-  s.v = *(const f4_t *)((const uint8_t *)(p.vm + u * 128) + 16u * lane);
-}
-template <typename L>
-__device__ __forceinline__ void put_tops(unsigned char *lds, int un, int len, const Tops4 &s) {
-  const int lane = threadIdx.x & 63;
-  const float tk = wave_max(fmaxf(range_top(make_float2(s.k[0], s.k[1])), range_top(make_float2(s.k[2], s.k[3]))));
-  const bool there = un * UNIT + (lane >> 1) < len;  // ranges behind the sequence's end are whatever they are
-  const float2 m0 = make_float2(s.v[0], s.v[1]), m1 = make_float2(s.v[2], s.v[3]);
-  const bool bad0 = there && bad_range(m0), bad1 = there && bad_range(m1);
-  const uint64_t b0 = __ballot(bad0), b1 = __ballot(bad1);
-  const float tv = wave_max(fmaxf(there && !bad0 ? range_top(m0) : 0.0f, there && !bad1 ? range_top(m1) : 0.0f));
-  if (lane == 0) {
-    Unit4 *u = (Unit4 *)(lds + L::TOPS) + (un & 7);
-    *u = Unit4{exponent_of(tk), exponent_of(tv), (b0 | b1) ? 1u : 0u, 0u, b0, b1};
-  }
+  for (uint32_t x = 0; x < (P2 ? 4 : 2); x++) s.mk[x] = *(const u4_t *)(r + (P2 ? 64 : 32) * (i & 15) + 16 * x);
+  const uint32_t *mv = (const uint32_t *)(r + R::K + (V2 ? 8 : 4) * ((i / VT) * 4 + N * (i % VT) / 32));
+#pragma unroll
+  for (int x = 0; x < (V2 ? 2 : 1); x++) s.mv[x] = mv[x];
 }
 
 // Eight codes as halves, less 8 and times 2^-9: pairs (0, 4), (1, 5), (2, 6), (3, 7).  The low ones of
@@ -150,63 +192,64 @@ __device__ __forceinline__ void put_two(unsigned char *p, int lo, uint32_t w, co
   *(h8_t *)(p + lo) = as_h8(l[0], l[1], l[2], l[3]);
 }
 
+// A unit into LDS in steps, to be taken between matrix instructions
 template <typename L, bool P2, bool V2, int N>
-__device__ __forceinline__ void put4(unsigned char *lds, int un, int len, const Regs4<N> &s) {
-  const int i = threadIdx.x;
-  constexpr int VT = D / N;
-  const Unit4 *u = (const Unit4 *)(lds + L::TOPS) + (un & 7);
-  const int sk = kTop - __builtin_amdgcn_readfirstlane(u->ek), sv = kTop - __builtin_amdgcn_readfirstlane(u->ev);
-  {
-    float m[8], st[8];
+struct Put4 {
+  static constexpr int VT = D / N;
+  const Regs4<P2, V2, N> &s;
+  unsigned char *k, *v;
+
+  __device__ __forceinline__ Put4(unsigned char *lds, int un, const Regs4<P2, V2, N> &regs) : s(regs) {
+    const int i = threadIdx.x;
+    k = lds + L::K + (un & 1) * KBYTES + (i >> 4) * KP + 16 * (i & 15);
+    v = lds + L::V + (un % 3) * VBYTES + (i / VT) * VP + 2 * N * (i % VT);
+  }
+  template <int S>
+  __device__ __forceinline__ void step() {
+    if constexpr (S < N / 8) {
+      if constexpr (P2) {
+        float m[8], st[8];
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-      m[k] = s.mk[k >> 1][2 * (k & 1)];
-      st[k] = s.mk[k >> 1][2 * (k & 1) + 1];
-    }
-    if (sk != 0) {
+        for (int c = 0; c < 8; c++) {
+          m[c] = __uint_as_float(s.mk[c >> 1][2 * (c & 1)]);
+          st[c] = __uint_as_float(s.mk[c >> 1][2 * (c & 1) + 1]);
+        }
+        put_two(k + 16 * S * KP, L::KLO - L::K, s.k[S], st, m);
+      } else {
+        h2_t hs[4], hm[4];
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        m[k] = __builtin_ldexpf(m[k], sk);
-        st[k] = __builtin_ldexpf(st[k], sk);
+        for (int x = 0; x < 4; x++) {
+          const uint32_t a = s.mk[0][x], c = s.mk[1][x];  // (a bit cast of a vector's element takes its first)
+          hs[x] = __builtin_bit_cast(h2_t, a);
+          hm[x] = __builtin_bit_cast(h2_t, c);
+        }
+        put_centred(k + 16 * S * KP, s.k[S], hs, hm);
       }
-    }
-    unsigned char *k = lds + L::K + (un & 1) * KBYTES + (i >> 4) * KP + 16 * (i & 15);
-    if constexpr (P2) {
+    } else if constexpr (S < N / 4) {
+      constexpr int T = S - N / 8;
+      if constexpr (V2) {
+        float ms[8], sts[8];
 #pragma unroll
-      for (int t = 0; t < N / 8; t++) put_two(k + 16 * t * KP, L::KLO - L::K, s.k[t], st, m);
-    } else {
-      h2_t hs[4], hm[4];
-#pragma unroll
-      for (int x = 0; x < 4; x++) {
-        hs[x] = pack2(st[x], st[x + 4]) * (_Float16)512.0f;  // 35000 at most
-        hm[x] = pack2(__builtin_fmaf(8.0f, st[x], m[x]), __builtin_fmaf(8.0f, st[x + 4], m[x + 4]));
+        for (int c = 0; c < 8; c++) {
+          ms[c] = __uint_as_float(s.mv[0]);
+          sts[c] = __uint_as_float(s.mv[1]);
+        }
+        put_two(v + 16 * T, L::VLO - L::V, s.v[T], sts, ms);
+      } else {
+        const h2_t m = __builtin_bit_cast(h2_t, s.mv[0]);
+        const h2_t st = {m.x, m.x}, mid = {m.y, m.y};
+        const h2_t hs[4] = {st, st, st, st}, hm[4] = {mid, mid, mid, mid};
+        put_centred(v + 16 * T, s.v[T], hs, hm);
       }
-#pragma unroll
-      for (int t = 0; t < N / 8; t++) put_centred(k + 16 * t * KP, s.k[t], hs, hm);
     }
   }
-  {
-    const bool there = un * UNIT + i / VT < len && !bad_range(s.mv);
-    const float m = there ? __builtin_ldexpf(s.mv.x, sv) : 0.0f, st = there ? __builtin_ldexpf(s.mv.y, sv) : 0.0f;
-    unsigned char *v = lds + L::V + (un % 3) * VBYTES + (i / VT) * VP + 2 * N * (i % VT);
-    if constexpr (V2) {
-      float ms[8], sts[8];
-#pragma unroll
-      for (int k = 0; k < 8; k++) {
-        ms[k] = m;
-        sts[k] = st;
-      }
-#pragma unroll
-      for (int t = 0; t < N / 8; t++) put_two(v + 16 * t, L::VLO - L::V, s.v[t], sts, ms);
-    } else {
-      const float c = __builtin_fmaf(8.0f, st, m);
-      const h2_t a = pack2(st, st) * (_Float16)512.0f, z = pack2(c, c);
-      const h2_t hs[4] = {a, a, a, a}, hm[4] = {z, z, z, z};
-#pragma unroll
-      for (int t = 0; t < N / 8; t++) put_centred(v + 16 * t, s.v[t], hs, hm);
-    }
+  __device__ __forceinline__ void all() {
+    step<0>();
+    step<1>();
+    step<2>();
+    step<3>();
   }
-}
+};
 
 // a lane's row (the same in lanes l and l + 32 but for l), as in attend_tile.hip; mu is -inf while the
 // row has seen nothing, f the log2 of the factor to the values' power of two
@@ -271,25 +314,10 @@ __device__ __forceinline__ void scores4(const unsigned char *kb, int klo, const 
   if constexpr (P2) z += zl;
 }
 
+// a unit's weights (times the values' factor) and the sum of those without it
 struct Weights4 {
   float p[16], ps;
 };
-
-// weights of a unit; vis: tokens of the unit, less 4 half, that the lane's row sees (MASKED).
-// Returns whether some weight is too large for its scale (or infinite: a row that has seen nothing yet).
-template <bool MASKED>
-__device__ __forceinline__ bool weights4(float A, float lv, const f16_t &z, int vis, const State4 &st, Weights4 &o) {
-  const float lw = fmaxf(lv + st.f, -60.0f), iw = exp2_fast(-lw), B = lw - st.mu;
-#pragma unroll
-  for (int r = 0; r < 16; r++) {
-    const float s = __builtin_fmaf(z[r], A, B);
-    o.p[r] = exp2_fast(MASKED && 8 * (r >> 2) + (r & 3) >= vis ? -INFINITY : s);
-  }
-  float sum[1];
-  sum_weights<1>(o.p, sum);
-  o.ps = sum[0] * iw;
-  return fmaxf(sum[0], o.ps * 128.0f) > 32768.0f;
-}
 
 // raise the row's maximum to the unit's scores, rescale what was summed, and form the
 // unit's weights again (rare: the scores are not kept for it)
@@ -369,17 +397,21 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
   const int h = bh % a.heads, b = bh / a.heads;
   const int r0 = grpi * TROWS, nr = min(TROWS, a.rows - r0);
   const Sequence sq = load_sequence(a, b);
+  const int blocks = (int)((a.tokens + UNIT - 1) / UNIT);
   const Place4 place{a.kpay + (int64_t)bh * a.tcap * HALF_D, a.vpay + (int64_t)bh * a.tcap * HALF_D,
-                     a.kmeta + (int64_t)bh * a.tcap * 4, a.vmeta + (int64_t)bh * a.tcap * 4, (int)a.nblk - 1};
+                     a.ranges + (int64_t)bh * blocks * Ranges4<P2, V2>::BYTES, (const Unit4 *)a.units + (int64_t)bh * blocks,
+                     blocks - 1};
   const int tmax = limit_of(a, sq, r0 / a.ratio, (r0 + nr - 1) / a.ratio);
   const int units = (tmax + UNIT - 1) / UNIT;
   const int u0 = split_begin(units, split, a.splits), u1 = split_begin(units, split + 1, a.splits);
-  Regs4<N> nx;
-  Tops4 tops;  // a wave's own of four units: a workgroup's first four waves find them every fourth turn
-  if (u0 < u1) {
-    fetch4(place, u0, nx);
-    if (wave < 4) fetch_tops(place, u0 + wave, tops);
-  }
+  // codes on their way, of units at even and odd distance from the first (with two parts, whose
+  // operands take registers, of one)
+  constexpr int SETS = P2 ? 1 : 2;
+  using In = Regs4<P2, V2, N>;
+  In nx[SETS];
+  if (u0 < u1)
+#pragma unroll
+    for (int x = 0; x < SETS; x++) fetch4(place, u0 + x, nx[x]);
 
   // gauged queries as operands
   Queries4 q;
@@ -428,37 +460,37 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
   const auto values_at = [&](int un) {
     return lds + L::V + (un % 3) * VBYTES + (4 * half + (n >> 2)) * VP + 32 * ((lane >> 4) & 1) + 8 * (n & 3);
   };
+  // a unit's powers of two, loaded a turn before they are used
+  int4 un_head;
+  const auto fetch_head = [&](int un) { un_head = *(const int4 *)(place.units + min(un, place.last)); };
   // the row's factor of a unit's scores and the log2 of its values' power of two; marks the rows that see
   // a value that is not a number
   const auto factors = [&](int un, float &A, float &lv) {
-    const Unit4 *u = (const Unit4 *)(lds + L::TOPS) + (un & 7);
-    const int4 e = *(const int4 *)u;
+    const int4 e = un_head;
     A = __builtin_ldexpf(q.ca, e.x - kTop);
     lv = (float)e.y;
     if (__builtin_amdgcn_readfirstlane(e.z)) {
-      const int vis = min(max(lim - un * UNIT, 0), UNIT);
-      const uint64_t see = vis < 32 ? (1ull << 2 * vis) - 1 : ~0ull;
-      const uint64_t b0 = u->bad0 & see, b1 = u->bad1 & see;
-      constexpr uint64_t EVEN = 0x5555555555555555ull;
-      st.poison |= (b0 & EVEN ? 1u : 0u) | (b1 & EVEN ? 2u : 0u) | (b0 & ~EVEN ? 4u : 0u) | (b1 & ~EVEN ? 8u : 0u);
+      const Unit4 *u = place.units + un;
+      const int vis = min(max(lim - un * UNIT, 0), UNIT), v0 = min(vis, 16), v1 = vis - v0;
+      uint64_t x = (v0 < 16 ? u->bad0 & ((1ull << 4 * v0) - 1) : u->bad0) | (v1 < 16 ? u->bad1 & ((1ull << 4 * v1) - 1) : u->bad1);
+#pragma unroll
+      for (int k = 32; k >= 4; k >>= 1) x |= x >> k;
+      st.poison |= (uint32_t)x & 15u;
     }
   };
 
   if (u0 < u1) {
     Weights4 o;
     UnitOperands<BF16> P;
-    if (wave < 4) {
-      put_tops<L>(lds, u0 + wave, sq.len, tops);
-      fetch_tops(place, u0 + 4 + wave, tops);
-    }
-    __syncthreads();
-    put4<L, P2, V2>(lds, u0, sq.len, nx);
-    fetch4(place, u0 + 1, nx);  // units past the last are fetched (rows that exist) and not used
-    if (u0 + 1 < u1) put4<L, P2, V2>(lds, u0 + 1, sq.len, nx);
-    fetch4(place, u0 + 2, nx);
+    Put4<L, P2, V2, N>(lds, u0, nx[0]).all();
+    fetch4(place, u0 + SETS, nx[0]);  // units past the last are fetched (blocks that exist), put and not used
+    fetch_head(u0);
+    Put4<L, P2, V2, N>(lds, u0 + 1, nx[SETS - 1]).all();
+    fetch4(place, u0 + 1 + SETS, nx[SETS - 1]);
     __syncthreads();
     float A, lv;
     factors(u0, A, lv);
+    fetch_head(u0 + 1);
     raise4<P2>(keys_at(u0), klo, lo, A, lv, q, lim - u0 * UNIT - 4 * half, st, acc, o);
     const auto store_sum = [&](int un) {
       const uint32_t x = __float_as_uint(o.ps);
@@ -467,30 +499,87 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
       if (half == 0 && wr < a.rows) a.bsum[((int64_t)bh * a.entries + un) * a.rows + wr] = make_float2(v, st.mu);
     };
     if constexpr (SUMS) store_sum(u0);
-    const auto turn = [&](int un, auto masked) {
+    const auto turn = [&](int un, auto masked, In &in) {
       __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
-      if (un + 2 < u1) put4<L, P2, V2>(lds, un + 2, sq.len, nx);
-      fetch4(place, un + 3, nx);
-      if (((un - u0) & 3) == 0 && wave < 4) {
-        put_tops<L>(lds, un + 4 + wave, sq.len, tops);
-        fetch_tops(place, un + 8 + wave, tops);
-      }
-      const int vis = lim - (un + 1) * UNIT - 4 * half;
-      st.l += o.ps;
-      pack_weights<BF16>(o.p, P);
       float A, lv;
       factors(un + 1, A, lv);
-      f16_t z;
-      scores4<P2>(keys_at(un + 1), klo, q, lo, z);
-      values4<V2>(values_at(un), vlo, P, acc);
-      const bool up = weights4<decltype(masked)::value>(A, lv, z, vis, st, o);
+      fetch_head(un + 2);
+      // One block from here on, in the order in which it is to be issued: a matrix instruction runs
+      // for 32 cycles beside what follows it.  The scores' products, with the next unit's
+      // widening between them, then the values', with the weights between them.
+      const int vis = lim - (un + 1) * UNIT - 4 * half;
+      const unsigned char *kb = keys_at(un + 1), *vb = values_at(un);
+      Put4<L, P2, V2, N> put(lds, un + 2, in);
+      f16_t z, zl;
+#pragma unroll
+      for (int r = 0; r < 16; r++) z[r] = zl[r] = 0.0f;
+      h8_t kc[2] = {*(const h8_t *)kb, *(const h8_t *)(kb + 32)};
+      const auto score = [&](auto step) {
+        constexpr int S = decltype(step)::value;
+        z = mfma32(kc[S & 1], q.hi[S], z);
+        if constexpr (P2) {
+          zl = mfma32(kc[S & 1], *(const h8_t *)(lo + 1024 * S), zl);
+          zl = mfma32(*(const h8_t *)(kb + klo + 32 * S), q.hi[S], zl);
+        }
+        if constexpr (S < 6) kc[S & 1] = *(const h8_t *)(kb + 32 * (S + 2));
+        put.template step<S>();
+        if constexpr (S == 4) pack_weights<BF16>(o.p, P);
+        if constexpr (S == 5) fetch4(place, un + 2 + SETS, in);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      score(std::integral_constant<int, 0>{});
+      score(std::integral_constant<int, 1>{});
+      score(std::integral_constant<int, 2>{});
+      score(std::integral_constant<int, 3>{});
+      score(std::integral_constant<int, 4>{});
+      score(std::integral_constant<int, 5>{});
+      score(std::integral_constant<int, 6>{});
+      score(std::integral_constant<int, 7>{});
+      st.l += o.ps;
+      const float lw = fmaxf(lv + st.f, -60.0f), iw = exp2_fast(-lw), B = lw - st.mu;
+      const auto at = [&](const unsigned char *p, int x, int j) {
+        const s4_t a = transposed(p + 16 * x * VP + 64 * j), b = transposed(p + (16 * x + 8) * VP + 64 * j);
+        return __builtin_bit_cast(h8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      h8_t vc[2] = {at(vb, 0, 0), at(vb, 0, 1)};
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (P2) z += zl;
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const int x = k >> 2, j = k & 3;
+        acc[j] = mfma32(vc[k & 1], P.hi[x], acc[j]);
+        if constexpr (V2) {
+          acc[j] = mfma32(vc[k & 1], P.lo[x], acc[j]);
+          acc[j] = mfma32(at(vb + vlo, x, j), P.hi[x], acc[j]);
+        }
+        if (k < 6) vc[k & 1] = at(vb, (k + 2) >> 2, (k + 2) & 3);
+#pragma unroll
+        for (int r = 2 * k; r < 2 * k + 2; r++) {
+          const float s = __builtin_fmaf(z[r], A, B);
+          o.p[r] = exp2_fast(decltype(masked)::value && 8 * (r >> 2) + (r & 3) >= vis ? -INFINITY : s);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      float sum[1];
+      sum_weights<1>(o.p, sum);
+      o.ps = sum[0] * iw;
+      // some weight is too large for its scale, or infinite: a row that has seen nothing yet
+      const bool up = fmaxf(sum[0], o.ps * 128.0f) > 32768.0f;
       if (__any(up)) raise4<P2>(keys_at(un + 1), klo, lo, A, lv, q, vis, st, acc, o);
       if constexpr (SUMS) store_sum(un + 1);
     };
     // units that every row of the wave sees whole, then the others
     const int ua = min(u1 - 1, max(all / UNIT - 1, u0));
-    for (int un = u0; un < ua; un++) turn(un, std::false_type{});
-    for (int un = max(ua, u0); un + 1 < u1; un++) turn(un, std::true_type{});
+    int un = u0;
+    for (; un + SETS <= ua; un += SETS) {
+      turn(un, std::false_type{}, nx[0]);
+      if constexpr (SETS == 2) turn(un + 1, std::false_type{}, nx[1]);
+    }
+    for (; un + 1 < u1; un += SETS) {
+      turn(un, std::true_type{}, nx[0]);
+      if constexpr (SETS == 2)
+        if (un + 2 < u1) turn(un + 1, std::true_type{}, nx[1]);
+    }
     st.l += o.ps;
     pack_weights<BF16>(o.p, P);
     values4<V2>(values_at(u1 - 1), vlo, P, acc);
@@ -549,9 +638,26 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
   store_rows<BF16, NT>(a, b, h, r0, nr, us);
 }
 
+int ranges4_bytes(bool bf16, bool two) { return (two ? 1024 : 512) + (bf16 ? 512 : 1024); }
+int units4_bytes() { return (int)sizeof(Unit4); }
+
+hipError_t ranges4_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
+  const int64_t blocks = (a.tokens + UNIT - 1) / UNIT, all = (int64_t)a.batch * a.heads * blocks;
+  if (all == 0) return hipSuccess;
+  const dim3 grid((unsigned)((all + NTH / 64 - 1) / (NTH / 64))), block(NTH);
+  if (!bf16) hipLaunchKernelGGL((k_ranges4<true, true>), grid, block, 0, s, a, (int)blocks);
+  else if (a.two) hipLaunchKernelGGL((k_ranges4<true, false>), grid, block, 0, s, a, (int)blocks);
+  else hipLaunchKernelGGL((k_ranges4<false, false>), grid, block, 0, s, a, (int)blocks);
+  return hipGetLastError();
+}
+
 hipError_t tile4_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
-  const bool p2 = !bf16 || a.lse || a.mass, sums = a.bsum != nullptr;
-  const int nw = p2 ? 8 : 4;
+  const bool p2 = a.two, sums = a.bsum != nullptr;
+  // Eight waves widen a unit for twice the rows, where that still gives every compute unit a workgroup:
+  // 2048 queries over 8192 tokens (256 workgroups) 309 us, by four 316; a prompt of 4000 196 and 209, of
+  // 1000 (128 workgroups) 51 and 42.  Two parts take most of a compute unit's LDS either way.
+  const int64_t wide = (int64_t)a.batch * a.heads * ((a.rows + 255) / 256) * a.splits;
+  const int nw = p2 || wide >= 256 ? 8 : 4;
   const int64_t groups = (a.rows + nw * WROWS - 1) / (nw * WROWS);
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * groups * a.splits)), block(64 * nw);
 #define CG_T(BF, P2, SUMS, NW)                                                             \

@@ -19,7 +19,10 @@ struct Plan {
   bool few;  // few row tiles: block sums come with the attention
   int64_t entries;
   size_t o_bytes, ml_bytes, dealt_bytes, bsum_bytes, lse2_bytes;
-  size_t total() const { return o_bytes + ml_bytes + dealt_bytes + bsum_bytes + lse2_bytes; }
+  // many rows over the 4-bit cache: sequences that are taken at once, ranges and powers of two of their blocks
+  int batch;
+  size_t ranges_bytes, units_bytes;
+  size_t total() const { return o_bytes + ml_bytes + dealt_bytes + bsum_bytes + lse2_bytes + ranges_bytes + units_bytes; }
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -88,9 +91,24 @@ int64_t tile_splits(int64_t work, int64_t rows, int64_t tokens) {
 // capacity pass it all the same.
 constexpr uint64_t kMaxSums = (uint64_t)1 << 30;
 
+// The ranges of many-row attention over the 4-bit cache take 1.5 or 2 KiB at most a KV head and 32 tokens of
+// shape->tokens; where that would pass 256 MiB the sequences are taken in turn.
+constexpr uint64_t kMaxRanges = (uint64_t)256 << 20;
+
 Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {
   Plan p{};
-  const int64_t fields = (int64_t)s->batch * s->heads, ratio = t->q_heads / s->heads;
+  const int64_t ratio = t->q_heads / s->heads;
+  const bool kivi = cgh::is_kivi4(c), many = t->n_queries * ratio > (int64_t)cga::FEW_TILES * cga::ROWS;
+  p.batch = s->batch;
+  if (kivi && many) {
+    const uint64_t blocks = (uint64_t)(s->tokens + cga::UNIT - 1) / cga::UNIT;
+    const uint64_t each = s->heads * blocks * (uint64_t)(cga::ranges4_bytes(s->dtype == CG_DTYPE_BF16, true) + cga::units4_bytes());
+    const uint64_t fit = each ? kMaxRanges / each : s->batch;
+    if (fit < (uint64_t)p.batch) p.batch = fit ? (int)fit : 1;
+    p.ranges_bytes = up256((size_t)p.batch * s->heads * blocks * cga::ranges4_bytes(s->dtype == CG_DTYPE_BF16, true));
+    p.units_bytes = up256((size_t)p.batch * s->heads * blocks * cga::units4_bytes());
+  }
+  const int64_t fields = (int64_t)p.batch * s->heads;
   const int64_t nblk = s->token_capacity / c->block_tokens;
   p.entries = c->block_tokens == 64 ? 2 * nblk : nblk;
   p.n = t->n_queries;
@@ -262,24 +280,50 @@ int cg_attend(const cg_shape *shape, const void *payload, uint64_t payload_cap, 
   a.bsum = (float2 *)take(p.bsum_bytes);
   a.lse2 = (float *)take(p.lse2_bytes);
 
+  a.ranges = (uint8_t *)take(p.ranges_bytes);
+  a.units = take(p.units_bytes);
+
   const bool bf16 = shape->dtype == CG_DTYPE_BF16;
+  a.two = !bf16 || lse || mass;
   hipStream_t st = (hipStream_t)stream;
-  for (int32_t first = 0; first < attn->n_queries; first += p.n) {
-    a.first = first;
-    a.n = attn->n_queries - first < p.n ? attn->n_queries - first : p.n;
-    a.rows = a.n * a.ratio;
-    a.tiles = (a.rows + cga::ROWS - 1) / cga::ROWS;
-    a.q = (const char *)q + (int64_t)first * ts * esz;
-    a.out = (char *)out + (int64_t)first * token * esz;
-    a.lse = lse ? lse + (int64_t)first * attn->q_heads : nullptr;
-    hipError_t e = kivi ? (p.few ? cga::rows4_launch(a, bf16, st) : cga::tile4_launch(a, bf16, st)) : p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
-    if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
-    if (p.merge && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
-      return cgh::hip_error(e, "cg_attend merge launch");
-    if (mass && shape->tokens > 0) {
-      // the merge of few rows has finished the weights
-      e = !p.few ? cga::mass_rows_launch(a, st) : p.merge ? hipSuccess : cga::mass_finish_launch(a, st);
-      if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
+  const cga::AttendArgs all = a;
+  for (int32_t b0 = 0; b0 < shape->batch; b0 += p.batch) {
+    if (b0) {  // the next sequences of all that goes by them
+      a = all;
+      const int64_t f = (int64_t)b0 * shape->heads;
+      a.kpay += f * pf;
+      a.vpay += f * pf;
+      a.kmeta = (const float2 *)((const char *)a.kmeta + f * mf);
+      a.vmeta = (const float2 *)((const char *)a.vmeta + f * mf);
+      if (a.lengths) a.lengths += b0;
+      if (a.starts) a.starts += b0;
+      if (a.mass) a.mass += f * a.nblk;
+    }
+    a.batch = shape->batch - b0 < p.batch ? shape->batch - b0 : p.batch;
+    if (p.ranges_bytes) {
+      a.q = q;
+      a.n = attn->n_queries;
+      a.first = 0;
+      const hipError_t e = cga::ranges4_launch(a, bf16, st);
+      if (e != hipSuccess) return cgh::hip_error(e, "cg_attend ranges launch");
+    }
+    for (int32_t first = 0; first < attn->n_queries; first += p.n) {
+      a.first = first;
+      a.n = attn->n_queries - first < p.n ? attn->n_queries - first : p.n;
+      a.rows = a.n * a.ratio;
+      a.tiles = (a.rows + cga::ROWS - 1) / cga::ROWS;
+      a.q = (const char *)q + ((int64_t)b0 * bs + (int64_t)first * ts) * esz;
+      a.out = (char *)out + ((int64_t)b0 * attn->n_queries + first) * token * esz;
+      a.lse = lse ? lse + ((int64_t)b0 * attn->n_queries + first) * attn->q_heads : nullptr;
+      hipError_t e = kivi ? (p.few ? cga::rows4_launch(a, bf16, st) : cga::tile4_launch(a, bf16, st)) : p.few ? cga::rows_launch(a, bf16, st) : cga::tile_launch(a, bf16, st);
+      if (e != hipSuccess) return cgh::hip_error(e, "cg_attend launch");
+      if (p.merge && (e = cga::merge_launch(a, bf16, st)) != hipSuccess)
+        return cgh::hip_error(e, "cg_attend merge launch");
+      if (mass && shape->tokens > 0) {
+        // the merge of few rows has finished the weights
+        e = !p.few ? cga::mass_rows_launch(a, st) : p.merge ? hipSuccess : cga::mass_finish_launch(a, st);
+        if (e != hipSuccess) return cgh::hip_error(e, "cg_attend mass launch");
+      }
     }
   }
   return CG_OK;
