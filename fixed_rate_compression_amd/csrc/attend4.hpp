@@ -1,0 +1,26 @@
+// Device pieces of attention over the 4-bit cache.  Not part of the public ABI.
+#pragma once
+
+#include "attend.hpp"
+
+namespace cga {
+
+constexpr int HALF_D = D / 2;  // bytes of a row of codes
+constexpr uint32_t INF = 0x7f800000u;
+
+// the largest bit pattern over a wave, of magnitudes
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+  const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(x[0], x[1]);
+  const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(y[0], y[1]);
+}
+__device__ __forceinline__ uint32_t range_bits(float2 m) {  // of the larger end of a range; a NaN is the largest
+  const uint32_t a = __float_as_uint(m.x) & 0x7fffffffu, b = __float_as_uint(__builtin_fmaf(15.0f, m.y, m.x)) & 0x7fffffffu;
+  return max(a, b);
+}
+}  // namespace cga

@@ -7,8 +7,8 @@
 // 128 products a row and unit, each lane those of two channels for all rows, which reach the
 // matrix cores' operand layout through the wave's own LDS; the codes are multiplied as they
 // are.  The values are widened to v' itself, since their ranges differ along both
-// axes of the second product: one packed multiply-add turns two centred codes
-// into fp16 values of a power-of-two scale that the unit's weights carry.
+// axes of the second product: one packed multiply-add turns two codes into
+// fp16 values of a power-of-two scale that the unit's weights carry.
 //
 // Precision of a score: a unit's power of two 2^E bounds |mk| and |mk + 15 sk|; the products
 // q'_c sk_c stand in two fp16 parts, a multiple of 2^3 and what is left, where q's
@@ -17,10 +17,13 @@
 // a rounding (128 multiples of 2^3 below 2^14, times 15).  For fp32 storage, log-sums and weights
 // there is a part between the two, a multiple of 2^-8, added exactly too (2^-34; in two parts
 // fp32 outputs of 4000 tokens were off by 1.4e-6, log-sums of 28 tokens by 1.35e-6, by fp32
-// products 0.4e-6 and 0.08e-6).  Values: the step, the centre and their sum rounded to
-// fp16 each (2^-12 of themselves, 2^-34 of the largest of the unit's 32 tokens), for fp32
-// storage in two parts.
+// products 0.4e-6 and 0.08e-6).  Values: the step and the centre of a range and the value
+// rounded to fp16 each, around the code 8 (2^-12 of themselves, 2^-34 of the largest of the unit's
+// 32 tokens), for fp32 storage in two parts.  With the code as it stands and the minimum, a third
+// of this work less, bf16 outputs were off by 1.95e-3 of themselves, by 1.72e-3 around the
+// centre, and 1.66e-3 is their own rounding; the time was the same (87 us for 262144 tokens).
 #include "attend.hpp"
+#include "attend4.hpp"
 #include "attend_few.hpp"
 
 namespace cga {
@@ -33,7 +36,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-constexpr int HALF_D = D / 2;  // bytes of a row of codes
 constexpr float kKeyUnit = 1.5f * 67108864.0f;  // x + u - u rounds to multiples of 2^3
 
 // A unit as it is loaded.  Keys: token 16 t + lane % 16, channels 32 (lane / 16) .. + 31, and
@@ -75,11 +77,8 @@ __device__ __forceinline__ void load_values4(const uint8_t *vf, const float2 *vm
   u.m[1] = m[4];
 }
 
-// smallest E with |x| < 2^E, of a wave-wide maximum
-__device__ __forceinline__ int top_exponent(float mx) {
-  return __builtin_amdgcn_readfirstlane((int)(__float_as_uint(wave_max(mx)) >> 23) - 126);
-}
-__device__ __forceinline__ float range_top(float2 m) { return fmaxf(fabsf(m.x), fabsf(__builtin_fmaf(15.0f, m.y, m.x))); }
+// smallest E with |x| < 2^E, of the largest magnitude's bits
+__device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 126; }
 
 // eight codes of a dword as halves: pairs (0, 4), (1, 5), (2, 6), (3, 7); the odd ones 16 times
 // themselves, which their queries make up for
@@ -99,7 +98,7 @@ __device__ __forceinline__ void centred4(uint32_t w0, uint32_t w1, uint32_t &eve
 }
 
 struct RowState4 {
-  float m, mu, mo, f;   // as in attend_rows.hip (f: log2); the values' scale is a power of two a unit
+  float m, mu, mo, f;   // maximum, the one used (-inf while none), value scale, log2 of the weights' factor
   float l;
   uint32_t poison;      // groups of channels of which the row has seen a value that is not a number
 };
@@ -231,8 +230,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
   all = __builtin_amdgcn_readfirstlane(all);  // every row sees the tokens before it
 
   RowState4 st;
-  st.m = st.mo = -INFINITY;
-  st.mu = 0.0f;
+  st.m = st.mu = st.mo = -INFINITY;
   st.f = 0.0f;
   st.l = 0.0f;
   st.poison = 0u;
@@ -244,7 +242,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
     const int t0 = un * UNIT;
     const bool more = un + NW < u1;
     // key steps into the queries
-    const int ek = top_exponent(fmaxf(range_top(uk.m[0]), range_top(uk.m[1])));
+    const int ek = exponent_of(__builtin_amdgcn_readfirstlane(wave_umax(max(range_bits(uk.m[0]), range_bits(uk.m[1])))));
     {
       const float s0 = __builtin_ldexpf(uk.m[0].y, 2 - ek), s1 = __builtin_ldexpf(uk.m[1].y, 2 - ek);
       const float m0 = __builtin_ldexpf(uk.m[0].x, msh - ek), m1 = __builtin_ldexpf(uk.m[1].x, msh - ek);
@@ -281,25 +279,26 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
     }
     // value ranges: those behind the sequence's end are whatever they are
     float2 vr[2] = {uv.m[0], uv.m[1]};
-    if (t0 + 2 * row >= sq.len) vr[0] = make_float2(0.f, 0.f);
-    if (t0 + 2 * row + 1 >= sq.len) vr[1] = make_float2(0.f, 0.f);
-    {
-      // a range that is not a number: its tokens count as zeros, and the rows that see them are marked
-      const float x0 = range_top(vr[0]), x1 = range_top(vr[1]);
-      const bool bad0 = !(x0 + fabsf(vr[0].x) < INFINITY && vr[0].y < INFINITY),
-                 bad1 = !(x1 + fabsf(vr[1].x) < INFINITY && vr[1].y < INFINITY);
-      if (__any(bad0 || bad1)) {
-        const uint64_t e = __ballot(bad0), o = __ballot(bad1);  // tokens 2 i and 2 i + 1 of group g: bit 16 g + i
-        const int vis = min(max(lim - t0, 0), UNIT);
-        const uint32_t se = (1u << ((vis + 1) >> 1)) - 1u, so = (1u << (vis >> 1)) - 1u;
-#pragma unroll
-        for (int g = 0; g < 4; g++)
-          if (((uint32_t)(e >> 16 * g) & se) | ((uint32_t)(o >> 16 * g) & so)) st.poison |= 1u << g;
-        if (bad0) vr[0] = make_float2(0.f, 0.f);
-        if (bad1) vr[1] = make_float2(0.f, 0.f);
-      }
+    if (t0 + UNIT > sq.len) {
+      if (t0 + 2 * row >= sq.len) vr[0] = make_float2(0.f, 0.f);
+      if (t0 + 2 * row + 1 >= sq.len) vr[1] = make_float2(0.f, 0.f);
     }
-    const int ev = max(top_exponent(fmaxf(range_top(vr[0]), range_top(vr[1]))), -126);
+    const uint32_t x0 = range_bits(vr[0]), x1 = range_bits(vr[1]);
+    uint32_t tv = __builtin_amdgcn_readfirstlane(wave_umax(max(x0, x1)));
+    if (tv >= INF) {
+      // a range that is not a number: its tokens count as zeros, and the rows that see them are marked
+      const bool bad0 = x0 >= INF, bad1 = x1 >= INF;
+      const uint64_t e = __ballot(bad0), o = __ballot(bad1);  // tokens 2 i and 2 i + 1 of group g: bit 16 g + i
+      const int vis = min(max(lim - t0, 0), UNIT);
+      const uint32_t se = (1u << ((vis + 1) >> 1)) - 1u, so = (1u << (vis >> 1)) - 1u;
+#pragma unroll
+      for (int g = 0; g < 4; g++)
+        if (((uint32_t)(e >> 16 * g) & se) | ((uint32_t)(o >> 16 * g) & so)) st.poison |= 1u << g;
+      if (bad0) vr[0] = make_float2(0.f, 0.f);
+      if (bad1) vr[1] = make_float2(0.f, 0.f);
+      tv = __builtin_amdgcn_readfirstlane(wave_umax(max(bad0 ? 0u : x0, bad1 ? 0u : x1)));
+    }
+    const int ev = exponent_of(tv);
     {
       // values below 2^9; the steps times the 2^9 that centred codes lack (34953 at most)
       const float s0 = __builtin_ldexpf(vr[0].y, 18 - ev), s1 = __builtin_ldexpf(vr[1].y, 18 - ev);
@@ -314,12 +313,12 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
       }
     }
     wave_sync();
-    // scores
-    float s[2][4];
+    // scores: fma(z, A, Bm)
+    f4_t z[2];
     {
-      f4_t z[2], zl[2], zm[2];
+      f4_t zl[2];
 #pragma unroll
-      for (int t = 0; t < 2; t++) z[t] = zl[t] = zm[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < 2; t++) z[t] = zl[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < 4; x++) {
         const h8_t hi = *(const h8_t *)(kget + x * STEP), lo = *(const h8_t *)(kget + (4 + x) * STEP);
@@ -327,65 +326,70 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
         for (int t = 0; t < 2; t++) {
           const h8_t c = nibbles8(uk.k[t][x]);
           z[t] = mfma(c, hi, z[t]);
-          zl[t] = mfma(c, lo, zl[t]);
-          if constexpr (P3) zm[t] = mfma(c, *(const h8_t *)(kget + (8 + x) * STEP), zm[t]);
+          if constexpr (P3) {
+            zl[t] = mfma(c, *(const h8_t *)(kget + (8 + x) * STEP), zl[t]);
+            zl[t] = mfma(c, lo, zl[t]);
+          } else {
+            z[t] = mfma(c, lo, z[t]);
+          }
         }
       }
-      const float A = __builtin_ldexpf(ca, ek + 22), Bm = __builtin_ldexpf(ca, ek) * msum[row & (NR - 1)];
+      if constexpr (P3)
 #pragma unroll
-      for (int t = 0; t < 2; t++)
-#pragma unroll
-        for (int r = 0; r < 4; r++)
-          s[t][r] = __builtin_fmaf(z[t][r] + (P3 ? zm[t][r] + zl[t][r] : zl[t][r]), A, Bm);
+        for (int t = 0; t < 2; t++) z[t] += zl[t];
     }
+    const float A = __builtin_ldexpf(ca, ek + 22), Bm = __builtin_ldexpf(ca, ek) * msum[row & (NR - 1)];
     if (more) load_keys4(kf, km, t0 + NW * UNIT, uk);
-    if (t0 + UNIT > all) {
+    const bool masked = t0 + UNIT > all;
+    const auto unseen = [&](int t, int r) { return masked && t0 + 16 * t + 4 * grp + r >= lim; };
+    // weights times their factor, with the maximum as it stands; a lane's sum tells whether one of them has
+    // outgrown its scale, or is infinite: a row that has seen nothing yet
+    float p[2][4], lw, sum, bs;
+    const auto weigh = [&](float B) {
 #pragma unroll
       for (int t = 0; t < 2; t++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) s[t][r] = t0 + 16 * t + 4 * grp + r < lim ? s[t][r] : -INFINITY;
-    }
+        for (int r = 0; r < 4; r++) p[t][r] = exp2_fast(unseen(t, r) ? -INFINITY : __builtin_fmaf(z[t][r], A, B));
+      sum = ((p[0][0] + p[0][1]) + (p[0][2] + p[0][3])) + ((p[1][0] + p[1][1]) + (p[1][2] + p[1][3]));
+      bs = sum * exp2_fast(-lw);
+    };
     const float lv = (float)ev;
-    const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                            fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-    if (__any(top > st.m + 8.0f || top + lv > st.mo + 6.0f)) {
+    lw = fmaxf(lv + st.f, -60.0f);  // below 2^-60 the weights vanish either way
+    weigh(Bm + (lw - st.mu));
+    if (__any(fmaxf(sum, bs * 256.0f) > 32768.0f)) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) top = fmaxf(top, unseen(t, r) ? -INFINITY : __builtin_fmaf(z[t][r], A, Bm));
       const float tm = row_max(top), mn = fmaxf(st.m, tm);
       float on = fmaxf(st.mo, tm + lv);
       const bool some = mn > -INFINITY;
       if (some) on = fmaxf(on, mn - 126.0f);  // keeps 2^(mo - m) a normal number beside weights that vanish
-      const float mu = some ? mn : 0.0f;
       const float al = st.m > -INFINITY ? exp2_fast(st.m - mn) : 0.0f;
       const float ao = st.mo > -INFINITY ? exp2_fast(st.mo - on) : 0.0f;
       st.l *= al;
 #pragma unroll
       for (int j = 0; j < 8; j++) acc[j] *= ao;
-      st.m = mn;
+      st.m = st.mu = mn;
       st.mo = on;
-      st.mu = mu;
       st.f = some ? mn - on + 9.0f : 0.0f;
+      lw = fmaxf(lv + st.f, -60.0f);
+      weigh(Bm + (lw - (some ? mn : 0.0f)));
     }
+    st.l += bs;
     uint32_t ph[2][2], pl[2][2];
-    float bs = 0.0f;
-    // the values' factor goes into the exponent; below 2^-60 the weights vanish either way
-    const float lw = fmaxf(lv + st.f, -60.0f), up = lw - st.mu;
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-      float p[4];
-#pragma unroll
-      for (int r = 0; r < 4; r++) p[r] = exp2_fast(s[t][r] + up);
-      bs += (p[0] + p[1]) + (p[2] + p[3]);
+    for (int t = 0; t < 2; t++)
 #pragma unroll
       for (int k = 0; k < 2; k++) {
-        const float x = p[2 * k], y = p[2 * k + 1];
+        const float x = p[t][2 * k], y = p[t][2 * k + 1];
         ph[t][k] = pack_f16x2(x, y);
         if constexpr (!BF16) {
           const f2_t hh = unpack_f16x2(ph[t][k]);
           pl[t][k] = pack_f16x2(x - hh.x, y - hh.y);
         }
       }
-    }
-    bs *= exp2_fast(-lw);
-    st.l += bs;
     const h8_t P = as_h8(ph[0][0], ph[0][1], ph[1][0], ph[1][1]);
     if constexpr (BF16) {
       h2_t vs[2][2], vc[2][2];
@@ -454,7 +458,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
 
   const float *gv = a.gv + (int64_t)h * D * a.g;
   if (splits == 1 && front) load_gauge<true>(gv, a.g, 0, gw);
-  // true sums: acc 2^-18 2^(mo - m); a lane's channels are of group grp
+  // true sums: acc 2^(mo - m) less the 2^9 of the weights and of the values; a lane's channels are of group grp
 #pragma unroll
   for (int j = 0; j < 8; j++) acc[j] *= 0x1p-18f;
   const float ks = st.m > -INFINITY ? exp2_fast(st.mo - st.m) : 0.0f;

@@ -13,13 +13,13 @@
 #include <type_traits>
 
 #include "attend.hpp"
+#include "attend4.hpp"
 #include "attend_tile.hpp"
 
 namespace cga {
 
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 
-constexpr int HALF_D = D / 2;  // bytes of a row of codes
 constexpr int kTop = 9;        // widened keys and values are below 2^9
 
 // LDS of a workgroup's token loop; two parts of the keys (P2), of the values (V2)
@@ -45,21 +45,6 @@ struct Ranges4 {
   static constexpr int K = P2 ? 1024 : 512, V = V2 ? 1024 : 512, BYTES = K + V;
 };
 
-// the largest bit pattern over a wave, of magnitudes
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
-  const auto x = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = max(x[0], x[1]);
-  const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return max(y[0], y[1]);
-}
-__device__ __forceinline__ uint32_t range_bits(float2 m) {  // of the larger end of a range; a NaN is the largest
-  const uint32_t a = __float_as_uint(m.x) & 0x7fffffffu, b = __float_as_uint(__builtin_fmaf(15.0f, m.y, m.x)) & 0x7fffffffu;
-  return max(a, b);
-}
 // A power of two above x: 2^9, which asks for no scaling, where x is in [2^-3, 2^8), so that small values keep
 // 2^-22 of the largest; else the smallest
 __device__ __forceinline__ int exponent_of(uint32_t bits) {
@@ -83,7 +68,6 @@ __global__ __launch_bounds__(NTH) void k_ranges4(const AttendArgs a, int blocks)
   float2 k[2] = {km[c0], km[c0 + 4]}, v[2] = {vm[lane], vm[lane + 64]};  // values: token, group of entry 4 token + group
   // ranges behind the sequence's end are whatever they are; one that gives a NaN or an infinity for some
   // code (15 steps alone may) counts as zeros and is marked
-  constexpr uint32_t INF = 0x7f800000u;
   uint64_t bad[2];
 #pragma unroll
   for (int x = 0; x < 2; x++) {

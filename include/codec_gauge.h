@@ -473,7 +473,7 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  * mass; weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
  * 4 bits: queries times key steps in two parts (2^-23 of the largest channel times the
  * block's largest key), in three (2^-34) for fp32 storage and with lse or mass; weights
- * and the values themselves for fp32 storage in two parts, for bf16 storage in one (2^-11, and 2^-34 of
+ * and the values themselves for fp32 storage in two parts, for bf16 storage in one (2^-11, and 2^-31 of
  * a block's largest value).
  * The order of sums depends on the shape and the lengths only (deterministic).
  * The workspace belongs to one call at a time.  Asynchronous on stream.
