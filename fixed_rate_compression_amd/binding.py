@@ -538,11 +538,13 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
     ptrs, (bs, rs) = _kv_rows(shape, n_new, (("k_new", k_new), ("v_new", v_new)))
     _gauge_sized(gauge, shape)
     dev = _here(k_new, v_new, tail, payload, meta, lengths, starts, gauge._keep)
-    _check("cg_append", lib().cg_append(
-        ctypes.byref(shape), ctypes.byref(gauge), ctypes.byref(codec), layer, n_new, *ptrs, bs, rs,
+    rc = lib().cg_append(
+        shape, gauge, codec, layer, n_new, *ptrs, bs, rs,
         _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
         _sized("tail", tail, st, shape.layers * 2 * shape.batch * row * codec.block_tokens),
-        _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream_on(stream, dev)))
+        _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream_on(stream, dev))
+    if rc != CG_OK:
+        _check("cg_append", rc)
 
 
 def cg_read(shape, payload, meta, gauge, codec, layer, k_out, v_out, lengths=None, starts=None, stream=None):
@@ -578,42 +580,53 @@ def make_rotary(freq, sections=None, interleaved=False, dealt=False, q_weight=No
     return r
 
 
-def _rows(name, t, shape, heads=None):
+def _rows(name, t, st, batch, n, heads, d):
     """[batch, n, heads, head_dim] of the storage format -> CgRows."""
-    st = _storage(shape)
-    if t.dtype != _dtype(st):
+    if t.dtype != st:
         raise ValueError(f"{name} must be {st}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != shape.batch or t.shape[3] != shape.head_dim or (heads is not None and t.shape[2] != heads):
-        raise ValueError(f"{name} must be [batch, n, {heads or 'q_heads'}, head_dim], got {tuple(t.shape)}")
-    b, n, h, d = t.shape
+    if t.shape != (batch, n, heads, d):
+        raise ValueError(f"{name} must be [{batch}, {n}, {heads}, {d}], got {tuple(t.shape)}")
     sb, sr, sh, sd = t.stride()
-    if t.numel() and ((b > 1 and sb == 0) or (n > 1 and sr == 0) or (h > 1 and sh != d) or sd != 1):
-        raise ValueError(f"{name} of strides {t.stride()}: contiguous heads are needed, and rows of their own")
-    return CgRows(t.data_ptr(), sb if b > 1 else 0, sr if n > 1 else 0)
+    if batch == 1:
+        sb = 0
+    elif sb == 0:
+        raise ValueError(f"{name}: rows of an expanded tensor")
+    if n == 1:
+        sr = 0
+    elif sr == 0:
+        raise ValueError(f"{name}: rows of an expanded tensor")
+    if (sh != d and heads > 1) or sd != 1:
+        raise ValueError(f"{name} of strides {t.stride()}: contiguous heads are needed")
+    return CgRows(t.data_ptr(), sb, sr)
 
 
 def cg_rotate(shape, rotary, q, k, q_out, k_out, lengths=None, starts=None, positions=None, stream=None):
     """Norm and rotation of q [batch, n, q_heads, 128] and k [batch, n, heads, 128] into q_out and k_out, which
     may be q and k themselves; either pair may be None.  positions: device int32 [axes, batch, n] or None."""
-    pairs = [(q, q_out), (k, k_out)]
-    if any((x is None) != (y is None) for x, y in pairs) or (q is None and k is None):
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
         raise ValueError("queries or keys, each with its output, are needed")
-    n, q_heads = (k if q is None else q).shape[1], 0 if q is None else q.shape[2]
-    rows = []
-    for name, x, heads in (("q", q, None), ("k", k, shape.heads), ("q_out", q_out, q_heads), ("k_out", k_out, shape.heads)):
-        if x is not None and x.dim() == 4 and x.shape[1] != n:
-            raise ValueError(f"{name} has {x.shape[1]} rows a sequence, not {n}")
-        rows.append(None if x is None else _rows(name, x, shape, heads))
-    for name, w in zip(("freq", "q_weight", "k_weight"), rotary._keep):
-        if w is not None and name != "freq" and w.numel() != shape.head_dim:
-            raise ValueError(f"{name}: {shape.head_dim} values are needed, got {w.numel()}")
-    if positions is not None and not isinstance(positions, int) and positions.shape != (rotary.axes, shape.batch, n):
+    lead = k if q is None else q
+    if lead.dim() != 4:
+        raise ValueError(f"rows must be [batch, n, heads, head_dim], got {tuple(lead.shape)}")
+    batch, heads, d, st = shape.batch, shape.heads, shape.head_dim, _dtype(_storage(shape))
+    n, q_heads = lead.shape[1], 0 if q is None else q.shape[2]
+    qi = ki = rq = rk = None
+    if q is not None:
+        qi = _rows("q", q, st, batch, n, q_heads, d)
+        rq = qi if q_out is q else _rows("q_out", q_out, st, batch, n, q_heads, d)
+    if k is not None:
+        ki = _rows("k", k, st, batch, n, heads, d)
+        rk = ki if k_out is k else _rows("k_out", k_out, st, batch, n, heads, d)
+    freq, wq, wk = rotary._keep
+    if (wq is not None and wq.numel() != d) or (wk is not None and wk.numel() != d):
+        raise ValueError(f"norm weights: {d} values are needed")
+    if positions is not None and not isinstance(positions, int) and positions.shape != (rotary.axes, batch, n):
         raise ValueError(f"positions must be [axes, batch, n], got {tuple(positions.shape)}")
-    dev = _here(q, k, q_out, k_out, lengths, starts, positions, *rotary._keep)
+    dev = _here(q, k, q_out, k_out, lengths, starts, positions, freq, wq, wk)
     rc = lib().cg_rotate(
-        shape, rotary, q_heads, n, _sized("positions", positions, "int32", rotary.axes * shape.batch * n),
-        _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
-        *rows, _stream_on(stream, dev))
+        shape, rotary, q_heads, n, _sized("positions", positions, "int32", rotary.axes * batch * n),
+        _sized("lengths", lengths, "int32", batch), _sized("starts", starts, "int32", batch), qi, ki, rq, rk,
+        _stream_on(stream, dev))
     if rc != CG_OK:
         _check("cg_rotate", rc)
 
@@ -625,14 +638,16 @@ def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape,
     nblk, nout = (s.token_capacity // codec.block_tokens if codec.block_tokens > 0 else 0
                   for s in (shape, out_shape))
     dev = _here(mass, payload, meta, payload_out, meta_out, mass_out, kept, lengths_out, lengths)
-    _check("cg_evict", lib().cg_evict(
-        ctypes.byref(shape), ctypes.byref(codec), budget, sink, recent,
+    rc = lib().cg_evict(
+        shape, codec, budget, sink, recent,
         _sized("mass", mass, "float32", heads * nblk), _ptr(payload), _nbytes(payload), _ptr(meta),
-        _nbytes(meta), _sized("lengths", lengths, "int32", shape.batch), ctypes.byref(out_shape),
+        _nbytes(meta), _sized("lengths", lengths, "int32", shape.batch), out_shape,
         _ptr(payload_out), _nbytes(payload_out), _ptr(meta_out), _nbytes(meta_out),
         _sized("mass_out", mass_out, "float32", heads * nout),
         _sized("kept", kept, "int32", heads * max(budget, 0)),
-        _sized("lengths_out", lengths_out, "int32", shape.batch), _stream_on(stream, dev)))
+        _sized("lengths_out", lengths_out, "int32", shape.batch), _stream_on(stream, dev))
+    if rc != CG_OK:
+        _check("cg_evict", rc)
 
 
 def cg_last_error() -> str:

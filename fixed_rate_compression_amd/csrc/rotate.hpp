@@ -23,7 +23,6 @@ struct RotateArgs {
   int32_t batch, n, dim, axes, interleaved, dealt;
   int32_t sections[4];
   float eps, magnitude;
-  int32_t each, chunks;  // heads of a row to a workgroup, workgroups to a row
 };
 hipError_t rotate_launch(const RotateArgs &a, bool bf16, hipStream_t s);
 

@@ -86,7 +86,7 @@ extern "C" int cg_rotate(const cg_shape *shape, const cg_rotary *rotary, int32_t
   if (q && (q_heads <= 0 || q_heads > (1 << 20))) return error(CG_E_SHAPE, "q_heads must be 1 to 2^20");
   if (n == 0) return CG_OK;
   const int64_t heads = (q ? q_heads : 0) + (k ? (int64_t)shape->heads : 0);
-  if (heads > (1 << 21) || (int64_t)shape->batch * n * ((heads + 15) / 16) >= (int64_t)1 << 31)
+  if (heads > (1 << 21) || (int64_t)shape->batch * n * heads >= (int64_t)1 << 31)
     return error(CG_E_SHAPE, "too many rows for one launch");
 
   cgr::RotateArgs a{};
