@@ -7,6 +7,19 @@
 
 namespace cgs {
 
+// x / d for x below 2^31: two scalar instructions, where a division takes some thirty
+struct Div {
+  uint32_t mul = 0, shift = 0;
+  Div() = default;
+  explicit Div(uint32_t d) {  // 2^(shift - 1) < d <= 2^shift
+    while (shift < 31 && (uint32_t)1 << shift < d) shift++;
+    mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+  }
+  __host__ __device__ uint32_t operator()(uint32_t x) const {
+    return ((uint32_t)(((uint64_t)x * mul) >> 32) + x) >> shift;
+  }
+};
+
 struct AppendArgs {
   uint8_t *payload;        // the layer's fields, (kind, b, h) at ((kind batch + b) heads + h) tcap 128 (4 bits: 64)
   float *meta;             // the layer's (minimum, step) pairs, nblk a field (4 bits: 4 tcap)
@@ -16,9 +29,11 @@ struct AppendArgs {
   const int32_t *lengths, *starts;
   const float *gauges;     // the layer's [kind][heads][128 g]
   int64_t tcap, tokens, nblk;
-  int32_t batch, heads, n, block, bshift, tiles;  // tiles: 64-row strips of a sequence at most
+  int32_t batch, heads, n, block, bshift, tiles;  // tiles: 64-row (4 bits: 32-row) strips of a sequence at most
+  Div by_tiles, by_heads;
 };
-hipError_t append_launch(const AppendArgs &a, bool bf16, int g, bool kivi, hipStream_t s);
+hipError_t append_launch(const AppendArgs &a, bool bf16, int g, hipStream_t s);
+hipError_t append4_launch(const AppendArgs &a, bool bf16, int g, hipStream_t s);
 
 struct ReadArgs {
   const uint8_t *payload;  // as above

@@ -41,8 +41,10 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
     return error(CG_E_INVAL, "row strides must be multiples of 16 bytes and not negative");
   cgs::AppendArgs a{};
   const int64_t fields = (int64_t)2 * shape->batch * shape->heads, f0 = layer * fields;
-  // strips of 64 rows from the block of the first new row on
-  const int64_t tiles = ((int64_t)n_new + codec->block_tokens - 1 + 63) / 64;
+  // strips of rows from the block of the first new row on
+  const bool kivi = cgh::is_kivi4(codec);
+  const int strip = kivi ? 32 : 64;
+  const int64_t tiles = ((int64_t)n_new + codec->block_tokens - 1 + strip - 1) / strip;
   if (fields * tiles >= (int64_t)1 << 31) return error(CG_E_SHAPE, "too many rows for one launch");
   const uint64_t esz = shape->dtype == CG_DTYPE_BF16 ? 2 : 4;
   const uint64_t in = cgh::reach(shape->batch, bs, n_new, rs, row) * esz;
@@ -70,7 +72,11 @@ int cg_append(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *code
   a.block = codec->block_tokens;
   a.bshift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
   a.tiles = (int32_t)tiles;
-  hipError_t e = cgs::append_launch(a, shape->dtype == CG_DTYPE_BF16, gauge->group, cgh::is_kivi4(codec), (hipStream_t)stream);
+  a.by_tiles = cgs::Div((uint32_t)tiles);
+  a.by_heads = cgs::Div((uint32_t)a.heads);
+  const bool bf16 = shape->dtype == CG_DTYPE_BF16;
+  const hipError_t e = kivi ? cgs::append4_launch(a, bf16, gauge->group, (hipStream_t)stream)
+                            : cgs::append_launch(a, bf16, gauge->group, (hipStream_t)stream);
   return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_append launch");
 }
 

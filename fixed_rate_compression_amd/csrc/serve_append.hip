@@ -1,9 +1,6 @@
-// New K/V rows into the serving caches: gauge and quantization of the blocks they
-// fall in, every sequence at its own position.
+// New K/V rows into the 8-bit block-uniform cache: gauge and quantization of
+// the blocks they fall in, every sequence at its own position.
 //
-// 4-bit KIVI-style cache: a key's range is that of 32 tokens of its channel, a value's that of 32
-// channels of its token; the block that receives a row is encoded again as in the 8-bit
-// cache:
 // A block's range is that of all its rows, so the block that receives a row
 // is encoded again from the raw rows (kept beside the cache, `tail`) and the
 // new ones.  Rows that are not there yet take no part in the range and their
@@ -22,10 +19,10 @@ namespace cgs {
 
 using namespace cgk;
 
-template <bool BF16, int G, bool KIVI>
+template <bool BF16, int G>
 __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   __shared__ __align__(16) float xs[TILE_T * PITCH];
-  __shared__ float2 red[KIVI ? 2 * D : 4];
+  __shared__ float red[8];
   constexpr size_t ESZ = BF16 ? 2 : 4;
   const uint32_t q1 = blockIdx.x / (uint32_t)a.tiles, q2 = q1 / (uint32_t)a.heads;
   const int strip = (int)(blockIdx.x - q1 * a.tiles), h = (int)(q1 - q2 * a.heads);
@@ -81,52 +78,6 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   }
   const int t = threadIdx.x >> 2, j = threadIdx.x & 3, w = threadIdx.x >> 6;
   const bool active = t < nrows && tb + t < p1;
-  if constexpr (KIVI) {
-    float *mf = a.meta + 8 * f * a.tcap;
-    if (kind == 0) {  // a thread a channel of one of the strip's two blocks
-      const int r0 = threadIdx.x & D ? 32 : 0, c = threadIdx.x & (D - 1);
-      const int there = (int)min((int64_t)32, p1 - tb - r0);
-      if (there > 0) {
-        float mn = INFINITY, mx = -INFINITY;
-        for (int r = 0; r < there; r++) {
-          const float x = xs[(r0 + r) * PITCH + c];
-          mn = fminf(mn, x);
-          mx = fmaxf(mx, x);
-        }
-        const cgq::Range r = cgq::make_range(mn, mx, 15);
-        red[threadIdx.x] = make_float2(r.mn, r.zero ? 0.0f : r.inv);
-        float *m = mf + 2 * (((tb + r0) >> 5) * D + c);
-        m[0] = r.mn;
-        m[1] = r.scale;
-      }
-      __syncthreads();
-    }
-    if (!active) return;
-    float v[32];
-    uint32_t q[32], wd[4];
-    cgq::read32(xs, t, j, v);
-    if (kind == 0) {
-#pragma unroll
-      for (int k = 0; k < 32; k++) {
-        const float2 m = red[(t >> 5) * D + 32 * j + k];
-        q[k] = cgq::quant1(v[k], cgq::Range{m.x, 0.0f, m.y, false}, 15);
-      }
-    } else {
-      float mn = v[0], mx = v[0];
-#pragma unroll
-      for (int k = 1; k < 32; k++) {
-        mn = fminf(mn, v[k]);
-        mx = fmaxf(mx, v[k]);
-      }
-      const cgq::Range r = cgq::make_range(mn, mx, 15);
-#pragma unroll
-      for (int k = 0; k < 32; k++) q[k] = cgq::quant1(v[k], r, 15);
-      *(float2 *)(mf + 2 * ((tb + t) * 4 + j)) = make_float2(r.mn, r.scale);
-    }
-    cgq::pack32<4>(q, wd);
-    cgq::store_words<4>(a.payload + (f * a.tcap + tb + t) * (D / 2) + 16 * j, wd);
-    return;
-  }
   float v[32];
   float mn = INFINITY, mx = -INFINITY;
   if (active) {
@@ -139,15 +90,18 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   }
   mn = cgq::wave_min(mn);
   mx = cgq::wave_max(mx);
-  if ((threadIdx.x & 63) == 0) red[w] = make_float2(mn, mx);
+  if ((threadIdx.x & 63) == 0) {
+    red[2 * w] = mn;
+    red[2 * w + 1] = mx;
+  }
   __syncthreads();
   if (!active) return;
   const int wpb = BT >> 4, w0 = (t & ~(BT - 1)) >> 4;
-  mn = red[w0].x;
-  mx = red[w0].y;
+  mn = red[2 * w0];
+  mx = red[2 * w0 + 1];
   for (int k = 1; k < wpb; k++) {
-    mn = fminf(mn, red[w0 + k].x);
-    mx = fmaxf(mx, red[w0 + k].y);
+    mn = fminf(mn, red[2 * (w0 + k)]);
+    mx = fmaxf(mx, red[2 * (w0 + k) + 1]);
   }
   const cgq::Range r = cgq::make_range(mn, mx, 255);
   uint32_t q[32], wd[8];
@@ -162,13 +116,12 @@ __global__ __launch_bounds__(NT) void k_append(const AppendArgs a) {
   }
 }
 
-hipError_t append_launch(const AppendArgs &a, bool bf16, int g, bool kivi, hipStream_t s) {
+hipError_t append_launch(const AppendArgs &a, bool bf16, int g, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)2 * a.batch * a.heads * a.tiles)), block(NT);
-#define CG_A(BF, GG)                                                                 \
-  if (bf16 == BF && g == GG) {                                                       \
-    if (kivi) hipLaunchKernelGGL((k_append<BF, GG, true>), grid, block, 0, s, a);    \
-    else hipLaunchKernelGGL((k_append<BF, GG, false>), grid, block, 0, s, a);        \
-    return hipGetLastError();                                                        \
+#define CG_A(BF, GG)                                               \
+  if (bf16 == BF && g == GG) {                                     \
+    hipLaunchKernelGGL((k_append<BF, GG>), grid, block, 0, s, a);  \
+    return hipGetLastError();                                      \
   }
   CG_A(true, 0) CG_A(true, 8) CG_A(true, 16) CG_A(true, 32) CG_A(true, 128)
   CG_A(false, 0) CG_A(false, 8) CG_A(false, 16) CG_A(false, 32) CG_A(false, 128)
