@@ -178,6 +178,15 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+def _span(t):
+    """(address, bytes) of an array."""
+    try:
+        assert t.is_contiguous(), "tensors must be contiguous"
+        return t.data_ptr(), t.nbytes
+    except AttributeError:          # none, a raw address or a numpy array
+        return _ptr(t), _nbytes(t)
+
+
 def _stream(stream):
     if stream is not None:
         return stream
@@ -419,17 +428,31 @@ def _here(*arrays):
     for t in arrays:
         if t is None or type(t) is int:
             continue
-        dev = -1 if isinstance(t, np.ndarray) else t.get_device()
+        try:
+            dev = t.get_device()
+        except AttributeError:      # a numpy array
+            dev = -1
         if dev == cur:
             continue
         if dev < 0:
             raise ValueError("device tensors are needed, got one in host memory")
         if cur is None:
-            import torch
-            cur = torch.cuda.current_device()
+            cur = _current_device()
         if dev != cur:
             raise ValueError(f"a tensor is on GPU {dev}, the current one is {cur}")
     return cur
+
+
+_raw_device = None
+
+
+def _current_device():
+    """torch.cuda.current_device of a process that has a device tensor, without its check for a first call."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_device()
 
 
 _raw_stream = None
@@ -498,11 +521,11 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
         _sized(name, t, "int32", batch)
     dev = _here(q, out, payload, meta, lse, mass, workspace, gauge._keep, *attn._keep)
     rc = lib().cg_attend(
-        shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, attn,
+        shape, *_span(payload), *_span(meta), gauge, codec, attn,
         q if isinstance(q, int) else q.data_ptr(),
         _sized("out", out, st, rows * d), _sized("lse", lse, "float32", rows),
         _sized("mass", mass, "float32", shape.layers * batch * shape.heads * (shape.token_capacity // blk if blk > 0 else 0)),
-        _ptr(workspace), _nbytes(workspace), _stream_on(stream, dev))
+        *_span(workspace), _stream_on(stream, dev))
     if rc != CG_OK:
         _check("cg_attend", rc)
 
@@ -542,7 +565,7 @@ def cg_append(shape, gauge, codec, layer, n_new, k_new, v_new, tail, payload, me
         shape, gauge, codec, layer, n_new, *ptrs, bs, rs,
         _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch),
         _sized("tail", tail, st, shape.layers * 2 * shape.batch * row * codec.block_tokens),
-        _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), _stream_on(stream, dev))
+        *_span(payload), *_span(meta), _stream_on(stream, dev))
     if rc != CG_OK:
         _check("cg_append", rc)
 
@@ -557,7 +580,7 @@ def cg_read(shape, payload, meta, gauge, codec, layer, k_out, v_out, lengths=Non
     _gauge_sized(gauge, shape)
     dev = _here(k_out, v_out, payload, meta, lengths, starts, gauge._keep)
     rc = lib().cg_read(
-        shape, _ptr(payload), _nbytes(payload), _ptr(meta), _nbytes(meta), gauge, codec, layer, n,
+        shape, *_span(payload), *_span(meta), gauge, codec, layer, n,
         _sized("lengths", lengths, "int32", shape.batch), _sized("starts", starts, "int32", shape.batch), *ptrs, bs, rs,
         _stream_on(stream, dev))
     if rc != CG_OK:
@@ -640,9 +663,9 @@ def cg_evict(shape, codec, budget, sink, recent, mass, payload, meta, out_shape,
     dev = _here(mass, payload, meta, payload_out, meta_out, mass_out, kept, lengths_out, lengths)
     rc = lib().cg_evict(
         shape, codec, budget, sink, recent,
-        _sized("mass", mass, "float32", heads * nblk), _ptr(payload), _nbytes(payload), _ptr(meta),
-        _nbytes(meta), _sized("lengths", lengths, "int32", shape.batch), out_shape,
-        _ptr(payload_out), _nbytes(payload_out), _ptr(meta_out), _nbytes(meta_out),
+        _sized("mass", mass, "float32", heads * nblk), *_span(payload), *_span(meta),
+        _sized("lengths", lengths, "int32", shape.batch), out_shape,
+        *_span(payload_out), *_span(meta_out),
         _sized("mass_out", mass_out, "float32", heads * nout),
         _sized("kept", kept, "int32", heads * max(budget, 0)),
         _sized("lengths_out", lengths_out, "int32", shape.batch), _stream_on(stream, dev))
