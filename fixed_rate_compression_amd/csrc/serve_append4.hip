@@ -7,12 +7,18 @@
 //
 // What bounds it is the chain of a call's loads and steps, so a workgroup takes one block of one (K/V,
 // sequence, head), each of its four waves 32 channels from the load to the store, and no wave waits for
-// another: a lane loads eight channels of a row, 4 x 4 transpositions over a row's lanes give the
-// matrix cores' operands (the gauge's are transposed likewise), the gauge is the encoder's fused multiply-add chains (cg_tile.hpp), and its
-// result has a lane hold 8 rows of each of two channels: a key's range is the lane's own
-// and three other lanes', a value's that of 16 lanes.  A byte holds the codes of two channels, lanes side by side; a 4 x 4
-// transposition of bytes over four such pairs gives each lane a row's dword.
+// another.  A lane loads eight channels of a row; 4 x 4 transpositions over a row's lanes give the
+// matrix cores' operands (the gauge's are loaded in whole lines too and transposed likewise: in single
+// values they took 128 of a wave's 350 cycles at the first cache).  The gauge is the encoder's chains of
+// fused multiply-adds (cg_tile.hpp); its result has a lane hold 8 rows of two channels: a key's range is
+// the lane's own and three other lanes', a value's that of 16 lanes.  Lanes side by side have the codes
+// of a byte; a 4 x 4 transposition of bytes over four such pairs gives each lane a row's dword.
 // The raw rows of the last block are stored by the wave that reads those of the first, after its reads.
+//
+// A token for 64 sequences of 8 heads 7.1 us on the device (rows in LDS, 64 to a workgroup whose waves
+// met four times: 9.5), of which a single workgroup takes 4; prompts of up to 2000 tokens for 4 sequences 13.4
+// (19.6), fp32 15.3.  Workgroups that take several blocks, the next one's rows on their way: 12.5 to 14.2, and
+// a token 8.0 for the registers.
 #include "cg_tile.hpp"
 #include "quant_kernels.hpp"
 #include "serve.hpp"
@@ -166,6 +172,18 @@ __global__ __launch_bounds__(NT, G == 128 ? 2 : G == 32 && !BF16 ? 4 : 8) void k
       if (r >= keep0 && r < keep1) raw[p].load(src + r * rs + 32 * ESZ * w, kr);
     }
   }
+
+  if constexpr (G == 128)  // here the waves read one another's channels of the old rows
+    if (strip == 0) {
+#pragma unroll
+      for (int p = 0; p < 2; p++)
+#pragma unroll
+        for (int k = 0; k < PIECES; k++) {
+          asm volatile("" ::"v"(in[p][k].w[0]));  // the rows have come
+          if constexpr (!BF16) asm volatile("" ::"v"(in[p][k].w[1]));
+        }
+      __syncthreads();
+    }
 
   // y[p][nb][j]: row 16 p + 4 kr + j, channel 32 w + 16 nb + n
   float y[2][2][4];
