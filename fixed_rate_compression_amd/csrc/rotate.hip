@@ -219,9 +219,9 @@ static hipError_t launch(const RotateArgs &a, hipStream_t s) {
 }
 
 hipError_t rotate_launch(const RotateArgs &a, bool bf16, hipStream_t s) {
-  // one head to a lane group while that leaves compute units free: each waits for its row's
-  // sines alone
-  const bool few = (int64_t)a.batch * a.n * (a.r[0].heads + a.r[1].heads) <= 16 * 2048;
+  // One head to a lane group while that leaves compute units free, four where they share the factors: 2560
+  // heads 4.1 us and 4.7, 20480 heads 5.9 and 5.6, 32000 7.5 and 6.2, 128000 18.9 and 13.6.
+  const bool few = (int64_t)a.batch * a.n * (a.r[0].heads + a.r[1].heads) <= 16 * 512;
   if (bf16) return few ? launch<true, 1>(a, s) : launch<true, 4>(a, s);
   return few ? launch<false, 1>(a, s) : launch<false, 4>(a, s);
 }
