@@ -423,6 +423,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
 #pragma unroll
       for (int s = 0; s < 8; s++) *(h8_t *)(lo + s * 1024) = part[s];
   }
+  // A wave without rows widens the units with the others, no more: 68 rows with log-sums 83 us, so 64.
+  // In one part, which fewer waves take, the test cost more than it saved (a prompt of 1000 36 us, 40).
+  const bool mine = !P2 || wave * WROWS < nr;
   // what the row sees; rows that are not there see everything
   const int lim = wr < a.rows ? query_limit(a, sq, (int)((uint32_t)wr / (uint32_t)a.ratio)) : tmax;
   int all = lim;
@@ -475,16 +478,22 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
     float A, lv;
     factors(u0, A, lv);
     fetch_head(u0 + 1);
-    raise4<P2>(keys_at(u0), klo, lo, A, lv, q, lim - u0 * UNIT - 4 * half, st, acc, o);
+    if (mine) raise4<P2>(keys_at(u0), klo, lo, A, lv, q, lim - u0 * UNIT - 4 * half, st, acc, o);
     const auto store_sum = [&](int un) {
       const uint32_t x = __float_as_uint(o.ps);
       const auto y = __builtin_amdgcn_permlane32_swap(x, x, false, false);
       const float v = __uint_as_float(y[0]) + __uint_as_float(y[1]);
       if (half == 0 && wr < a.rows) a.bsum[((int64_t)bh * a.entries + un) * a.rows + wr] = make_float2(v, st.mu);
     };
-    if constexpr (SUMS) store_sum(u0);
+    if constexpr (SUMS)
+      if (mine) store_sum(u0);
     const auto turn = [&](int un, auto masked, In &in) {
       __syncthreads();  // unit un + 1 is there, unit un - 1 is done with
+      if (!mine) {
+        Put4<L, P2, V2, N>(lds, un + 2, in).all();
+        fetch4(place, un + 2 + SETS, in);
+        return;
+      }
       float A, lv;
       factors(un + 1, A, lv);
       fetch_head(un + 2);
@@ -564,9 +573,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
       if constexpr (SETS == 2)
         if (un + 2 < u1) turn(un + 1, std::true_type{}, nx[1]);
     }
-    st.l += o.ps;
-    pack_weights<BF16>(o.p, P);
-    values4<V2>(values_at(u1 - 1), vlo, P, acc);
+    if (mine) {
+      st.l += o.ps;
+      pack_weights<BF16>(o.p, P);
+      values4<V2>(values_at(u1 - 1), vlo, P, acc);
+    }
   }
   __syncthreads();
 
@@ -639,9 +650,10 @@ hipError_t tile4_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const bool p2 = a.two, sums = a.bsum != nullptr;
   // Eight waves widen a unit for twice the rows, where that still gives every compute unit a workgroup:
   // 2048 queries over 8192 tokens (256 workgroups) 309 us, by four 316; a prompt of 4000 196 and 209, of
-  // 1000 (128 workgroups) 51 and 42.  Two parts take most of a compute unit's LDS either way.
+  // 1000 (128 workgroups) 51 and 42; and where there are rows for them: 68 rows a head of 8 sequences of
+  // 4096 tokens 57 us, by four 35.  Two parts take most of a compute unit's LDS either way.
   const int64_t wide = (int64_t)a.batch * a.heads * ((a.rows + 255) / 256) * a.splits;
-  const int nw = p2 || wide >= 256 ? 8 : 4;
+  const int nw = p2 || (wide >= 256 && a.rows > 4 * WROWS) ? 8 : 4;
   const int64_t groups = (a.rows + nw * WROWS - 1) / (nw * WROWS);
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * groups * a.splits)), block(64 * nw);
 #define CG_T(BF, P2, SUMS, NW)                                                             \

@@ -95,10 +95,20 @@ constexpr uint64_t kMaxSums = (uint64_t)1 << 30;
 // shape->tokens; where that would pass 256 MiB the sequences are taken in turn.
 constexpr uint64_t kMaxRanges = (uint64_t)256 << 20;
 
+constexpr double kManyTokens = 262144;  // of all heads, from which four row tiles are taken as many rows
+
 Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass) {
   Plan p{};
   const int64_t ratio = t->q_heads / s->heads;
-  const bool kivi = cgh::is_kivi4(c), many = t->n_queries * ratio > (int64_t)cga::FEW_TILES * cga::ROWS;
+  const int64_t rows = t->n_queries * ratio;
+  const bool kivi = cgh::is_kivi4(c);
+  // Four row tiles over the 4-bit cache: each decodes the same codes, the many-row form once.  64 rows of 8 KV
+  // heads, us by row tiles and by tiles of 128: 8 sequences of 500, 2048, 4096 and 16384 tokens 14 and 33, 33 and
+  // 45, 78 and 56, 185 and 133, 32 of 2048 104 and 77; with log-sums of 4096 88 and 86, 32 of 4096 242 and
+  // 208.  48 rows: 8 of 4096 52 and 52, of 16384 144 and 130, with log-sums 190 and 200.
+  const bool many = rows > (int64_t)cga::FEW_TILES * cga::ROWS ||
+                    (kivi && rows > (int64_t)(cga::FEW_TILES - 1) * cga::ROWS &&
+                     (double)s->batch * s->heads * (double)s->tokens >= kManyTokens);
   p.batch = s->batch;
   if (kivi && many) {
     const uint64_t blocks = (uint64_t)(s->tokens + cga::UNIT - 1) / cga::UNIT;
@@ -123,7 +133,7 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   // 8 KV heads x 4096 tokens with 32, 48 and 64 rows a head: one sequence 14, 17 and 17
   // us by row tiles of 16, 21, 22 and 23 by tiles of 128 (merges with them), 8
   // sequences 31, 37 and 45 against 40, 45 and 47
-  p.few = p.tiles <= cga::FEW_TILES;
+  p.few = p.tiles <= cga::FEW_TILES && !(kivi && many);
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
   int64_t sp = 1;
   if (work > 0 && p.few) {

@@ -57,6 +57,17 @@ def test_sequences_and_queries_in_turn(bf16):
         check(c, blocks_first(c.run(lse=lse, mass=mass), small), ref, (lse, mass))
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("n,R", [(13, 4), (16, 4), (49, 1), (12, 4)])
+def test_four_row_tiles_of_many_tokens(n, R, bf16):
+    """Past 262144 tokens of all heads 49 to 64 rows are taken by the many-row form."""
+    c = Case4(905 + n, B=8, H=8, R=R, n=n, T=4096, lengths=[4096, 130, 64, 33, 97, 0, 1, 200], bf16=bf16).device()
+    two = c.reference()
+    one = c.reference(one_part=True) if bf16 and n * R > 48 else two
+    for lse, mass, ref in ((False, False, one), (True, False, two), (True, True, two)):
+        check(c, c.run(lse=lse, mass=mass), ref, (lse, mass))
+
+
 @pytest.mark.parametrize("n", [1, 5, 40])
 @pytest.mark.parametrize("cap", [0, 32, 4096])
 def test_no_tokens(n, cap):
