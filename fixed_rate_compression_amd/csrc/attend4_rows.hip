@@ -21,7 +21,12 @@
 // rounded to fp16 each, around the code 8 (2^-12 of themselves, 2^-34 of the largest of the unit's
 // 32 tokens), for fp32 storage in two parts.  With the code as it stands and the minimum, a third
 // of this work less, bf16 outputs were off by 1.95e-3 of themselves, by 1.72e-3 around the
-// centre, and 1.66e-3 is their own rounding; the time was the same (87 us for 262144 tokens).
+// centre, and 1.66e-3 is their own rounding; 262144 tokens took 86.5 us for 87.7.
+//
+// 262144 tokens of 8 KV heads, four query heads each: 80 us (4.9 TB/s, a sum of as many bytes 5.9; 412 vector
+// instructions a unit) and a merge of 5; 16 sequences of up to 8192 with log-sums 26 (13 of them units, 5
+// the query's way into its operands) and 4.8.  Up to 1024 tokens in one workgroup of eight waves 13.9: its
+// chain takes 8, four units a wave 1.5 each; sixteen waves 15.4 (spills).  Two units' keys in flight: the same.
 #include "attend.hpp"
 #include "attend4.hpp"
 #include "attend_few.hpp"

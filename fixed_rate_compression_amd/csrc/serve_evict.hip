@@ -247,7 +247,8 @@ __global__ __launch_bounds__(ST) void k_evict_select(const EvictArgs a) {
 // read by all threads everything up to it may be overwritten.  Into another
 // cache the field is cut into `chunks`.  Half of 32 layers x 8 heads x 8192 tokens
 // (269 MB each way): 106 us, 4.9 TB/s, a large copy's 5.1.
-// KIVI: a block's ranges move as its codes do.
+// KIVI: a block's ranges move as its codes do (half of 32 layers x 8 heads x 8192 tokens, 201 MB each way:
+// 79 us of 85, 5.1 TB/s).
 template <bool KIVI>
 __global__ __launch_bounds__(MT) void k_evict_move(const EvictArgs a, int chunks) {
   const uint32_t f32 = blockIdx.x / (uint32_t)chunks, heads = (uint32_t)(a.batch * a.heads);

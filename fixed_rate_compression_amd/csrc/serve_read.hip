@@ -6,6 +6,10 @@
 // keys, one for a channel and 32 tokens, through LDS, since every row of a block reads them
 // all.  The inverse gauge is the decoders': fmaf chains, or for bf16 storage and groups of
 // 16 and 32 split bf16 products (split_gauge.hpp).
+//
+// 131072 rows of 8 heads in 8 bits 183 us (805 MB, 4.4 TB/s; a copy runs at 5.1), 1000 of 3 sequences in 4
+// bits 7.7, which is a launch, the lengths, the codes and the gauge one after another.  Waves that keep 32
+// channels of 32 rows in registers from the codes to the outputs took 258 and 8.8: 64-byte pieces of rows.
 #include "cg_tile.hpp"
 #include "quant_kernels.hpp"
 #include "serve.hpp"
