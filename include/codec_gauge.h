@@ -444,6 +444,10 @@ typedef struct cg_attn {
  * 128 rows a KV head (or one query's) at least: 1 KiB for every KV head of the batch
  * and 32 tokens, 2 GiB for 64 sequences of 8 KV heads and 131072 tokens.  Fewer rows
  * are never taken in turn: 512 bytes at most.
+ * Over 4 bits calls of more than 64 rows a KV head (of more than 48 where all heads of the batch
+ * have 262144 tokens of shape->tokens) take the blocks' ranges in another form: 1.5 KiB (fp32
+ * storage: 2 KiB) for every KV head and 32 tokens of shape->tokens, for as many sequences
+ * at once as fit 256 MiB, one at least.
  * The size does not depend on which arrays attn gives.
  */
 int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, const cg_codec *codec,
@@ -472,9 +476,10 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  * of a channel) for bf16 storage with more than 64 rows a KV head and neither lse nor
  * mass; weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
  * 4 bits: queries times key steps in two parts (2^-23 of the largest channel times the
- * block's largest key), in three (2^-34) for fp32 storage and with lse or mass; weights
- * and the values themselves for fp32 storage in two parts, for bf16 storage in one (2^-11, and 2^-31 of
- * a block's largest value).
+ * block's largest key), in three (2^-34) for fp32 storage and with lse or mass; calls that take the
+ * ranges in another form (above): queries and keys in one part (2^-11 of each), in two (2^-22) for fp32
+ * storage and with lse or mass; weights and the values themselves for fp32 storage in two parts, for
+ * bf16 storage in one (2^-11, and 2^-31 of a block's largest value).
  * The order of sums depends on the shape and the lengths only (deterministic).
  * The workspace belongs to one call at a time.  Asynchronous on stream.
  */
