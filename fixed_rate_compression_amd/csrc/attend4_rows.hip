@@ -473,13 +473,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
 hipError_t rows4_launch(const AttendArgs &a, bool bf16, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.heads * a.tiles * a.slots));
   const bool mass = a.mass && a.bsum, p3 = !bf16 || mass || a.lse;
-  const int nr = a.rows <= 4 ? 4 : 16;
+  const int nr = a.rows <= 4 ? 4 : a.rows <= 8 ? 8 : 16;
 #define CG_R(BF, P3, MA, NW, NR)                                                                 \
   if (bf16 == BF && p3 == P3 && mass == MA && a.waves == NW && nr == NR) {                       \
     hipLaunchKernelGGL((k_attend4_rows<BF, P3, MA, NW, NR>), grid, dim3(64 * NW), 0, s, a);      \
     return hipGetLastError();                                                                    \
   }
-#define CG_RR(BF, P3, MA) CG_R(BF, P3, MA, 4, 4) CG_R(BF, P3, MA, 8, 4) CG_R(BF, P3, MA, 4, 16) CG_R(BF, P3, MA, 8, 16)
+#define CG_RR(BF, P3, MA)                                                                        \
+  CG_R(BF, P3, MA, 4, 4) CG_R(BF, P3, MA, 8, 4) CG_R(BF, P3, MA, 4, 8) CG_R(BF, P3, MA, 8, 8)    \
+  CG_R(BF, P3, MA, 4, 16) CG_R(BF, P3, MA, 8, 16)
   CG_RR(true, false, false) CG_RR(true, true, false) CG_RR(true, true, true) CG_RR(false, true, false) CG_RR(false, true, true)
 #undef CG_RR
 #undef CG_R
