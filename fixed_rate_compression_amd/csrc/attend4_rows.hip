@@ -27,6 +27,8 @@
 // instructions a unit) and a merge of 5; 16 sequences of up to 8192 with log-sums 26 (13 of them units, 5
 // the query's way into its operands) and 4.8.  Up to 1024 tokens in one workgroup of eight waves 13.9: its
 // chain takes 8, four units a wave 1.5 each; sixteen waves 15.4 (spills).  Two units' keys in flight: the same.
+// Rows beyond 4 and 8 have forms of their own, whose queries take as much work: eight query heads and
+// 262144 tokens 96 us, in the form of 16 rows 106; five, 16 sequences with log-sums 28 and 44.
 #include "attend.hpp"
 #include "attend4.hpp"
 #include "attend_few.hpp"
@@ -116,7 +118,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
   // values' centres and steps [4][32]
   static_assert(P3 || (BF16 && !MASS), "two parts for bf16 outputs alone");
   constexpr int PARTS = P3 ? 3 : 2;
-  constexpr int STEP = NR * 64 + 64, KOPS = 4 * PARTS * STEP, VB = BF16 ? 2 : 4, VR = 32 * VB;
+  // 64 bytes between the steps: other banks.  Half of them for 16 rows in three parts, for a third workgroup on a
+  // compute unit (4 queries of 16 sequences of up to 8192 with log-sums 37 us for 41)
+  constexpr int STEP = NR * 64 + (BF16 && P3 && NR == 16 && !MASS ? 32 : 64), KOPS = 4 * PARTS * STEP, VB = BF16 ? 2 : 4, VR = 32 * VB;
   constexpr int WAVE = KOPS + 64 + 8 * VR, JOIN = ROWS * PITCH * 4;
   constexpr int PER = WAVE > JOIN ? WAVE : JOIN;
   static_assert(PER * NW >= 3 * ROWS * PITCH * 4, "gauged rows and their factors");

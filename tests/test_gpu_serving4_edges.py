@@ -68,6 +68,17 @@ def test_four_row_tiles_of_many_tokens(n, R, bf16):
         check(c, c.run(lse=lse, mass=mass), ref, (lse, mass))
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("R,n", [(5, 1), (7, 1), (8, 1), (4, 2), (2, 3), (1, 9), (3, 4), (4, 4)])
+@pytest.mark.parametrize("T,lengths", [(700, [700, 33, 300]), (5000, [5000, 31, 2300])])
+def test_five_to_sixteen_rows(R, n, bf16, T, lengths):
+    """The forms of 8 and of 16 rows, by eight waves and in splits that follow the lengths."""
+    c = Case4(920 + R + n, B=3, H=2, R=R, n=n, T=T, lengths=lengths, bf16=bf16).device()
+    ref = c.reference()
+    for lse, mass in ((False, False), (True, False), (True, True)):
+        check(c, c.run(lse=lse, mass=mass), ref, (lse, mass))
+
+
 @pytest.mark.parametrize("n", [1, 5, 40])
 @pytest.mark.parametrize("cap", [0, 32, 4096])
 def test_no_tokens(n, cap):
