@@ -44,6 +44,7 @@ struct ReadArgs {
   const float *gauges;     // the layer's [kind][heads][128 g]
   int64_t tcap, tokens, nblk;
   int32_t batch, heads, n, bshift, tiles;  // tiles: 64-row strips of the rows
+  Div by_tiles, by_heads;
 };
 hipError_t read_launch(const ReadArgs &a, bool bf16, int g, bool kivi, hipStream_t s);
 

@@ -142,6 +142,8 @@ int cg_read(const cg_shape *shape, const void *payload, uint64_t payload_cap, co
   a.n = n;
   a.bshift = codec->block_tokens == 16 ? 4 : codec->block_tokens == 32 ? 5 : 6;
   a.tiles = (int32_t)tiles;
+  a.by_tiles = cgs::Div((uint32_t)tiles);
+  a.by_heads = cgs::Div((uint32_t)a.heads);
   hipError_t e = cgs::read_launch(a, shape->dtype == CG_DTYPE_BF16, gauge->group, cgh::is_kivi4(codec), (hipStream_t)stream);
   return e == hipSuccess ? CG_OK : cgh::hip_error(e, "cg_read launch");
 }

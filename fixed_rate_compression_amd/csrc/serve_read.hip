@@ -26,7 +26,7 @@ __global__ __launch_bounds__(NT) void k_read(const ReadArgs a) {
   __shared__ __align__(16) float2 kr[KIVI ? 3 * D : 1];
   constexpr size_t ESZ = BF16 ? 2 : 4;
   // heads side by side: their rows lie next to one another in the output
-  const uint32_t q1 = blockIdx.x / (uint32_t)a.heads, q2 = q1 / (uint32_t)a.tiles, q3 = q2 / 2;
+  const uint32_t q1 = a.by_heads(blockIdx.x), q2 = a.by_tiles(q1), q3 = q2 / 2;
   const int h = (int)(blockIdx.x - q1 * a.heads), strip = (int)(q1 - q2 * a.tiles), kind = (int)(q2 & 1), b = (int)q3;
   uint8_t *dst = (uint8_t *)(kind ? a.v : a.k);
   if (!dst) return;

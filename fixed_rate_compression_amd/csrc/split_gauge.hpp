@@ -80,15 +80,6 @@ struct SplitGaugeFrags {
   sg_bf16x8_t b[2][2];  // [output block nb][g = 16: B1, B2 | g = 32: B_hi, B_lo]
 };
 
-__device__ __forceinline__ sg_bf16x8_t sg_pack8(const uint32_t (&h)[8]) {
-  sg_u32x4_t u;
-  u.x = h[0] | (h[1] << 16);
-  u.y = h[2] | (h[3] << 16);
-  u.z = h[4] | (h[5] << 16);
-  u.w = h[6] | (h[7] << 16);
-  return __builtin_bit_cast(sg_bf16x8_t, u);
-}
-
 // B operands of this wave for G^T (inverse): B[k][n] = G[input k][output c]
 template <int G>
 __device__ __forceinline__ void load_split_gauge(const float *__restrict__ Gf, SplitGaugeFrags<G> &f) {
@@ -101,15 +92,16 @@ __device__ __forceinline__ void load_split_gauge(const float *__restrict__ Gf, S
     const float *Gr = Gf + (col / G) * G * G;
     const int c = col % G;
     const int i0 = G == 16 ? 8 * (kg & 1) : 8 * kg;   // first input of this lane's k range
-    uint32_t h[8], l[8];
+    sg_u32x4_t h, l;
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const float gv = Gr[(i0 + e) * G + c];
-      h[e] = bf16_rne(gv);
-      l[e] = bf16_rne(gv - __uint_as_float(h[e] << 16));
+    for (int e = 0; e < 4; e++) {
+      const float x = Gr[(i0 + 2 * e) * G + c], y = Gr[(i0 + 2 * e + 1) * G + c];
+      const uint32_t hi = pack_bf16x2(x, y);
+      h[e] = hi;
+      l[e] = pack_bf16x2(x - bf16lo(hi), y - bf16hi(hi));
     }
-    f.b[nb][0] = sg_pack8(h);
-    f.b[nb][1] = sg_pack8(l);
+    f.b[nb][0] = __builtin_bit_cast(sg_bf16x8_t, h);
+    f.b[nb][1] = __builtin_bit_cast(sg_bf16x8_t, l);
   }
 }
 
