@@ -33,13 +33,14 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // tokens, plus each workgroup's tokens at its share of 5.5 TB/s, at best 12.5 ns a
 // token; a merge takes about 4.5 us.  Of one split and the most that one, two,
 // three or four rounds hold the fastest by that sum is taken, with at least 256
-// tokens (two units a wave) to a workgroup.  80 KV heads of 3000 tokens: 9 splits
+// tokens (two units a wave) to a workgroup.  (4 bits: 4.9 TB/s; 32 sequences of 8 KV heads and 4096 tokens 46 us
+// in three splits, 59 in one.)  80 KV heads of 3000 tokens: 9 splits
 // (one round) 19 us, 10 splits 24; 200 heads of 4000 tokens: one split 55 us, 3
 // splits and merge 49; 800 heads: 171 and 162; 300 heads of 8000 tokens: one split
 // 121, 2 splits 130; 131072 tokens with sums by 512 workgroups 54 us, by 768 66.
 constexpr int64_t kResident = 768, kResidentSums = 512, kMinTokens = 256;
 
-int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
+int64_t few_splits(int64_t work, int64_t tokens, int64_t resident, double token_us) {
   const int64_t most = (tokens + kMinTokens - 1) / kMinTokens;
   int64_t best = 1;
   double best_us = 0.0;
@@ -50,7 +51,7 @@ int64_t few_splits(int64_t work, int64_t tokens, int64_t resident) {
     if (sp < 1) sp = 1;
     // whole rounds, then what is left, at its share of the bandwidth
     const int64_t groups = work * sp, full = groups / resident, rest = groups % resident;
-    const double each = (double)tokens / sp, whole = resident * 256.0 / 5.5e6;
+    const double each = (double)tokens / sp, whole = resident * token_us;
     const double part = whole * rest / resident;
     const double us = full * (6.0 + each * (whole > 0.0125 ? whole : 0.0125)) +
                       (rest ? 6.0 + each * (part > 0.0125 ? part : 0.0125) : 0.0) + (sp > 1 ? 4.5 : 0.0);
@@ -137,7 +138,9 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
   int64_t sp = 1;
   if (work > 0 && p.few) {
-    sp = few_splits(work, s->tokens, mass ? kResidentSums : kResident);
+    // a token's codes (and ranges) at what the many workgroups reach
+    const double token_us = kivi ? 192.0 / 4.9e6 : 256.0 / 5.5e6;
+    sp = few_splits(work, s->tokens, mass ? kResidentSums : kResident, token_us);
   } else if (work > 0) {
     sp = tile_splits(work, fields * p.rows, s->tokens);
   }
@@ -159,10 +162,18 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   // 32 sequences of 2000 tokens but one of 131072: the whole call 72 and 428; 64 of
   // 16000 in one split each, with a merge that finds nothing to do: 390 and 389.
   // (The workspace is the same with and without lengths.)
+  // Over 4 bits also one split of shorter ones, with as many more as fill the compute units, where those are
+  // half as many at least: 8 KV heads, 48 sequences of 0 .. 4096 tokens 46 us, undealt 63 (all of 4096: 71 and 84),
+  // 40 of 3000 36 and 45, 64 of 8000 114 and 145 (204 and 194), of 2100 40 and 43 (49 and 46); 64 of 3000 and 12
+  // heads, which fill them as they are, 76 and 68.
+  const bool one = p.splits == 1;
+  const int64_t half = s->batch / 2, room = p.few && work > 0 ? (kResident - 1 - (work - 1) % kResident) / (s->heads * p.tiles) : 0;
+  const bool fills = kivi && one && room >= half;
   const bool may = p.few && p.waves == 4 && s->batch > 1 && s->batch <= 64 &&
-                   s->tokens > (p.splits > 1 ? 2048 : 16384) && s->tokens < (int64_t)1 << 30;
+                   s->tokens > (one && !fills ? 16384 : 2048) && s->tokens < (int64_t)1 << 30;
   p.ragged = may && t->lengths;
-  const int64_t more = may && p.splits == 1 ? s->batch / 2 : 0, slots = (int64_t)s->batch * p.splits;
+  const int64_t more = !may || !one ? 0 : !fills ? half : room < s->batch ? room : s->batch;
+  const int64_t slots = (int64_t)s->batch * p.splits;
   p.slots = (int)(slots + (p.ragged ? more : 0));
   p.least = (int)((s->tokens + cga::UNIT - 1) / cga::UNIT / cga::MERGE_SPLITS + 1);
   if (p.least < kMinTokens / cga::UNIT) p.least = kMinTokens / cga::UNIT;

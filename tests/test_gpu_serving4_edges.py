@@ -79,6 +79,19 @@ def test_five_to_sixteen_rows(R, n, bf16, T, lengths):
         check(c, c.run(lse=lse, mass=mass), ref, (lse, mass))
 
 
+@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("B,H", [(48, 8), (64, 12), (33, 10)])
+def test_many_sequences_of_unlike_lengths(B, H, n):
+    """One split each, the workgroups that fill the compute units dealt by length."""
+    rng = np.random.default_rng(B)
+    lengths = np.where(rng.random(B) < 0.1, rng.integers(1500, 2301, B), rng.integers(0, 90, B)).tolist()
+    lengths[1:4] = [2300, 0, 1]
+    c = Case4(925 + B, B=B, H=H, R=2, n=n, T=2300, lengths=lengths).device()
+    ref = c.reference()
+    check(c, c.run(lse=False, mass=False), ref)
+    check(c, c.run(lse=True, mass=True), ref)
+
+
 @pytest.mark.parametrize("n", [1, 5, 40])
 @pytest.mark.parametrize("cap", [0, 32, 4096])
 def test_no_tokens(n, cap):
