@@ -416,7 +416,7 @@ def _sized(name, t, dtype, count):
     """A device array argument whose size and type the C call cannot see."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype != _dtype(dtype) or t.numel() < count or not t.is_contiguous():
+    if t.dtype is not (_dtypes.get(dtype) or _dtype(dtype)) or t.numel() < count or not t.is_contiguous():
         raise ValueError(f"{name}: {count} contiguous values of {dtype} are needed, got {t.numel()} of {t.dtype}")
     return t.data_ptr()
 
@@ -472,7 +472,10 @@ def _stream_on(stream, device):
 
 def _gauge_sized(gauge, shape):
     """The gauge's tensor holds what the C call reads of it."""
-    G, need = gauge._keep, shape.layers * 2 * shape.heads * shape.head_dim * gauge.group
+    G = gauge._keep
+    if G is None:
+        return
+    need = shape.layers * 2 * shape.heads * shape.head_dim * gauge.group
     if hasattr(G, "numel") and (G.dtype != _dtype("float32") or G.numel() < need):
         raise ValueError(f"gauge: {need} values of float32 are needed, got {G.numel()} of {G.dtype}")
 
@@ -533,20 +536,21 @@ def cg_attend(shape, payload, meta, gauge, codec, attn, q, out, lse=None, mass=N
 def _kv_rows(shape, n, named):
     """Rows [batch, n, heads, head_dim] of the storage format with contiguous heads, all lying alike
     -> their addresses and (strides between sequences, between rows)."""
-    st, at, ptrs = _storage(shape), None, []
+    st, at, ptrs = _dtype(_storage(shape)), None, []
+    batch, heads, d = shape.batch, shape.heads, shape.head_dim
     for name, t in named:
         if t is None:
             ptrs.append(None)
             continue
-        if t.dtype != _dtype(st):
-            raise ValueError(f"{name} must be {st}, got {t.dtype}")
-        if t.shape != (shape.batch, n, shape.heads, shape.head_dim):
+        if t.dtype is not st:
+            raise ValueError(f"{name} must be {_storage(shape)}, got {t.dtype}")
+        if t.shape != (batch, n, heads, d):
             raise ValueError(f"{name} must be [batch, {n}, heads, head_dim], got {tuple(t.shape)}")
         sb, sr, sh, sd = t.stride()
-        if (shape.batch > 1 and sb == 0) or (n > 1 and sr == 0):
+        if (batch > 1 and sb == 0) or (n > 1 and sr == 0):
             raise ValueError(f"{name}: rows of an expanded tensor")
-        lie = (sb if shape.batch > 1 else 0, sr if n > 1 else 0)
-        if (sh != shape.head_dim and shape.heads > 1) or sd != 1 or lie != (at or lie):
+        lie = (sb if batch > 1 else 0, sr if n > 1 else 0)
+        if (sh != d and heads > 1) or sd != 1 or lie != (at or lie):
             raise ValueError(f"{name} of strides {t.stride()}: contiguous heads and equal strides are needed")
         at = lie
         ptrs.append(t.data_ptr())
@@ -605,7 +609,7 @@ def make_rotary(freq, sections=None, interleaved=False, dealt=False, q_weight=No
 
 def _rows(name, t, st, batch, n, heads, d):
     """[batch, n, heads, head_dim] of the storage format -> CgRows."""
-    if t.dtype != st:
+    if t.dtype is not st:
         raise ValueError(f"{name} must be {st}, got {t.dtype}")
     if t.shape != (batch, n, heads, d):
         raise ValueError(f"{name} must be [{batch}, {n}, {heads}, {d}], got {tuple(t.shape)}")
