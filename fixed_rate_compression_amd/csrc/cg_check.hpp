@@ -18,6 +18,12 @@ inline uint64_t reach(int64_t batch, int64_t bs, int64_t n, int64_t rs, int64_t 
   const unsigned __int128 e = (unsigned __int128)(batch - 1) * bs + (unsigned __int128)(n - 1) * rs + row;
   return e >> 60 ? 0 : (uint64_t)e;
 }
+// whether rows of w elements at b bs + i rs (b < batch, i < n; strides that reach() takes) lie apart: the smaller stride
+// passes a row, the larger one all rows of the smaller.  The stride of a single row or sequence is not looked at.
+inline bool rows_apart(int64_t batch, int64_t bs, int64_t n, int64_t rs, int64_t w) {
+  if (batch == 1 || n == 1) return (n == 1 || rs >= w) && (batch == 1 || bs >= w);
+  return (rs >= w && bs >= rs * (n - 1) + w) || (bs >= w && rs >= bs * (batch - 1) + w);
+}
 int check_shape_of(const cg_shape *s);
 // a K/V cache in 8-bit block-uniform or 4-bit KIVI-style form with its buffers (gauge
 // may be NULL: not looked at)

@@ -42,9 +42,7 @@ int span_of(const cg_rows *r, const cg_shape *s, int32_t n, int32_t heads, bool 
   // one row a sequence: the sequences are the rows; one sequence: it has no next
   if (n == 1 && s->batch > 1) o->rs = o->bs;
   if (s->batch == 1) o->bs = o->rs * n;
-  if (written && (o->rs < row ||
-                  (s->batch > 1 && o->bs < o->rs * (n - 1) + row && o->rs < o->bs * (s->batch - 1) + row)))
-    return error(CG_E_INVAL, "rows of an output overlap");
+  if (written && !cgh::rows_apart(s->batch, o->bs, n, o->rs, row)) return error(CG_E_INVAL, "rows of an output overlap");
   return CG_OK;
 }
 

@@ -110,8 +110,7 @@ int cg_read(const cg_shape *shape, const void *payload, uint64_t payload_cap, co
   if (n == 1 && shape->batch > 1) rs = bs;
   if (shape->batch == 1) bs = rs * n;
   // rows that lie in one another would be written by several workgroups
-  if (rs < row || (shape->batch > 1 && bs < (rs * (n - 1) + row) && rs < bs * (shape->batch - 1) + row))
-    return error(CG_E_INVAL, "rows of the output overlap");
+  if (!cgh::rows_apart(shape->batch, bs, n, rs, row)) return error(CG_E_INVAL, "rows of the output overlap");
   cgs::ReadArgs a{};
   const uint64_t pb = (uint64_t)shape->layers * fields * cgh::payload_field(codec, shape->token_capacity),
                  mb = (uint64_t)shape->layers * fields * cgh::meta_field(codec, shape->token_capacity);
