@@ -23,4 +23,7 @@ __device__ __forceinline__ uint32_t range_bits(float2 m) {  // of the larger end
   const uint32_t a = __float_as_uint(m.x) & 0x7fffffffu, b = __float_as_uint(__builtin_fmaf(15.0f, m.y, m.x)) & 0x7fffffffu;
   return max(a, b);
 }
+// smallest E with |x| < 2^E, of the largest magnitude's bits
+__device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 126; }
+
 }  // namespace cga

@@ -84,9 +84,6 @@ __device__ __forceinline__ void load_values4(const uint8_t *vf, const float2 *vm
   u.m[1] = m[4];
 }
 
-// smallest E with |x| < 2^E, of the largest magnitude's bits
-__device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 126; }
-
 // eight codes of a dword as halves: pairs (0, 4), (1, 5), (2, 6), (3, 7); the odd ones 16 times
 // themselves, which their queries make up for
 __device__ __forceinline__ h8_t nibbles8(uint32_t w) {

@@ -6,10 +6,10 @@
 // Keys and values are widened to what they stand for, since their ranges differ along the
 // contraction (keys: by channel) or along both axes (values): two packed fp16
 // multiply-adds a pair of codes, once for all rows, or in fp32 and in two parts (keys where
-// log-sums or weights are asked for, both for fp32 storage).  Where a unit's values leave
-// fp16's range a power of two brings them back.  That and the ranges in the form in which they are
-// used come from a launch before (k_ranges4): the vector units bound this kernel, and forming
-// them at every use took 64 of its 235 vector instructions a wave and unit.
+// log-sums or weights are asked for, both for fp32 storage).  A power of two brings a unit's
+// largest value to [2^8, 2^9), so that halves keep 2^-33 of it.  That and the ranges in the
+// form in which they are used come from a launch before (k_ranges4): the vector units bound
+// this kernel, and forming them at every use took 64 of its 235 vector instructions a wave and unit.
 #include <type_traits>
 
 #include "attend.hpp"
@@ -44,13 +44,6 @@ template <bool P2, bool V2>
 struct Ranges4 {
   static constexpr int K = P2 ? 1024 : 512, V = V2 ? 1024 : 512, BYTES = K + V;
 };
-
-// A power of two above x: 2^9, which asks for no scaling, where x is in [2^-3, 2^8), so that small values keep
-// 2^-22 of the largest; else the smallest
-__device__ __forceinline__ int exponent_of(uint32_t bits) {
-  const int e = (int)(bits >> 23) - 126;
-  return e >= -2 && e <= 8 ? kTop : e;
-}
 
 // One wave to a block of a sequence's tokens.
 template <bool P2, bool V2>
