@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/codec_gauge.h"
 
 namespace cgh {
@@ -23,6 +25,23 @@ inline uint64_t reach(int64_t batch, int64_t bs, int64_t n, int64_t rs, int64_t 
 inline bool rows_apart(int64_t batch, int64_t bs, int64_t n, int64_t rs, int64_t w) {
   if (batch == 1 || n == 1) return (n == 1 || rs >= w) && (batch == 1 || bs >= w);
   return (rs >= w && bs >= rs * (n - 1) + w) || (bs >= w && rs >= bs * (batch - 1) + w);
+}
+// whether rows of wa elements, laid out so that rows of one of the widths lie apart, and rows of wb elements laid out
+// alike d elements further on share memory.  Two rows' distance is d + x so + y si, x below the larger stride's
+// count and y below the smaller's; few x bring them near one another.
+inline bool rows_meet(int64_t batch, int64_t bs, int64_t n, int64_t rs, int64_t d, int64_t wa, int64_t wb) {
+  const bool by_row = batch == 1 || (n > 1 && rs > bs);  // the larger stride is that of the rows
+  const int64_t co = by_row ? n : batch, so = by_row ? rs : bs, ci = by_row ? batch : n, si = by_row ? bs : rs;
+  const int64_t all = ci > 1 ? (ci - 1) * si : 0;
+  const auto down = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+  // y with -wb < e + y s < wa, |y| < count
+  const auto first = [&](int64_t e, int64_t w, int64_t s, int64_t count) { return std::max(1 - count, down(-w - e, s) + 1); };
+  const auto last = [&](int64_t e, int64_t w, int64_t s, int64_t count) { return std::min(count - 1, down(w - e - 1, s)); };
+  for (int64_t x = co > 1 ? first(d, wb + all, so, co) : 0; x <= (co > 1 ? last(d, wa + all, so, co) : 0); x++) {
+    const int64_t e = d + (co > 1 ? x * so : 0);
+    if (ci > 1 ? first(e, wb, si, ci) <= last(e, wa, si, ci) : e > -wb && e < wa) return true;
+  }
+  return false;
 }
 int check_shape_of(const cg_shape *s);
 // a K/V cache in 8-bit block-uniform or 4-bit KIVI-style form with its buffers (gauge

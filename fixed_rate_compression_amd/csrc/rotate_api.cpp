@@ -17,14 +17,11 @@ struct Span {
   int64_t bs, rs;
 };
 
-// whether rows of the two (wa and wb bytes) may share memory; parts of the same rows, side by
-// side, do not
-bool clash(const Span &a, uint64_t wa, const Span &b, uint64_t wb, int64_t esz) {
+// whether rows of the two (wa and wb elements) may share memory; parts of the same rows, side by side, do not
+bool clash(const cg_shape *s, int32_t n, const Span &a, int64_t wa, const Span &b, int64_t wb, int64_t esz) {
   if (a.at >= b.at + b.bytes || b.at >= a.at + a.bytes) return false;
-  if (a.rs != b.rs || a.bs != b.bs || a.rs <= 0 || a.bs % a.rs) return true;
-  const int64_t rs = a.rs * esz, d = (b.at - a.at) % rs;
-  const uint64_t m = (uint64_t)(d < 0 ? d + rs : d);  // from a row of a to one of b
-  return m < wa || m + wb > (uint64_t)rs;
+  if (a.rs != b.rs || a.bs != b.bs) return true;
+  return cgh::rows_meet(s->batch, a.bs, n, a.rs, (b.at - a.at) / esz, wa, wb);
 }
 
 // rows of `heads` heads; 0 strides: dense
@@ -101,12 +98,12 @@ extern "C" int cg_rotate(const cg_shape *shape, const cg_rotary *rotary, int32_t
   }
   // rows are written where others are read only in place
   const int64_t esz = shape->dtype == CG_DTYPE_BF16 ? 2 : 4;
-  const uint64_t w[2] = {(uint64_t)hs[0] * shape->head_dim * esz, (uint64_t)hs[1] * shape->head_dim * esz};
+  const int64_t w[2] = {(int64_t)hs[0] * shape->head_dim, (int64_t)hs[1] * shape->head_dim};
   for (int x = 0; x < 2; x++)
     for (int y = 0; y < 2; y++)
-      if (in[x] && in[y] && (x != y || !inplace[x]) && clash(so[x], w[x], si[y], w[y], esz))
+      if (in[x] && in[y] && (x != y || !inplace[x]) && clash(shape, n, so[x], w[x], si[y], w[y], esz))
         return error(CG_E_INVAL, "an output overlaps an input");
-  if (q && k && clash(so[0], w[0], so[1], w[1], esz)) return error(CG_E_INVAL, "the outputs overlap");
+  if (q && k && clash(shape, n, so[0], w[0], so[1], w[1], esz)) return error(CG_E_INVAL, "the outputs overlap");
   for (int x = 0; x < 2; x++) {
     if (!in[x]) continue;
     a.r[x] = cgr::Rows{si[x].at, (void *)so[x].at, si[x].bs, si[x].rs, so[x].bs, so[x].rs, x ? t.k_weight : t.q_weight, hs[x]};

@@ -118,11 +118,9 @@ int cg_read(const cg_shape *shape, const void *payload, uint64_t payload_cap, co
     if (o && (overlap(o, span, payload, pb) || overlap(o, span, meta, mb)))
       return error(CG_E_INVAL, "the rows overlap the cache");
   // keys and values may be parts of the same rows, side by side
-  if (k_out && v_out && overlap(k_out, span, v_out, span)) {
-    const int64_t d = ((const char *)v_out - (const char *)k_out) % (int64_t)(rs * esz);
-    const uint64_t m = (uint64_t)(d < 0 ? d + rs * (int64_t)esz : d);
-    if (bs % rs || m < row * esz || m + row * esz > rs * esz) return error(CG_E_INVAL, "k_out and v_out overlap");
-  }
+  if (k_out && v_out && overlap(k_out, span, v_out, span) &&
+      cgh::rows_meet(shape->batch, bs, n, rs, ((const char *)v_out - (const char *)k_out) / (int64_t)esz, row, row))
+    return error(CG_E_INVAL, "k_out and v_out overlap");
   if (shape->tokens == 0) return CG_OK;
   a.tcap = shape->token_capacity;
   a.tokens = shape->tokens;
