@@ -30,7 +30,8 @@ and 213 at 131072.
 
 Sequences grow by steps and shrink by evict() alone: only the raw rows of a sequence's
 last block are kept, so rows that were appended (drafts that were not accepted) cannot
-be taken back by setting `lengths`.
+be taken back by setting `lengths`.  Evicted rows go on counting in the positions by which
+rotate() turns the rows behind them (`gone`): the keys that stay keep theirs.
 
 All arithmetic runs in the HIP library; this class only owns buffers.  A cache
 belongs to one stream at a time.
@@ -59,8 +60,12 @@ class ServingCache:
         self.meta = torch.zeros(meta // 4, **dev)   # (minimum, step) pairs
         self.tail = torch.zeros((layers, 2, batch, heads, block_tokens, head_dim), dtype=self.dtype, **dev)
         self.mass = torch.zeros((layers, batch, heads, capacity // block_tokens), **dev) if with_mass else None
-        self.lengths = torch.zeros(batch, dtype=torch.int32, **dev)
-        self.starts = torch.zeros(batch, dtype=torch.int32, **dev)   # of the present step
+        self._span = torch.zeros((2, batch), dtype=torch.int32, **dev)
+        self.starts, self.lengths = self._span   # of the present step; with its rows
+        # positions that the rows are turned by: their places and, where blocks may leave, the rows that have left
+        self.gone = torch.zeros(batch, dtype=torch.int32, **dev) if with_mass else None
+        self._turned = torch.zeros_like(self._span) if with_mass else self._span
+        self._turns = cg.make_shape(layers, 2, batch, heads, (1 << 31) - 1, (1 << 31) - 1, head_dim, dtype)
         self._counts = (torch.int32, torch.int64)                    # types of a step's valid rows
         self.n = 0                                                   # rows of the present step
         self._put = set()                                            # layers that have them
@@ -89,12 +94,17 @@ class ServingCache:
             self.lengths.add_(n)
         else:
             self.lengths.add_(valid)
+        if self.gone is not None:
+            import torch
+
+            torch.add(self._span, self.gone, out=self._turned)
 
     def rotate(self, q, k, rotary, positions=None, q_out=None, k_out=None):
-        """Norms and rotation of the step's queries and keys, in place or into q_out and k_out, at the rows' places
-        in the cache or at positions [axes, batch, n]; padding rows are left as they were.  -> (q, k) as rotated."""
+        """Norms and rotation of the step's queries and keys, in place or into q_out and k_out, at the rows' positions
+        in their sequences (also after evictions: every row that a sequence has had counts) or at positions [axes,
+        batch, n]; padding rows are left as they were.  -> (q, k) as rotated."""
         q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-        cg.cg_rotate(self.shape, rotary, q, k, q_out, k_out, self.lengths, self.starts, positions)
+        cg.cg_rotate(self._turns, rotary, q, k, q_out, k_out, self._turned[1], self._turned[0], positions)
         return q_out, k_out
 
     def append(self, layer, k, v):
@@ -140,15 +150,18 @@ class ServingCache:
     def evict(self, budget, sink=1, recent=1):
         """Keep `budget` blocks of every (layer, sequence, head), in place; -> the kept blocks' former numbers.
 
-        Between steps: the rows' positions change, so the present step ends here."""
+        Between steps: the rows' places change, so the present step ends here.  Their positions do not: keys stay
+        as they were turned, and rotate() goes on counting."""
         import torch
 
         if self.mass is None:
             raise ValueError("the cache was made without with_mass")
         s = self.shape
         kept = torch.empty((s.layers, s.batch, s.heads, max(budget, 0)), dtype=torch.int32, device=self.payload.device)
+        had = self.lengths.clone()
         cg.cg_evict(s, self.codec, budget, sink, recent, self.mass, self.payload, self.meta, s, self.payload, self.meta,
                     self.mass, kept, self.lengths, self.lengths)
+        self.gone.add_(had.sub_(self.lengths))
         self.most = min(self.most, budget * self.codec.block_tokens)
         self.n = 0
         return kept
