@@ -103,6 +103,9 @@ class ServingCache:
         """Norms and rotation of the step's queries and keys, in place or into q_out and k_out, at the rows' positions
         in their sequences (also after evictions: every row that a sequence has had counts) or at positions [axes,
         batch, n]; padding rows are left as they were.  -> (q, k) as rotated."""
+        rows = k if q is None else q
+        if rows is not None and rows.shape[1] != self.n:
+            raise ValueError(f"{rows.shape[1]} rows a sequence, the step has {self.n}")
         q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
         cg.cg_rotate(self._turns, rotary, q, k, q_out, k_out, self._turned[1], self._turned[0], positions)
         return q_out, k_out

@@ -173,3 +173,34 @@ def test_a_recorded_step_counts_on_after_evictions(bits):
         if i in (3, 7):
             c.evict(4 if i == 3 else 2, 1, 1)
     assert c.gone.tolist() != [0, 0]
+
+
+def test_rotation_belongs_to_a_step():
+    """Before the first step, after an eviction and for other numbers of rows it is refused, and nothing is turned."""
+    t = torch()
+    c = ServingCache(1, 1, 1, 2, 128, cg.make_gauge(0), with_mass=True, bits=4)
+    rotary = cg.make_rotary(to_dev(np.ones(64, np.float32)))
+    x = t.ones((1, 40, 3, D), dtype=t.bfloat16, device="cuda")
+    q, k, v = x[:, :, :2], x[:, :, 2:], t.ones((1, 40, 1, D), dtype=t.bfloat16, device="cuda")
+
+    def refused(n):
+        for a, b in ((q[:, :n], k[:, :n]), (q[:, :n], None), (None, k[:, :n])):
+            with pytest.raises(ValueError):
+                c.rotate(a, b, rotary)
+        with pytest.raises(ValueError):
+            c.rotate(q[:, :n], k[:, :n], rotary, positions=t.zeros((1, 1, n), dtype=t.int32, device="cuda"))
+        assert bool((x == 1).all())
+
+    refused(1)
+    with pytest.raises(ValueError):
+        c.rotate(None, None, rotary)
+    c.begin(40)
+    refused(39)
+    c.append(0, k.contiguous(), v)
+    c.attend(0, q)
+    c.evict(1, 0, 1)
+    refused(40)
+    c.begin(1)
+    refused(40)
+    y = c.rotate(q[:, :1], None, rotary, q_out=t.empty_like(q[:, :1]))
+    assert y[1] is None and not bool((y[0] == 1).any())
