@@ -38,6 +38,7 @@ __device__ __forceinline__ float lanes(float v) {
 constexpr int XOR1 = 0xB1, XOR2 = 0x4E, XOR3 = 0x1B, MIRROR8 = 0x141, TURN8 = 0x128;
 
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+typedef float gauge4_t __attribute__((ext_vector_type(4), aligned(4)));  // gauges are aligned as floats are
 
 // 8 of 32 channels of a row: bf16 8 q .. + 7 of quarter q of the wave, fp32 4 q .. + 3 and 16 + 4 q .. + 3
 template <bool BF16>
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(NT, G == 128 ? 2 : G == 32 && !BF16 ? 4 : 8) void k
       const float *row = gf + (32 * w + 16 * nb + n) * G + 4 * kr;  // the groups follow one another
 #pragma unroll
       for (int k = 0; k < G / 16; k++) {
-        const float4 g = *(const float4 *)(row + 16 * k);
+        const gauge4_t g = *(const gauge4_t *)(row + 16 * k);
         fr.b[nb][4 * k] = g.x;
         fr.b[nb][4 * k + 1] = g.y;
         fr.b[nb][4 * k + 2] = g.z;
