@@ -26,4 +26,18 @@ __device__ __forceinline__ uint32_t range_bits(float2 m) {  // of the larger end
 // smallest E with |x| < 2^E, of the largest magnitude's bits
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 126; }
 
+// How a row's sums leave its wave.  Sums of weights (the largest 1) times values of 2^64 and more are kept 2^-32 of
+// themselves beside a maximum 32 higher, and so is the sum of the weights: over 2^31 tokens at most they then stay
+// below the largest value, and 2^up, which may be 2^128, is not formed alone.
+struct FarSums {
+  bool is;
+  float up, less, shift;  // log2 of the sums' scale, what is taken off it (18 with the weights' and values' own), and the maximum's
+  __device__ __forceinline__ FarSums(float m, float mo) {
+    up = m > -INFINITY ? mo - m : 0.0f;
+    is = up > 64.0f;
+    shift = is ? 32.0f : 0.0f;
+    less = is ? 50.0f : 0.0f;
+  }
+};
+
 }  // namespace cga

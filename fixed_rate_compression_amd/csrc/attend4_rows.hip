@@ -465,9 +465,12 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !MASS ? 3 : 2) void k_attend4_r
   const float *gv = a.gv + (int64_t)h * D * a.g;
   if (splits == 1 && front) load_gauge<true>(gv, a.g, 0, gw);
   // true sums: acc 2^(mo - m) less the 2^9 of the weights and of the values; a lane's channels are of group grp
+  const FarSums far(st.m, st.mo);
 #pragma unroll
-  for (int j = 0; j < 8; j++) acc[j] *= 0x1p-18f;
-  const float ks = st.m > -INFINITY ? exp2_fast(st.mo - st.m) : 0.0f;
+  for (int j = 0; j < 8; j++) acc[j] *= far.is ? 1.0f : 0x1p-18f;
+  const float ks = st.m > -INFINITY ? exp2_fast(far.up - far.less) : 0.0f;
+  st.m += far.shift;
+  st.l *= far.is ? 0x1p-32f : 1.0f;
   finish_few<BF16, NW>(a, fp, lds, ml, gv, gw, front, st.m, st.l, ks, (st.poison >> grp) & 1u ? NAN : 0.0f, acc);
 }
 

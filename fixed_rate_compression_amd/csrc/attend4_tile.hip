@@ -584,7 +584,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
     const float Ls = st.l + __shfl_xor(st.l, 32);
     const bool some = st.m > -INFINITY;
     const float inv = a.splits > 1 ? 1.0f : Ls > 0.0f ? 1.0f / Ls : 0.0f;
-    const float ks = some ? inv * exp2_fast(st.mo - st.m) : 0.0f;
+    const FarSums far(st.m, st.mo);  // one split: divided by the sum of the weights already
+    const float less = !far.is || a.splits > 1 ? far.less : far.less - far.shift;
+    const float ks = some ? inv * exp2_fast(far.up - less) : 0.0f, kv = far.is ? 1.0f : 0x1p-18f;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       const float k = (st.poison >> j) & 1u ? NAN : 0.0f;  // a group of 32 channels
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
       for (int r = 0; r < 16; r += 4) {
         f4_t v;
 #pragma unroll
-        for (int x = 0; x < 4; x++) v[x] = __builtin_fmaf(acc[j][r + x] * 0x1p-18f, ks, k);  // 2^9 of the values, 2^9 of f
+        for (int x = 0; x < 4; x++) v[x] = __builtin_fmaf(acc[j][r + x] * kv, ks, k);  // 2^9 of the values, 2^9 of f
         float *o = us + rr * PITCH + 32 * j + 2 * r;
         if constexpr (V2) {
           *(f4_t *)(o + 4 * half) = v;
@@ -604,7 +606,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
     }
     if (half == 0 && rr < nr) {
       if (a.splits > 1) {
-        a.part_ml[((int64_t)bh * a.splits + split) * a.rows + wr] = make_float2(st.m, Ls);
+        a.part_ml[((int64_t)bh * a.splits + split) * a.rows + wr] = make_float2(st.m + far.shift, far.is ? Ls * 0x1p-32f : Ls);
       } else {
         if (a.lse) store_lse(a, b, h, wr, st.m, Ls);
         if (a.lse2) a.lse2[(int64_t)bh * a.rows + wr] = Ls != 0.0f ? st.m + __builtin_log2f(Ls) : INFINITY;
