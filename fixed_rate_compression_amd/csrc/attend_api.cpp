@@ -29,7 +29,8 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Splits of the few-row form.  256 compute units hold `kResident` of its
 // workgroups at once (three on each; two where block sums are gathered: more
-// registers).  A round of them takes about 6 us for what does not depend on the
+// registers; and two for 9 rows and more over 4 bits in fp32 storage: 57 KB of LDS each.  8 KV heads and 12 rows,
+// 65536 tokens 47 us, split for three 54; 4 sequences to 16384 30 and 37, 32 to 4096 62 and 67).  A round of them takes about 6 us for what does not depend on the
 // tokens, plus each workgroup's tokens at its share of 5.5 TB/s, at best 12.5 ns a
 // token; a merge takes about 4.5 us.  Of one split and the most that one, two,
 // three or four rounds hold the fastest by that sum is taken, with at least 256
@@ -38,7 +39,7 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // (one round) 19 us, 10 splits 24; 200 heads of 4000 tokens: one split 55 us, 3
 // splits and merge 49; 800 heads: 171 and 162; 300 heads of 8000 tokens: one split
 // 121, 2 splits 130; 131072 tokens with sums by 512 workgroups 54 us, by 768 66.
-constexpr int64_t kResident = 768, kResidentSums = 512, kMinTokens = 256;
+constexpr int64_t kResident = 768, kResidentTwo = 512, kMinTokens = 256;
 
 int64_t few_splits(int64_t work, int64_t tokens, int64_t resident, double token_us) {
   const int64_t most = (tokens + kMinTokens - 1) / kMinTokens;
@@ -136,11 +137,12 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   // sequences 31, 37 and 45 against 40, 45 and 47
   p.few = p.tiles <= cga::FEW_TILES && !(kivi && many);
   const int64_t work = fields * (p.few ? p.tiles : (p.rows + 127) / 128);
+  const int64_t resident = mass || (kivi && s->dtype != CG_DTYPE_BF16 && p.rows > 8) ? kResidentTwo : kResident;
   int64_t sp = 1;
   if (work > 0 && p.few) {
     // a token's codes (and ranges) at what the many workgroups reach
     const double token_us = kivi ? 192.0 / 4.9e6 : 256.0 / 5.5e6;
-    sp = few_splits(work, s->tokens, mass ? kResidentSums : kResident, token_us);
+    sp = few_splits(work, s->tokens, resident, token_us);
   } else if (work > 0) {
     sp = tile_splits(work, fields * p.rows, s->tokens);
   }
