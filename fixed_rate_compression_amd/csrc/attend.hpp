@@ -83,12 +83,12 @@ struct AttendArgs {
 // rows [0, rows) of every field over its tokens, one workgroup per (field,
 // row tile, split); splits > 1 leaves parts for merge_launch
 hipError_t rows_launch(const AttendArgs &a, bool bf16, hipStream_t s);
-// the same over the 4-bit cache, of any number of rows
+// the same over the 4-bit cache
 hipError_t rows4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // the same for many rows, one workgroup per (field, 128 rows, split)
 hipError_t tile_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 // and over the 4-bit cache, one per (field, 128 or 256 rows, split), after ranges4_launch
-int ranges4_bytes(bool bf16, bool two);  // of a block
+int ranges4_bytes(bool bf16);  // of a block, at most
 int units4_bytes();
 hipError_t ranges4_launch(const AttendArgs &a, bool bf16, hipStream_t s);
 hipError_t tile4_launch(const AttendArgs &a, bool bf16, hipStream_t s);

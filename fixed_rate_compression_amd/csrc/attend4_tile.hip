@@ -37,7 +37,7 @@ struct Lds4 {
 // (minimum, step) in fp32.  Values likewise, a pair a token and group.
 struct Unit4 {
   int ek, ev;
-  uint32_t bad, none;  // whether there is such a range
+  uint32_t bad;  // whether there is such a range
   uint64_t bad0, bad1;
 };
 template <bool P2, bool V2>
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(NTH) void k_ranges4(const AttendArgs a, int blocks)
   }
   const int ek = exponent_of(wave_umax(max(range_bits(k[0]), range_bits(k[1]))));
   const int ev = exponent_of(wave_umax(max(range_bits(v[0]), range_bits(v[1]))));
-  if (lane == 0) ((Unit4 *)a.units)[at] = Unit4{ek, ev, bad[0] | bad[1] ? 1u : 0u, 0u, bad[0], bad[1]};
+  if (lane == 0) ((Unit4 *)a.units)[at] = Unit4{ek, ev, bad[0] | bad[1] ? 1u : 0u, bad[0], bad[1]};
   uint8_t *o = a.ranges + at * R::BYTES;
 #pragma unroll
   for (int x = 0; x < 2; x++) {
@@ -628,7 +628,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attend4_tile(const AttendArgs a)
   store_rows<BF16, NT>(a, b, h, r0, nr, us);
 }
 
-int ranges4_bytes(bool bf16, bool two) { return (two ? 1024 : 512) + (bf16 ? 512 : 1024); }
+int ranges4_bytes(bool bf16) { return bf16 ? Ranges4<true, false>::BYTES : Ranges4<true, true>::BYTES; }
 int units4_bytes() { return (int)sizeof(Unit4); }
 
 hipError_t ranges4_launch(const AttendArgs &a, bool bf16, hipStream_t s) {

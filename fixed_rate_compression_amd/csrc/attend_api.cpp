@@ -114,10 +114,10 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   p.batch = s->batch;
   if (kivi && many) {
     const uint64_t blocks = (uint64_t)(s->tokens + cga::UNIT - 1) / cga::UNIT;
-    const uint64_t each = s->heads * blocks * (uint64_t)(cga::ranges4_bytes(s->dtype == CG_DTYPE_BF16, true) + cga::units4_bytes());
+    const uint64_t each = s->heads * blocks * (uint64_t)(cga::ranges4_bytes(s->dtype == CG_DTYPE_BF16) + cga::units4_bytes());
     const uint64_t fit = each ? kMaxRanges / each : s->batch;
     if (fit < (uint64_t)p.batch) p.batch = fit ? (int)fit : 1;
-    p.ranges_bytes = up256((size_t)p.batch * s->heads * blocks * cga::ranges4_bytes(s->dtype == CG_DTYPE_BF16, true));
+    p.ranges_bytes = up256((size_t)p.batch * s->heads * blocks * cga::ranges4_bytes(s->dtype == CG_DTYPE_BF16));
     p.units_bytes = up256((size_t)p.batch * s->heads * blocks * cga::units4_bytes());
   }
   const int64_t fields = (int64_t)p.batch * s->heads;

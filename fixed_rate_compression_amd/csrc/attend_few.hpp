@@ -61,8 +61,6 @@ __device__ __forceinline__ void finish_few(const AttendArgs &a, const FewPlace &
     if (c == 0 && r < nr) {
       if (a.part_ml) a.part_ml[pr] = make_float2(M, L);
       if (splits == 1 && a.lse) store_lse(a, b, h, r0 + r, M, L);
-      if (splits == 1 && a.lse2)
-        a.lse2[((int64_t)b * a.heads + h) * a.rows + r0 + r] = L != 0.0f ? M + __builtin_log2f(L) : INFINITY;
     }
     if (splits > 1) {
       if (r < nr) *(f4_t *)(a.part_o + pr * D + c) = v;
