@@ -10,6 +10,10 @@
 // largest value to [2^8, 2^9), so that halves keep 2^-33 of it.  That and the ranges in the
 // form in which they are used come from a launch before (k_ranges4): the vector units bound
 // this kernel, and forming them at every use took 64 of its 235 vector instructions a wave and unit.
+//
+// 2048 queries over 8192 tokens, 8 KV heads, four query heads each: 292 us, 825 TFLOP/s (a library product of 8192^3
+// 1221 in fp16): matrix cores 38 % of the cycles, vector instructions 41 %, hardly at once.  With log-sums, keys and
+// queries in two parts, 501; fp32 storage 701.
 #include <type_traits>
 
 #include "attend.hpp"

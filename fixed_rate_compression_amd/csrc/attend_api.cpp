@@ -107,7 +107,9 @@ Plan make_plan(const cg_shape *s, const cg_codec *c, const cg_attn *t, bool mass
   // Four row tiles over the 4-bit cache: each decodes the same codes, the many-row form once.  64 rows of 8 KV
   // heads, us by row tiles and by tiles of 128: 8 sequences of 500, 2048, 4096 and 16384 tokens 14 and 33, 33 and
   // 45, 78 and 56, 185 and 133, 32 of 2048 104 and 77; with log-sums of 4096 88 and 86, 32 of 4096 242 and
-  // 208.  48 rows: 8 of 4096 52 and 52, of 16384 144 and 130, with log-sums 190 and 200.
+  // 208.  48 rows: 8 of 4096 52 and 52, of 16384 144 and 130, with log-sums 190 and 200.  The bound decides, not
+  // what is there (lengths are on the device): at a bound of 4096, 8 sequences of 100, 500, 2000 and 4000 tokens take
+  // 14, 27, 42 and 58 by row tiles (splits planned for the bound) and 36, 39, 41 and 50 by tiles of 128.
   const bool many = rows > (int64_t)cga::FEW_TILES * cga::ROWS ||
                     (kivi && rows > (int64_t)(cga::FEW_TILES - 1) * cga::ROWS &&
                      (double)s->batch * s->heads * (double)s->tokens >= kManyTokens);

@@ -4,9 +4,10 @@
 //
 // A row's query heads, and its key heads, go in groups of PER; 16 lanes take a group, 16 bytes a lane to a
 // head (fp32: 32 bytes), and a workgroup 16 groups.  The loads are asked for before the sines and cosines of
-// the rows are formed, and those go into one pair of factors a channel with the norm's weights, once a group.  An angle is a product of far positions, so it is taken in fp64, in turns,
-// and only what is left of whole turns goes on in fp32.  The other half of a pair comes
-// from another lane's registers, a row rotation where all 128 channels turn.
+// the rows are formed, and those go into one pair of factors a channel with the norm's weights, once a group.
+// An angle is a product of far positions, so it is taken in fp64, in turns, and only what is left of whole
+// turns goes on in fp32.  The other half of a pair comes from another lane's registers, a row rotation where
+// all 128 channels turn.  Squares are summed in fp32: a head whose sum passes it (values of 1e19) is zeros.
 //
 // Bound by memory traffic where there are many rows: 4000 rows of 2 sequences, 32 + 8 heads, three axes, both
 // norms (164 MB) take 34.5 us, 4750 GB/s, where a copy of the same size runs at 5100.  With factors formed a

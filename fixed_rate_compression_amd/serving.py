@@ -23,10 +23,10 @@ fit, does not see replays: rows past the capacity are dropped).
 
 Attention is planned for sequences as long as the capacity (a recorded step has to
 serve them at any length), so a capacity far above what is there costs splits and
-a merge: with 8 KV heads x 4 query heads a token over 1000 takes 13 us at a capacity
-of 131072 and 11 at 1024, a prompt of 300 tokens 32 us from 1024 on and 18.5 at 320, four
-prompts of 1000 with weights 93 us up to 32768 (1000 MiB of workspace there, 32 at 1024)
-and 213 at 131072.
+a merge.  With 8 KV heads x 4 query heads, 8 bits and 4: a token over 1000 takes 14 and 14 us at a
+capacity of 131072, 12 and 14 at 1024, 11 at 2048; a prompt of 300 tokens 32 and 34 from 1024 on,
+22 at 320; four prompts of 1000 with weights 110 and 113 up to 32768 (1000 and 1049 MiB of workspace there, 31
+and 33 at 1024), 231 and 246 at 131072; 16 queries of 8 sequences of 500 11 and 37 at 4096, 10 and 12 at 1024.
 
 Sequences grow by steps and shrink by evict() alone: only the raw rows of a sequence's
 last block are kept, so rows that were appended (drafts that were not accepted) cannot

@@ -559,7 +559,8 @@ typedef struct cg_rows {  /* device, storage format, [batch][n][heads][head_dim]
  *   positions     device int32 [axes][batch][n], or NULL (axes 1): the rows' places,
  *                 starts + i
  * Rows that are padding are left as they were.  Angles are taken in fp64 and their whole turns
- * left out; norms, products and sums are fp32, rounded to the storage format once.
+ * left out; norms, products and sums are fp32, rounded to the storage format once (the squares of a
+ * head have to be summed in fp32: values of 1e19 and more give zeros).
  * Asynchronous on stream.
  */
 int cg_rotate(const cg_shape *shape, const cg_rotary *rotary, int32_t q_heads, int32_t n,
