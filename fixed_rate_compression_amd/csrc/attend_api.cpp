@@ -29,13 +29,14 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Splits of the few-row form.  256 compute units hold `kResident` of its
 // workgroups at once (three on each; two where block sums are gathered: more
-// registers; and two for 9 rows and more over 4 bits in fp32 storage: 57 KB of LDS each.  8 KV heads and 12 rows,
-// 65536 tokens 47 us, split for three 54; 4 sequences to 16384 30 and 37, 32 to 4096 62 and 67).  A round of them takes about 6 us for what does not depend on the
+// registers; and two for 9 rows and more over 4 bits in fp32 storage: 57 KB of LDS
+// each).  A round of them takes about 6 us for what does not depend on the
 // tokens, plus each workgroup's tokens at its share of 5.5 TB/s, at best 12.5 ns a
 // token; a merge takes about 4.5 us.  Of one split and the most that one, two,
 // three or four rounds hold the fastest by that sum is taken, with at least 256
 // tokens (two units a wave) to a workgroup.  (4 bits: 4.9 TB/s; 32 sequences of 8 KV heads and 4096 tokens 46 us
-// in three splits, 59 in one.)  80 KV heads of 3000 tokens: 9 splits
+// in three splits, 59 in one; 12 rows of fp32 storage, 65536 tokens 47 us, split for three to a unit 54, 4
+// sequences to 16384 30 and 37, 32 to 4096 62 and 67.)  80 KV heads of 3000 tokens: 9 splits
 // (one round) 19 us, 10 splits 24; 200 heads of 4000 tokens: one split 55 us, 3
 // splits and merge 49; 800 heads: 171 and 162; 300 heads of 8000 tokens: one split
 // 121, 2 splits 130; 131072 tokens with sums by 512 workgroups 54 us, by 768 66.

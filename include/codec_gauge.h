@@ -471,7 +471,8 @@ int cg_attend_workspace_bytes(const cg_shape *shape, const cg_gauge *gauge, cons
  * is NaN; a value block's NaN range reaches out alone (4 bits: a NaN or infinity in
  * a token's range, the 32 channels of that range before the inverse gauge).
  * Queries that see nothing of such a block (4-bit values: token) are not touched by it.
- * Scores, sums and weights of a sum are fp32; the operands of the matrix products
+ * Scores, sums and weights of a sum are fp32 (8 bits: with a row's largest weight as 1, so that a sum of
+ * weights times values past 3.4e38 is not finite; 4 bits: at any size); the operands of the matrix products
  * are fp16.  8 bits: queries in two parts (2^-23 of a row's largest channel), in one (2^-11
  * of a channel) for bf16 storage with more than 64 rows a KV head and neither lse nor
  * mass; weights for fp32 storage in two parts, for bf16 storage in one (2^-11).
